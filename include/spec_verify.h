@@ -52,7 +52,9 @@ typedef enum {
     SPEC_ERR_WORKSPACE = 4    /* workspace too small or not 256-byte aligned */
 } spec_status;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* Logits are f32 or bf16; the operators around the verification (below) also
+ * take f16, and e4m3 (8 bits, with a scale per row) as a cache's type. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2, SPEC_E4M3 = 3 } spec_dtype;
 
 #define SPEC_MAX_K 31
 
@@ -63,7 +65,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_BADBIT_EMPTY_ROW 8u   /* a sampling row j <= num_draft[b] whose logits are all -inf */
 #define SPEC_BADBIT_NO_PROBS 16u   /* a sampling request with drafts but draft_probs == NULL */
 #define SPEC_BADBIT_TIMEOUT 32u    /* an internal bounded wait gave up (never expected) */
-#define SPEC_BADBIT_TREE 64u       /* spec_verify_tree: a node whose parent is not an earlier node */
+#define SPEC_BADBIT_TREE 64u       /* a tree node whose parent is not an earlier node */
+#define SPEC_BADBIT_PAGE 128u      /* a context past its page table, a page or a slot outside the cache */
 
 /* Human-readable name of a status code (static string). */
 const char* spec_status_str(spec_status s);
@@ -495,6 +498,231 @@ spec_status spec_verify_host(const void* h_logits, spec_dtype logits_dtype, cons
  */
 spec_status spec_philox_fill(uint64_t seed, const uint32_t* ctrs, int64_t n, uint32_t* out,
                              spec_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the verification: what every layer of the target does
+ * in the pass that scores the drafted nodes ("投机采样", 第二步: the target
+ * scores all candidates in one forward; 验证方案: the nodes of a trie in one
+ * pass), over a paged key/value cache.  One decoding step is
+ *   spec_tree_plan        once: positions, cache slots and ancestor masks of
+ *                         the nodes, and the division of the attention's work
+ *   per layer:
+ *     spec_kv_write       rotates the nodes' queries and keys and writes their
+ *                         key and value rows to their slots
+ *     spec_tree_attention every node's attention over its context and ancestors
+ *   spec_verify_tree (or spec_verify for a chain): which nodes are kept
+ *   spec_kv_commit        the kept path's rows become part of the context.
+ * Node 0 of a request is the token emitted last (its row is not in the cache
+ * yet), nodes 1.. are drafts, exactly as spec_verify_tree numbers them.
+ * The conventions at the top of this file hold, except that tensors have
+ * strides where an argument says so.
+ */
+
+/*
+ * A paged key/value cache of one layer (a plain description, passed by host
+ * pointer; the library keeps nothing of it).
+ *   k, v              [num_pages, heads, page_size, head_dim], dtype bf16, f16
+ *                     or e4m3, 16-byte aligned; element (p, h, t, d) lies at
+ *                     p * page_stride + h * head_stride + t * token_stride + d
+ *                     (strides in elements, each a multiple of 16 bytes; any
+ *                     order of the page, head and token dimensions).
+ *   k_scale, v_scale  e4m3 only: [num_pages, heads, page_size] bytes, dense,
+ *                     16-byte aligned.  Byte s of a row, 1 <= s <= 253, stands
+ *                     for the factor 2^(s - 127) of that row's values.
+ *   page_size         tokens of a page, a multiple of 16 in [16, 65536].
+ *   head_dim          a multiple of 8 (e4m3: of 16) in [8, 256].
+ * Slot s is token s % page_size of page s / page_size.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int dtype; /* spec_dtype */
+    int num_pages, page_size, heads, head_dim;
+    int64_t page_stride, head_stride, token_stride;
+} spec_kv_cache;
+
+/*
+ * Rotary positions: pair i < rot / 2 of a head turns by the angle
+ * position * theta_i.
+ *   turns   [rot / 2] uint64, device: theta_i / (2 pi) in units of 2^-64 turns
+ *           (spec_rope_turns fills a host array).  A position's phase is the
+ *           low 64 bits of position * turns[i]: whole turns drop out exactly,
+ *           at any position.
+ *   rot     channels that turn, even, 2 <= rot <= head_dim; the others are
+ *           copied.
+ *   layout  SPEC_ROPE_HALF: pair i is channels (i, i + rot / 2);
+ *           SPEC_ROPE_INTERLEAVED: channels (2 i, 2 i + 1).
+ *   scale   factor on the rotated channels (1 unless a scaling wants another).
+ */
+enum { SPEC_ROPE_HALF = 0, SPEC_ROPE_INTERLEAVED = 1 };
+typedef struct {
+    const uint64_t* turns;
+    int rot, layout;
+    float scale;
+} spec_rope_table;
+
+/*
+ * spec_rope_turns -- the frequencies theta_i = base^(-2 i / rot) as turns, for
+ * a context stretched by `factor` >= 1:
+ *   SPEC_ROPE_PLAIN     as they are (factor is not used)
+ *   SPEC_ROPE_LINEAR    theta_i / factor
+ *   SPEC_ROPE_NTK       with base * factor^(rot / (rot - 2)): the slowest pair
+ *                       slows by factor, the fastest keeps its pace
+ *   SPEC_ROPE_BY_PARTS  theta_i ((1 - g) / factor + g), g = clamp((r_i - slow)
+ *                       / (fast - slow), 0, 1) for r_i = original_len theta_i
+ *                       / (2 pi) turns within the original context; *scale =
+ *                       0.1 ln(factor) + 1 (1 for the other kinds).
+ * Host code in double precision; out_turns [rot / 2] and out_scale are host
+ * memory.  SPEC_ERR_INVALID_ARG for an odd rot or one outside [2, 256], base
+ * <= 1, factor < 1, and for BY_PARTS original_len <= 0 or fast <= slow.
+ */
+enum { SPEC_ROPE_PLAIN = 0, SPEC_ROPE_LINEAR = 1, SPEC_ROPE_NTK = 2, SPEC_ROPE_BY_PARTS = 3 };
+spec_status spec_rope_turns(int rot, double base, int scaling, double factor, double original_len,
+                            double fast, double slow, uint64_t* out_turns, float* out_scale);
+
+/*
+ * spec_rope -- rotate the heads of up to two tensors (queries and keys).
+ *   q, k          [T, q_heads, D] and [T, k_heads, D], dtype f32, bf16 or f16,
+ *                 token and head strides in elements, channels contiguous;
+ *                 either may be NULL (with 0 heads).
+ *   out_q, out_k  the same shapes with strides of their own; out_q == q with
+ *                 equal strides rotates in place (so for k).  Other overlap of
+ *                 inputs and outputs is not allowed.
+ *   positions     [T] int32 (a negative position turns backwards).
+ *   inverse       non-zero turns by the negative angle (and the same scale):
+ *                 the transpose of the rotation, which takes the gradient of
+ *                 its output to the gradient of its input.
+ * (a, b) -> scale (a cos - b sin, a sin + b cos) in float32, one rounding.
+ */
+spec_status spec_rope(const void* q, int q_heads, int64_t q_token_stride, int64_t q_head_stride,
+                      void* out_q, int64_t oq_token_stride, int64_t oq_head_stride, const void* k,
+                      int k_heads, int64_t k_token_stride, int64_t k_head_stride, void* out_k,
+                      int64_t ok_token_stride, int64_t ok_head_stride, spec_dtype dtype, int D,
+                      int64_t T, const int32_t* positions, const spec_rope_table* table,
+                      int inverse, spec_stream_t stream);
+
+/*
+ * spec_kv_write -- write T tokens' key and value rows to their cache slots.
+ *   k, v       [T, heads, head_dim], dtype: the cache's own type, or f32, bf16
+ *              or f16 into an e4m3 cache; strides as in spec_rope.
+ *   slots      [T] int64; a token with a negative slot is not written.  A slot
+ *              at or past num_pages * page_size is not written either and
+ *              sets SPEC_BADBIT_PAGE in *dev_status (where given).  No two
+ *              tokens may name one slot.
+ *   table, positions  NULL, or the rotation of the keys on their way (and
+ *              of q [T, q_heads, head_dim] into out_q, strides as in
+ *              spec_rope; q may be NULL; out_q of a token whose slot is
+ *              negative is written all the same).
+ *   dev_status NULL or one device int32, or-ed into (not zeroed).
+ * An e4m3 row is stored as x 2^-e rounded to the nearest e4m3 value (ties to
+ * even), with e the least integer for which max |x| <= 448 2^e, clamped to
+ * [-126, 127]: powers of two make the division exact, so that a value is
+ * rounded once.  Infinities and NaN become NaN and do not count for the max.
+ */
+spec_status spec_kv_write(const spec_kv_cache* cache, const void* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                          int64_t v_head_stride, spec_dtype dtype, int64_t T,
+                          const int64_t* slots, const int32_t* positions,
+                          const spec_rope_table* table, const void* q, int q_heads,
+                          int64_t q_token_stride, int64_t q_head_stride, void* out_q,
+                          int64_t oq_token_stride, int64_t oq_head_stride, int32_t* dev_status,
+                          spec_stream_t stream);
+
+/*
+ * spec_kv_read -- the rows of T slots as out_k, out_v [T, heads, head_dim] of
+ * `dtype` (dense; f32, bf16 or f16, rounded to nearest).  A slot outside the
+ * cache (a negative one among them) reads as zeros.
+ */
+spec_status spec_kv_read(const spec_kv_cache* cache, int64_t T, const int64_t* slots,
+                         spec_dtype dtype, void* out_k, void* out_v, spec_stream_t stream);
+
+/*
+ * spec_tree_plan -- where the nodes of B requests stand.
+ *   tree_parents [B, N] int32, num_nodes [B]: as in spec_verify_tree, N <= 32
+ *                (a chain of K drafts has N = K + 1 and parents c - 1).
+ *   context_len  [B] int32: tokens of the request already in the cache.
+ *   page_table   [B, max_pages] int32: the request's pages in order.
+ *   page_size, num_pages  of the caches that the plan will be used with.
+ *   positions    [B, N] int32 (written): context_len + depth of the node.
+ *   slots        [B, N] int64 (written): the cache slot of token context_len +
+ *                v of the request, for node v.
+ *   masks        [B, N] uint32 (written): bit u of node v is set iff u is v or
+ *                one of its ancestors.
+ *   plan         at least spec_tree_plan_size(B) bytes, 256-byte aligned
+ *                (written): the requests' lengths and their tiles, which
+ *                spec_tree_attention divides over the GPU.
+ *   dev_status   NULL or one device int32 (zeroed, then or-ed into).
+ * Nodes v >= num_nodes[b] get position 0, slot -1 and mask 0.  A bad request
+ * (num_nodes outside [1, N]: SPEC_BADBIT_NUM_DRAFT; a parent that is not an
+ * earlier node: SPEC_BADBIT_TREE; a negative context, one past its page table, or
+ * a page outside the cache: SPEC_BADBIT_PAGE) gets that for all of its nodes:
+ * nothing of it is written or read.
+ * One plan serves every layer of the step; the calls that use it must not
+ * overlap on the GPU.
+ */
+size_t spec_tree_plan_size(int B);
+spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes,
+                           const int32_t* context_len, const int32_t* page_table, int B, int N,
+                           int max_pages, int page_size, int num_pages, int32_t* positions,
+                           int64_t* slots, uint32_t* masks, void* plan, size_t plan_bytes,
+                           int32_t* dev_status, spec_stream_t stream);
+
+/*
+ * spec_tree_attention -- attention of the drafted nodes over the cache:
+ * node v of request b sees the request's context_len tokens and node u iff
+ * bit u of masks[b, v] is set,
+ *   out[b, v, h] = sum_t softmax_t(scale q[b, v, h] . K[t, h / G]) V[t, h / G],
+ * G = q_heads / cache.heads.  N = 1 is ordinary decoding of one token.
+ *   q            [B, N, q_heads, head_dim], bf16 or f16 (a 16-bit cache: its
+ *                own type), 16-byte aligned, batch, node and head strides in
+ *                elements, multiples of 8; channels contiguous.
+ *   masks        [B, N] uint32: the plan's, or any other (bits of nodes at
+ *                or past num_nodes are ignored).
+ *   out          [B, N, q_heads, head_dim] of q's type, dense, 16-byte aligned
+ *                (written).  A row that sees nothing, a node past num_nodes and
+ *                a bad request's nodes get zeros.
+ *   lse          NULL or [B, N, q_heads] f32 (written): the natural logarithm of
+ *                sum_t exp(scale q . K[t]); -inf for a row that sees nothing.
+ *   plan         of spec_tree_plan, with the same B, N and page table.
+ *   workspace    at least spec_tree_attention_workspace_size(...) bytes,
+ *                256-byte aligned, no initialisation.
+ *   dev_status   NULL or one device int32, or-ed into (SPEC_BADBIT_TIMEOUT).
+ * Scores and sums are float32; weights are rounded to q's type (an e4m3
+ * cache: to f16) before they meet V.  What a row does not see has no effect on it,
+ * whatever it holds (infinities and NaN too).
+ * SPEC_ERR_UNSUPPORTED: N > 32, q_heads not a multiple of the cache's heads,
+ * misaligned pointers or strides.
+ */
+size_t spec_tree_attention_workspace_size(const spec_kv_cache* cache, int q_heads);
+spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q_node_stride,
+                                int64_t q_head_stride, spec_dtype dtype, int B, int N, int q_heads,
+                                const spec_kv_cache* cache, const int32_t* page_table,
+                                int max_pages, const uint32_t* masks, const void* plan,
+                                float scale, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_status,
+                                spec_stream_t stream);
+
+/*
+ * spec_kv_commit -- after the verification: the rows of the kept nodes move to
+ * the places right after the context, in path order, in each of num_caches
+ * caches (the layers; <= SPEC_MAX_COMMIT_CACHES a call, equal shapes).
+ *   masks, slots, context_len: those of the step's plan.
+ *   last_node    [B] int32: the last kept node (spec_verify_tree's
+ *                out_last_node, or out_num_accepted of a chain, whose nodes
+ *                are numbered by depth); negative for a bad request.
+ *   new_context_len [B] int32 (written; may be context_len itself):
+ *                context_len + depth of last_node + 1, or context_len as it
+ *                was where last_node is negative or not a node of the request
+ *                (SPEC_BADBIT_TREE).
+ *   dev_status   NULL or one device int32, or-ed into.
+ */
+#define SPEC_MAX_COMMIT_CACHES 64
+spec_status spec_kv_commit(const spec_kv_cache* caches, int num_caches, const uint32_t* masks,
+                           const int64_t* slots, const int32_t* last_node,
+                           const int32_t* context_len, int B, int N, int32_t* new_context_len,
+                           int32_t* dev_status, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

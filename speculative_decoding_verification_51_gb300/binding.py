@@ -9,17 +9,20 @@ the library's kernels; there is no fallback.  torch is used for allocation
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 import threading
+from dataclasses import dataclass
 
 import torch
 
 from . import build as _build
 
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA, SPEC_ERR_WORKSPACE = range(5)
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16, SPEC_E4M3 = 0, 1, 2, 3
 BADBIT = {"num_draft": 1, "temperature": 2, "draft_id": 4, "empty_row": 8, "no_probs": 16,
-          "timeout": 32, "tree": 64}
+          "timeout": 32, "tree": 64, "page": 128}
 MODE_BAD, MODE_GREEDY, MODE_RESIDUAL, MODE_BONUS, MODE_FALLBACK, MODE_TYPICAL = -1, 0, 1, 2, 3, 4
 MAX_K = 31
 # kernels of one call, in launch order: the request-by-request verifier
@@ -89,6 +92,29 @@ def _declare(lib):
                                      vp, vp, sz, vp]
     lib.spec_philox_fill.restype = i32
     lib.spec_philox_fill.argtypes = [u64, vp, i64, vp, vp]
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    side = [vp, i32, i64, i64]  # a tensor of heads: pointer, heads, token and head strides
+    lib.spec_rope_turns.restype = i32
+    lib.spec_rope_turns.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.spec_rope.restype = i32
+    lib.spec_rope.argtypes = 2 * (side + [vp, i64, i64]) + [i32, i32, i64, vp, vp, i32, vp]
+    lib.spec_kv_write.restype = i32
+    lib.spec_kv_write.argtypes = [vp, vp, i64, i64, vp, i64, i64, i32, i64, vp, vp, vp] + side + \
+        [vp, i64, i64, vp, vp]
+    lib.spec_kv_read.restype = i32
+    lib.spec_kv_read.argtypes = [vp, i64, vp, i32, vp, vp, vp]
+    lib.spec_tree_plan_size.restype = sz
+    lib.spec_tree_plan_size.argtypes = [i32]
+    lib.spec_tree_plan.restype = i32
+    lib.spec_tree_plan.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp,
+                                   vp]
+    lib.spec_tree_attention_workspace_size.restype = sz
+    lib.spec_tree_attention_workspace_size.argtypes = [vp, i32]
+    lib.spec_tree_attention.restype = i32
+    lib.spec_tree_attention.argtypes = [vp, i64, i64, i64, i32, i32, i32, i32, vp, vp, i32, vp, vp,
+                                        f32, vp, vp, vp, sz, vp, vp]
+    lib.spec_kv_commit.restype = i32
+    lib.spec_kv_commit.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp]
     return lib
 
 
@@ -520,3 +546,413 @@ def spec_verify_lmhead(hidden: torch.Tensor, lm_head: torch.Tensor, draft_probs:
     if debug:
         return out_ids, out_num_accepted, logits_out, dbg_rows, dbg_req
     return out_ids, out_num_accepted, logits_out
+
+
+# ---------------------------------------------------------------- around the verification
+# The pass that scores the drafted nodes, over a paged key/value cache:
+# rotary positions, the cache written and read, the step's plan, the nodes'
+# attention, and the kept path's rows (include/spec_verify.h).
+
+_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+MAX_NODES = 32
+MAX_COMMIT_CACHES = 64
+
+
+class _CCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class _CTable(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("layout", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+def _dtype_code(t, name):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
+    """Makes `device` current for a call (nothing to do where it is)."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _streamed(fn):
+    """A call with stream=s runs with s current, so that what it allocates
+    (outputs, workspaces) belongs to the stream that its kernels run on."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _raise(rc, what):
+    if rc != SPEC_OK:
+        raise SpecVerifyError(rc, what)
+
+
+def _heads(t, name, heads, D, dtype, device, tokens=None):
+    """[..., heads, D] as (tokens, token stride, head stride): the leading
+    dimensions must be one run of tokens."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() < 3 or t.shape[-1] != D or (heads is not None and t.shape[-2] != heads):
+        raise ValueError(f"{name} must be [tokens, {heads if heads is not None else 'heads'}, {D}], "
+                         f"got {tuple(t.shape)}")
+    st, sh = t.stride(), t.shape
+    if sh[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    n, step = sh[-3], st[-3]
+    for i in range(t.dim() - 4, -1, -1):
+        if sh[i] != 1 and n != 1 and st[i] != n * step:
+            raise ValueError(f"the leading dimensions of {name} must be one run of tokens")
+        if n == 1:
+            step = st[i]
+        n *= sh[i]
+    if tokens is not None and n != tokens:
+        raise ValueError(f"{name} has {n} tokens, expected {tokens}")
+    return n, step, st[-2]
+
+
+class RopeTable:
+    """Rotary frequencies on the device (spec_rope_table)."""
+
+    def __init__(self, turns: torch.Tensor, layout: str, scale: float):
+        _check(turns, "turns", torch.int64)
+        self.turns, self.rot, self.layout, self.scale = turns, 2 * turns.numel(), layout, scale
+        self._c = _CTable(turns.data_ptr(), self.rot, ROPE_LAYOUT[layout], scale)
+        self._ref = ctypes.addressof(self._c)
+
+
+def rope_table(rot: int, *, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+               factor: float = 1.0, original_len: float = 0.0, fast: float = 32.0,
+               slow: float = 1.0, device="cuda") -> RopeTable:
+    """The frequencies of `rot` rotated channels (spec_rope_turns): `layout`
+    "half" or "interleaved"; `scaling` "none", "linear", "ntk" or "by_parts"
+    (which needs the original context's length) by `factor`."""
+    if layout not in ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUT)}")
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    turns = torch.empty(max(int(rot) // 2, 1), dtype=torch.int64)
+    scale = ctypes.c_float()
+    _raise(lib().spec_rope_turns(rot, base, ROPE_SCALING[scaling], factor, original_len, fast,
+                                 slow, turns.data_ptr(), ctypes.addressof(scale)),
+           "spec_rope_turns")
+    return RopeTable(turns.to(device), layout, scale.value)
+
+
+@_streamed
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: RopeTable, *,
+         out_q: torch.Tensor | None = None, out_k: torch.Tensor | None = None,
+         inverse: bool = False, stream=None):
+    """Rotary positions (spec_rope): q [..., q_heads, D] and k [..., k_heads,
+    D] (or None) turned by positions [tokens] int32.  out_q / out_k: new
+    tensors, or given ones (q and k themselves: in place).  inverse=True turns
+    back, which takes gradients of the outputs to gradients of the inputs.
+    Returns (out_q, out_k), or out_q where k is None."""
+    dev, D = q.device, q.shape[-1]
+    T, qt, qh = _heads(q, "q", None, D, q.dtype, dev)
+    dt = _dtype_code(q, "q")
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _, ot, oh = _heads(out_q, "out_q", q.shape[-2], D, q.dtype, dev, T)
+    kt = kh = okt = okh = hk = 0
+    if k is not None:
+        hk = k.shape[-2]
+        _, kt, kh = _heads(k, "k", hk, D, q.dtype, dev, T)
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        _, okt, okh = _heads(out_k, "out_k", hk, D, q.dtype, dev, T)
+    _check(positions, "positions", torch.int32, device=dev)
+    if positions.numel() != T:
+        raise ValueError(f"positions has {positions.numel()} entries for {T} tokens")
+    with _on(dev):
+        rc = lib().spec_rope(_ptr(q), q.shape[-2], qt, qh, _ptr(out_q), ot, oh, _ptr(k), hk, kt, kh,
+                             _ptr(out_k), okt, okh, dt, D, T, _ptr(positions), table._ref,
+                             int(inverse), _stream(None))
+    _raise(rc, "spec_rope")
+    return out_q if k is None else (out_q, out_k)
+
+
+class KVCache:
+    """A paged key/value cache of one layer (spec_kv_cache): k and v
+    [num_pages, heads, page_size, head_dim] (bfloat16, float16, or uint8 /
+    float8_e4m3fn with k_scale and v_scale [num_pages, heads, page_size]
+    uint8).  Any strides with contiguous channels, the same for k and v: a
+    [num_pages, page_size, heads, head_dim] allocation is passed as its
+    transpose(1, 2).  The tensors stay the caller's."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [num_pages, heads, page_size, head_dim], alike")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have equal strides and contiguous channels")
+        if not k.is_cuda:
+            raise ValueError("the cache must be CUDA tensors")
+        P, H, S, D = k.shape
+        if k.dtype in (torch.uint8, torch.float8_e4m3fn):
+            dt = SPEC_E4M3
+            if k_scale is None or v_scale is None:
+                raise ValueError("an 8-bit cache needs k_scale and v_scale")
+            for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _check(t, n, torch.uint8, (P, H, S), k.device)
+        elif k.dtype in (torch.bfloat16, torch.float16):
+            dt = _DTYPES[k.dtype]
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a 16-bit cache has no scales")
+        else:
+            raise ValueError(f"a cache of {k.dtype} is not supported")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = P, H, S, D
+        self.device, self.dtype = k.device, dt
+        self._c = _CCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), dt, P, S, H, D,
+                          k.stride(0), k.stride(1), k.stride(2))
+        self._ref = ctypes.addressof(self._c)
+
+
+def new_kv_cache(num_pages: int, page_size: int, heads: int, head_dim: int, *,
+                 dtype=torch.bfloat16, device="cuda") -> KVCache:
+    """A cache of its own memory; dtype bfloat16, float16 or float8_e4m3fn."""
+    shape = (num_pages, heads, page_size, head_dim)
+    if dtype == torch.float8_e4m3fn:
+        dtype = torch.uint8
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    sc = (None, None)
+    if dtype == torch.uint8:
+        sc = tuple(torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2))
+    return KVCache(k, v, *sc)
+
+
+@_streamed
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
+             positions: torch.Tensor | None = None, table: RopeTable | None = None,
+             q: torch.Tensor | None = None, out_q: torch.Tensor | None = None,
+             dev_status: torch.Tensor | None = None, stream=None):
+    """Write key and value rows [..., heads, head_dim] to their cache slots
+    (spec_kv_write); slots [tokens] int64, negative: not written.  With
+    `table` and `positions` the keys are rotated on the way, and q [...,
+    q_heads, head_dim] into out_q (a new tensor by default), which is
+    returned."""
+    dev, D = cache.device, cache.head_dim
+    T, kt, kh = _heads(k, "k", cache.heads, D, k.dtype, dev)
+    _, vt, vh = _heads(v, "v", cache.heads, D, k.dtype, dev, T)
+    dt = _dtype_code(k, "k")
+    _check(slots, "slots", torch.int64, device=dev)
+    if slots.numel() != T:
+        raise ValueError(f"slots has {slots.numel()} entries for {T} tokens")
+    if (table is None) != (positions is None):
+        raise ValueError("a rotation needs positions and a table")
+    if positions is not None:
+        _check(positions, "positions", torch.int32, device=dev)
+        if positions.numel() != T:
+            raise ValueError(f"positions has {positions.numel()} entries for {T} tokens")
+    qt = qh = ot = oh = hq = 0
+    if q is not None:
+        if table is None:
+            raise ValueError("q is taken along only to be rotated")
+        hq = q.shape[-2]
+        _, qt, qh = _heads(q, "q", hq, D, k.dtype, dev, T)
+        if out_q is None:
+            out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _, ot, oh = _heads(out_q, "out_q", hq, D, k.dtype, dev, T)
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (1,), dev)
+    with _on(dev):
+        rc = lib().spec_kv_write(cache._ref, _ptr(k), kt, kh, _ptr(v), vt, vh, dt, T, _ptr(slots),
+                                 _ptr(positions), None if table is None else table._ref, _ptr(q),
+                                 hq, qt, qh, _ptr(out_q) if q is not None else None, ot, oh,
+                                 _ptr(dev_status), _stream(None))
+    _raise(rc, "spec_kv_write")
+    return out_q if q is not None else None
+
+
+@_streamed
+def kv_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype | None = None,
+            out_k: torch.Tensor | None = None, out_v: torch.Tensor | None = None, stream=None):
+    """The rows of `slots` (int64, any shape) as (k, v) [*slots.shape, heads,
+    head_dim] of `dtype` (the cache's own by default, bfloat16 for an 8-bit
+    one); a slot outside the cache reads as zeros (spec_kv_read)."""
+    dev = cache.device
+    _check(slots, "slots", torch.int64, device=dev)
+    if dtype is None:
+        dtype = torch.bfloat16 if cache.dtype == SPEC_E4M3 else cache.k.dtype
+    shape = (*slots.shape, cache.heads, cache.head_dim)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=dev)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=dev)
+    _check(out_k, "out_k", dtype, shape, dev)
+    _check(out_v, "out_v", dtype, shape, dev)
+    with _on(dev):
+        rc = lib().spec_kv_read(cache._ref, slots.numel(), _ptr(slots), _dtype_code(out_k, "dtype"),
+                                _ptr(out_k), _ptr(out_v), _stream(None))
+    _raise(rc, "spec_kv_read")
+    return out_k, out_v
+
+
+@dataclass
+class TreePlan:
+    """Where the nodes of a step stand (spec_tree_plan).  One plan serves every
+    layer of the step; calls that use it must not overlap on the GPU."""
+    positions: torch.Tensor    # [B, N] int32
+    slots: torch.Tensor        # [B, N] int64
+    masks: torch.Tensor        # [B, N] int32: bit u: node u is this one or above it
+    context_len: torch.Tensor  # [B] int32 (the caller's)
+    page_table: torch.Tensor   # [B, max_pages] int32 (the caller's)
+    page_size: int
+    num_pages: int
+    buffer: torch.Tensor       # the division of the attention's work
+    workspace: dict            # of tree_attention, by (device, bytes)
+
+
+@_streamed
+def tree_plan(tree_parents: torch.Tensor, num_nodes: torch.Tensor, context_len: torch.Tensor,
+              page_table: torch.Tensor, cache: KVCache, *, dev_status: torch.Tensor | None = None,
+              stream=None) -> TreePlan:
+    """Positions, cache slots and ancestor masks of the nodes [B, N] that
+    follow each request's context (spec_tree_plan); `cache` gives the pages'
+    size and number."""
+    if tree_parents.dim() != 2 or page_table.dim() != 2:
+        raise ValueError("tree_parents must be [B, N] and page_table [B, max_pages]")
+    B, N = tree_parents.shape
+    dev = cache.device
+    _check(tree_parents, "tree_parents", torch.int32, device=dev)
+    _check(num_nodes, "num_nodes", torch.int32, (B,), dev)
+    _check(context_len, "context_len", torch.int32, (B,), dev)
+    _check(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (1,), dev)
+    n = int(lib().spec_tree_plan_size(B))
+    buffer = torch.empty(n, dtype=torch.uint8, device=dev)
+    positions = torch.empty((B, N), dtype=torch.int32, device=dev)
+    masks = torch.empty((B, N), dtype=torch.int32, device=dev)
+    slots = torch.empty((B, N), dtype=torch.int64, device=dev)
+    with _on(dev):
+        rc = lib().spec_tree_plan(_ptr(tree_parents), _ptr(num_nodes), _ptr(context_len),
+                                  _ptr(page_table), B, N, page_table.shape[1], cache.page_size,
+                                  cache.num_pages, _ptr(positions), _ptr(slots), _ptr(masks),
+                                  _ptr(buffer), n, _ptr(dev_status), _stream(None))
+    _raise(rc, "spec_tree_plan")
+    return TreePlan(positions, slots, masks, context_len, page_table, cache.page_size,
+                    cache.num_pages, buffer, {})
+
+
+@_streamed
+def tree_attention(q: torch.Tensor, cache: KVCache, plan: TreePlan, *, scale: float | None = None,
+                   masks: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the nodes' queries q [B, N, q_heads, head_dim] over the
+    cache (spec_tree_attention).  scale: 1 / sqrt(head_dim) by default; masks
+    [B, N] int32: the plan's by default; lse [B, N, q_heads] float32: written
+    where given.  The workspace is kept with the plan unless one is given."""
+    if q.dim() != 4 or q.shape[3] != cache.head_dim:
+        raise ValueError("q must be [B, N, q_heads, head_dim]")
+    B, N, Hq, D = q.shape
+    dev = cache.device
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, expected {dev}")
+    st = q.stride()
+    if st[3] != 1:
+        raise ValueError("the channels of q must be contiguous")
+    if plan.positions.shape != (B, N):
+        raise ValueError(f"the plan is for {tuple(plan.positions.shape)}, q for {(B, N)}")
+    if (plan.page_size, plan.num_pages) != (cache.page_size, cache.num_pages):
+        raise ValueError("the plan was made for a cache of other pages")
+    dt = _dtype_code(q, "q")
+    if masks is None:
+        masks = plan.masks
+    else:
+        _check(masks, "masks", torch.int32, (B, N), dev)
+    if out is None:
+        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _check(out, "out", q.dtype, (B, N, Hq, D), dev)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (B, N, Hq), dev)
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (1,), dev)
+    with _on(dev):
+        if workspace is None:
+            workspace = plan.workspace.get((Hq, cache.heads, D))
+            if workspace is None:
+                n = int(lib().spec_tree_attention_workspace_size(cache._ref, Hq))
+                if n == 0:
+                    raise ValueError(f"unsupported: {Hq} query heads over {cache.heads} of {D}")
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+                plan.workspace[(Hq, cache.heads, D)] = workspace
+        rc = lib().spec_tree_attention(
+            _ptr(q), st[0], st[1], st[2], dt, B, N, Hq, cache._ref, _ptr(plan.page_table),
+            plan.page_table.shape[1], _ptr(masks), _ptr(plan.buffer),
+            1.0 / math.sqrt(D) if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel(), _ptr(dev_status), _stream(None))
+    _raise(rc, "spec_tree_attention")
+    return out
+
+
+@_streamed
+def kv_commit(caches: list, plan: TreePlan, last_node: torch.Tensor, *,
+              new_context_len: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """After the verification: move the kept path's rows to the places after
+    the context in every cache of `caches` (the layers) and return the new
+    context lengths (spec_kv_commit).  last_node: spec_verify_tree's third
+    result, or spec_verify's second for a chain.  new_context_len may be the
+    plan's context_len itself."""
+    B, N = plan.positions.shape
+    if not caches:
+        raise ValueError("no caches")
+    dev = caches[0].device
+    _check(last_node, "last_node", torch.int32, (B,), dev)
+    if new_context_len is None:
+        new_context_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    _check(new_context_len, "new_context_len", torch.int32, (B,), dev)
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (1,), dev)
+    for c in caches:
+        if (plan.page_size, plan.num_pages) != (c.page_size, c.num_pages) or c.device != dev:
+            raise ValueError("the plan was made for a cache of other pages")
+    with _on(dev):
+        st = _stream(None)
+        # the lengths are written once, by the last group of caches: it may be
+        # the plan's own context_len, which the earlier groups still read
+        scratch = new_context_len if len(caches) <= MAX_COMMIT_CACHES else torch.empty_like(new_context_len)
+        for i in range(0, len(caches), MAX_COMMIT_CACHES):
+            group = caches[i:i + MAX_COMMIT_CACHES]
+            arr = (_CCache * len(group))(*[c._c for c in group])
+            last = i + MAX_COMMIT_CACHES >= len(caches)
+            rc = lib().spec_kv_commit(ctypes.addressof(arr), len(group), _ptr(plan.masks),
+                                      _ptr(plan.slots), _ptr(last_node), _ptr(plan.context_len), B,
+                                      N, _ptr(new_context_len if last else scratch),
+                                      _ptr(dev_status), st)
+            _raise(rc, "spec_kv_commit")
+    return new_context_len

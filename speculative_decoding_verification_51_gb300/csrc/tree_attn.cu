@@ -1,0 +1,140 @@
+// tree_attn.cu -- spec_tree_attention: argument checks, tensor maps and the
+// choice of the kernel.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "tree_attn.cuh"
+
+using namespace sv;
+
+namespace {
+
+std::mutex g_mu;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+bool encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return false;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    *out = g_encode;
+    return true;
+}
+
+// One side of a cache as (channel, token of the page, head, page), in boxes
+// of 128 bytes of a row (channels past head_dim read as zeros) x 16 tokens.
+spec_status cache_map(CUtensorMap* map, const spec_kv_cache& c, void* base) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (!encoder(&enc)) return SPEC_ERR_CUDA;
+    const cuuint64_t es = cuuint64_t(dtype_bytes(c.dtype));
+    const cuuint64_t dims[4] = {cuuint64_t(c.head_dim), cuuint64_t(c.page_size),
+                                cuuint64_t(c.heads), cuuint64_t(c.num_pages)};
+    const cuuint64_t strides[3] = {c.token_stride * es, c.head_stride * es, c.page_stride * es};
+    const cuuint32_t box[4] = {cuuint32_t(128 / es), 16, 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType t = c.dtype == SPEC_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : c.dtype == SPEC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUresult r = enc(map, t, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPEC_OK : SPEC_ERR_UNSUPPORTED;
+}
+
+constexpr int MAX_R = 32;  // rows of the largest tile
+
+// channels of a row as the kernels lay them out
+int width_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_tree_attention_workspace_size(const spec_kv_cache* cache, int q_heads) {
+    if (check_cache(cache) != SPEC_OK || q_heads < 1 || q_heads % cache->heads) return 0;
+    const int sms = sm_count();
+    if (sms <= 0) return 0;
+    return align256(size_t(2) * sms * MAX_R * width_of(cache->head_dim) * 4) +
+           align256(size_t(2) * sms * MAX_R * 2 * 4);
+}
+
+spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q_node_stride,
+                                int64_t q_head_stride, spec_dtype dtype, int B, int N, int q_heads,
+                                const spec_kv_cache* cache, const int32_t* page_table,
+                                int max_pages, const uint32_t* masks, const void* plan,
+                                float scale, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_status,
+                                spec_stream_t stream) {
+    const spec_status cs = check_cache(cache);
+    if (cs != SPEC_OK) return cs;
+    if (B < 0 || B > (1 << 24) || N < 1 || q_heads < 1 || max_pages < 1 || !(scale == scale))
+        return SPEC_ERR_INVALID_ARG;
+    if (dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_ERR_INVALID_ARG;
+    if (cache->dtype != SPEC_E4M3 && cache->dtype != int(dtype)) return SPEC_ERR_INVALID_ARG;
+    if (N > 32 || q_heads % cache->heads || q_heads > 65536) return SPEC_ERR_UNSUPPORTED;
+    if (B == 0) return SPEC_OK;
+    if (!q || !page_table || !masks || !plan || !out || !workspace) return SPEC_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || q_batch_stride % 8 || q_node_stride % 8 ||
+        q_head_stride % 8)
+        return SPEC_ERR_UNSUPPORTED;
+    if (!aligned(workspace, 256) || !aligned(plan, 256) ||
+        workspace_bytes < spec_tree_attention_workspace_size(cache, q_heads))
+        return SPEC_ERR_WORKSPACE;
+    const int sms = sm_count();
+    if (sms <= 0 || sms > PLAN_PARTS) return SPEC_ERR_CUDA;
+
+    AttnLaunch L;
+    spec_status r = cache_map(&L.mk, *cache, cache->k);
+    if (r == SPEC_OK) r = cache_map(&L.mv, *cache, cache->v);
+    if (r != SPEC_OK) return r;
+    AttnArgs& A = L.A;
+    A.q = q;
+    A.qb = q_batch_stride;
+    A.qn = q_node_stride;
+    A.qh = q_head_stride;
+    A.out = out;
+    A.lse = lse;
+    A.table = page_table;
+    A.masks = masks;
+    A.plan = plan_view(const_cast<void*>(plan), B);
+    A.v = cache->v;
+    A.ks = cache->k_scale;
+    A.vs = cache->v_scale;
+    A.v_page = cache->page_stride;
+    A.v_head = cache->head_stride;
+    A.v_token = cache->token_stride;
+    A.B = B;
+    A.N = N;
+    A.Hq = q_heads;
+    A.Hkv = cache->heads;
+    A.G = q_heads / cache->heads;
+    A.D = cache->head_dim;
+    A.page = cache->page_size;
+    A.max_pages = max_pages;
+    A.rows = N * A.G;
+    A.c = scale * 1.4426950408889634f;
+    A.q_f16 = dtype == SPEC_F16;
+    A.part_o = static_cast<float*>(workspace);
+    A.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                         align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
+    A.status = dev_status;
+    const int mt = A.rows <= 16 || A.D > 128 ? 1 : 2;
+    A.tiles_r = (A.rows + mt * 16 - 1) / (mt * 16);
+    L.ctas = sms;
+    L.st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache->dtype == SPEC_E4M3  ? launch_attn_e4m3(L, mt)
+                          : cache->dtype == SPEC_F16 ? launch_attn_f16(L, mt)
+                                                     : launch_attn_bf16(L, mt);
+    return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"

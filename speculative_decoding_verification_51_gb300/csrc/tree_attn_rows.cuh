@@ -1,0 +1,618 @@
+// tree_attn_rows.cuh -- k_attn_rows: the attention for few rows a key head
+// (16 or 32 a tile), where the cache's bytes are what counts.
+//
+// A CTA (one per SM) has 8 warps, and every warp is a pipeline of its own: it
+// takes every eighth chunk of 16 tokens of the segment, loads the chunk's K
+// and V rows by TMA into its own ring of stages (a chunk lies in one page,
+// whose size is a multiple of 16), and keeps the running reference, total and
+// sums of all rows of the tile in its registers.  No warp waits for another
+// until the segment ends, when the eight states are joined in shared memory.
+//
+// Mathematics.  With scores in powers of two, s_t = c q.k_t, and a reference
+// m: o = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m), for any m.  The reference
+// is raised only when a chunk's maximum passes it by 2^6, so that the sums are
+// seldom rescaled; the weights stay below 2^6 times the chunk's 16 tokens,
+// far inside float32 (the sums) and both 16-bit types (the weights).
+//
+// Products are mma.sync m16n8k16 on 16-bit operands with float32 sums: with 16
+// rows a chunk's 8 KB (128 channels) need 32 of them, a small part of what an SM
+// does in the 350 cycles that HBM takes to deliver the chunk.  tcgen05 would pad
+// 16 rows to 128.
+//
+// e4m3 rows.  ldmatrix moves byte pairs, so a lane gets 4 consecutive channels
+// of a K row where the 16-bit fragment has two pairs 8 apart; the query's
+// channels are permuted alike in shared memory, which leaves the products'
+// sum as it is.  V comes transposed in pairs of channels: a byte permutation
+// separates even channels from odd, and the accumulator's columns are then
+// channels 4 apart.  Both are converted to f16, exactly.  K's scale multiplies
+// the score; V's scale 2^e joins the exponent of its weight, w_t = 2^(s_t + e_t -
+// m) with m the running maximum of s_t + e_t: then the weights are as large as
+// their tokens' contributions, and f16's range is no limit.  The total is the
+// sum of 2^(s_t - m).  The reference takes e_t at -100 or more, so that a row
+// of zeros (e = -126) does not push the total out of float32.
+#pragma once
+
+#include "tree_attn.cuh"
+
+namespace sv {
+
+constexpr float AR_SLACK = 6.f;
+
+template <int KIND, int NK, int MT>
+struct RowsShape {
+    static constexpr bool E4 = KIND == SPEC_E4M3;
+    static constexpr int DP = NK * 16, R = MT * 16;
+    // eight warps, or four where the stages of eight would not fit
+    static constexpr int WARPS = !E4 && NK > 8 ? 4 : 8, THREADS = WARPS * 32;
+    static constexpr int BOXES = E4 ? (DP + 127) / 128 : (DP + 63) / 64;  // 128 bytes of a row each
+    static constexpr int SIDE = BOXES * 2048;                             // K (or V) of a chunk
+    static constexpr int STAGE = 2 * SIDE;
+    static constexpr int OB = R * (DP + 8) * 4;  // one warp's sums, at the join
+    static constexpr int FIXED = 4 * OB + R * (DP + 8) * 2 + (2 * WARPS + 4) * R * 4 + 4096;
+    static constexpr int ROOM = (232448 - 1024 - FIXED) / (WARPS * STAGE);
+    static constexpr int STAGES = ROOM < 6 ? ROOM : 6;
+    static_assert(STAGES >= 2, "no room for a ring");
+    static constexpr size_t SMEM = 1024 + size_t(WARPS) * STAGES * STAGE + FIXED;
+    // the query's fragments stay in registers where they are few
+    static constexpr bool QREG = MT * NK <= 8;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, "
+            "%7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int KIND, int NK, int MT>
+__global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
+    k_attn_rows(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                const __grid_constant__ AttnArgs A) {
+    using S = RowsShape<KIND, NK, MT>;
+    constexpr bool E4 = S::E4, F16 = KIND != SPEC_BF16;
+    constexpr int DP = S::DP, R = S::R, OP = DP + 8, QP = DP + 8, AR_WARPS = S::WARPS, AR_THREADS = S::THREADS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ring = smem + size_t(warp) * S::STAGES * S::STAGE;
+    float* sm_o = reinterpret_cast<float*>(smem + size_t(AR_WARPS) * S::STAGES * S::STAGE);
+    uint16_t* sm_q = reinterpret_cast<uint16_t*>(sm_o + 4 * R * OP);
+    float* sm_m = reinterpret_cast<float*>(sm_q + R * QP);  // [warps][R]
+    float* sm_l = sm_m + AR_WARPS * R;
+    float* sm_ref = sm_l + AR_WARPS * R;   // [R] joined reference
+    float* sm_tot = sm_ref + R;            // [R] joined total
+    uint32_t* sm_qmax = reinterpret_cast<uint32_t*>(sm_tot + R);  // [R]
+    uint32_t* sm_mask = sm_qmax + R;                              // [R]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm_mask + R);    // [warps][stages]
+    uint8_t* sm_sc = reinterpret_cast<uint8_t*>(bars + AR_WARPS * S::STAGES);  // [warps][stages][32]
+    int* sm_flag = reinterpret_cast<int*>(sm_sc + AR_WARPS * S::STAGES * 32);  // [2]
+    uint64_t* bar = bars + warp * S::STAGES;
+    uint8_t* sc = sm_sc + warp * S::STAGES * 32;
+
+    const Share share = share_of(A);
+    if (share.begin >= share.end) return;  // the whole CTA
+    if (lane == 0) {
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(&bar[i], 1);
+        fence_mbarrier_init();
+    }
+    if (threadIdx.x == 0) sm_flag[1] = 0;
+    __syncwarp();
+
+    const int first = request_of(A, share.begin);
+
+    // ---- this warp's copies: the next chunk to load, a page index ahead
+    Segment ps = segment_at(A, share, share.begin, first);
+    int pc = ps.c0 + warp, page_at = 0, off_at = 0;
+    bool more = true;
+    auto seek = [&]() {  // to the next chunk this warp has, if any
+        while (pc >= ps.c1) {
+            const long long g = ps.g + (ps.t1 - ps.t0);
+            if (g >= share.end) {
+                more = false;
+                return;
+            }
+            ps = segment_at(A, share, g, ps.b);
+            pc = ps.c0 + warp;
+        }
+        const int t = pc * 16, p = t / A.page;
+        off_at = t - p * A.page;
+        page_at = __ldg(A.table + (long long)ps.b * A.max_pages + p);
+    };
+    seek();
+    uint32_t issued = 0, used = 0;
+    auto issue = [&]() {
+        if (!more) return;
+        const uint32_t st = issued % S::STAGES;
+        if (lane == 0) {
+            uint8_t* d = ring + st * S::STAGE;
+            mbar_arrive_expect_tx(&bar[st], uint32_t(S::STAGE) + (E4 ? 32u : 0u));
+#pragma unroll
+            for (int x = 0; x < S::BOXES; ++x) {
+                tma_load_4d(d + x * 2048, &mk, x * (E4 ? 128 : 64), off_at, ps.h, page_at, &bar[st]);
+                tma_load_4d(d + S::SIDE + x * 2048, &mv, x * (E4 ? 128 : 64), off_at, ps.h, page_at,
+                            &bar[st]);
+            }
+            if constexpr (E4) {
+                const long long at = ((long long)page_at * A.Hkv + ps.h) * A.page + off_at;
+                bulk_g2s(sc + st * 32, A.ks + at, 16, &bar[st]);
+                bulk_g2s(sc + st * 32 + 16, A.vs + at, 16, &bar[st]);
+            }
+        }
+        ++issued;
+        pc += AR_WARPS;
+        seek();
+    };
+    for (int i = 0; i < S::STAGES; ++i) issue();
+
+    bool dead = false;  // a copy did not arrive in time: no more waits, SPEC_BADBIT_TIMEOUT
+    int b_at = first;
+    for (long long g = share.begin; g < share.end;) {
+        const Segment s = segment_at(A, share, g, b_at);
+        b_at = s.b;
+        g += s.t1 - s.t0;
+
+        // ---- the query's rows to shared memory (e4m3: as f16, a power of two
+        // a row bringing its largest value to [1, 2))
+        if constexpr (E4) {
+            for (int r = threadIdx.x; r < R; r += AR_THREADS) sm_qmax[r] = 0;
+            __syncthreads();
+        }
+        constexpr int QV = R * DP / 8;  // vectors of 8 channels
+#pragma unroll 1
+        for (int pass = E4 ? 0 : 1; pass < 2; ++pass) {
+            for (int i = threadIdx.x; i < QV; i += AR_THREADS) {
+                const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8, row = s.rt * R + r;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                const int v = row / A.G;
+                if (row < A.rows && d < A.D && v < s.n)
+                    w = *reinterpret_cast<const uint4*>(
+                        static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                        (s.h * A.G + row - v * A.G) * A.qh + d);
+                if constexpr (!E4) {
+                    *reinterpret_cast<uint4*>(sm_q + r * QP + d) = w;
+                } else {
+                    float f[8];
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (A.q_f16) {
+                            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+                            f[2 * e] = x.x;
+                            f[2 * e + 1] = x.y;
+                        } else {
+                            f[2 * e] = bf16_lo(u[e]);
+                            f[2 * e + 1] = bf16_hi(u[e]);
+                        }
+                    }
+                    if (pass == 0) {
+                        float m = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[e]));
+                        atomicMax(&sm_qmax[r], __float_as_uint(m));
+                    } else {
+                        // 2^-e for the row's exponent e (its largest value >= 2^-126)
+                        const uint32_t ex = max(min(sm_qmax[r] >> 23, 253u), 1u);
+                        const float f2 = __uint_as_float((254u - ex) << 23);
+                        // channels d = 16 j + 4 t + e of a lane's K fragment go to
+                        // 2 t + e (e < 2) and 8 + 2 t + e - 2
+                        const int at = (d & ~15) + ((d & 8) ? 4 : 0);
+                        uint32_t* dst = reinterpret_cast<uint32_t*>(sm_q + r * QP + at);
+                        dst[0] = pack16<true>(f[0] * f2, f[1] * f2);
+                        dst[1] = pack16<true>(f[4] * f2, f[5] * f2);
+                        dst[4] = pack16<true>(f[2] * f2, f[3] * f2);
+                        dst[5] = pack16<true>(f[6] * f2, f[7] * f2);
+                    }
+                }
+            }
+            if (pass == 0) __syncthreads();
+        }
+        if (threadIdx.x < R) {
+            const int row = s.rt * R + threadIdx.x, v = row / A.G;
+            uint32_t m = 0;
+            if (row < A.rows && v < s.n)
+                m = A.masks[(long long)s.b * A.N + v] & (0xffffffffu >> (32 - s.n));
+            sm_mask[threadIdx.x] = m;
+        }
+        __syncthreads();
+
+        // ---- this warp's chunks
+        const uint32_t qa = smem_u32(sm_q) + (((lane & 7) + ((lane >> 3) & 1) * 8) * QP + (lane >> 4) * 8) * 2;
+        uint32_t qf[S::QREG ? MT : 1][S::QREG ? NK : 1][4];
+        if constexpr (S::QREG) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < NK; ++k) ldsm4(qa + (m * 16 * QP + k * 16) * 2, qf[m][k]);
+        }
+        float o[MT][2 * NK][4], ref[MT][2], tot[MT][2], rc[MT][2];
+        uint32_t mask[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int n = 0; n < 2 * NK; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[m][n][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = m * 16 + x * 8 + (lane >> 2);
+                ref[m][x] = -INFINITY;
+                tot[m][x] = 0.f;
+                mask[m][x] = sm_mask[r];
+                rc[m][x] = A.c;
+                if constexpr (E4) rc[m][x] = A.c * exp2_int(int(max(min(sm_qmax[r] >> 23, 253u), 1u)) - 127);
+            }
+        }
+        uint32_t v_bad = 0;  // nodes of which some value is not finite
+        for (int c = s.c0 + warp; c < s.c1; c += AR_WARPS) {
+            const uint32_t st = used % S::STAGES;
+            uint8_t* kp = ring + st * S::STAGE;
+            uint8_t* vp = kp + S::SIDE;
+            if (!dead && __any_sync(0xffffffffu, !mbar_wait_bounded(&bar[st], (used / S::STAGES) & 1u))) {
+                dead = true;
+                if (lane == 0 && A.status) atomicOr(A.status, int(SPEC_BADBIT_TIMEOUT));
+            }
+            ++used;
+            const int t0 = c * 16;
+            const bool tail = t0 + 16 > s.ctx;
+
+            // scores
+            float p[MT][2][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[m][n][e] = 0.f;
+            const uint32_t ka = smem_u32(kp);
+            if constexpr (E4) {
+                const int tk = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                for (int k = 0; k < NK; k += 2) {
+                    uint32_t w[4];
+                    const int j = k + (lane >> 4);
+                    ldsm4(ka + (j >> 3) * 2048 + tk * 128 + (((j & 7) ^ (tk & 7)) << 4), w);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t b00 = e4m3x2_to_f16x2(uint16_t(w[2 * i])),
+                                       b01 = e4m3x2_to_f16x2(uint16_t(w[2 * i] >> 16)),
+                                       b10 = e4m3x2_to_f16x2(uint16_t(w[2 * i + 1])),
+                                       b11 = e4m3x2_to_f16x2(uint16_t(w[2 * i + 1] >> 16));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            uint32_t a[4];
+                            if constexpr (S::QREG) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) a[e] = qf[m][k + i][e];
+                            } else {
+                                ldsm4(qa + (m * 16 * QP + (k + i) * 16) * 2, a);
+                            }
+                            mma16<true>(p[m][0], a, b00, b01);
+                            mma16<true>(p[m][1], a, b10, b11);
+                        }
+                    }
+                }
+            } else {
+                const int tk = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    uint32_t w[4];
+                    const int j = 2 * k + ((lane >> 3) & 1);
+                    ldsm4(ka + (j >> 3) * 2048 + tk * 128 + (((j & 7) ^ (tk & 7)) << 4), w);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        uint32_t a[4];
+                        if constexpr (S::QREG) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) a[e] = qf[m][k][e];
+                        } else {
+                            ldsm4(qa + (m * 16 * QP + k * 16) * 2, a);
+                        }
+                        mma16<F16>(p[m][0], a, w[0], w[1]);
+                        mma16<F16>(p[m][1], a, w[2], w[3]);
+                    }
+                }
+            }
+            // this lane's tokens: t0 + 8 n + 2 (lane % 4) + e
+            float kf[2][2], ve[2][2];
+            if constexpr (E4) {
+                const uint8_t* z = sc + st * 32;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint16_t a = *reinterpret_cast<const uint16_t*>(z + n * 8 + 2 * (lane & 3));
+                    const uint16_t b = *reinterpret_cast<const uint16_t*>(z + 16 + n * 8 + 2 * (lane & 3));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        kf[n][e] = exp2_int(min(max(int((a >> (8 * e)) & 255), 1), 253) - 127);
+                        ve[n][e] = float(min(max(int((b >> (8 * e)) & 255), 1), 253) - 127);
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                bool raise = false;
+                float top[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    top[x] = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = p[m][n][2 * x + e] * rc[m][x];
+                            if constexpr (E4) v *= kf[n][e];
+                            if (tail) {
+                                const int u = t0 + n * 8 + 2 * (lane & 3) + e - s.ctx;
+                                if (u >= 0 && (u >= 32 || !(mask[m][x] >> u & 1u))) v = -INFINITY;
+                            }
+                            p[m][n][2 * x + e] = v;
+                            if constexpr (E4) v += fmaxf(ve[n][e], -100.f);
+                            top[x] = fmaxf(top[x], v);
+                        }
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+                    raise |= top[x] > ref[m][x] + AR_SLACK;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float to = top[x] > ref[m][x] + AR_SLACK ? top[x] : ref[m][x];
+                        // a reference of -inf has sums of zero
+                        const float f = ref[m][x] == to ? 1.f : ex2_approx(ref[m][x] - to);
+                        ref[m][x] = to;
+                        tot[m][x] *= f;
+#pragma unroll
+                        for (int n = 0; n < 2 * NK; ++n) {
+                            o[m][n][2 * x] *= f;
+                            o[m][n][2 * x + 1] *= f;
+                        }
+                    }
+                }
+                // weights
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float at = ref[m][x] == -INFINITY ? 0.f : ref[m][x];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = p[m][n][2 * x + e] - at;
+                            if constexpr (E4) {
+                                tot[m][x] += ex2_approx(v);
+                                v = ex2_approx(v + ve[n][e]);
+                            } else {
+                                v = ex2_approx(v);
+                                tot[m][x] += v;
+                            }
+                            p[m][n][2 * x + e] = v;
+                        }
+                }
+            }
+            // values of tokens past the request's end, and values of nodes
+            // that are not finite, must not meet a weight of zero
+            if (tail) {
+                uint32_t bad = 0;
+                for (int i = lane; i < S::SIDE / 16; i += 32) {
+                    const int t = t0 + ((i & 127) >> 3);
+                    if (t < s.ctx) continue;
+                    uint4* w = reinterpret_cast<uint4*>(vp) + i;
+                    if (t >= s.ctx + s.n) {
+                        *w = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint32_t u[4] = {w->x, w->y, w->z, w->w};
+                    bool hit = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (E4) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                if ((u[e] >> (8 * y) & 0x7fu) == 0x7fu) {
+                                    u[e] &= ~(0xffu << (8 * y));
+                                    hit = true;
+                                }
+                        } else {
+                            constexpr uint32_t EX = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if ((u[e] >> (16 * y) & EX) == EX) {
+                                    u[e] &= ~(0xffffu << (16 * y));
+                                    hit = true;
+                                }
+                        }
+                    }
+                    if (hit) {
+                        *w = make_uint4(u[0], u[1], u[2], u[3]);
+                        bad |= 1u << (t - s.ctx);
+                    }
+                }
+                v_bad |= __reduce_or_sync(0xffffffffu, bad);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+                __syncwarp();
+            }
+            // sums
+            const uint32_t va = smem_u32(vp);
+            uint32_t a[MT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                a[m][0] = pack16<F16>(p[m][0][0], p[m][0][1]);
+                a[m][1] = pack16<F16>(p[m][0][2], p[m][0][3]);
+                a[m][2] = pack16<F16>(p[m][1][0], p[m][1][1]);
+                a[m][3] = pack16<F16>(p[m][1][2], p[m][1][3]);
+            }
+            const int tv = (lane & 7) + ((lane >> 3) & 1) * 8;
+            if constexpr (E4) {
+#pragma unroll
+                for (int k = 0; k < NK; k += 2) {
+                    uint32_t w[4];
+                    const int j = k + (lane >> 4);
+                    ldsm4t(va + (j >> 3) * 2048 + tv * 128 + (((j & 7) ^ (tv & 7)) << 4), w);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t lo = __byte_perm(w[2 * i], 0, 0x3120),
+                                       hi = __byte_perm(w[2 * i + 1], 0, 0x3120);
+                        const uint32_t e0 = e4m3x2_to_f16x2(uint16_t(lo)),
+                                       o0 = e4m3x2_to_f16x2(uint16_t(lo >> 16)),
+                                       e1 = e4m3x2_to_f16x2(uint16_t(hi)),
+                                       o1 = e4m3x2_to_f16x2(uint16_t(hi >> 16));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            mma16<true>(o[m][2 * (k + i)], a[m], e0, e1);
+                            mma16<true>(o[m][2 * (k + i) + 1], a[m], o0, o1);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    uint32_t w[4];
+                    const int j = 2 * k + (lane >> 4);
+                    ldsm4t(va + (j >> 3) * 2048 + tv * 128 + (((j & 7) ^ (tv & 7)) << 4), w);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma16<F16>(o[m][2 * k], a[m], w[0], w[1]);
+                        mma16<F16>(o[m][2 * k + 1], a[m], w[2], w[3]);
+                    }
+                }
+            }
+            __syncwarp();  // every lane is done with the stage
+            issue();
+        }
+
+        // ---- join the warps
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = tot[m][x];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                if ((lane & 3) == 0) {
+                    const int r = m * 16 + x * 8 + (lane >> 2);
+                    sm_m[warp * R + r] = ref[m][x];
+                    sm_l[warp * R + r] = l;
+                }
+            }
+        if (lane == 0 && v_bad) atomicOr(reinterpret_cast<unsigned*>(&sm_flag[1]), v_bad);
+        __syncthreads();
+        if (threadIdx.x < R) {
+            float mm = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < AR_WARPS; ++w) mm = fmaxf(mm, sm_m[w * R + threadIdx.x]);
+            const float at = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+            for (int w = 0; w < AR_WARPS; ++w)
+                l += sm_l[w * R + threadIdx.x] * ex2_approx(sm_m[w * R + threadIdx.x] - at);
+            sm_ref[threadIdx.x] = mm;
+            sm_tot[threadIdx.x] = l;
+        }
+        float* ob = sm_o + (warp & 3) * R * OP;
+        auto col = [&](int n, int e) {
+            if constexpr (E4) return (n >> 1) * 16 + 4 * (lane & 3) + 2 * e + (n & 1);
+            else return n * 8 + 2 * (lane & 3) + e;
+        };
+#pragma unroll
+        for (int half = AR_WARPS / 4 - 1; half >= 0; --half) {
+            if ((warp >> 2) == half) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = m * 16 + x * 8 + (lane >> 2);
+                        float mm = -INFINITY;
+#pragma unroll
+                        for (int w = 0; w < AR_WARPS; ++w) mm = fmaxf(mm, sm_m[w * R + r]);
+                        const float f = ref[m][x] == -INFINITY ? 0.f : ex2_approx(ref[m][x] - mm);
+#pragma unroll
+                        for (int n = 0; n < 2 * NK; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float* z = ob + r * OP + col(n, e);
+                                const float v = o[m][n][2 * x + e] * f;
+                                *z = half == AR_WARPS / 4 - 1 ? v : *z + v;
+                            }
+                    }
+            }
+            __syncthreads();
+        }
+        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+        const uint32_t bad_nodes = uint32_t(sm_flag[1]);
+        const long long slot = part_slot(share, s);
+        for (int i = threadIdx.x; i < R * (DP / 4); i += AR_THREADS) {
+            const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4, row = s.rt * R + r;
+            if (row >= A.rows) break;
+            float4 x = *reinterpret_cast<const float4*>(sm_o + r * OP + d);
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+                const float4 y = *reinterpret_cast<const float4*>(sm_o + w * R * OP + r * OP + d);
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+            }
+            float v[4] = {x.x, x.y, x.z, x.w};
+            if (bad_nodes & sm_mask[r])  // values that are not finite, for the rows that see them
+                for (uint32_t m = bad_nodes & sm_mask[r]; m; m &= m - 1)
+                    for (int e = 0; e < 4; ++e)
+                        if (d + e < A.D) v[e] += not_finite_v<KIND>(A, s.b, s.h, s.ctx + __ffs(m) - 1, d + e);
+            if (whole) {
+                put_row(A, s, row, d, v, sm_tot[r]);
+                if (d == 0) put_lse(A, s, row, sm_ref[r], sm_tot[r]);
+            } else {
+                *reinterpret_cast<float4*>(A.part_o + (slot * R + r) * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
+                if (d == 0)
+                    *reinterpret_cast<float2*>(A.part_ml + (slot * R + r) * 2) = make_float2(sm_ref[r], sm_tot[r]);
+            }
+        }
+        if (!whole) join_parts(A, share, s, R, DP, sm_flag);
+        __syncthreads();
+        if (threadIdx.x == 0) sm_flag[1] = 0;
+    }
+}
+
+template <int KIND, int NK, int MT>
+cudaError_t launch_rows(const AttnLaunch& L) {
+    using S = RowsShape<KIND, NK, MT>;
+    static bool ready[64] = {};  // per device; setting it twice does no harm
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(k_attn_rows<KIND, NK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM));
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    k_attn_rows<KIND, NK, MT><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
+    return cudaGetLastError();
+}
+
+template <int KIND>
+cudaError_t launch_rows_any(const AttnLaunch& L, int mt) {
+    const int D = L.A.D;
+    if (D > 128) return launch_rows<KIND, 16, 1>(L);
+    if (mt == 1)
+        return D <= 64 ? launch_rows<KIND, 4, 1>(L) : D <= 96 ? launch_rows<KIND, 6, 1>(L) : launch_rows<KIND, 8, 1>(L);
+    return D <= 64 ? launch_rows<KIND, 4, 2>(L) : D <= 96 ? launch_rows<KIND, 6, 2>(L) : launch_rows<KIND, 8, 2>(L);
+}
+
+}  // namespace sv
