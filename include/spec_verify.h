@@ -689,8 +689,8 @@ spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes
  *   workspace    at least spec_tree_attention_workspace_size(...) bytes,
  *                256-byte aligned, no initialisation.
  *   dev_status   NULL or one device int32, or-ed into (SPEC_BADBIT_TIMEOUT).
- * Scores and sums are float32; weights are rounded to q's type (an e4m3
- * cache: to f16) before they meet V.  What a row does not see has no effect on it,
+ * Scores and sums are float32; weights are rounded to q's type (or, over an
+ * e4m3 cache, to f16) before they meet V.  What a row does not see has no effect on it,
  * whatever it holds (infinities and NaN too).
  * SPEC_ERR_UNSUPPORTED: N > 32, q_heads not a multiple of the cache's heads,
  * misaligned pointers or strides.

@@ -50,7 +50,7 @@ spec_status cache_map(CUtensorMap* map, const spec_kv_cache& c, void* base) {
     return r == CUDA_SUCCESS ? SPEC_OK : SPEC_ERR_UNSUPPORTED;
 }
 
-constexpr int MAX_R = 32;  // rows of the largest tile
+constexpr int MAX_R = 128;  // rows of the largest tile
 
 // channels of a row as the kernels lay them out
 int width_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
@@ -127,11 +127,16 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                          align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
     A.status = dev_status;
-    const int mt = A.rows <= 16 || A.D > 128 ? 1 : 2;
-    A.tiles_r = (A.rows + mt * 16 - 1) / (mt * 16);
+    // Many rows go to the tcgen05 kernel (128 a tile).  It takes up to 128
+    // channels, and queries of the type that K becomes (an e4m3 cache: bf16).
+    const bool e4 = cache->dtype == SPEC_E4M3;
+    const bool tiles = A.rows > 32 && A.D <= 128 && !(e4 && dtype == SPEC_F16);
+    const int mt = tiles ? 0 : A.rows <= 16 || A.D > 128 ? 1 : 2;
+    const int R = tiles ? 128 : mt * 16;
+    A.tiles_r = (A.rows + R - 1) / R;
     L.ctas = sms;
     L.st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->dtype == SPEC_E4M3  ? launch_attn_e4m3(L, mt)
+    const cudaError_t e = e4                         ? launch_attn_e4m3(L, mt)
                           : cache->dtype == SPEC_F16 ? launch_attn_f16(L, mt)
                                                      : launch_attn_bf16(L, mt);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

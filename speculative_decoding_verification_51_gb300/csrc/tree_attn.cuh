@@ -177,23 +177,26 @@ __device__ __forceinline__ void put_lse(const AttnArgs& A, const Segment& s, int
 
 // After this CTA's part of an item lies in the workspace: the CTA that
 // arrives last joins the parts (R rows of `width` channels each).
-// Call with the whole CTA; `flag` is one shared word.
+// `threads` threads call it together (tid their index), `sync` is their barrier
+// and `flag` a shared word of theirs.
+template <typename Sync>
 __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, const Segment& s,
-                                           int R, int width, int* flag) {
+                                           int R, int width, int* flag, int tid, int threads,
+                                           Sync&& sync) {
     const long long g0 = s.g - s.t0;  // the item's first tile
     const int c0 = cta_of(sh, g0), c1 = cta_of(sh, g0 + s.tiles - 1);
     __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    sync();
+    if (tid == 0) {
         const int last = atomicAdd(&A.plan.arrived[c0], 1) == c1 - c0;
         if (last) A.plan.arrived[c0] = 0;  // as the next call finds it
         *flag = last;
     }
-    __syncthreads();
+    sync();
     if (!*flag) return;
     __threadfence();
     const int quads = width / 4;
-    for (int i = threadIdx.x; i < R * quads; i += blockDim.x) {
+    for (int i = tid; i < R * quads; i += threads) {
         const int r = i / quads, d = (i - r * quads) * 4, row = s.rt * R + r;
         if (row >= A.rows) break;
         float ref = -INFINITY, total = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -223,13 +226,14 @@ __device__ __forceinline__ long long part_slot(const Share& sh, const Segment& s
     return 2ll * blockIdx.x + (s.g - s.t0 >= sh.begin ? 1 : 0);
 }
 
-// Launchers (tree_attn_*.cu); rows of a tile in *R.
+// Launchers (tree_attn_*.cu).
 struct AttnLaunch {
     CUtensorMap mk, mv;
     AttnArgs A;
     int ctas;
     cudaStream_t st;
 };
+// mt: row tiles of 16 of k_attn_rows (1 or 2), or 0 for k_attn_tiles
 cudaError_t launch_attn_bf16(const AttnLaunch& L, int mt);
 cudaError_t launch_attn_f16(const AttnLaunch& L, int mt);
 cudaError_t launch_attn_e4m3(const AttnLaunch& L, int mt);

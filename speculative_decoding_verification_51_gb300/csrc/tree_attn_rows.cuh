@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                     *reinterpret_cast<float2*>(A.part_ml + (slot * R + r) * 2) = make_float2(sm_ref[r], sm_tot[r]);
             }
         }
-        if (!whole) join_parts(A, share, s, R, DP, sm_flag);
+        if (!whole) join_parts(A, share, s, R, DP, sm_flag, threadIdx.x, AR_THREADS, [] { __syncthreads(); });
         __syncthreads();
         if (threadIdx.x == 0) sm_flag[1] = 0;
     }

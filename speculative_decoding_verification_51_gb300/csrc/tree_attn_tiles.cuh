@@ -1,0 +1,625 @@
+// tree_attn_tiles.cuh -- k_attn_tiles: the attention for many rows a key head
+// (up to 128 a tile), on the tcgen05 tensor cores.
+//
+// One CTA per SM, warps by role:
+//   warp 0        TMA: the K and V rows of a tile of 128 tokens, 16-token boxes
+//                 by the page table, 128-byte swizzle
+//   warp 1        one thread issues the products: S = Q K^T (M = 128 rows, N = 128
+//                 tokens) into one of two TMEM buffers, O += P V with P in TMEM
+//                 and V as it lies (token rows: a transposed B operand)
+//   warps 4..7    softmax, one row a thread: S from TMEM, the weights back to it
+//                 as 16-bit P, the row's reference and total in registers; between
+//                 segments the next rows of Q, and the finished rows of O
+//   warps 8..11   (e4m3 cache) K and V from bytes to bf16 in shared memory, the
+//                 row's scale multiplied in
+// S of tile i + 1 is computed while the weights of tile i are made.
+//
+// As in k_attn_rows the reference of a row is raised only when a score passes
+// it by 2^8, so that O in TMEM is seldom rescaled; a weight is then at most
+// 2^8, which bf16 and f16 hold and whose rounding is relative.
+//
+// e4m3: a byte s eeee mmm shifted into bf16's fields is its value times 2^-120,
+// lowest binade included; one bf16 product by 2^(120 + e) gives value times
+// scale exactly (4 significant bits), except NaN, which is looked for apart.
+#pragma once
+
+#include "tree_attn.cuh"
+
+namespace sv {
+
+constexpr float AT_SLACK = 8.f;
+constexpr uint64_t AT_WAIT_NS = 200000000ull;
+
+template <int KIND, int DP>
+struct TilesShape {
+    static constexpr bool E4 = KIND == SPEC_E4M3;
+    static constexpr int R = 128, HALVES = DP / 64;
+    static constexpr int OPERAND = HALVES * 16384;  // 128 tokens (or rows) of 16-bit channels
+    static constexpr int STAGES = E4 ? 2 : DP == 64 ? 5 : 3;
+    static constexpr int RAW = 16384, RAW_STAGES = E4 ? (DP == 64 ? 4 : 2) : 0;
+    static constexpr size_t SMEM = 1024 + size_t(OPERAND) * (1 + 2 * STAGES) + size_t(RAW_STAGES) * 2 * RAW;
+    static_assert(SMEM + 1024 <= 232448, "shared memory");
+    static constexpr int THREADS = E4 ? 384 : 256;
+};
+
+// ---------------------------------------------------------------- tcgen05
+
+template <bool F16>
+__host__ __device__ constexpr uint32_t at_idesc(int n, bool b_mn) {
+    return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) |
+           (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+// K-major: 128-byte rows, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t at_desc_k(uint32_t a) {
+    return uint64_t((a >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// the other way round (64 channels of a token in a 128-byte row): channel
+// blocks 16 KB apart, groups of 8 tokens 1024 bytes apart
+__device__ __forceinline__ uint64_t at_desc_mn(uint32_t a) {
+    return uint64_t((a >> 4) & 0x3FFFu) | (uint64_t(16384 >> 4) << 16) |
+           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+__device__ __forceinline__ void at_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void at_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void at_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void at_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void at_ld32(uint32_t t, float (&f)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(t));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void at_st16(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void at_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void at_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Four e4m3 bytes times 2^e (f: 2^(120 + e) twice, bf16) -> bf16.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w, uint32_t f) {
+    uint2 o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = __byte_perm(w, 0, i ? 0x3424 : 0x1404);  // bytes in the top halves
+        const uint32_t b = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+        uint32_t r;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(f));
+        (i ? o.y : o.x) = r;
+    }
+    // 0x7f and 0xff are NaN
+    if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {
+        if ((w & 0x7fu) == 0x7fu) o.x |= 0x7fffu;
+        if ((w >> 8 & 0x7fu) == 0x7fu) o.x |= 0x7fff0000u;
+        if ((w >> 16 & 0x7fu) == 0x7fu) o.y |= 0x7fffu;
+        if ((w >> 24 & 0x7fu) == 0x7fu) o.y |= 0x7fff0000u;
+    }
+    return o;
+}
+
+__device__ __forceinline__ uint2 bf16x4_mul(uint2 x, uint32_t f) {
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x.x) : "r"(f));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x.y) : "r"(f));
+    return x;
+}
+
+template <int KIND, int DP>
+__global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
+    k_attn_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const __grid_constant__ AttnArgs A) {
+    using S = TilesShape<KIND, DP>;
+    constexpr bool E4 = S::E4, F16 = KIND == SPEC_F16;
+    constexpr int ST = S::STAGES, NR = E4 ? S::RAW_STAGES : 1;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sm_q = smem;
+    uint8_t* sm_k = sm_q + S::OPERAND;
+    uint8_t* sm_v = sm_k + ST * S::OPERAND;
+    uint8_t* sm_raw = sm_v + ST * S::OPERAND;  // [raw stages][K, V][128 tokens][128]
+    __shared__ __align__(16) uint8_t sm_sc[E4 ? NR * 256 : 16];
+    // operands: full / empty; e4m3 bytes: full / empty
+    __shared__ __align__(8) uint64_t kf[ST], ke[ST], vf[ST], ve[ST], rkf[NR], rke[NR], rvf[NR], rve[NR];
+    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag, join_flag;
+    __shared__ uint32_t bad_nodes[2];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Share share = share_of(A);
+    if (share.begin >= share.end) return;  // the whole CTA
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&kf[i], E4 ? 4 : 1);
+            mbar_init(&ke[i], 1);
+            mbar_init(&vf[i], E4 ? 4 : 1);
+            mbar_init(&ve[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&rkf[i], 1);
+            mbar_init(&rke[i], 4);
+            mbar_init(&rvf[i], 1);
+            mbar_init(&rve[i], 4);
+        }
+        mbar_init(&sf[0], 1);
+        mbar_init(&sf[1], 1);
+        mbar_init(&pf[0], 4);
+        mbar_init(&pf[1], 4);
+        mbar_init(&pv[0], 1);
+        mbar_init(&pv[1], 1);
+        mbar_init(&qf, 4);
+        mbar_init(&of, 4);
+        mbar_init(&fin, 1);
+        abort_flag = 0;
+        bad_nodes[0] = bad_nodes[1] = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const int first = request_of(A, share.begin);
+    at_before();
+    __syncthreads();
+    at_after();
+    const uint32_t tbase = tmem_base;
+    constexpr uint32_t T_O = 256, T_P = 384;  // S buffers at 0 and 128, then O, and P (64 columns each)
+    volatile int* gone = &abort_flag;
+    // a bounded wait; once one has run out nobody waits any more
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (*gone) return;
+        if (!mbar_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
+    };
+
+    if (warp == 0) {
+        // ---- copies: lane = (box, chunk of 16 tokens)
+        const int chunk = lane & 7, part = lane >> 3;
+        uint32_t i = 0;  // tiles so far
+        int b_at = first;
+        for (long long g = share.begin; g < share.end;) {
+            const Segment s = segment_at(A, share, g, b_at);
+            b_at = s.b;
+            g += s.t1 - s.t0;
+            const int chunks = (s.ctx + s.n + 15) / 16;
+            const int32_t* table = A.table + (long long)s.b * A.max_pages;
+            auto page_of = [&](int t, int& off) {
+                const int tok = (t * 8 + chunk) * 16;
+                if (t >= s.t1 || t * 8 + chunk >= chunks) return -1;
+                const int p = tok / A.page;
+                off = tok - p * A.page;
+                return __ldg(table + p);
+            };
+            int off = 0, page = page_of(s.t0, off);
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const int nv = min(8, max(0, chunks - t * 8));
+                int off2 = 0;
+                const int page2 = page_of(t + 1, off2);
+                if constexpr (!E4) {
+                    const uint32_t st = i % ST, ph = i / ST;
+                    if (lane == 0) {
+                        wait(&ke[st], ph ^ 1u);
+                        if (!*gone) mbar_arrive_expect_tx(&kf[st], uint32_t(nv * S::HALVES * 2048));
+                    }
+                    __syncwarp();
+                    if (part < S::HALVES && page >= 0 && !*gone)
+                        tma_load_4d(sm_k + st * S::OPERAND + part * 16384 + chunk * 2048, &mk, part * 64, off, s.h, page, &kf[st]);
+                    if (lane == 0) {
+                        wait(&ve[st], ph ^ 1u);
+                        if (!*gone) mbar_arrive_expect_tx(&vf[st], uint32_t(nv * S::HALVES * 2048));
+                    }
+                    __syncwarp();
+                    if (part < S::HALVES && page >= 0 && !*gone)
+                        tma_load_4d(sm_v + st * S::OPERAND + part * 16384 + chunk * 2048, &mv, part * 64, off, s.h, page, &vf[st]);
+                } else {
+                    const uint32_t st = i % NR, ph = i / NR;
+                    uint8_t* raw = sm_raw + st * 2 * S::RAW;
+                    const long long sc = ((long long)page * A.Hkv + s.h) * A.page + off;
+                    if (lane == 0) {
+                        wait(&rke[st], ph ^ 1u);
+                        if (!*gone) mbar_arrive_expect_tx(&rkf[st], uint32_t(nv * (2048 + 16)));
+                    }
+                    __syncwarp();
+                    if (page >= 0 && !*gone) {
+                        if (part == 0) tma_load_4d(raw + chunk * 2048, &mk, 0, off, s.h, page, &rkf[st]);
+                        if (part == 1) bulk_g2s(sm_sc + st * 256 + chunk * 16, A.ks + sc, 16, &rkf[st]);
+                    }
+                    if (lane == 0) {
+                        wait(&rve[st], ph ^ 1u);
+                        if (!*gone) mbar_arrive_expect_tx(&rvf[st], uint32_t(nv * (2048 + 16)));
+                    }
+                    __syncwarp();
+                    if (page >= 0 && !*gone) {
+                        if (part == 0) tma_load_4d(raw + S::RAW + chunk * 2048, &mv, 0, off, s.h, page, &rvf[st]);
+                        if (part == 1) bulk_g2s(sm_sc + st * 256 + 128 + chunk * 16, A.vs + sc, 16, &rvf[st]);
+                    }
+                }
+                page = page2;
+                off = off2;
+            }
+        }
+        // every copy has landed before the CTA leaves (they have, unless a wait ran out)
+        if (lane == 0 && *gone) {
+            for (uint32_t j = i > 8 ? i - 8 : 0; j < i; ++j) {
+                if constexpr (!E4) {
+                    mbar_wait_bounded(&kf[j % ST], (j / ST) & 1u, AT_WAIT_NS / 8);
+                    mbar_wait_bounded(&vf[j % ST], (j / ST) & 1u, AT_WAIT_NS / 8);
+                } else {
+                    mbar_wait_bounded(&rkf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
+                    mbar_wait_bounded(&rvf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t id_s = at_idesc<F16>(128, false), id_o = at_idesc<F16>(DP, true);
+            uint32_t i = 0, seg = 0;
+            int b_at = first;
+            const uint32_t qa = smem_u32(sm_q);
+            auto scores = [&](uint32_t j) {
+                const uint32_t st = j % ST;
+                wait(&kf[st], j / ST);
+                at_after();
+                const uint32_t ka = smem_u32(sm_k) + st * S::OPERAND;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    at_mma_ss(tbase + (j & 1) * 128, at_desc_k(qa + (k >> 2) * 16384 + (k & 3) * 32),
+                              at_desc_k(ka + (k >> 2) * 16384 + (k & 3) * 32), id_s, k > 0);
+                at_commit(&ke[st]);
+                at_commit(&sf[j & 1]);
+            };
+            for (long long g = share.begin; g < share.end; ++seg) {
+                const Segment s = segment_at(A, share, g, b_at);
+                b_at = s.b;
+                g += s.t1 - s.t0;
+                wait(&qf, seg);
+                at_after();
+                scores(i);
+                for (int t = s.t0; t < s.t1; ++t, ++i) {
+                    if (t + 1 < s.t1) scores(i + 1);
+                    const uint32_t st = i % ST;
+                    wait(&vf[st], i / ST);
+                    wait(&pf[i & 1], i >> 1);
+                    if (t == s.t0) wait(&of, seg ^ 1u);  // the last segment's rows have been read
+                    at_after();
+                    const uint32_t va = smem_u32(sm_v) + st * S::OPERAND;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        at_mma_ts(tbase + T_O, tbase + T_P + (i & 1) * 64 + k * 8, at_desc_mn(va + k * 2048), id_o,
+                                  t > s.t0 || k > 0);
+                    at_commit(&ve[st]);
+                    at_commit(&pv[i & 1]);
+                }
+            }
+            at_commit(&fin);  // every product is done before TMEM is freed
+            mbar_wait_bounded(&fin, 0, AT_WAIT_NS);
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---- softmax: row = this thread's TMEM lane
+        const int w = warp - 4, r = w * 32 + lane, tid = r;
+        const uint32_t lanes = uint32_t(w * 32) << 16;
+        const float c = fabsf(A.c);
+        const uint32_t flip = A.c < 0.f ? 0x80008000u : 0u;
+        auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        auto load_q = [&](const Segment& s) {
+            for (int x = tid; x < 128 * (DP / 8); x += 128) {
+                const int rr = x / (DP / 8), j = x - rr * (DP / 8), row = s.rt * 128 + rr, v = row / A.G;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (row < A.rows && j * 8 < A.D && v < s.n)
+                    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                                                        (s.h * A.G + row - v * A.G) * A.qh + j * 8);
+                u.x ^= flip;
+                u.y ^= flip;
+                u.z ^= flip;
+                u.w ^= flip;
+                *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + rr * 128 + (((j & 7) ^ (rr & 7)) << 4)) = u;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) at_arrive(&qf);
+        };
+        uint32_t i = 0, seg = 0;
+        Segment s = segment_at(A, share, share.begin, first);
+        load_q(s);
+        for (;; ++seg) {
+            const int row = s.rt * 128 + r, node = row / A.G;
+            uint32_t mask = 0;
+            if (row < A.rows && node < s.n)
+                mask = A.masks[(long long)s.b * A.N + node] & (0xffffffffu >> (32 - s.n));
+            float ref = -INFINITY, tot = 0.f;
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const uint32_t sa = tbase + lanes + (i & 1) * 128;
+                const uint32_t pa = tbase + lanes + T_P + (i & 1) * 64;  // PV of tile i - 2 is done with it
+                const int t0 = t * 128;
+                const bool tail = t0 + 128 > s.ctx;
+                // which of 32 tokens from t0 + j on this row sees
+                auto sees = [&](int j) {
+                    const int u = t0 + j - s.ctx;
+                    return u <= -32 ? 0xffffffffu
+                           : u < 0  ? (0xffffffffu >> (32 + u)) | (mask << -u)
+                           : u < 32 ? mask >> u
+                                    : 0u;
+                };
+                wait(&sf[i & 1], i >> 1);
+                at_after();
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 128; j += 32) {
+                    float f[32];
+                    at_ld32(sa + j, f);
+                    if (tail) {
+                        const uint32_t on = sees(j);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = on >> e & 1u ? f[e] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) mx = fmaxf(fmaxf(f[e], f[e + 1]), mx);
+                }
+                const float top = mx == -INFINITY ? mx : mx * c;
+                const bool raise = top > ref + AT_SLACK;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float to = raise ? top : ref;
+                    const float f = ref == to ? 1.f : ex2_approx(ref - to);
+                    ref = to;
+                    tot *= f;
+                    if (t > s.t0) {  // O holds sums by the old reference
+                        wait(&pv[(i - 1) & 1], (i - 1) >> 1);
+                        at_after();
+#pragma unroll 1
+                        for (int j = 0; j < DP; j += 32) {
+                            float o[32];
+                            at_ld32(tbase + lanes + T_O + j, o);
+                            uint32_t u[16], v[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                u[e] = __float_as_uint(o[e] * f);
+                                v[e] = __float_as_uint(o[e + 16] * f);
+                            }
+                            at_st16(tbase + lanes + T_O + j, u);
+                            at_st16(tbase + lanes + T_O + j + 16, v);
+                        }
+                    }
+                }
+                const float at = ref == -INFINITY ? 0.f : -ref;
+                uint64_t sum = f2_pack(0.f, 0.f);
+                const uint64_t c2 = f2_pack(c, c), at2 = f2_pack(at, at);
+#pragma unroll
+                for (int j = 0; j < 128; j += 32) {
+                    float f[32];
+                    at_ld32(sa + j, f);
+                    const uint32_t on = tail ? sees(j) : 0xffffffffu;
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(f[2 * e], f[2 * e + 1]), c2, at2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        if (tail) {
+                            a = on >> (2 * e) & 1u ? a : 0.f;
+                            b = on >> (2 * e + 1) & 1u ? b : 0.f;
+                        }
+                        sum = f2_add(sum, f2_pack(a, b));
+                        p[e] = pack16<F16>(a, b);
+                    }
+                    at_st16(pa + j / 2, p);
+                }
+                float s0, s1;
+                f2_unpack(sum, s0, s1);
+                tot += s0 + s1;
+                if (tail) {
+                    // values of tokens past the request's end, and values of
+                    // nodes that are not finite, must not meet a weight of zero
+                    const uint32_t st = i % ST;
+                    wait(&vf[st], i / ST);
+                    uint32_t bad = 0;
+                    for (int x = tid; x < S::OPERAND / 16; x += 128) {
+                        const int tok = t0 + ((x >> 3) & 127);
+                        if (tok < s.ctx) continue;
+                        uint4* p = reinterpret_cast<uint4*>(sm_v + st * S::OPERAND) + x;
+                        if (tok >= s.ctx + s.n) {
+                            *p = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint32_t u[4] = {p->x, p->y, p->z, p->w};
+                        bool hit = false;
+                        constexpr uint32_t EX = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if ((u[e] >> (16 * y) & EX) == EX) {
+                                    u[e] &= ~(0xffffu << (16 * y));
+                                    hit = true;
+                                }
+                        if (hit) {
+                            *p = make_uint4(u[0], u[1], u[2], u[3]);
+                            bad |= 1u << (tok - s.ctx);
+                        }
+                    }
+                    if (bad) atomicOr(&bad_nodes[seg & 1], bad);
+                    fence_proxy_async_smem();
+                }
+                at_st_wait();
+                at_before();
+                __syncwarp();
+                if (lane == 0) at_arrive(&pf[i & 1]);
+            }
+            // the next segment's queries (every product of this one's is done)
+            const Segment done = s;
+            const long long next = s.g + (s.t1 - s.t0);
+            const bool more = next < share.end;
+            sync();  // every warp has marked its nodes
+            const uint32_t nodes_bad = bad_nodes[seg & 1];
+            // the other word is for the next segment, which starts when all
+            // four warps have arrived at qf: nobody reads or marks it now
+            if (tid == 0) bad_nodes[(seg & 1) ^ 1] = 0;
+            if (more) {
+                s = segment_at(A, share, next, s.b);
+                load_q(s);
+            }
+            // (the last scores say that all products but the last two are done,
+            // so that of either barrier only the last phase can be open)
+            wait(&pv[(i - 1) & 1], (i - 1) >> 1);
+            at_after();
+            const bool whole = done.t0 == 0 && done.t1 == done.tiles;
+            const long long slot = part_slot(share, done);
+            const float inv = node < done.n && tot != 0.f ? 1.f / tot : 0.f;
+            const bool none = inv == 0.f && tot == tot;
+            const long long at = (((long long)done.b * A.N + node) * A.Hq + done.h * A.G + row - node * A.G) * A.D;
+#pragma unroll 1
+            for (int j = 0; j < DP; j += 32) {
+                float o[32];
+                at_ld32(tbase + lanes + T_O + j, o);
+                if (row < A.rows) {
+                    for (uint32_t m = nodes_bad & mask; m; m &= m - 1)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (j + e < A.D) o[e] += not_finite_v<KIND>(A, done.b, done.h, done.ctx + __ffs(m) - 1, j + e);
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float lo = none ? 0.f : o[e + 2 * x] * inv, hi = none ? 0.f : o[e + 2 * x + 1] * inv;
+                                u[x] = A.q_f16 ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
+                            }
+                            if (j + e < A.D)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at + j + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(A.part_o + (slot * 128 + r) * DP + j + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+            at_before();
+            __syncwarp();
+            if (lane == 0) at_arrive(&of);
+            if (whole) {
+                put_lse(A, done, row, ref, tot);
+            } else {
+                if (row < A.rows) *reinterpret_cast<float2*>(A.part_ml + (slot * 128 + r) * 2) = make_float2(ref, tot);
+                join_parts(A, share, done, 128, DP, &join_flag, tid, 128, sync);
+            }
+            if (!more) break;
+        }
+    } else if (E4 && warp >= 8) {
+        // ---- bytes to bf16: 8 lanes a token
+        const int tid = threadIdx.x - 256;
+        const uint32_t n = uint32_t(share.end - share.begin);
+        auto side = [&](const uint8_t* raw, const uint8_t* sc, uint8_t* out) {
+            const int x = tid & 7;
+#pragma unroll 4
+            for (int t = tid >> 3; t < (x * 16 < DP ? 128 : 0); t += 16) {
+                const uint4 w = *reinterpret_cast<const uint4*>(raw + t * 128 + ((x ^ (t & 7)) << 4));
+                const int e = min(max(int(sc[t]), 1), 253) - 127;
+                // 2^(120 + e), in two factors where it is past bf16's range
+                const uint32_t f = uint32_t(min(120 + e, 127) + 127) * 0x00800080u;
+                uint2 a = e4m3x4_to_bf16(w.x, f), b = e4m3x4_to_bf16(w.y, f),
+                      c = e4m3x4_to_bf16(w.z, f), d = e4m3x4_to_bf16(w.w, f);
+                if (e > 7) {
+                    const uint32_t f2 = uint32_t(e - 7 + 127) * 0x00800080u;
+                    a = bf16x4_mul(a, f2);
+                    b = bf16x4_mul(b, f2);
+                    c = bf16x4_mul(c, f2);
+                    d = bf16x4_mul(d, f2);
+                }
+                uint8_t* o = out + (x >> 2) * 16384 + t * 128;
+                const int j = 2 * (x & 3);
+                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
+                // the lanes of the two channel halves write odd and even chunks in
+                // turn, so that the 8 lanes of a token touch all banks
+                const int swap = x >> 2;
+                *reinterpret_cast<uint4*>(o + (((j + swap) ^ (t & 7)) << 4)) = swap ? hi : lo;
+                *reinterpret_cast<uint4*>(o + (((j + 1 - swap) ^ (t & 7)) << 4)) = swap ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint32_t rs = i % NR, st = i % ST;
+            const uint8_t* raw = sm_raw + rs * 2 * S::RAW;
+            wait(&rkf[rs], i / NR);
+            wait(&ke[st], (i / ST) ^ 1u);
+            side(raw, sm_sc + rs * 256, sm_k + st * S::OPERAND);
+            if (lane == 0) {
+                at_arrive(&kf[st]);
+                at_arrive(&rke[rs]);
+            }
+            wait(&rvf[rs], i / NR);
+            wait(&ve[st], (i / ST) ^ 1u);
+            side(raw + S::RAW, sm_sc + rs * 256 + 128, sm_v + st * S::OPERAND);
+            if (lane == 0) {
+                at_arrive(&vf[st]);
+                at_arrive(&rve[rs]);
+            }
+        }
+    }
+
+    at_before();
+    __syncthreads();
+    at_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
+    if (threadIdx.x == 0 && *gone && A.status) atomicOr(A.status, int(SPEC_BADBIT_TIMEOUT));
+}
+
+template <int KIND, int DP>
+cudaError_t launch_tiles(const AttnLaunch& L) {
+    using S = TilesShape<KIND, DP>;
+    static bool ready[64] = {};  // per device; setting it twice does no harm
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(k_attn_tiles<KIND, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM));
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    k_attn_tiles<KIND, DP><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
+    return cudaGetLastError();
+}
+
+}  // namespace sv

@@ -163,7 +163,7 @@ def attention(q, cache, table, ctx, nodes, masks, scale):
             lse[b, :n, h * G:(h + 1) * G] = torch.where(tot > 0, top[..., 0] + torch.log(tot), torch.full_like(tot, -math.inf))
             va = torch.nan_to_num(V[:, h], 0, 0, 0).abs()
             pv = torch.einsum("ngt,td->ngd", torch.nan_to_num(p), va)
-            uw = U[torch.float16] if e4 else U[q.dtype]
+            uw = U[q.dtype]  # weights are rounded to q's type, or to f16
             bd = pv * (uw + 2 * ds[..., None] + 2.0 ** -19)
             if e4:  # f16 weights below 2^-14 of the largest contribution
                 big = (torch.nan_to_num(p) * va.amax(-1)).amax(-1)

@@ -371,6 +371,23 @@ def test_attention(B, N, Hq, Hkv, D, page, rng, qdt, kind):
 
 
 @pytest.mark.parametrize("qdt,kind", KINDS)
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,page,ctx", [
+    # every CTA has a dozen tiles and more, across several items
+    (3, 12, 16, 4, 128, 64, (30000, 17, 21111)),
+    (2, 9, 36, 6, 64, 128, (20000, 20001)),
+    (3, 2, 12, 4, 128, 16, (30000, 300, 22222)),
+    (2, 5, 20, 4, 96, 32, (15003, 29999)),
+    (2, 3, 8, 2, 256, 32, (9000, 14001)),
+    (300, 5, 28, 4, 64, 16, None),
+])
+def test_attention_long(B, N, Hq, Hkv, D, page, ctx, qdt, kind):
+    r = np.random.default_rng(N)
+    ctx = np.array(ctx) if ctx else r.integers(0, 700, B)
+    nodes = np.maximum(1, N - np.arange(B) % 3)
+    check_attention(*attn_case(B, N, Hq, Hkv, D, page, qdt, kind, ctx, nodes, 5 * N + D))
+
+
+@pytest.mark.parametrize("qdt,kind", KINDS)
 @pytest.mark.parametrize("N,Hq", [(6, 4), (12, 24)])
 def test_attention_masks_and_bad_values(N, Hq, qdt, kind):
     """Arbitrary masks, rows that see nothing, bad requests, infinities and NaN in
