@@ -127,10 +127,9 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                          align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
     A.status = dev_status;
-    // Many rows go to the tcgen05 kernel (128 a tile).  It takes up to 128
-    // channels, and queries of the type that K becomes (an e4m3 cache: bf16).
+    // Many rows go to the tcgen05 kernel (128 a tile), which takes up to 128 channels.
     const bool e4 = cache->dtype == SPEC_E4M3;
-    const bool tiles = A.rows > 32 && A.D <= 128 && !(e4 && dtype == SPEC_F16);
+    const bool tiles = A.rows > 32 && A.D <= 128;
     const int mt = tiles ? 0 : A.rows <= 16 || A.D > 128 ? 1 : 2;
     const int R = tiles ? 128 : mt * 16;
     A.tiles_r = (A.rows + R - 1) / R;

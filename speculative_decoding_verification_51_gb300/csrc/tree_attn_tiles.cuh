@@ -10,17 +10,21 @@
 //   warps 4..7    softmax, one row a thread: S from TMEM, the weights back to it
 //                 as 16-bit P, the row's reference and total in registers; between
 //                 segments the next rows of Q, and the finished rows of O
-//   warps 8..11   (e4m3 cache) K and V from bytes to bf16 in shared memory, the
-//                 row's scale multiplied in
+//   warps 8..11   (e4m3 cache) K and V from bytes to f16 in shared memory
 // S of tile i + 1 is computed while the weights of tile i are made.
 //
 // As in k_attn_rows the reference of a row is raised only when a score passes
 // it by 2^8, so that O in TMEM is seldom rescaled; a weight is then at most
 // 2^8, which bf16 and f16 hold and whose rounding is relative.
 //
-// e4m3: a byte s eeee mmm shifted into bf16's fields is its value times 2^-120,
-// lowest binade included; one bf16 product by 2^(120 + e) gives value times
-// scale exactly (4 significant bits), except NaN, which is looked for apart.
+// e4m3: a value v 2^e is stored as f16 v 2^(e - E), E the largest exponent of
+// the tile's rows (one for K, one for V): exact for rows within 2^15 of the
+// tile's largest, and off by 2^-33 of the largest below.  2^E is then one factor
+// for the whole tile: for K it joins the scale of the scores, for V the
+// exponents of the weights, w_t = 2^(s_t + E - m), so that the tiles' sums are in
+// one unit; the total takes 2^-E times the tile's weights.  E is taken as
+// -100 or more, so that a tile of zeros does not push the total out of float32.
+// Queries become f16 by a power of two a row that brings the largest to [1, 2).
 #pragma once
 
 #include "tree_attn.cuh"
@@ -81,8 +85,8 @@ __device__ __forceinline__ void at_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void at_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void at_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void at_ld32(uint32_t t, float (&f)[32]) {
-    uint32_t r[32];
+// 32 columns of this thread's lane; at_ld_wait before they are used
+__device__ __forceinline__ void at_ld32(uint32_t t, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
@@ -94,9 +98,18 @@ __device__ __forceinline__ void at_ld32(uint32_t t, float (&f)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
           "=r"(r[31])
         : "r"(t));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+// (the registers pass through, so that nothing reads them before the wait)
+__device__ __forceinline__ void at_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                   "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                   "+r"(r[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void at_st16(uint32_t t, const uint32_t (&r)[16]) {
     asm volatile(
@@ -111,31 +124,15 @@ __device__ __forceinline__ void at_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Four e4m3 bytes times 2^e (f: 2^(120 + e) twice, bf16) -> bf16.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w, uint32_t f) {
-    uint2 o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t x = __byte_perm(w, 0, i ? 0x3424 : 0x1404);  // bytes in the top halves
-        const uint32_t b = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
-        uint32_t r;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(f));
-        (i ? o.y : o.x) = r;
-    }
-    // 0x7f and 0xff are NaN
-    if (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {
-        if ((w & 0x7fu) == 0x7fu) o.x |= 0x7fffu;
-        if ((w >> 8 & 0x7fu) == 0x7fu) o.x |= 0x7fff0000u;
-        if ((w >> 16 & 0x7fu) == 0x7fu) o.y |= 0x7fffu;
-        if ((w >> 24 & 0x7fu) == 0x7fu) o.y |= 0x7fff0000u;
-    }
-    return o;
+// 2^d as two halves (d <= 0; 0 below f16's least subnormal)
+__device__ __forceinline__ uint32_t half2_exp2(int d) {
+    const uint32_t h = d >= -14 ? uint32_t(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+    return h * 0x10001u;
 }
-
-__device__ __forceinline__ uint2 bf16x4_mul(uint2 x, uint32_t f) {
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x.x) : "r"(f));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x.y) : "r"(f));
-    return x;
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 template <int KIND, int DP>
@@ -143,7 +140,7 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
     k_attn_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ AttnArgs A) {
     using S = TilesShape<KIND, DP>;
-    constexpr bool E4 = S::E4, F16 = KIND == SPEC_F16;
+    constexpr bool E4 = S::E4, F16 = KIND != SPEC_BF16;
     constexpr int ST = S::STAGES, NR = E4 ? S::RAW_STAGES : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -159,6 +156,9 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, join_flag;
     __shared__ uint32_t bad_nodes[2];
+    // e4m3: the exponents E of the last tiles' K and V (a slot is written again
+    // only after the products of tile i + 2, so after softmax has read tile i's)
+    __shared__ int unit_k[4], unit_v[4];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Share share = share_of(A);
@@ -336,9 +336,58 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
         const int w = warp - 4, r = w * 32 + lane, tid = r;
         const uint32_t lanes = uint32_t(w * 32) << 16;
         const float c = fabsf(A.c);
+        // a factor of zero would make NaN of -inf; no score of this size counts
+        constexpr float LEAST = 1e-30f;
         const uint32_t flip = A.c < 0.f ? 0x80008000u : 0u;
         auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        float rc = c;  // the row's factor on scores
         auto load_q = [&](const Segment& s) {
+            if constexpr (E4) {
+                // a row a thread: its largest value, then f16
+                const int row = s.rt * 128 + r, v = row / A.G;
+                const bool on = row < A.rows && v < s.n;
+                const uint16_t* src = static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                                      (s.h * A.G + row - v * A.G) * A.qh;
+                float f[8], m = 0.f;
+                auto get = [&](int j) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (on && j * 8 < A.D) u = __ldg(reinterpret_cast<const uint4*>(src + j * 8));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (A.q_f16) {
+                            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                            f[2 * e] = x.x;
+                            f[2 * e + 1] = x.y;
+                        } else {
+                            f[2 * e] = bf16_lo(w[e]);
+                            f[2 * e + 1] = bf16_hi(w[e]);
+                        }
+                    }
+                };
+#pragma unroll 4
+                for (int j = 0; j < DP / 8; ++j) {
+                    get(j);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[e]));
+                }
+                const uint32_t ex = max(min(__float_as_uint(m) >> 23, 253u), 1u);
+                const float f2 = __uint_as_float((254u - ex) << 23);
+                rc = c * exp2_int(int(ex) - 127);
+#pragma unroll 4
+                for (int j = 0; j < DP / 8; ++j) {
+                    get(j);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack16<true>(f[2 * e] * f2, f[2 * e + 1] * f2) ^ flip;
+                    *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) at_arrive(&qf);
+                return;
+            }
             for (int x = tid; x < 128 * (DP / 8); x += 128) {
                 const int rr = x / (DP / 8), j = x - rr * (DP / 8), row = s.rt * 128 + rr, v = row / A.G;
                 uint4 u = make_uint4(0, 0, 0, 0);
@@ -379,20 +428,48 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 };
                 wait(&sf[i & 1], i >> 1);
                 at_after();
-                float mx = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < 128; j += 32) {
-                    float f[32];
-                    at_ld32(sa + j, f);
-                    if (tail) {
+                if (tail) {
+                    // what the row does not see becomes -inf, in place
+#pragma unroll 1
+                    for (int j = 0; j < 128; j += 32) {
                         const uint32_t on = sees(j);
+                        uint32_t f[32], u[16], v[16];
+                        at_ld32(sa + j, f);
+                        at_ld_wait(f);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = on >> e & 1u ? f[e] : -INFINITY;
+                        for (int e = 0; e < 16; ++e) {
+                            u[e] = on >> e & 1u ? f[e] : 0xff800000u;
+                            v[e] = on >> (e + 16) & 1u ? f[e + 16] : 0xff800000u;
+                        }
+                        at_st16(sa + j, u);
+                        at_st16(sa + j + 16, v);
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) mx = fmaxf(fmaxf(f[e], f[e + 1]), mx);
+                    at_st_wait();
                 }
-                const float top = mx == -INFINITY ? mx : mx * c;
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int j = 0; j < 128; j += 64) {
+                    uint32_t f[32], g[32];
+                    at_ld32(sa + j, f);
+                    at_ld32(sa + j + 32, g);
+                    at_ld_wait(f);
+                    at_ld_wait(g);
+                    float m2 = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        mx = fmaxf(fmaxf(__uint_as_float(f[e]), __uint_as_float(f[e + 1])), mx);
+                        m2 = fmaxf(fmaxf(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), m2);
+                    }
+                    mx = fmaxf(mx, m2);
+                }
+                // the tile's factor on scores, and the unit of its values
+                float ct = fmaxf(c, LEAST), unit = 0.f;
+                if constexpr (E4) {
+                    wait(&vf[i % ST], i / ST);
+                    ct = fmaxf(rc * exp2_int(unit_k[i & 3]), LEAST);
+                    unit = float(unit_v[i & 3]);
+                }
+                const float top = mx == -INFINITY ? mx : fmaf(mx, ct, unit);
                 const bool raise = top > ref + AT_SLACK;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float to = raise ? top : ref;
@@ -404,46 +481,48 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                         at_after();
 #pragma unroll 1
                         for (int j = 0; j < DP; j += 32) {
-                            float o[32];
+                            uint32_t o[32], u[16], v[16];
                             at_ld32(tbase + lanes + T_O + j, o);
-                            uint32_t u[16], v[16];
+                            at_ld_wait(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                u[e] = __float_as_uint(o[e] * f);
-                                v[e] = __float_as_uint(o[e + 16] * f);
+                                u[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                v[e] = __float_as_uint(__uint_as_float(o[e + 16]) * f);
                             }
                             at_st16(tbase + lanes + T_O + j, u);
                             at_st16(tbase + lanes + T_O + j + 16, v);
                         }
                     }
                 }
-                const float at = ref == -INFINITY ? 0.f : -ref;
+                const float at = (ref == -INFINITY ? 0.f : -ref) + unit;
                 uint64_t sum = f2_pack(0.f, 0.f);
-                const uint64_t c2 = f2_pack(c, c), at2 = f2_pack(at, at);
+                const uint64_t c2 = f2_pack(ct, ct), at2 = f2_pack(at, at);
+#pragma unroll 1
+                for (int j = 0; j < 128; j += 64) {
+                    uint32_t f[2][32];
+                    at_ld32(sa + j, f[0]);
+                    at_ld32(sa + j + 32, f[1]);
+                    at_ld_wait(f[0]);
+                    at_ld_wait(f[1]);
 #pragma unroll
-                for (int j = 0; j < 128; j += 32) {
-                    float f[32];
-                    at_ld32(sa + j, f);
-                    const uint32_t on = tail ? sees(j) : 0xffffffffu;
-                    uint32_t p[16];
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float a, b;
-                        f2_unpack(f2_fma(f2_pack(f[2 * e], f[2 * e + 1]), c2, at2), a, b);
-                        a = ex2_approx(a);
-                        b = ex2_approx(b);
-                        if (tail) {
-                            a = on >> (2 * e) & 1u ? a : 0.f;
-                            b = on >> (2 * e + 1) & 1u ? b : 0.f;
+                        for (int e = 0; e < 16; ++e) {
+                            float a, b;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(f[x][2 * e]), __uint_as_float(f[x][2 * e + 1])), c2, at2), a, b);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            sum = f2_add(sum, f2_pack(a, b));
+                            p[e] = pack16<F16>(a, b);
                         }
-                        sum = f2_add(sum, f2_pack(a, b));
-                        p[e] = pack16<F16>(a, b);
+                        at_st16(pa + j / 2 + x * 16, p);
                     }
-                    at_st16(pa + j / 2, p);
                 }
                 float s0, s1;
                 f2_unpack(sum, s0, s1);
-                tot += s0 + s1;
+                if constexpr (E4) tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 3]), tot);
+                else tot += s0 + s1;
                 if (tail) {
                     // values of tokens past the request's end, and values of
                     // nodes that are not finite, must not meet a weight of zero
@@ -506,8 +585,12 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
             const long long at = (((long long)done.b * A.N + node) * A.Hq + done.h * A.G + row - node * A.G) * A.D;
 #pragma unroll 1
             for (int j = 0; j < DP; j += 32) {
+                uint32_t u0[32];
+                at_ld32(tbase + lanes + T_O + j, u0);
+                at_ld_wait(u0);
                 float o[32];
-                at_ld32(tbase + lanes + T_O + j, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u0[e]);
                 if (row < A.rows) {
                     for (uint32_t m = nodes_bad & mask; m; m &= m - 1)
 #pragma unroll
@@ -545,54 +628,73 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
             if (!more) break;
         }
     } else if (E4 && warp >= 8) {
-        // ---- bytes to bf16: 8 lanes a token
-        const int tid = threadIdx.x - 256;
-        const uint32_t n = uint32_t(share.end - share.begin);
-        auto side = [&](const uint8_t* raw, const uint8_t* sc, uint8_t* out) {
-            const int x = tid & 7;
-#pragma unroll 4
-            for (int t = tid >> 3; t < (x * 16 < DP ? 128 : 0); t += 16) {
-                const uint4 w = *reinterpret_cast<const uint4*>(raw + t * 128 + ((x ^ (t & 7)) << 4));
-                const int e = min(max(int(sc[t]), 1), 253) - 127;
-                // 2^(120 + e), in two factors where it is past bf16's range
-                const uint32_t f = uint32_t(min(120 + e, 127) + 127) * 0x00800080u;
-                uint2 a = e4m3x4_to_bf16(w.x, f), b = e4m3x4_to_bf16(w.y, f),
-                      c = e4m3x4_to_bf16(w.z, f), d = e4m3x4_to_bf16(w.w, f);
-                if (e > 7) {
-                    const uint32_t f2 = uint32_t(e - 7 + 127) * 0x00800080u;
-                    a = bf16x4_mul(a, f2);
-                    b = bf16x4_mul(b, f2);
-                    c = bf16x4_mul(c, f2);
-                    d = bf16x4_mul(d, f2);
-                }
-                uint8_t* o = out + (x >> 2) * 16384 + t * 128;
-                const int j = 2 * (x & 3);
-                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-                // the lanes of the two channel halves write odd and even chunks in
-                // turn, so that the 8 lanes of a token touch all banks
-                const int swap = x >> 2;
-                *reinterpret_cast<uint4*>(o + (((j + swap) ^ (t & 7)) << 4)) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(o + (((j + 1 - swap) ^ (t & 7)) << 4)) = swap ? lo : hi;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+        // ---- bytes to f16: 8 lanes a token, 8 tokens a thread
+        const int tid = threadIdx.x - 256, x = tid & 7;
+        // largest scale byte of the tile's first `valid` tokens (all lanes)
+        auto largest = [&](const uint8_t* sc, int valid) {
+            uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
+            const int left = valid - lane * 4;
+            w = left >= 4 ? w : left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u);
+            w = __vmaxu4(w, w >> 16);
+            return min(max(int(__reduce_max_sync(0xffffffffu, max(w & 255u, w >> 8 & 255u))), 1), 253) - 127;
         };
-        for (uint32_t i = 0; i < n; ++i) {
-            const uint32_t rs = i % NR, st = i % ST;
-            const uint8_t* raw = sm_raw + rs * 2 * S::RAW;
-            wait(&rkf[rs], i / NR);
-            wait(&ke[st], (i / ST) ^ 1u);
-            side(raw, sm_sc + rs * 256, sm_k + st * S::OPERAND);
-            if (lane == 0) {
-                at_arrive(&kf[st]);
-                at_arrive(&rke[rs]);
-            }
-            wait(&rvf[rs], i / NR);
-            wait(&ve[st], (i / ST) ^ 1u);
-            side(raw + S::RAW, sm_sc + rs * 256 + 128, sm_v + st * S::OPERAND);
-            if (lane == 0) {
-                at_arrive(&vf[st]);
-                at_arrive(&rve[rs]);
+        uint32_t i = 0;
+        int b_at = first;
+        for (long long g = share.begin; g < share.end;) {
+            const Segment s = segment_at(A, share, g, b_at);
+            b_at = s.b;
+            g += s.t1 - s.t0;
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const int valid = s.ctx + s.n - t * 128;
+                const uint32_t rs = i % NR, st = i % ST;
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side) {  // K, then V
+                    const uint8_t* raw = sm_raw + (rs * 2 + side) * S::RAW;
+                    const uint8_t* sc = sm_sc + rs * 256 + side * 128;
+                    uint8_t* out = (side ? sm_v : sm_k) + st * S::OPERAND + (x >> 2) * 16384;
+                    wait(side ? &rvf[rs] : &rkf[rs], i / NR);
+                    int unit = largest(sc, valid);
+                    wait(side ? &ve[st] : &ke[st], (i / ST) ^ 1u);
+                    if (side) unit = max(unit, -100);
+                    if (tid == 0) (side ? unit_v : unit_k)[i & 3] = unit;
+                    if (x * 16 < DP) {
+#pragma unroll 1
+                        for (int k0 = tid >> 3; k0 < 128; k0 += 64) {
+                            uint4 w[4];
+                            uint32_t f[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int tk = k0 + k * 16;
+                                w[k] = *reinterpret_cast<const uint4*>(raw + tk * 128 + ((x ^ (tk & 7)) << 4));
+                                f[k] = half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int tk = k0 + k * 16;
+                                const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                                uint32_t h[8];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    h[2 * e] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e])), f[k]);
+                                    h[2 * e + 1] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e] >> 16)), f[k]);
+                                }
+                                uint8_t* o = out + tk * 128;
+                                const int j = 2 * (x & 3), swap = x >> 2;
+                                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                                // the lanes of the two channel halves write odd and even
+                                // chunks in turn, so that a token's 8 lanes touch all banks
+                                *reinterpret_cast<uint4*>(o + (((j + swap) ^ (tk & 7)) << 4)) = swap ? hi : lo;
+                                *reinterpret_cast<uint4*>(o + (((j + 1 - swap) ^ (tk & 7)) << 4)) = swap ? lo : hi;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        at_arrive(side ? &vf[st] : &kf[st]);
+                        at_arrive(side ? &rve[rs] : &rke[rs]);
+                    }
+                }
             }
         }
     }
