@@ -31,15 +31,15 @@ bool encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
 }
 
 // One side of a cache as (channel, token of the page, head, page), in boxes
-// of 128 bytes of a row (channels past head_dim read as zeros) x 16 tokens.
-spec_status cache_map(CUtensorMap* map, const spec_kv_cache& c, void* base) {
+// of 128 bytes of a row (channels past head_dim read as zeros) x `tokens` rows.
+spec_status cache_map(CUtensorMap* map, const spec_kv_cache& c, void* base, int tokens) {
     PFN_cuTensorMapEncodeTiled_v12000 enc;
     if (!encoder(&enc)) return SPEC_ERR_CUDA;
     const cuuint64_t es = cuuint64_t(dtype_bytes(c.dtype));
     const cuuint64_t dims[4] = {cuuint64_t(c.head_dim), cuuint64_t(c.page_size),
                                 cuuint64_t(c.heads), cuuint64_t(c.num_pages)};
     const cuuint64_t strides[3] = {c.token_stride * es, c.head_stride * es, c.page_stride * es};
-    const cuuint32_t box[4] = {cuuint32_t(128 / es), 16, 1, 1};
+    const cuuint32_t box[4] = {cuuint32_t(128 / es), cuuint32_t(tokens), 1, 1};
     const cuuint32_t one[4] = {1, 1, 1, 1};
     const CUtensorMapDataType t = c.dtype == SPEC_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                   : c.dtype == SPEC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -93,9 +93,6 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     if (sms <= 0 || sms > PLAN_PARTS) return SPEC_ERR_CUDA;
 
     AttnLaunch L;
-    spec_status r = cache_map(&L.mk, *cache, cache->k);
-    if (r == SPEC_OK) r = cache_map(&L.mv, *cache, cache->v);
-    if (r != SPEC_OK) return r;
     AttnArgs& A = L.A;
     A.q = q;
     A.qb = q_batch_stride;
@@ -133,6 +130,12 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     const int mt = tiles ? 0 : A.rows <= 16 || A.D > 128 ? 1 : 2;
     const int R = tiles ? 128 : mt * 16;
     A.tiles_r = (A.rows + R - 1) / R;
+    // A copy lies in one page: k_attn_rows takes chunks of 16 tokens,
+    // k_attn_tiles the longest power of two up to a tile that divides a page.
+    A.box = tiles ? std::min(TREE_TILE, A.page & -A.page) : 16;
+    spec_status r = cache_map(&L.mk, *cache, cache->k, A.box);
+    if (r == SPEC_OK) r = cache_map(&L.mv, *cache, cache->v, A.box);
+    if (r != SPEC_OK) return r;
     L.ctas = sms;
     L.st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = e4                         ? launch_attn_e4m3(L, mt)

@@ -31,6 +31,7 @@ struct AttnArgs {
     long long v_page, v_head, v_token;
     int B, N, Hq, Hkv, G, D, page, max_pages;
     int rows, tiles_r;  // rows of a (request, key head), row tiles of them
+    int box;            // tokens of one copy (k_attn_tiles)
     float c;            // scale * log2(e): scores are exponents of two
     int q_f16;          // q and out are f16 (else bf16)
     float* part_o;      // [2 * CTAs][R][width] unnormalised sums
@@ -52,47 +53,82 @@ struct Share {
     int ctas;
 };
 
-__device__ __forceinline__ Share share_of(const AttnArgs& A) {
+__device__ __forceinline__ Share share_of(long long total) {
     Share s;
-    s.total = (long long)A.plan.tiles[A.B] * A.Hkv * A.tiles_r;
-    s.ctas = int(s.total < (long long)gridDim.x ? s.total : (long long)gridDim.x);
+    s.total = total;
+    s.ctas = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
     s.begin = s.end = 0;
     if ((int)blockIdx.x < s.ctas) {
-        s.begin = s.total * blockIdx.x / s.ctas;
-        s.end = s.total * (blockIdx.x + 1) / s.ctas;
+        s.begin = total * blockIdx.x / s.ctas;
+        s.end = total * (blockIdx.x + 1) / s.ctas;
     }
     return s;
 }
+
+// The part of the plan's lists that a CTA starts with, in shared memory: their
+// reads depend on one another, and each would wait for L2 or HBM.  Requests
+// past the window are read where they lie.
+constexpr int PLAN_WINDOW = 32;
+struct PlanWindow {
+    int b0;
+    int tiles[PLAN_WINDOW + 1], ctx[PLAN_WINDOW], nodes[PLAN_WINDOW];
+};
+struct Lists {
+    const PlanWindow& w;
+    const PlanView& p;
+    int b0;
+    __device__ __forceinline__ int tiles(int b) const {
+        return b - b0 <= PLAN_WINDOW ? w.tiles[b - b0] : p.tiles[b];
+    }
+    __device__ __forceinline__ int ctx(int b) const { return b - b0 < PLAN_WINDOW ? w.ctx[b - b0] : p.ctx[b]; }
+    __device__ __forceinline__ int nodes(int b) const {
+        return b - b0 < PLAN_WINDOW ? w.nodes[b - b0] : p.nodes[b];
+    }
+};
+
+// This CTA's share, and the window from the request that holds its first tile
+// on.  Call with the whole CTA; false (for all of it) where there is no share.
+__device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Share& s) {
+    const long long hr = (long long)A.Hkv * A.tiles_r;
+    const int last = A.plan.tiles[A.B];
+    bool any = false;
+    for (int i = threadIdx.x; i < A.B; i += blockDim.x) {
+        const int lo = A.plan.tiles[i], hi = A.plan.tiles[i + 1];
+        if (!any) {
+            s = share_of(last * hr);
+            any = true;
+        }
+        if (lo * hr <= s.begin && s.begin < hi * hr) w.b0 = i;
+    }
+    s = share_of(last * hr);
+    if (s.begin >= s.end) return false;
+    __syncthreads();
+    const int b0 = w.b0;
+    for (int i = threadIdx.x; i <= PLAN_WINDOW && b0 + i <= A.B; i += blockDim.x) {
+        w.tiles[i] = A.plan.tiles[b0 + i];
+        if (i < PLAN_WINDOW && b0 + i < A.B) {
+            w.ctx[i] = A.plan.ctx[b0 + i];
+            w.nodes[i] = A.plan.nodes[b0 + i];
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
 // the CTA whose share holds tile g
 __device__ __forceinline__ int cta_of(const Share& s, long long g) {
     return int(((g + 1) * s.ctas - 1) / s.total);
 }
 
-// The request whose tiles hold g (a whole warp searches, 32 ways a step).
-__device__ __forceinline__ int request_of(const AttnArgs& A, long long g) {
-    const int lane = threadIdx.x & 31;
-    const long long hr = (long long)A.Hkv * A.tiles_r;
-    int lo = 0, hi = A.B;  // tiles[lo] * hr <= g < tiles[hi] * hr
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + (lane + 1) * step;
-        const bool le = i < hi && A.plan.tiles[i] * hr <= g;
-        const int k = __popc(__ballot_sync(0xffffffffu, le));
-        hi = min(hi, lo + (k + 1) * step);
-        lo += k * step;
-    }
-    return lo;
-}
-
 // The segment that starts at tile g; b is the request that holds g or one before.
-__device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Share& s, long long g, int b) {
+__device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Lists& L, const Share& s, long long g, int b) {
     const long long hr = (long long)A.Hkv * A.tiles_r;
     Segment x;
-    int lo = A.plan.tiles[b], hi = A.plan.tiles[b + 1];
+    int lo = L.tiles(b), hi = L.tiles(b + 1);
     while (hi * hr <= g) {
         ++b;
         lo = hi;
-        hi = A.plan.tiles[b + 1];
+        hi = L.tiles(b + 1);
     }
     x.b = b;
     x.g = g;
@@ -103,8 +139,8 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Share& s,
     x.t1 = int(min((long long)x.tiles, x.t0 + (s.end - g)));
     x.h = item / A.tiles_r;
     x.rt = item - x.h * A.tiles_r;
-    x.ctx = A.plan.ctx[b];
-    x.n = A.plan.nodes[b];
+    x.ctx = L.ctx(b);
+    x.n = L.nodes(b);
     const int chunks = (x.ctx + x.n + 15) / 16;
     x.c0 = x.t0 * (TREE_TILE / 16);
     x.c1 = min(x.t1 * (TREE_TILE / 16), chunks);
@@ -177,12 +213,13 @@ __device__ __forceinline__ void put_lse(const AttnArgs& A, const Segment& s, int
 
 // After this CTA's part of an item lies in the workspace: the CTA that
 // arrives last joins the parts (R rows of `width` channels each).
-// `threads` threads call it together (tid their index), `sync` is their barrier
-// and `flag` a shared word of theirs.
-template <typename Sync>
+// JP: parts read at a time.  `threads` threads call it together (tid their index, `bar` their barrier) and
+// `flag` is a shared word of theirs.
+template <int JP>
 __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, const Segment& s,
                                            int R, int width, int* flag, int tid, int threads,
-                                           Sync&& sync) {
+                                           int bar) {
+    auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory"); };
     const long long g0 = s.g - s.t0;  // the item's first tile
     const int c0 = cta_of(sh, g0), c1 = cta_of(sh, g0 + s.tiles - 1);
     __threadfence();
@@ -195,30 +232,69 @@ __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, c
     sync();
     if (!*flag) return;
     __threadfence();
-    const int quads = width / 4;
-    for (int i = tid; i < R * quads; i += threads) {
-        const int r = i / quads, d = (i - r * quads) * 4, row = s.rt * R + r;
-        if (row >= A.rows) break;
-        float ref = -INFINITY, total = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = c0; c <= c1; ++c) {
-            const long long slot = 2 * c + (c == c0 ? 1 : 0);
-            ref = fmaxf(ref, __ldcg(A.part_ml + (slot * R + r) * 2));
+    // A warp takes 32 rows at most.  Each lane knows one row's references and
+    // totals; then the rows' sums are read four rows and JP parts at a
+    // time (4 JP loads a lane in flight), a lane 4 channels of each.
+    const int lane = tid & 31, parts = c1 - c0 + 1, warps = threads >> 5;
+    const int per = (R + warps - 1) / warps;  // rows of a warp
+    const int r0 = (tid >> 5) * per;
+    const int rows = min(min(per, R - r0), A.rows - s.rt * R - r0);
+    auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
+    const int mine = r0 + min(lane, max(rows - 1, 0));
+    float ref = -INFINITY, total = 0.f;
+    if (rows > 0) {
+        const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + mine;
+        for (int c = 0; c < parts; c += 4) {  // the running form of the total
+            float2 x[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) x[y] = c + y < parts ? __ldcg(ml + slot(c + y) * R) : make_float2(-INFINITY, 0.f);
+            const float to = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), ref);
+            const float at = to == -INFINITY ? 0.f : to;
+            total *= ex2_approx(ref - at);
+            ref = to;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) total = fmaf(ex2_approx(x[y].x - at), x[y].y, total);
         }
-        const float at = ref == -INFINITY ? 0.f : ref;
-        for (int c = c0; c <= c1; ++c) {
-            const long long slot = 2 * c + (c == c0 ? 1 : 0);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(A.part_ml) + slot * R + r);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(A.part_o + (slot * R + r) * width + d));
-            const float f = ex2_approx(ml.x - at);
-            total += f * ml.y;
-            o[0] = fmaf(f, x.x, o[0]);
-            o[1] = fmaf(f, x.y, o[1]);
-            o[2] = fmaf(f, x.z, o[2]);
-            o[3] = fmaf(f, x.w, o[3]);
-        }
-        put_row(A, s, row, d, o, total);
-        if (d == 0) put_lse(A, s, row, ref, total);
     }
+    const float at = ref == -INFINITY ? 0.f : ref;
+    for (int d0 = 0; d0 < width; d0 += 128) {
+        const int d = d0 + lane * 4;
+        for (int q = 0; q < rows; q += 4) {
+            float o[4][4] = {};
+            for (int c = 0; c < parts; c += JP) {
+                float4 x[JP][4];
+                float f[JP];
+#pragma unroll
+                for (int y = 0; y < JP; ++y)
+                    f[y] = c + y < parts ? __ldcg(A.part_ml + (slot(c + y) * R + mine) * 2) : -INFINITY;
+#pragma unroll
+                for (int y = 0; y < JP; ++y)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        x[y][z] = c + y < parts && q + z < rows && d < width
+                                      ? __ldcg(reinterpret_cast<const float4*>(A.part_o + (slot(c + y) * R + r0 + q + z) * width + d))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < JP; ++y) {
+                    const float fy = ex2_approx(f[y] - at);  // 0 for a part that is not there
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float w = __shfl_sync(0xffffffffu, fy, (q + z) & 31);
+                        o[z][0] = fmaf(w, x[y][z].x, o[z][0]);
+                        o[z][1] = fmaf(w, x[y][z].y, o[z][1]);
+                        o[z][2] = fmaf(w, x[y][z].z, o[z][2]);
+                        o[z][3] = fmaf(w, x[y][z].w, o[z][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const float tz = __shfl_sync(0xffffffffu, total, (q + z) & 31);
+                if (q + z < rows && d < width) put_row(A, s, s.rt * R + r0 + q + z, d, o[z], tz);
+            }
+        }
+    }
+    if (lane < rows) put_lse(A, s, s.rt * R + r0 + lane, ref, total);
 }
 // the workspace slot of this CTA's part: the second where the item starts in
 // its share (join_parts)

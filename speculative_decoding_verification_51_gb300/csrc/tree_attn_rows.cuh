@@ -49,7 +49,7 @@ struct RowsShape {
     static constexpr int STAGE = 2 * SIDE;
     static constexpr int OB = R * (DP + 8) * 4;  // one warp's sums, at the join
     static constexpr int FIXED = 4 * OB + R * (DP + 8) * 2 + (2 * WARPS + 4) * R * 4 + 4096;
-    static constexpr int ROOM = (232448 - 1024 - FIXED) / (WARPS * STAGE);
+    static constexpr int ROOM = (232448 - 1024 - int(sizeof(PlanWindow)) - FIXED) / (WARPS * STAGE);
     static constexpr int STAGES = ROOM < 6 ? ROOM : 6;
     static_assert(STAGES >= 2, "no room for a ring");
     static constexpr size_t SMEM = 1024 + size_t(WARPS) * STAGES * STAGE + FIXED;
@@ -109,8 +109,11 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     uint64_t* bar = bars + warp * S::STAGES;
     uint8_t* sc = sm_sc + warp * S::STAGES * 32;
 
-    const Share share = share_of(A);
-    if (share.begin >= share.end) return;  // the whole CTA
+    __shared__ PlanWindow window;
+    Share share;
+    if (!read_plan(A, window, share)) return;  // the whole CTA
+    const int first = window.b0;
+    const Lists L = {window, A.plan, first};
     if (lane == 0) {
         for (int i = 0; i < S::STAGES; ++i) mbar_init(&bar[i], 1);
         fence_mbarrier_init();
@@ -118,10 +121,8 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     if (threadIdx.x == 0) sm_flag[1] = 0;
     __syncwarp();
 
-    const int first = request_of(A, share.begin);
-
     // ---- this warp's copies: the next chunk to load, a page index ahead
-    Segment ps = segment_at(A, share, share.begin, first);
+    Segment ps = segment_at(A, L, share, share.begin, first);
     int pc = ps.c0 + warp, page_at = 0, off_at = 0;
     bool more = true;
     auto seek = [&]() {  // to the next chunk this warp has, if any
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                 more = false;
                 return;
             }
-            ps = segment_at(A, share, g, ps.b);
+            ps = segment_at(A, L, share, g, ps.b);
             pc = ps.c0 + warp;
         }
         const int t = pc * 16, p = t / A.page;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     bool dead = false;  // a copy did not arrive in time: no more waits, SPEC_BADBIT_TIMEOUT
     int b_at = first;
     for (long long g = share.begin; g < share.end;) {
-        const Segment s = segment_at(A, share, g, b_at);
+        const Segment s = segment_at(A, L, share, g, b_at);
         b_at = s.b;
         g += s.t1 - s.t0;
 
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                     *reinterpret_cast<float2*>(A.part_ml + (slot * R + r) * 2) = make_float2(sm_ref[r], sm_tot[r]);
             }
         }
-        if (!whole) join_parts(A, share, s, R, DP, sm_flag, threadIdx.x, AR_THREADS, [] { __syncthreads(); });
+        if (!whole) join_parts<2>(A, share, s, R, DP, sm_flag, threadIdx.x, AR_THREADS, 0);
         __syncthreads();
         if (threadIdx.x == 0) sm_flag[1] = 0;
     }

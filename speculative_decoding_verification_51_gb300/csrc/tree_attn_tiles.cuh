@@ -2,15 +2,16 @@
 // (up to 128 a tile), on the tcgen05 tensor cores.
 //
 // One CTA per SM, warps by role:
-//   warp 0        TMA: the K and V rows of a tile of 128 tokens, 16-token boxes
-//                 by the page table, 128-byte swizzle
+//   warp 0        TMA: the K and V rows of a tile of 128 tokens by the page table,
+//                 in boxes as long as a page allows (a copy costs the unit some
+//                 100 cycles whatever its size up to 2 KB), 128-byte swizzle
 //   warp 1        one thread issues the products: S = Q K^T (M = 128 rows, N = 128
 //                 tokens) into one of two TMEM buffers, O += P V with P in TMEM
 //                 and V as it lies (token rows: a transposed B operand)
 //   warps 4..7    softmax, one row a thread: S from TMEM, the weights back to it
 //                 as 16-bit P, the row's reference and total in registers; between
 //                 segments the next rows of Q, and the finished rows of O
-//   warps 8..11   (e4m3 cache) K and V from bytes to f16 in shared memory
+//   warps 8..15   (e4m3 cache) K (8..11) and V from bytes to f16 in shared memory
 // S of tile i + 1 is computed while the weights of tile i are made.
 //
 // As in k_attn_rows the reference of a row is raised only when a score passes
@@ -43,7 +44,7 @@ struct TilesShape {
     static constexpr int RAW = 16384, RAW_STAGES = E4 ? (DP == 64 ? 4 : 2) : 0;
     static constexpr size_t SMEM = 1024 + size_t(OPERAND) * (1 + 2 * STAGES) + size_t(RAW_STAGES) * 2 * RAW;
     static_assert(SMEM + 1024 <= 232448, "shared memory");
-    static constexpr int THREADS = E4 ? 384 : 256;
+    static constexpr int THREADS = E4 ? 512 : 256;
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -152,17 +153,21 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
     __shared__ __align__(16) uint8_t sm_sc[E4 ? NR * 256 : 16];
     // operands: full / empty; e4m3 bytes: full / empty
     __shared__ __align__(8) uint64_t kf[ST], ke[ST], vf[ST], ve[ST], rkf[NR], rke[NR], rvf[NR], rve[NR];
-    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
+    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], uk[4], qf, of, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, join_flag;
     __shared__ uint32_t bad_nodes[2];
-    // e4m3: the exponents E of the last tiles' K and V (a slot is written again
-    // only after the products of tile i + 2, so after softmax has read tile i's)
+    __shared__ PlanWindow window;
+    // e4m3: the exponents E of the last tiles' K (published by uk) and V (by vf); a
+    // slot is written again only when the products of tile i + 2 say that its
+    // stage is free, so after softmax is through with tile i
     __shared__ int unit_k[4], unit_v[4];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Share share = share_of(A);
-    if (share.begin >= share.end) return;  // the whole CTA
+    Share share;
+    if (!read_plan(A, window, share)) return;  // the whole CTA
+    const int first = window.b0;
+    const Lists L = {window, A.plan, first};
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&kf[i], E4 ? 4 : 1);
@@ -182,6 +187,7 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
         mbar_init(&pf[1], 4);
         mbar_init(&pv[0], 1);
         mbar_init(&pv[1], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&uk[i], 1);
         mbar_init(&qf, 4);
         mbar_init(&of, 4);
         mbar_init(&fin, 1);
@@ -195,7 +201,6 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const int first = request_of(A, share.begin);
     at_before();
     __syncthreads();
     at_after();
@@ -208,66 +213,72 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
         if (!mbar_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
     };
 
+    // e4m3: registers from the other warpgroups to softmax (200 + 3 * 104 = 4 * 128)
+    if constexpr (E4) {
+        if (warp >= 4 && warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    }
     if (warp == 0) {
-        // ---- copies: lane = (box, chunk of 16 tokens)
-        const int chunk = lane & 7, part = lane >> 3;
+        // ---- copies: lane = (128-byte part of the rows, box of A.box tokens)
+        const int chunk = lane & 7, part = lane >> 3, boxes = 128 / A.box;
+        const uint32_t box_bytes = uint32_t(A.box) * 128;
         uint32_t i = 0;  // tiles so far
         int b_at = first;
         for (long long g = share.begin; g < share.end;) {
-            const Segment s = segment_at(A, share, g, b_at);
+            const Segment s = segment_at(A, L, share, g, b_at);
             b_at = s.b;
             g += s.t1 - s.t0;
-            const int chunks = (s.ctx + s.n + 15) / 16;
+            const int len = s.ctx + s.n;
             const int32_t* table = A.table + (long long)s.b * A.max_pages;
             auto page_of = [&](int t, int& off) {
-                const int tok = (t * 8 + chunk) * 16;
-                if (t >= s.t1 || t * 8 + chunk >= chunks) return -1;
+                const int tok = t * 128 + chunk * A.box;
+                if (t >= s.t1 || chunk >= boxes || tok >= len) return -1;
                 const int p = tok / A.page;
                 off = tok - p * A.page;
                 return __ldg(table + p);
             };
             int off = 0, page = page_of(s.t0, off);
             for (int t = s.t0; t < s.t1; ++t, ++i) {
-                const int nv = min(8, max(0, chunks - t * 8));
+                const int nv = min(boxes, max(0, (len - t * 128 + A.box - 1) / A.box));
                 int off2 = 0;
                 const int page2 = page_of(t + 1, off2);
                 if constexpr (!E4) {
                     const uint32_t st = i % ST, ph = i / ST;
                     if (lane == 0) {
                         wait(&ke[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&kf[st], uint32_t(nv * S::HALVES * 2048));
+                        if (!*gone) mbar_arrive_expect_tx(&kf[st], nv * S::HALVES * box_bytes);
                     }
                     __syncwarp();
                     if (part < S::HALVES && page >= 0 && !*gone)
-                        tma_load_4d(sm_k + st * S::OPERAND + part * 16384 + chunk * 2048, &mk, part * 64, off, s.h, page, &kf[st]);
+                        tma_load_4d(sm_k + st * S::OPERAND + part * 16384 + chunk * box_bytes, &mk, part * 64, off, s.h, page, &kf[st]);
                     if (lane == 0) {
                         wait(&ve[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&vf[st], uint32_t(nv * S::HALVES * 2048));
+                        if (!*gone) mbar_arrive_expect_tx(&vf[st], nv * S::HALVES * box_bytes);
                     }
                     __syncwarp();
                     if (part < S::HALVES && page >= 0 && !*gone)
-                        tma_load_4d(sm_v + st * S::OPERAND + part * 16384 + chunk * 2048, &mv, part * 64, off, s.h, page, &vf[st]);
+                        tma_load_4d(sm_v + st * S::OPERAND + part * 16384 + chunk * box_bytes, &mv, part * 64, off, s.h, page, &vf[st]);
                 } else {
                     const uint32_t st = i % NR, ph = i / NR;
                     uint8_t* raw = sm_raw + st * 2 * S::RAW;
                     const long long sc = ((long long)page * A.Hkv + s.h) * A.page + off;
                     if (lane == 0) {
                         wait(&rke[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&rkf[st], uint32_t(nv * (2048 + 16)));
+                        if (!*gone) mbar_arrive_expect_tx(&rkf[st], nv * (box_bytes + A.box));
                     }
                     __syncwarp();
                     if (page >= 0 && !*gone) {
-                        if (part == 0) tma_load_4d(raw + chunk * 2048, &mk, 0, off, s.h, page, &rkf[st]);
-                        if (part == 1) bulk_g2s(sm_sc + st * 256 + chunk * 16, A.ks + sc, 16, &rkf[st]);
+                        if (part == 0) tma_load_4d(raw + chunk * box_bytes, &mk, 0, off, s.h, page, &rkf[st]);
+                        if (part == 1) bulk_g2s(sm_sc + st * 256 + chunk * A.box, A.ks + sc, A.box, &rkf[st]);
                     }
                     if (lane == 0) {
                         wait(&rve[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&rvf[st], uint32_t(nv * (2048 + 16)));
+                        if (!*gone) mbar_arrive_expect_tx(&rvf[st], nv * (box_bytes + A.box));
                     }
                     __syncwarp();
                     if (page >= 0 && !*gone) {
-                        if (part == 0) tma_load_4d(raw + S::RAW + chunk * 2048, &mv, 0, off, s.h, page, &rvf[st]);
-                        if (part == 1) bulk_g2s(sm_sc + st * 256 + 128 + chunk * 16, A.vs + sc, 16, &rvf[st]);
+                        if (part == 0) tma_load_4d(raw + S::RAW + chunk * box_bytes, &mv, 0, off, s.h, page, &rvf[st]);
+                        if (part == 1) bulk_g2s(sm_sc + st * 256 + 128 + chunk * A.box, A.vs + sc, A.box, &rvf[st]);
                     }
                 }
                 page = page2;
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 at_commit(&sf[j & 1]);
             };
             for (long long g = share.begin; g < share.end; ++seg) {
-                const Segment s = segment_at(A, share, g, b_at);
+                const Segment s = segment_at(A, L, share, g, b_at);
                 b_at = s.b;
                 g += s.t1 - s.t0;
                 wait(&qf, seg);
@@ -348,38 +359,34 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 const bool on = row < A.rows && v < s.n;
                 const uint16_t* src = static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
                                       (s.h * A.G + row - v * A.G) * A.qh;
-                float f[8], m = 0.f;
-                auto get = [&](int j) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (on && j * 8 < A.D) u = __ldg(reinterpret_cast<const uint4*>(src + j * 8));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint4 u[DP / 8];  // every load in flight at once
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j)
+                    u[j] = on && j * 8 < A.D ? __ldg(reinterpret_cast<const uint4*>(src + j * 8)) : make_uint4(0, 0, 0, 0);
+                auto pair = [&](uint32_t w) {
+                    return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w)) : make_float2(bf16_lo(w), bf16_hi(w));
+                };
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j) {
+                    const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (A.q_f16) {
-                            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-                            f[2 * e] = x.x;
-                            f[2 * e + 1] = x.y;
-                        } else {
-                            f[2 * e] = bf16_lo(w[e]);
-                            f[2 * e + 1] = bf16_hi(w[e]);
-                        }
+                        const float2 x = pair(w[e]);
+                        m = fmaxf(m, fmaxf(finite_abs(x.x), finite_abs(x.y)));
                     }
-                };
-#pragma unroll 4
-                for (int j = 0; j < DP / 8; ++j) {
-                    get(j);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[e]));
                 }
                 const uint32_t ex = max(min(__float_as_uint(m) >> 23, 253u), 1u);
                 const float f2 = __uint_as_float((254u - ex) << 23);
                 rc = c * exp2_int(int(ex) - 127);
-#pragma unroll 4
-                for (int j = 0; j < DP / 8; ++j) {
-                    get(j);
-                    uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = pack16<true>(f[2 * e] * f2, f[2 * e + 1] * f2) ^ flip;
+                for (int j = 0; j < DP / 8; ++j) {
+                    uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = pair(w[e]);
+                        w[e] = pack16<true>(x.x * f2, x.y * f2) ^ flip;
+                    }
                     *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -388,24 +395,27 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 if (lane == 0) at_arrive(&qf);
                 return;
             }
-            for (int x = tid; x < 128 * (DP / 8); x += 128) {
-                const int rr = x / (DP / 8), j = x - rr * (DP / 8), row = s.rt * 128 + rr, v = row / A.G;
-                uint4 u = make_uint4(0, 0, 0, 0);
+            uint4 u[DP / 8];  // every load in flight at once
+#pragma unroll
+            for (int k = 0; k < DP / 8; ++k) {
+                const int x = tid + k * 128, rr = x / (DP / 8), j = x - rr * (DP / 8), row = s.rt * 128 + rr, v = row / A.G;
+                u[k] = make_uint4(0, 0, 0, 0);
                 if (row < A.rows && j * 8 < A.D && v < s.n)
-                    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
-                                                        (s.h * A.G + row - v * A.G) * A.qh + j * 8);
-                u.x ^= flip;
-                u.y ^= flip;
-                u.z ^= flip;
-                u.w ^= flip;
-                *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + rr * 128 + (((j & 7) ^ (rr & 7)) << 4)) = u;
+                    u[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                                                                (s.h * A.G + row - v * A.G) * A.qh + j * 8));
+            }
+#pragma unroll
+            for (int k = 0; k < DP / 8; ++k) {
+                const int x = tid + k * 128, rr = x / (DP / 8), j = x - rr * (DP / 8);
+                *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + rr * 128 + (((j & 7) ^ (rr & 7)) << 4)) =
+                    make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) at_arrive(&qf);
         };
         uint32_t i = 0, seg = 0;
-        Segment s = segment_at(A, share, share.begin, first);
+        Segment s = segment_at(A, L, share, share.begin, first);
         load_q(s);
         for (;; ++seg) {
             const int row = s.rt * 128 + r, node = row / A.G;
@@ -446,81 +456,79 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                     }
                     at_st_wait();
                 }
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int j = 0; j < 128; j += 64) {
-                    uint32_t f[32], g[32];
-                    at_ld32(sa + j, f);
-                    at_ld32(sa + j + 32, g);
-                    at_ld_wait(f);
-                    at_ld_wait(g);
-                    float m2 = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        mx = fmaxf(fmaxf(__uint_as_float(f[e]), __uint_as_float(f[e + 1])), mx);
-                        m2 = fmaxf(fmaxf(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), m2);
-                    }
-                    mx = fmaxf(mx, m2);
-                }
                 // the tile's factor on scores, and the unit of its values
                 float ct = fmaxf(c, LEAST), unit = 0.f;
                 if constexpr (E4) {
+                    wait(&uk[i & 3], i >> 2);
                     wait(&vf[i % ST], i / ST);
                     ct = fmaxf(rc * exp2_int(unit_k[i & 3]), LEAST);
                     unit = float(unit_v[i & 3]);
                 }
-                const float top = mx == -INFINITY ? mx : fmaf(mx, ct, unit);
-                const bool raise = top > ref + AT_SLACK;
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float to = raise ? top : ref;
-                    const float f = ref == to ? 1.f : ex2_approx(ref - to);
-                    ref = to;
-                    tot *= f;
-                    if (t > s.t0) {  // O holds sums by the old reference
-                        wait(&pv[(i - 1) & 1], (i - 1) >> 1);
-                        at_after();
-#pragma unroll 1
-                        for (int j = 0; j < DP; j += 32) {
-                            uint32_t o[32], u[16], v[16];
-                            at_ld32(tbase + lanes + T_O + j, o);
-                            at_ld_wait(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                u[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                v[e] = __float_as_uint(__uint_as_float(o[e + 16]) * f);
-                            }
-                            at_st16(tbase + lanes + T_O + j, u);
-                            at_st16(tbase + lanes + T_O + j + 16, v);
-                        }
-                    }
-                }
-                const float at = (ref == -INFINITY ? 0.f : -ref) + unit;
-                uint64_t sum = f2_pack(0.f, 0.f);
-                const uint64_t c2 = f2_pack(ct, ct), at2 = f2_pack(at, at);
-#pragma unroll 1
-                for (int j = 0; j < 128; j += 64) {
-                    uint32_t f[2][32];
-                    at_ld32(sa + j, f[0]);
-                    at_ld32(sa + j + 32, f[1]);
-                    at_ld_wait(f[0]);
-                    at_ld_wait(f[1]);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                // One pass makes the weights by the reference as it is and finds the
+                // largest score; where some row's passes the reference by too
+                // much (seldom, but for a segment's first tile), the reference is
+                // raised and the weights are made again.
+                float s0, s1;
+                for (;;) {
+                    const float at = (ref == -INFINITY ? 0.f : -ref) + unit;
+                    const uint64_t c2 = f2_pack(ct, ct), at2 = f2_pack(at, at);
+                    uint64_t sum = f2_pack(0.f, 0.f);
+                    float mx = -INFINITY;
+                    auto piece = [&](const uint32_t (&f)[32], int j) {
                         uint32_t p[16];
+                        float m2 = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
+                            const float x = __uint_as_float(f[2 * e]), y = __uint_as_float(f[2 * e + 1]);
                             float a, b;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(f[x][2 * e]), __uint_as_float(f[x][2 * e + 1])), c2, at2), a, b);
+                            m2 = fmaxf(fmaxf(x, y), m2);
+                            f2_unpack(f2_fma(f2_pack(x, y), c2, at2), a, b);
                             a = ex2_approx(a);
                             b = ex2_approx(b);
                             sum = f2_add(sum, f2_pack(a, b));
                             p[e] = pack16<F16>(a, b);
                         }
-                        at_st16(pa + j / 2 + x * 16, p);
+                        mx = fmaxf(mx, m2);
+                        at_st16(pa + j / 2, p);
+                    };
+                    uint32_t f[32], g[32];
+                    at_ld32(sa, f);
+#pragma unroll 1
+                    for (int j = 0; j < 128; j += 64) {
+                        at_ld_wait(f);
+                        at_ld32(sa + j + 32, g);
+                        piece(f, j);
+                        at_ld_wait(g);
+                        if (j == 0) at_ld32(sa + 64, f);
+                        piece(g, j + 32);
                     }
+                    f2_unpack(sum, s0, s1);
+                    const float top = mx == -INFINITY ? mx : fmaf(mx, ct, unit);
+                    const bool raise = top > ref + AT_SLACK;
+                    if (!__any_sync(0xffffffffu, raise)) break;
+                    const float to = raise ? top : ref;
+                    const float f2 = ref == to ? 1.f : ex2_approx(ref - to);
+                    ref = to;
+                    tot *= f2;
+                    if (t > s.t0) {  // O holds sums by the old reference
+                        wait(&pv[(i - 1) & 1], (i - 1) >> 1);
+                        at_after();
+#pragma unroll 1
+                        for (int j = 0; j < DP; j += 32) {
+                            uint32_t u[16], v[16];
+                            at_ld32(tbase + lanes + T_O + j, f);
+                            at_ld_wait(f);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                u[e] = __float_as_uint(__uint_as_float(f[e]) * f2);
+                                v[e] = __float_as_uint(__uint_as_float(f[e + 16]) * f2);
+                            }
+                            at_st16(tbase + lanes + T_O + j, u);
+                            at_st16(tbase + lanes + T_O + j + 16, v);
+                        }
+                    }
+                    at_st_wait();
                 }
-                float s0, s1;
-                f2_unpack(sum, s0, s1);
                 if constexpr (E4) tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 3]), tot);
                 else tot += s0 + s1;
                 if (tail) {
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
             // four warps have arrived at qf: nobody reads or marks it now
             if (tid == 0) bad_nodes[(seg & 1) ^ 1] = 0;
             if (more) {
-                s = segment_at(A, share, next, s.b);
+                s = segment_at(A, L, share, next, s.b);
                 load_q(s);
             }
             // (the last scores say that all products but the last two are done,
@@ -623,13 +631,20 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 put_lse(A, done, row, ref, tot);
             } else {
                 if (row < A.rows) *reinterpret_cast<float2*>(A.part_ml + (slot * 128 + r) * 2) = make_float2(ref, tot);
-                join_parts(A, share, done, 128, DP, &join_flag, tid, 128, sync);
+                join_parts<E4 ? 2 : 4>(A, share, done, 128, DP, &join_flag, tid, 128, 1);
             }
             if (!more) break;
         }
     } else if (E4 && warp >= 8) {
-        // ---- bytes to f16: 8 lanes a token, 8 tokens a thread
-        const int tid = threadIdx.x - 256, x = tid & 7;
+        // ---- bytes to f16, four warps for K and four for V: 4 lanes a token, two
+        // 16-byte chunks (16 channels each) a lane, 4 tokens a thread.  Eight
+        // lanes take tokens 4 apart, whose swizzles differ in their top bit.
+        const int side = warp >= 12, tid = threadIdx.x & 127, x = lane & 3;
+        const int tok0 = (tid >> 5) * 8 + (lane >> 2 & 1) * 4 + (lane >> 3), odd = lane >> 2 & 1;
+        uint64_t* const raw_full = side ? rvf : rkf;
+        uint64_t* const raw_empty = side ? rve : rke;
+        uint64_t* const full = side ? vf : kf;
+        uint64_t* const empty = side ? ve : ke;
         // largest scale byte of the tile's first `valid` tokens (all lanes)
         auto largest = [&](const uint8_t* sc, int valid) {
             uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
@@ -641,59 +656,56 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
         uint32_t i = 0;
         int b_at = first;
         for (long long g = share.begin; g < share.end;) {
-            const Segment s = segment_at(A, share, g, b_at);
+            const Segment s = segment_at(A, L, share, g, b_at);
             b_at = s.b;
             g += s.t1 - s.t0;
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int valid = s.ctx + s.n - t * 128;
                 const uint32_t rs = i % NR, st = i % ST;
+                const uint8_t* raw = sm_raw + (rs * 2 + side) * S::RAW;
+                const uint8_t* sc = sm_sc + rs * 256 + side * 128;
+                uint8_t* out = (side ? sm_v : sm_k) + st * S::OPERAND;
+                wait(&raw_full[rs], i / NR);
+                int unit = largest(sc, valid);
+                if (side) unit = max(unit, -100);
+                wait(&empty[st], (i / ST) ^ 1u);
+                if (tid == 0) {
+                    (side ? unit_v : unit_k)[i & 3] = unit;
+                    if (!side) at_arrive(&uk[i & 3]);
+                }
 #pragma unroll 1
-                for (int side = 0; side < 2; ++side) {  // K, then V
-                    const uint8_t* raw = sm_raw + (rs * 2 + side) * S::RAW;
-                    const uint8_t* sc = sm_sc + rs * 256 + side * 128;
-                    uint8_t* out = (side ? sm_v : sm_k) + st * S::OPERAND + (x >> 2) * 16384;
-                    wait(side ? &rvf[rs] : &rkf[rs], i / NR);
-                    int unit = largest(sc, valid);
-                    wait(side ? &ve[st] : &ke[st], (i / ST) ^ 1u);
-                    if (side) unit = max(unit, -100);
-                    if (tid == 0) (side ? unit_v : unit_k)[i & 3] = unit;
-                    if (x * 16 < DP) {
-#pragma unroll 1
-                        for (int k0 = tid >> 3; k0 < 128; k0 += 64) {
-                            uint4 w[4];
-                            uint32_t f[4];
+                for (int c0 = 0; c0 < DP / 64; ++c0) {  // chunks x, then x + 4: channels from 64 on
+                    uint4 w[4];
+                    uint32_t f[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int tk = k0 + k * 16;
-                                w[k] = *reinterpret_cast<const uint4*>(raw + tk * 128 + ((x ^ (tk & 7)) << 4));
-                                f[k] = half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
-                            }
+                    for (int k = 0; k < 4; ++k) {
+                        const int tk = tok0 + k * 32;
+                        w[k] = *reinterpret_cast<const uint4*>(raw + tk * 128 + (((x + c0 * 4) ^ (tk & 7)) << 4));
+                        f[k] = half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
+                    }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int tk = k0 + k * 16;
-                                const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                                uint32_t h[8];
+                    for (int k = 0; k < 4; ++k) {
+                        const int tk = tok0 + k * 32;
+                        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                        uint32_t h[8];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    h[2 * e] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e])), f[k]);
-                                    h[2 * e + 1] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e] >> 16)), f[k]);
-                                }
-                                uint8_t* o = out + tk * 128;
-                                const int j = 2 * (x & 3), swap = x >> 2;
-                                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                                // the lanes of the two channel halves write odd and even
-                                // chunks in turn, so that a token's 8 lanes touch all banks
-                                *reinterpret_cast<uint4*>(o + (((j + swap) ^ (tk & 7)) << 4)) = swap ? hi : lo;
-                                *reinterpret_cast<uint4*>(o + (((j + 1 - swap) ^ (tk & 7)) << 4)) = swap ? lo : hi;
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            h[2 * e] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e])), f[k]);
+                            h[2 * e + 1] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e] >> 16)), f[k]);
                         }
+                        uint8_t* o = out + c0 * 16384 + tk * 128;
+                        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                        // of the two tokens of 8 lanes one writes its even chunks
+                        // first and one its odd ones: all banks at once
+                        *reinterpret_cast<uint4*>(o + (((2 * x + odd) ^ (tk & 7)) << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(o + (((2 * x + 1 - odd) ^ (tk & 7)) << 4)) = odd ? lo : hi;
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        at_arrive(side ? &vf[st] : &kf[st]);
-                        at_arrive(side ? &rve[rs] : &rke[rs]);
-                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    at_arrive(&full[st]);
+                    at_arrive(&raw_empty[rs]);
                 }
             }
         }
