@@ -34,7 +34,7 @@ struct AttnArgs {
     int box;            // tokens of one copy (k_attn_tiles)
     float c;            // scale * log2(e): scores are exponents of two
     int q_f16;          // q and out are f16 (else bf16)
-    float* part_o;      // [2 * CTAs][R][width] unnormalised sums
+    float* part_o;      // [2 * CTAs][width / 4][R][4] unnormalised sums
     float* part_ml;     // [2 * CTAs][R][2] reference and total
     int32_t* status;
 };
@@ -213,9 +213,9 @@ __device__ __forceinline__ void put_lse(const AttnArgs& A, const Segment& s, int
 
 // After this CTA's part of an item lies in the workspace: the CTA that
 // arrives last joins the parts (R rows of `width` channels each).
-// JP: parts read at a time.  `threads` threads call it together (tid their index, `bar` their barrier) and
+// `threads` threads call it together (tid their index, `bar` their barrier) and
 // `flag` is a shared word of theirs.
-template <int JP>
+template <int U>
 __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, const Segment& s,
                                            int R, int width, int* flag, int tid, int threads,
                                            int bar) {
@@ -232,69 +232,58 @@ __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, c
     sync();
     if (!*flag) return;
     __threadfence();
-    // A warp takes 32 rows at most.  Each lane knows one row's references and
-    // totals; then the rows' sums are read four rows and JP parts at a
-    // time (4 JP loads a lane in flight), a lane 4 channels of each.
-    const int lane = tid & 31, parts = c1 - c0 + 1, warps = threads >> 5;
-    const int per = (R + warps - 1) / warps;  // rows of a warp
-    const int r0 = (tid >> 5) * per;
-    const int rows = min(min(per, R - r0), A.rows - s.rt * R - r0);
+    // A thread keeps one row (R divides the number of threads) and takes U groups
+    // of 4 channels at a time, up to 4 parts of each in flight; the lanes' rows lie
+    // side by side, so that every read is coalesced.
+    const int r = tid % R, row = s.rt * R + r, parts = c1 - c0 + 1, step = threads / R;
     auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
-    const int mine = r0 + min(lane, max(rows - 1, 0));
+    const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + r;
     float ref = -INFINITY, total = 0.f;
-    if (rows > 0) {
-        const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + mine;
-        for (int c = 0; c < parts; c += 4) {  // the running form of the total
-            float2 x[4];
+    for (int c = 0; c < parts; c += 4) {  // the running form of the total
+        float2 x[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) x[y] = c + y < parts ? __ldcg(ml + slot(c + y) * R) : make_float2(-INFINITY, 0.f);
-            const float to = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), ref);
-            const float at = to == -INFINITY ? 0.f : to;
-            total *= ex2_approx(ref - at);
-            ref = to;
+        for (int y = 0; y < 4; ++y) x[y] = c + y < parts ? __ldcg(ml + slot(c + y) * R) : make_float2(-INFINITY, 0.f);
+        const float to = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), ref);
+        const float at = to == -INFINITY ? 0.f : to;
+        total *= ex2_approx(ref - at);
+        ref = to;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) total = fmaf(ex2_approx(x[y].x - at), x[y].y, total);
-        }
+        for (int y = 0; y < 4; ++y) total = fmaf(ex2_approx(x[y].x - at), x[y].y, total);
     }
     const float at = ref == -INFINITY ? 0.f : ref;
-    for (int d0 = 0; d0 < width; d0 += 128) {
-        const int d = d0 + lane * 4;
-        for (int q = 0; q < rows; q += 4) {
-            float o[4][4] = {};
-            for (int c = 0; c < parts; c += JP) {
-                float4 x[JP][4];
-                float f[JP];
+    const int quads = width / 4;
+    for (int q = tid / R; q < quads; q += U * step) {
+        float o[U][4] = {};
+        for (int c = 0; c < parts; c += 4) {
+            float4 x[4][U];
+            float f[4];
 #pragma unroll
-                for (int y = 0; y < JP; ++y)
-                    f[y] = c + y < parts ? __ldcg(A.part_ml + (slot(c + y) * R + mine) * 2) : -INFINITY;
+            for (int y = 0; y < 4; ++y)
+                f[y] = c + y < parts ? __ldcg(reinterpret_cast<const float*>(ml + slot(c + y) * R)) : -INFINITY;
 #pragma unroll
-                for (int y = 0; y < JP; ++y)
+            for (int y = 0; y < 4; ++y)
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        x[y][z] = c + y < parts && q + z < rows && d < width
-                                      ? __ldcg(reinterpret_cast<const float4*>(A.part_o + (slot(c + y) * R + r0 + q + z) * width + d))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int z = 0; z < U; ++z)
+                    x[y][z] = c + y < parts && q + z * step < quads
+                                  ? __ldcg(reinterpret_cast<const float4*>(A.part_o) + (slot(c + y) * quads + q + z * step) * R + r)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int y = 0; y < JP; ++y) {
-                    const float fy = ex2_approx(f[y] - at);  // 0 for a part that is not there
+            for (int y = 0; y < 4; ++y) {
+                const float w = ex2_approx(f[y] - at);  // 0 for a part that is not there
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float w = __shfl_sync(0xffffffffu, fy, (q + z) & 31);
-                        o[z][0] = fmaf(w, x[y][z].x, o[z][0]);
-                        o[z][1] = fmaf(w, x[y][z].y, o[z][1]);
-                        o[z][2] = fmaf(w, x[y][z].z, o[z][2]);
-                        o[z][3] = fmaf(w, x[y][z].w, o[z][3]);
-                    }
+                for (int z = 0; z < U; ++z) {
+                    o[z][0] = fmaf(w, x[y][z].x, o[z][0]);
+                    o[z][1] = fmaf(w, x[y][z].y, o[z][1]);
+                    o[z][2] = fmaf(w, x[y][z].z, o[z][2]);
+                    o[z][3] = fmaf(w, x[y][z].w, o[z][3]);
                 }
             }
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const float tz = __shfl_sync(0xffffffffu, total, (q + z) & 31);
-                if (q + z < rows && d < width) put_row(A, s, s.rt * R + r0 + q + z, d, o[z], tz);
-            }
         }
+#pragma unroll
+        for (int z = 0; z < U; ++z)
+            if (q + z * step < quads) put_row(A, s, row, (q + z * step) * 4, o[z], total);
     }
-    if (lane < rows) put_lse(A, s, s.rt * R + r0 + lane, ref, total);
+    if (tid < R) put_lse(A, s, row, ref, total);
 }
 // the workspace slot of this CTA's part: the second where the item starts in
 // its share (join_parts)

@@ -559,8 +559,11 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
         const uint32_t bad_nodes = uint32_t(sm_flag[1]);
         const long long slot = part_slot(share, s);
         for (int i = threadIdx.x; i < R * (DP / 4); i += AR_THREADS) {
-            const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4, row = s.rt * R + r;
-            if (row >= A.rows) break;
+            // a whole item: channels side by side, as in the output; a part: rows
+            // side by side, as in the workspace
+            const int r = whole ? i / (DP / 4) : i % R, d = (whole ? i - r * (DP / 4) : i / R) * 4;
+            const int row = s.rt * R + r;
+            if (row >= A.rows) continue;
             float4 x = *reinterpret_cast<const float4*>(sm_o + r * OP + d);
 #pragma unroll
             for (int w = 1; w < 4; ++w) {
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                 put_row(A, s, row, d, v, sm_tot[r]);
                 if (d == 0) put_lse(A, s, row, sm_ref[r], sm_tot[r]);
             } else {
-                *reinterpret_cast<float4*>(A.part_o + (slot * R + r) * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(A.part_o)[(slot * (DP / 4) + d / 4) * R + r] = make_float4(v[0], v[1], v[2], v[3]);
                 if (d == 0)
                     *reinterpret_cast<float2*>(A.part_ml + (slot * R + r) * 2) = make_float2(sm_ref[r], sm_tot[r]);
             }

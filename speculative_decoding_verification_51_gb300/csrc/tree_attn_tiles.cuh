@@ -1,31 +1,25 @@
 // tree_attn_tiles.cuh -- k_attn_tiles: the attention for many rows a key head
-// (up to 128 a tile), on the tcgen05 tensor cores.
+// (up to 128 a tile) over a 16-bit cache, on the tcgen05 tensor cores.
 //
 // One CTA per SM, warps by role:
 //   warp 0        TMA: the K and V rows of a tile of 128 tokens by the page table,
-//                 in boxes as long as a page allows (a copy costs the unit some
-//                 100 cycles whatever its size up to 2 KB), 128-byte swizzle
+//                 in boxes as long as a page allows, 128-byte swizzle
 //   warp 1        one thread issues the products: S = Q K^T (M = 128 rows, N = 128
 //                 tokens) into one of two TMEM buffers, O += P V with P in TMEM
 //                 and V as it lies (token rows: a transposed B operand)
 //   warps 4..7    softmax, one row a thread: S from TMEM, the weights back to it
-//                 as 16-bit P, the row's reference and total in registers; between
-//                 segments the next rows of Q, and the finished rows of O
-//   warps 8..15   (e4m3 cache) K (8..11) and V from bytes to f16 in shared memory
+//                 as 16-bit P, the row's reference and total in registers;
+//                 between segments the next rows of Q, and the finished rows of O
 // S of tile i + 1 is computed while the weights of tile i are made.
 //
 // As in k_attn_rows the reference of a row is raised only when a score passes
 // it by 2^8, so that O in TMEM is seldom rescaled; a weight is then at most
 // 2^8, which bf16 and f16 hold and whose rounding is relative.
 //
-// e4m3: a value v 2^e is stored as f16 v 2^(e - E), E the largest exponent of
-// the tile's rows (one for K, one for V): exact for rows within 2^15 of the
-// tile's largest, and off by 2^-33 of the largest below.  2^E is then one factor
-// for the whole tile: for K it joins the scale of the scores, for V the
-// exponents of the weights, w_t = 2^(s_t + E - m), so that the tiles' sums are in
-// one unit; the total takes 2^-E times the tile's weights.  E is taken as
-// -100 or more, so that a tile of zeros does not push the total out of float32.
-// Queries become f16 by a power of two a row that brings the largest to [1, 2).
+// The loops over a tile's columns are rolled where they can be: the roles' code
+// together has to stay in the SM's instruction cache.  (Unrolled, the stall
+// for instructions was the largest of all, and a tile of an 8-bit cache took
+// three times as long.)
 #pragma once
 
 #include "tree_attn.cuh"
@@ -35,16 +29,35 @@ namespace sv {
 constexpr float AT_SLACK = 8.f;
 constexpr uint64_t AT_WAIT_NS = 200000000ull;
 
-template <int KIND, int DP>
+// As mbar_wait_bounded, for warps that wait long: the hint lets the hardware suspend
+// the thread for up to 20 us a try, where bare tries take issue slots from
+// the SM's other warps.
+__device__ __forceinline__ bool at_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t t = globaltimer_ns();
+        if (!t0) t0 = t;
+        else if (t - t0 > limit_ns) return false;
+    }
+}
+
+template <int DP>
 struct TilesShape {
-    static constexpr bool E4 = KIND == SPEC_E4M3;
-    static constexpr int R = 128, HALVES = DP / 64;
+    static constexpr int HALVES = DP / 64;
     static constexpr int OPERAND = HALVES * 16384;  // 128 tokens (or rows) of 16-bit channels
-    static constexpr int STAGES = E4 ? 2 : DP == 64 ? 5 : 3;
-    static constexpr int RAW = 16384, RAW_STAGES = E4 ? (DP == 64 ? 4 : 2) : 0;
-    static constexpr size_t SMEM = 1024 + size_t(OPERAND) * (1 + 2 * STAGES) + size_t(RAW_STAGES) * 2 * RAW;
+    static constexpr int STAGES = DP == 64 ? 6 : 3;
+    static constexpr size_t SMEM = 1024 + size_t(OPERAND) * (1 + 2 * STAGES);
     static_assert(SMEM + 1024 <= 232448, "shared memory");
-    static constexpr int THREADS = E4 ? 512 : 256;
+    static constexpr int THREADS = 256;
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -125,43 +138,151 @@ __device__ __forceinline__ void at_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 2^d as two halves (d <= 0; 0 below f16's least subnormal)
-__device__ __forceinline__ uint32_t half2_exp2(int d) {
-    const uint32_t h = d >= -14 ? uint32_t(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
-    return h * 0x10001u;
+// S in place: what the row does not see becomes -inf.  u0: node index of the
+// tile's first token (negative: within the context).
+__device__ __forceinline__ void hide_unseen(uint32_t sa, int u0, uint32_t mask) {
+#pragma unroll 1
+    for (int j = 0; j < 128; j += 32) {
+        const int u = u0 + j;
+        const uint32_t on = u <= -32 ? 0xffffffffu
+                            : u < 0  ? (0xffffffffu >> (32 + u)) | (mask << -u)
+                            : u < 32 ? mask >> u
+                                     : 0u;
+        uint32_t f[32], x[16], y[16];
+        at_ld32(sa + j, f);
+        at_ld_wait(f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            x[e] = on >> e & 1u ? f[e] : 0xff800000u;
+            y[e] = on >> (e + 16) & 1u ? f[e + 16] : 0xff800000u;
+        }
+        at_st16(sa + j, x);
+        at_st16(sa + j + 16, y);
+    }
+    at_st_wait();
 }
-__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+
+// A row's sums times f (the products that add to them are done).
+template <int DP>
+__device__ __forceinline__ void scale_rows(uint32_t o, float f) {
+    at_after();
+#pragma unroll 1
+    for (int j = 0; j < DP; j += 32) {
+        uint32_t u[32], x[16], y[16];
+        at_ld32(o + j, u);
+        at_ld_wait(u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            x[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+            y[e] = __float_as_uint(__uint_as_float(u[e + 16]) * f);
+        }
+        at_st16(o + j, x);
+        at_st16(o + j + 16, y);
+    }
+    at_st_wait();
+}
+
+// In a tile of values (128 threads): rows past the request's end become zero,
+// and so do elements of nodes that are not finite, since neither must meet a
+// weight of zero.  Returns the nodes that had such elements.
+template <bool F16, int DP>
+__device__ __forceinline__ uint32_t clean_values(uint8_t* tile, int t0, const Segment& s, int tid) {
+    uint32_t bad = 0;
+    for (int x = tid; x < DP * 16; x += 128) {
+        const int tok = t0 + ((x >> 3) & 127);
+        if (tok < s.ctx) continue;
+        uint4* p = reinterpret_cast<uint4*>(tile) + x;
+        if (tok >= s.ctx + s.n) {
+            *p = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        uint32_t u[4] = {p->x, p->y, p->z, p->w};
+        bool hit = false;
+        constexpr uint32_t EX = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                if ((u[e] >> (16 * y) & EX) == EX) {
+                    u[e] &= ~(0xffffu << (16 * y));
+                    hit = true;
+                }
+        if (hit) {
+            *p = make_uint4(u[0], u[1], u[2], u[3]);
+            bad |= 1u << (tok - s.ctx);
+        }
+    }
+    return bad;
+}
+
+// A thread's finished row (r of the tile; its sums in TMEM at o): to the output
+// where the segment is the whole item, else to the workspace.  `bad`: the
+// nodes it sees that have values which are not finite.
+template <int KIND, int DP>
+__device__ __forceinline__ void put_tile(const AttnArgs& A, const Share& share, const Segment& s, uint32_t o,
+                                         int r, int node, uint32_t bad, float ref, float tot) {
+    const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+    const long long slot = part_slot(share, s);
+    const int row = s.rt * 128 + r;
+    const float inv = node < s.n && tot != 0.f ? 1.f / tot : 0.f;
+    const bool none = inv == 0.f && tot == tot;
+    const long long at = (((long long)s.b * A.N + node) * A.Hq + s.h * A.G + row - node * A.G) * A.D;
+#pragma unroll 1
+    for (int j = 0; j < DP; j += 32) {
+        uint32_t u0[32];
+        at_ld32(o + j, u0);
+        at_ld_wait(u0);
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(u0[e]);
+        if (row < A.rows) {
+            for (uint32_t m = bad; m; m &= m - 1)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (j + e < A.D) f[e] += not_finite_v<KIND>(A, s.b, s.h, s.ctx + __ffs(m) - 1, j + e);
+            if (whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float lo = none ? 0.f : f[e + 2 * x] * inv, hi = none ? 0.f : f[e + 2 * x + 1] * inv;
+                        u[x] = A.q_f16 ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
+                    }
+                    if (j + e < A.D)
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at + j + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    reinterpret_cast<float4*>(A.part_o)[(slot * (DP / 4) + (j + e) / 4) * 128 + r] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
+        }
+        __syncwarp();
+    }
+    if (whole) put_lse(A, s, row, ref, tot);
+    else if (row < A.rows) *reinterpret_cast<float2*>(A.part_ml + (slot * 128 + r) * 2) = make_float2(ref, tot);
 }
 
 template <int KIND, int DP>
-__global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
+__global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
     k_attn_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ AttnArgs A) {
-    using S = TilesShape<KIND, DP>;
-    constexpr bool E4 = S::E4, F16 = KIND != SPEC_BF16;
-    constexpr int ST = S::STAGES, NR = E4 ? S::RAW_STAGES : 1;
+    using S = TilesShape<DP>;
+    constexpr bool F16 = KIND == SPEC_F16;
+    constexpr int ST = S::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     uint8_t* sm_q = smem;
     uint8_t* sm_k = sm_q + S::OPERAND;
     uint8_t* sm_v = sm_k + ST * S::OPERAND;
-    uint8_t* sm_raw = sm_v + ST * S::OPERAND;  // [raw stages][K, V][128 tokens][128]
-    __shared__ __align__(16) uint8_t sm_sc[E4 ? NR * 256 : 16];
-    // operands: full / empty; e4m3 bytes: full / empty
-    __shared__ __align__(8) uint64_t kf[ST], ke[ST], vf[ST], ve[ST], rkf[NR], rke[NR], rvf[NR], rve[NR];
-    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], uk[4], qf, of, fin;
+    __shared__ __align__(8) uint64_t kf[ST], ke[ST], vf[ST], ve[ST];  // stages full and empty
+    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, join_flag;
     __shared__ uint32_t bad_nodes[2];
     __shared__ PlanWindow window;
-    // e4m3: the exponents E of the last tiles' K (published by uk) and V (by vf); a
-    // slot is written again only when the products of tile i + 2 say that its
-    // stage is free, so after softmax is through with tile i
-    __shared__ int unit_k[4], unit_v[4];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Share share;
@@ -170,16 +291,10 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
     const Lists L = {window, A.plan, first};
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&kf[i], E4 ? 4 : 1);
+            mbar_init(&kf[i], 1);
             mbar_init(&ke[i], 1);
-            mbar_init(&vf[i], E4 ? 4 : 1);
+            mbar_init(&vf[i], 1);
             mbar_init(&ve[i], 1);
-        }
-        for (int i = 0; i < NR; ++i) {
-            mbar_init(&rkf[i], 1);
-            mbar_init(&rke[i], 4);
-            mbar_init(&rvf[i], 1);
-            mbar_init(&rve[i], 4);
         }
         mbar_init(&sf[0], 1);
         mbar_init(&sf[1], 1);
@@ -187,7 +302,6 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
         mbar_init(&pf[1], 4);
         mbar_init(&pv[0], 1);
         mbar_init(&pv[1], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&uk[i], 1);
         mbar_init(&qf, 4);
         mbar_init(&of, 4);
         mbar_init(&fin, 1);
@@ -209,15 +323,10 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
     volatile int* gone = &abort_flag;
     // a bounded wait; once one has run out nobody waits any more
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (*gone) return;
-        if (!mbar_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
+        if (mbar_try_wait(bar, parity & 1u) || *gone) return;
+        if (!at_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
     };
 
-    // e4m3: registers from the other warpgroups to softmax (200 + 3 * 104 = 4 * 128)
-    if constexpr (E4) {
-        if (warp >= 4 && warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    }
     if (warp == 0) {
         // ---- copies: lane = (128-byte part of the rows, box of A.box tokens)
         const int chunk = lane & 7, part = lane >> 3, boxes = 128 / A.box;
@@ -242,44 +351,18 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 const int nv = min(boxes, max(0, (len - t * 128 + A.box - 1) / A.box));
                 int off2 = 0;
                 const int page2 = page_of(t + 1, off2);
-                if constexpr (!E4) {
-                    const uint32_t st = i % ST, ph = i / ST;
+                const uint32_t st = i % ST, ph = i / ST;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    uint64_t* full = side ? &vf[st] : &kf[st];
                     if (lane == 0) {
-                        wait(&ke[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&kf[st], nv * S::HALVES * box_bytes);
+                        wait(side ? &ve[st] : &ke[st], ph ^ 1u);
+                        if (!*gone) mbar_arrive_expect_tx(full, nv * S::HALVES * box_bytes);
                     }
                     __syncwarp();
                     if (part < S::HALVES && page >= 0 && !*gone)
-                        tma_load_4d(sm_k + st * S::OPERAND + part * 16384 + chunk * box_bytes, &mk, part * 64, off, s.h, page, &kf[st]);
-                    if (lane == 0) {
-                        wait(&ve[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&vf[st], nv * S::HALVES * box_bytes);
-                    }
-                    __syncwarp();
-                    if (part < S::HALVES && page >= 0 && !*gone)
-                        tma_load_4d(sm_v + st * S::OPERAND + part * 16384 + chunk * box_bytes, &mv, part * 64, off, s.h, page, &vf[st]);
-                } else {
-                    const uint32_t st = i % NR, ph = i / NR;
-                    uint8_t* raw = sm_raw + st * 2 * S::RAW;
-                    const long long sc = ((long long)page * A.Hkv + s.h) * A.page + off;
-                    if (lane == 0) {
-                        wait(&rke[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&rkf[st], nv * (box_bytes + A.box));
-                    }
-                    __syncwarp();
-                    if (page >= 0 && !*gone) {
-                        if (part == 0) tma_load_4d(raw + chunk * box_bytes, &mk, 0, off, s.h, page, &rkf[st]);
-                        if (part == 1) bulk_g2s(sm_sc + st * 256 + chunk * A.box, A.ks + sc, A.box, &rkf[st]);
-                    }
-                    if (lane == 0) {
-                        wait(&rve[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(&rvf[st], nv * (box_bytes + A.box));
-                    }
-                    __syncwarp();
-                    if (page >= 0 && !*gone) {
-                        if (part == 0) tma_load_4d(raw + S::RAW + chunk * box_bytes, &mv, 0, off, s.h, page, &rvf[st]);
-                        if (part == 1) bulk_g2s(sm_sc + st * 256 + 128 + chunk * A.box, A.vs + sc, A.box, &rvf[st]);
-                    }
+                        tma_load_4d((side ? sm_v : sm_k) + st * S::OPERAND + part * 16384 + chunk * box_bytes,
+                                    side ? &mv : &mk, part * 64, off, s.h, page, full);
                 }
                 page = page2;
                 off = off2;
@@ -287,14 +370,9 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
         }
         // every copy has landed before the CTA leaves (they have, unless a wait ran out)
         if (lane == 0 && *gone) {
-            for (uint32_t j = i > 8 ? i - 8 : 0; j < i; ++j) {
-                if constexpr (!E4) {
-                    mbar_wait_bounded(&kf[j % ST], (j / ST) & 1u, AT_WAIT_NS / 8);
-                    mbar_wait_bounded(&vf[j % ST], (j / ST) & 1u, AT_WAIT_NS / 8);
-                } else {
-                    mbar_wait_bounded(&rkf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
-                    mbar_wait_bounded(&rvf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
-                }
+            for (uint32_t j = i > ST ? i - ST : 0; j < i; ++j) {
+                at_wait_bounded(&kf[j % ST], (j / ST) & 1u, AT_WAIT_NS / 8);
+                at_wait_bounded(&vf[j % ST], (j / ST) & 1u, AT_WAIT_NS / 8);
             }
         }
     } else if (warp == 1) {
@@ -340,76 +418,29 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 }
             }
             at_commit(&fin);  // every product is done before TMEM is freed
-            mbar_wait_bounded(&fin, 0, AT_WAIT_NS);
+            at_wait_bounded(&fin, 0, AT_WAIT_NS);
         }
     } else if (warp >= 4 && warp < 8) {
         // ---- softmax: row = this thread's TMEM lane
         const int w = warp - 4, r = w * 32 + lane, tid = r;
         const uint32_t lanes = uint32_t(w * 32) << 16;
-        const float c = fabsf(A.c);
         // a factor of zero would make NaN of -inf; no score of this size counts
-        constexpr float LEAST = 1e-30f;
+        const float c = fmaxf(fabsf(A.c), 1e-30f);
         const uint32_t flip = A.c < 0.f ? 0x80008000u : 0u;
         auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-        float rc = c;  // the row's factor on scores
         auto load_q = [&](const Segment& s) {
-            if constexpr (E4) {
-                // a row a thread: its largest value, then f16
-                const int row = s.rt * 128 + r, v = row / A.G;
-                const bool on = row < A.rows && v < s.n;
-                const uint16_t* src = static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
-                                      (s.h * A.G + row - v * A.G) * A.qh;
-                uint4 u[DP / 8];  // every load in flight at once
-#pragma unroll
-                for (int j = 0; j < DP / 8; ++j)
-                    u[j] = on && j * 8 < A.D ? __ldg(reinterpret_cast<const uint4*>(src + j * 8)) : make_uint4(0, 0, 0, 0);
-                auto pair = [&](uint32_t w) {
-                    return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w)) : make_float2(bf16_lo(w), bf16_hi(w));
-                };
-                float m = 0.f;
-#pragma unroll
-                for (int j = 0; j < DP / 8; ++j) {
-                    const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 x = pair(w[e]);
-                        m = fmaxf(m, fmaxf(finite_abs(x.x), finite_abs(x.y)));
-                    }
-                }
-                const uint32_t ex = max(min(__float_as_uint(m) >> 23, 253u), 1u);
-                const float f2 = __uint_as_float((254u - ex) << 23);
-                rc = c * exp2_int(int(ex) - 127);
-#pragma unroll
-                for (int j = 0; j < DP / 8; ++j) {
-                    uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 x = pair(w[e]);
-                        w[e] = pack16<true>(x.x * f2, x.y * f2) ^ flip;
-                    }
-                    *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) at_arrive(&qf);
-                return;
-            }
+            const int row = s.rt * 128 + r, v = row / A.G;
+            const bool on = row < A.rows && v < s.n;
+            const uint16_t* src = static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                                  (s.h * A.G + row - v * A.G) * A.qh;
             uint4 u[DP / 8];  // every load in flight at once
 #pragma unroll
-            for (int k = 0; k < DP / 8; ++k) {
-                const int x = tid + k * 128, rr = x / (DP / 8), j = x - rr * (DP / 8), row = s.rt * 128 + rr, v = row / A.G;
-                u[k] = make_uint4(0, 0, 0, 0);
-                if (row < A.rows && j * 8 < A.D && v < s.n)
-                    u[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
-                                                                (s.h * A.G + row - v * A.G) * A.qh + j * 8));
-            }
+            for (int j = 0; j < DP / 8; ++j)
+                u[j] = on && j * 8 < A.D ? __ldg(reinterpret_cast<const uint4*>(src + j * 8)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < DP / 8; ++k) {
-                const int x = tid + k * 128, rr = x / (DP / 8), j = x - rr * (DP / 8);
-                *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + rr * 128 + (((j & 7) ^ (rr & 7)) << 4)) =
-                    make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
-            }
+            for (int j = 0; j < DP / 8; ++j)
+                *reinterpret_cast<uint4*>(sm_q + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(u[j].x ^ flip, u[j].y ^ flip, u[j].z ^ flip, u[j].w ^ flip);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) at_arrive(&qf);
@@ -428,50 +459,17 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                 const uint32_t pa = tbase + lanes + T_P + (i & 1) * 64;  // PV of tile i - 2 is done with it
                 const int t0 = t * 128;
                 const bool tail = t0 + 128 > s.ctx;
-                // which of 32 tokens from t0 + j on this row sees
-                auto sees = [&](int j) {
-                    const int u = t0 + j - s.ctx;
-                    return u <= -32 ? 0xffffffffu
-                           : u < 0  ? (0xffffffffu >> (32 + u)) | (mask << -u)
-                           : u < 32 ? mask >> u
-                                    : 0u;
-                };
                 wait(&sf[i & 1], i >> 1);
                 at_after();
-                if (tail) {
-                    // what the row does not see becomes -inf, in place
-#pragma unroll 1
-                    for (int j = 0; j < 128; j += 32) {
-                        const uint32_t on = sees(j);
-                        uint32_t f[32], u[16], v[16];
-                        at_ld32(sa + j, f);
-                        at_ld_wait(f);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            u[e] = on >> e & 1u ? f[e] : 0xff800000u;
-                            v[e] = on >> (e + 16) & 1u ? f[e + 16] : 0xff800000u;
-                        }
-                        at_st16(sa + j, u);
-                        at_st16(sa + j + 16, v);
-                    }
-                    at_st_wait();
-                }
-                // the tile's factor on scores, and the unit of its values
-                float ct = fmaxf(c, LEAST), unit = 0.f;
-                if constexpr (E4) {
-                    wait(&uk[i & 3], i >> 2);
-                    wait(&vf[i % ST], i / ST);
-                    ct = fmaxf(rc * exp2_int(unit_k[i & 3]), LEAST);
-                    unit = float(unit_v[i & 3]);
-                }
+                if (tail) hide_unseen(sa, t0 - s.ctx, mask);
                 // One pass makes the weights by the reference as it is and finds the
                 // largest score; where some row's passes the reference by too
                 // much (seldom, but for a segment's first tile), the reference is
                 // raised and the weights are made again.
                 float s0, s1;
                 for (;;) {
-                    const float at = (ref == -INFINITY ? 0.f : -ref) + unit;
-                    const uint64_t c2 = f2_pack(ct, ct), at2 = f2_pack(at, at);
+                    const float at = ref == -INFINITY ? 0.f : -ref;
+                    const uint64_t c2 = f2_pack(c, c), at2 = f2_pack(at, at);
                     uint64_t sum = f2_pack(0.f, 0.f);
                     float mx = -INFINITY;
                     auto piece = [&](const uint32_t (&f)[32], int j) {
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                         piece(g, j + 32);
                     }
                     f2_unpack(sum, s0, s1);
-                    const float top = mx == -INFINITY ? mx : fmaf(mx, ct, unit);
+                    const float top = mx * c;
                     const bool raise = top > ref + AT_SLACK;
                     if (!__any_sync(0xffffffffu, raise)) break;
                     const float to = raise ? top : ref;
@@ -512,55 +510,14 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
                     tot *= f2;
                     if (t > s.t0) {  // O holds sums by the old reference
                         wait(&pv[(i - 1) & 1], (i - 1) >> 1);
-                        at_after();
-#pragma unroll 1
-                        for (int j = 0; j < DP; j += 32) {
-                            uint32_t u[16], v[16];
-                            at_ld32(tbase + lanes + T_O + j, f);
-                            at_ld_wait(f);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                u[e] = __float_as_uint(__uint_as_float(f[e]) * f2);
-                                v[e] = __float_as_uint(__uint_as_float(f[e + 16]) * f2);
-                            }
-                            at_st16(tbase + lanes + T_O + j, u);
-                            at_st16(tbase + lanes + T_O + j + 16, v);
-                        }
+                        scale_rows<DP>(tbase + lanes + T_O, f2);
                     }
-                    at_st_wait();
                 }
-                if constexpr (E4) tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 3]), tot);
-                else tot += s0 + s1;
+                tot += s0 + s1;
                 if (tail) {
-                    // values of tokens past the request's end, and values of
-                    // nodes that are not finite, must not meet a weight of zero
                     const uint32_t st = i % ST;
                     wait(&vf[st], i / ST);
-                    uint32_t bad = 0;
-                    for (int x = tid; x < S::OPERAND / 16; x += 128) {
-                        const int tok = t0 + ((x >> 3) & 127);
-                        if (tok < s.ctx) continue;
-                        uint4* p = reinterpret_cast<uint4*>(sm_v + st * S::OPERAND) + x;
-                        if (tok >= s.ctx + s.n) {
-                            *p = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint32_t u[4] = {p->x, p->y, p->z, p->w};
-                        bool hit = false;
-                        constexpr uint32_t EX = F16 ? 0x7c00u : 0x7f80u;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                if ((u[e] >> (16 * y) & EX) == EX) {
-                                    u[e] &= ~(0xffffu << (16 * y));
-                                    hit = true;
-                                }
-                        if (hit) {
-                            *p = make_uint4(u[0], u[1], u[2], u[3]);
-                            bad |= 1u << (tok - s.ctx);
-                        }
-                    }
+                    const uint32_t bad = clean_values<F16, DP>(sm_v + st * S::OPERAND, t0, s, tid);
                     if (bad) atomicOr(&bad_nodes[seg & 1], bad);
                     fence_proxy_async_smem();
                 }
@@ -586,128 +543,12 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
             // so that of either barrier only the last phase can be open)
             wait(&pv[(i - 1) & 1], (i - 1) >> 1);
             at_after();
-            const bool whole = done.t0 == 0 && done.t1 == done.tiles;
-            const long long slot = part_slot(share, done);
-            const float inv = node < done.n && tot != 0.f ? 1.f / tot : 0.f;
-            const bool none = inv == 0.f && tot == tot;
-            const long long at = (((long long)done.b * A.N + node) * A.Hq + done.h * A.G + row - node * A.G) * A.D;
-#pragma unroll 1
-            for (int j = 0; j < DP; j += 32) {
-                uint32_t u0[32];
-                at_ld32(tbase + lanes + T_O + j, u0);
-                at_ld_wait(u0);
-                float o[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u0[e]);
-                if (row < A.rows) {
-                    for (uint32_t m = nodes_bad & mask; m; m &= m - 1)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (j + e < A.D) o[e] += not_finite_v<KIND>(A, done.b, done.h, done.ctx + __ffs(m) - 1, j + e);
-                    if (whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float lo = none ? 0.f : o[e + 2 * x] * inv, hi = none ? 0.f : o[e + 2 * x + 1] * inv;
-                                u[x] = A.q_f16 ? pack16<true>(lo, hi) : pack16<false>(lo, hi);
-                            }
-                            if (j + e < A.D)
-                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at + j + e) = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(A.part_o + (slot * 128 + r) * DP + j + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    }
-                }
-                __syncwarp();
-            }
+            put_tile<KIND, DP>(A, share, done, tbase + lanes + T_O, r, node, nodes_bad & mask, ref, tot);
             at_before();
             __syncwarp();
             if (lane == 0) at_arrive(&of);
-            if (whole) {
-                put_lse(A, done, row, ref, tot);
-            } else {
-                if (row < A.rows) *reinterpret_cast<float2*>(A.part_ml + (slot * 128 + r) * 2) = make_float2(ref, tot);
-                join_parts<E4 ? 2 : 4>(A, share, done, 128, DP, &join_flag, tid, 128, 1);
-            }
+            if (!(done.t0 == 0 && done.t1 == done.tiles)) join_parts<4>(A, share, done, 128, DP, &join_flag, tid, 128, 1);
             if (!more) break;
-        }
-    } else if (E4 && warp >= 8) {
-        // ---- bytes to f16, four warps for K and four for V: 4 lanes a token, two
-        // 16-byte chunks (16 channels each) a lane, 4 tokens a thread.  Eight
-        // lanes take tokens 4 apart, whose swizzles differ in their top bit.
-        const int side = warp >= 12, tid = threadIdx.x & 127, x = lane & 3;
-        const int tok0 = (tid >> 5) * 8 + (lane >> 2 & 1) * 4 + (lane >> 3), odd = lane >> 2 & 1;
-        uint64_t* const raw_full = side ? rvf : rkf;
-        uint64_t* const raw_empty = side ? rve : rke;
-        uint64_t* const full = side ? vf : kf;
-        uint64_t* const empty = side ? ve : ke;
-        // largest scale byte of the tile's first `valid` tokens (all lanes)
-        auto largest = [&](const uint8_t* sc, int valid) {
-            uint32_t w = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
-            const int left = valid - lane * 4;
-            w = left >= 4 ? w : left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u);
-            w = __vmaxu4(w, w >> 16);
-            return min(max(int(__reduce_max_sync(0xffffffffu, max(w & 255u, w >> 8 & 255u))), 1), 253) - 127;
-        };
-        uint32_t i = 0;
-        int b_at = first;
-        for (long long g = share.begin; g < share.end;) {
-            const Segment s = segment_at(A, L, share, g, b_at);
-            b_at = s.b;
-            g += s.t1 - s.t0;
-            for (int t = s.t0; t < s.t1; ++t, ++i) {
-                const int valid = s.ctx + s.n - t * 128;
-                const uint32_t rs = i % NR, st = i % ST;
-                const uint8_t* raw = sm_raw + (rs * 2 + side) * S::RAW;
-                const uint8_t* sc = sm_sc + rs * 256 + side * 128;
-                uint8_t* out = (side ? sm_v : sm_k) + st * S::OPERAND;
-                wait(&raw_full[rs], i / NR);
-                int unit = largest(sc, valid);
-                if (side) unit = max(unit, -100);
-                wait(&empty[st], (i / ST) ^ 1u);
-                if (tid == 0) {
-                    (side ? unit_v : unit_k)[i & 3] = unit;
-                    if (!side) at_arrive(&uk[i & 3]);
-                }
-#pragma unroll 1
-                for (int c0 = 0; c0 < DP / 64; ++c0) {  // chunks x, then x + 4: channels from 64 on
-                    uint4 w[4];
-                    uint32_t f[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int tk = tok0 + k * 32;
-                        w[k] = *reinterpret_cast<const uint4*>(raw + tk * 128 + (((x + c0 * 4) ^ (tk & 7)) << 4));
-                        f[k] = half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int tk = tok0 + k * 32;
-                        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                        uint32_t h[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            h[2 * e] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e])), f[k]);
-                            h[2 * e + 1] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e] >> 16)), f[k]);
-                        }
-                        uint8_t* o = out + c0 * 16384 + tk * 128;
-                        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                        // of the two tokens of 8 lanes one writes its even chunks
-                        // first and one its odd ones: all banks at once
-                        *reinterpret_cast<uint4*>(o + (((2 * x + odd) ^ (tk & 7)) << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(o + (((2 * x + 1 - odd) ^ (tk & 7)) << 4)) = odd ? lo : hi;
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    at_arrive(&full[st]);
-                    at_arrive(&raw_empty[rs]);
-                }
-            }
         }
     }
 
@@ -721,7 +562,7 @@ __global__ void __launch_bounds__(TilesShape<KIND, DP>::THREADS, 1)
 
 template <int KIND, int DP>
 cudaError_t launch_tiles(const AttnLaunch& L) {
-    using S = TilesShape<KIND, DP>;
+    using S = TilesShape<DP>;
     static bool ready[64] = {};  // per device; setting it twice does no harm
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -1,0 +1,548 @@
+// tree_attn_tiles_e4m3.cuh -- k_attn_tiles_e4m3: k_attn_tiles over an 8-bit cache.
+//
+// An SM's shared memory moves 128 bytes a cycle, and over an 8-bit cache that is
+// what runs out first: a tile of 128 tokens (32 KB) has some 1400 cycles to
+// match HBM.  So K's bytes are the operand as they lie, and only V becomes
+// 16-bit (bytes in by TMA 32 KB, V read 16 and written 32 as f16, operands read
+// 32-48 + 32).  Queries and weights are operands in TMEM.
+//
+// Scores.  Products of 8-bit types (kind::f8f6f4) take e4m3 queries, 4
+// significant bits each.  A query is split: q 2^-a = h1 + h2 (+ h3), h1 = e4m3(q
+// 2^-a), h2 = e4m3(q 2^-a - h1), .., a power of two a row that brings the largest
+// to 448 or less.  Two terms hold bf16's 8 bits and three f16's 11, down to
+// 2^-18 of the row's largest value; the terms' products add up in one
+// accumulator.  K's scale comes afterwards: a warp turns a tile's scale bytes to
+// factors, and the exponent of a weight is (s rc) ck[t] - m.
+//
+// Values.  v 2^e is stored as f16 v 2^(e - E), E the largest exponent of the
+// tile's rows: exact for rows within 2^15 of the largest, and off by 2^-33 of the
+// largest below.  2^E joins the exponents of the tile's weights, w_t = 2^(s_t + E -
+// m), so that all tiles' sums are in one unit; the total takes 2^-E times the
+// tile's weights.  E is taken as -100 or more, so that a tile of zeros does not
+// push the total out of float32.
+//
+// Warps: 0 copies; 1 products; 2 K's factors; 4..7 softmax (as in
+// k_attn_tiles, but P lies over S, since TMEM holds the queries); 8..15 V.
+#pragma once
+
+#include "tree_attn_tiles.cuh"
+
+namespace sv {
+
+template <int DP>
+struct TilesE4Shape {
+    static constexpr int HALVES = DP / 64;
+    static constexpr int OPERAND = HALVES * 16384;  // 128 tokens of f16 channels
+    static constexpr int RAW = 16384, RAWS = 4;     // 128 tokens of 128 bytes
+    static constexpr size_t SMEM = 1024 + size_t(RAWS) * 2 * RAW + 2 * OPERAND;
+    static constexpr int THREADS = 512;
+};
+
+// D f32, A and B e4m3, both K-major, M = N = 128
+constexpr uint32_t AT_ID_E4 = (1u << 4) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+__device__ __forceinline__ void at_mma_e4(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(AT_ID_E4), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void at_st8(uint32_t t, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// 2^d as two halves (d <= 0; 0 below f16's least subnormal)
+__device__ __forceinline__ uint32_t half2_exp2(int d) {
+    const uint32_t h = d >= -14 ? uint32_t(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+    return h * 0x10001u;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The next term of two halves: their e4m3 bytes; the halves keep what is left
+// (a difference of neighbours, so exact).
+__device__ __forceinline__ uint32_t e4m3_term(uint32_t& x) {
+    uint16_t w;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(w) : "r"(x));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(e4m3x2_to_f16x2(w)));
+    return w;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
+    k_attn_tiles_e4m3(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                      const __grid_constant__ AttnArgs A) {
+    using S = TilesE4Shape<DP>;
+    constexpr int NR = S::RAWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sm_raw = smem;                     // [raws][K, V][128 tokens][128]
+    uint8_t* sm_v = smem + NR * 2 * S::RAW;     // [2] f16 values
+    __shared__ __align__(16) uint8_t sm_sc[NR * 256];     // scale bytes
+    __shared__ __align__(16) float sm_ck[8][128];         // K's factors
+    __shared__ __align__(8) uint64_t rkf[NR], rke[NR], rvf[NR], rve[NR], vf[2], ve[2], uk[8];
+    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag, join_flag, unit_v[2];
+    __shared__ uint32_t bad_nodes[2];
+    __shared__ PlanWindow window;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Share share;
+    if (!read_plan(A, window, share)) return;  // the whole CTA
+    const int first = window.b0;
+    const Lists L = {window, A.plan, first};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&rkf[i], 1);
+            mbar_init(&rke[i], 2);  // the products, and the factors' warp
+            mbar_init(&rvf[i], 1);
+            mbar_init(&rve[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&vf[i], 8);
+            mbar_init(&ve[i], 1);
+            mbar_init(&sf[i], 1);
+            mbar_init(&pf[i], 4);
+            mbar_init(&pv[i], 1);
+        }
+        for (int i = 0; i < 8; ++i) mbar_init(&uk[i], 1);
+        mbar_init(&qf, 4);
+        mbar_init(&of, 4);
+        mbar_init(&fin, 1);
+        abort_flag = 0;
+        bad_nodes[0] = bad_nodes[1] = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    at_before();
+    __syncthreads();
+    at_after();
+    const uint32_t tbase = tmem_base;
+    // S (then P in its first 64 columns) at 0 and 128, O, the queries' terms
+    constexpr uint32_t T_O = 256, T_Q = 384, TERM = DP / 4;
+    const int terms = A.q_f16 ? 3 : 2;
+    volatile int* gone = &abort_flag;
+    // a bounded wait; once one has run out nobody waits any more
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity & 1u) || *gone) return;
+        if (!at_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
+    };
+
+    // registers from the other warpgroups to softmax (232 + 3 * 88 <= 4 * 128): in
+    // 128 its columns spill, to an L1 that shared memory has left little of
+    if (warp < 4 || warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+        // ---- copies: lane = (rows or scales, box of A.box tokens)
+        const int chunk = lane & 7, part = lane >> 3, boxes = 128 / A.box;
+        const uint32_t box_bytes = uint32_t(A.box) * 128;
+        uint32_t i = 0;  // tiles so far
+        int b_at = first;
+        for (long long g = share.begin; g < share.end;) {
+            const Segment s = segment_at(A, L, share, g, b_at);
+            b_at = s.b;
+            g += s.t1 - s.t0;
+            const int len = s.ctx + s.n;
+            const int32_t* table = A.table + (long long)s.b * A.max_pages;
+            auto page_of = [&](int t, int& off) {
+                const int tok = t * 128 + chunk * A.box;
+                if (t >= s.t1 || chunk >= boxes || tok >= len) return -1;
+                const int p = tok / A.page;
+                off = tok - p * A.page;
+                return __ldg(table + p);
+            };
+            int off = 0, page = page_of(s.t0, off);
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const int nv = min(boxes, max(0, (len - t * 128 + A.box - 1) / A.box));
+                int off2 = 0;
+                const int page2 = page_of(t + 1, off2);
+                const uint32_t st = i % NR, ph = i / NR;
+                uint8_t* raw = sm_raw + st * 2 * S::RAW;
+                const long long sc = ((long long)page * A.Hkv + s.h) * A.page + off;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    uint64_t* full = side ? &rvf[st] : &rkf[st];
+                    if (lane == 0) {
+                        wait(side ? &rve[st] : &rke[st], ph ^ 1u);
+                        if (!*gone) mbar_arrive_expect_tx(full, nv * (box_bytes + A.box));
+                    }
+                    __syncwarp();
+                    if (page >= 0 && !*gone) {
+                        if (part == 0)
+                            tma_load_4d(raw + side * S::RAW + chunk * box_bytes, side ? &mv : &mk, 0, off, s.h, page, full);
+                        if (part == 1)
+                            bulk_g2s(sm_sc + st * 256 + side * 128 + chunk * A.box, (side ? A.vs : A.ks) + sc, A.box, full);
+                    }
+                }
+                page = page2;
+                off = off2;
+            }
+        }
+        // every copy has landed before the CTA leaves (they have, unless a wait ran out)
+        if (lane == 0 && *gone) {
+            for (uint32_t j = i > NR ? i - NR : 0; j < i; ++j) {
+                at_wait_bounded(&rkf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
+                at_wait_bounded(&rvf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t id_o = at_idesc<true>(DP, true);
+            uint32_t i = 0, seg = 0;
+            int b_at = first;
+            auto scores = [&](uint32_t j) {
+                const uint32_t rs = j % NR;
+                wait(&rkf[rs], j / NR);
+                if (j >= 2) wait(&pv[j & 1], (j - 2) >> 1);  // P of tile j - 2 lies there
+                at_after();
+                const uint32_t ka = smem_u32(sm_raw) + rs * 2 * S::RAW;
+                for (int x = 0; x < terms; ++x)
+#pragma unroll
+                    for (int k = 0; k < DP / 32; ++k)
+                        at_mma_e4(tbase + (j & 1) * 128, tbase + T_Q + x * TERM + k * 8, at_desc_k(ka + k * 32),
+                                  x > 0 || k > 0);
+                at_commit(&rke[rs]);
+                at_commit(&sf[j & 1]);
+            };
+            for (long long g = share.begin; g < share.end; ++seg) {
+                const Segment s = segment_at(A, L, share, g, b_at);
+                b_at = s.b;
+                g += s.t1 - s.t0;
+                wait(&qf, seg);
+                at_after();
+                scores(i);
+                for (int t = s.t0; t < s.t1; ++t, ++i) {
+                    if (t + 1 < s.t1) scores(i + 1);
+                    wait(&vf[i & 1], i >> 1);
+                    wait(&pf[i & 1], i >> 1);
+                    if (t == s.t0) wait(&of, seg ^ 1u);  // the last segment's rows have been read
+                    at_after();
+                    const uint32_t va = smem_u32(sm_v) + (i & 1) * S::OPERAND;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        at_mma_ts(tbase + T_O, tbase + (i & 1) * 128 + k * 8, at_desc_mn(va + k * 2048), id_o,
+                                  t > s.t0 || k > 0);
+                    at_commit(&ve[i & 1]);
+                    at_commit(&pv[i & 1]);
+                }
+            }
+            at_commit(&fin);  // every product is done before TMEM is freed
+            at_wait_bounded(&fin, 0, AT_WAIT_NS);
+        }
+    } else if (warp == 2) {
+        // ---- K's factors, 4 tokens a lane (1 past the request's end).  A slot is
+        // written again 8 tiles on, when the scores of tile i + 4 are done, which
+        // take the place of the weights of tile i + 2: softmax is through with i.
+        uint32_t i = 0;
+        int b_at = first;
+        for (long long g = share.begin; g < share.end;) {
+            const Segment s = segment_at(A, L, share, g, b_at);
+            b_at = s.b;
+            g += s.t1 - s.t0;
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const uint32_t rs = i % NR;
+                wait(&rkf[rs], i / NR);
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(sm_sc + rs * 256 + lane * 4);
+                const int left = s.ctx + s.n - t * 128 - lane * 4;
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[e] = e < left ? exp2_int(min(max(int(w >> (8 * e) & 255u), 1), 253) - 127) : 1.f;
+                *reinterpret_cast<float4*>(&sm_ck[i & 7][lane * 4]) = make_float4(f[0], f[1], f[2], f[3]);
+                __syncwarp();
+                if (lane == 0) {
+                    at_arrive(&uk[i & 7]);
+                    at_arrive(&rke[rs]);
+                }
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---- softmax: row = this thread's TMEM lane
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int w = warp - 4, r = w * 32 + lane, tid = r;
+        const uint32_t lanes = uint32_t(w * 32) << 16;
+        const float c = fabsf(A.c), sign = A.c < 0.f ? -1.f : 1.f;
+        auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        float rc = 0.f;  // the row's factor on scores
+        auto load_q = [&](const Segment& s) {
+            const int row = s.rt * 128 + r, v = row / A.G;
+            const bool on = row < A.rows && v < s.n;
+            const uint16_t* src = static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                                  (s.h * A.G + row - v * A.G) * A.qh;
+            uint4 u[DP / 8];  // every load in flight at once
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j)
+                u[j] = on && j * 8 < A.D ? __ldg(reinterpret_cast<const uint4*>(src + j * 8)) : make_uint4(0, 0, 0, 0);
+            auto pair = [&](uint32_t x) {
+                return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&x)) : make_float2(bf16_lo(x), bf16_hi(x));
+            };
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j) {
+                const uint32_t x[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = pair(x[e]);
+                    m = fmaxf(m, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+                }
+            }
+            const int ex = e4m3_exponent(m);
+            const float down = exp2_int(-ex) * sign, nan = __int_as_float(0x7fc00000);
+            // a factor of zero would make NaN of -inf; no score of this size counts
+            rc = fmaxf(c * exp2_int(ex), 1e-30f);
+#pragma unroll
+            for (int j = 0; j < DP / 32; ++j) {
+                // as halves: 11 bits, and below 2^-14 of the scale steps of 2^-24
+                uint32_t f[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint4& y = u[j * 4 + e / 4];
+                    const float2 z = pair(e % 4 == 0 ? y.x : e % 4 == 1 ? y.y : e % 4 == 2 ? y.z : y.w);
+                    f[e] = pack16<true>(fabsf(z.x) < INFINITY ? z.x * down : nan, fabsf(z.y) < INFINITY ? z.y * down : nan);
+                }
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    if (x == 2 && !A.q_f16) break;
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        o[e] = e4m3_term(f[2 * e]);
+                        o[e] |= e4m3_term(f[2 * e + 1]) << 16;
+                    }
+                    at_st8(tbase + lanes + T_Q + x * TERM + j * 8, o);
+                }
+            }
+            at_st_wait();
+            at_before();
+            __syncwarp();
+            if (lane == 0) at_arrive(&qf);
+        };
+        uint32_t i = 0, seg = 0;
+        Segment s = segment_at(A, L, share, share.begin, first);
+        load_q(s);
+        for (;; ++seg) {
+            const int row = s.rt * 128 + r, node = row / A.G;
+            uint32_t mask = 0;
+            if (row < A.rows && node < s.n)
+                mask = A.masks[(long long)s.b * A.N + node] & (0xffffffffu >> (32 - s.n));
+            float ref = -INFINITY, tot = 0.f;
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const uint32_t sa = tbase + lanes + (i & 1) * 128;
+                const int t0 = t * 128;
+                const bool tail = t0 + 128 > s.ctx;
+                wait(&sf[i & 1], i >> 1);
+                at_after();
+                if (tail) hide_unseen(sa, t0 - s.ctx, mask);
+                wait(&uk[i & 7], i >> 3);
+                wait(&vf[i & 1], i >> 1);
+                const float unit = float(unit_v[i & 1]);
+                const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 7]);
+                // 32 tokens at a time: exponents relative to the reference, their
+                // largest, the weights.  Where a row's largest is too far above the
+                // reference (seldom, but for a segment's first tokens), the
+                // reference is raised and what was made by the old one rescaled.
+                uint64_t sum = f2_pack(0.f, 0.f);
+                auto piece = [&](uint32_t (&x)[32], int j) {
+                    const float base = ref == -INFINITY ? 0.f : ref;
+                    const uint64_t rc2 = f2_pack(rc, rc), at2 = f2_pack(unit - base, unit - base);
+                    float mx = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 k4 = ck[j / 4 + e];
+                        float a0, b0, a1, b1;
+                        f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), rc2),
+                                         f2_pack(k4.x, k4.y), at2), a0, b0);
+                        f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), rc2),
+                                         f2_pack(k4.z, k4.w), at2), a1, b1);
+                        mx = fmaxf(fmaxf(a0, b0), mx);
+                        m2 = fmaxf(fmaxf(a1, b1), m2);
+                        x[4 * e] = __float_as_uint(a0);
+                        x[4 * e + 1] = __float_as_uint(b0);
+                        x[4 * e + 2] = __float_as_uint(a1);
+                        x[4 * e + 3] = __float_as_uint(b1);
+                    }
+                    mx = fmaxf(mx, m2);
+                    const bool raise = mx > (ref == -INFINITY ? -INFINITY : AT_SLACK);
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float d = raise ? mx : 0.f;
+                        const float f = !raise ? 1.f : ref == -INFINITY ? 0.f : ex2_approx(-d);
+                        if (raise) ref = base + d;
+                        tot *= f;
+                        sum = f2_mul(sum, f2_pack(f, f));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - d);
+                        const uint32_t h = pack16<true>(f, f);
+#pragma unroll 1
+                        for (int y = 0; y < j; y += 32) {
+                            uint32_t old[32], to[16];
+                            at_ld32(sa + y / 2, old);
+                            at_ld_wait(old);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) to[e] = half2_mul(old[e], h);
+                            at_st16(sa + y / 2, to);
+                        }
+                        if (t > s.t0) {  // O holds sums by the old reference
+                            wait(&pv[(i - 1) & 1], (i - 1) >> 1);
+                            scale_rows<DP>(tbase + lanes + T_O, f);
+                        }
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = ex2_approx(__uint_as_float(x[2 * e])), b = ex2_approx(__uint_as_float(x[2 * e + 1]));
+                        sum = f2_add(sum, f2_pack(a, b));
+                        p[e] = pack16<true>(a, b);
+                    }
+                    at_st16(sa + j / 2, p);
+                };
+                uint32_t f[32], g[32];
+                at_ld32(sa, f);
+#pragma unroll 1
+                for (int j = 0; j < 128; j += 64) {
+                    at_ld_wait(f);
+                    at_ld32(sa + j + 32, g);
+                    piece(f, j);
+                    at_ld_wait(g);
+                    if (j == 0) at_ld32(sa + 64, f);
+                    piece(g, j + 32);
+                }
+                float s0, s1;
+                f2_unpack(sum, s0, s1);
+                tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 1]), tot);
+                if (tail) {
+                    const uint32_t bad = clean_values<true, DP>(sm_v + (i & 1) * S::OPERAND, t0, s, tid);
+                    if (bad) atomicOr(&bad_nodes[seg & 1], bad);
+                    fence_proxy_async_smem();
+                }
+                at_st_wait();
+                at_before();
+                __syncwarp();
+                if (lane == 0) at_arrive(&pf[i & 1]);
+            }
+            // the next segment's queries (every product of this one's is done)
+            const Segment done = s;
+            const long long next = s.g + (s.t1 - s.t0);
+            const bool more = next < share.end;
+            sync();  // every warp has marked its nodes
+            const uint32_t nodes_bad = bad_nodes[seg & 1];
+            // the other word is for the next segment, which starts when all
+            // four warps have arrived at qf: nobody reads or marks it now
+            if (tid == 0) bad_nodes[(seg & 1) ^ 1] = 0;
+            if (more) {
+                s = segment_at(A, L, share, next, s.b);
+                load_q(s);
+            }
+            // (the last scores say that all products but the last two are done,
+            // so that of either barrier only the last phase can be open)
+            wait(&pv[(i - 1) & 1], (i - 1) >> 1);
+            at_after();
+            put_tile<SPEC_E4M3, DP>(A, share, done, tbase + lanes + T_O, r, node, nodes_bad & mask, ref, tot);
+            at_before();
+            __syncwarp();
+            if (lane == 0) at_arrive(&of);
+            if (!(done.t0 == 0 && done.t1 == done.tiles)) join_parts<4>(A, share, done, 128, DP, &join_flag, tid, 128, 1);
+            if (!more) break;
+        }
+    } else if (warp >= 8) {
+        // ---- V to f16: 4 lanes a token, two 16-byte chunks (16 channels each) a
+        // lane, 2 tokens a thread.  Eight lanes take tokens 4 apart, whose
+        // swizzles differ in their top bit.
+        const int tid = threadIdx.x - 256, x = lane & 3, odd = lane >> 2 & 1;
+        const int tok0 = (warp - 8) * 8 + odd * 4 + (lane >> 3);
+        uint32_t i = 0;
+        int b_at = first;
+        for (long long g = share.begin; g < share.end;) {
+            const Segment s = segment_at(A, L, share, g, b_at);
+            b_at = s.b;
+            g += s.t1 - s.t0;
+            for (int t = s.t0; t < s.t1; ++t, ++i) {
+                const int valid = s.ctx + s.n - t * 128;
+                const uint32_t rs = i % NR, st = i & 1;
+                const uint8_t* raw = sm_raw + (rs * 2 + 1) * S::RAW;
+                const uint8_t* sc = sm_sc + rs * 256 + 128;
+                uint8_t* out = sm_v + st * S::OPERAND;
+                wait(&rvf[rs], i / NR);
+                // the largest scale byte of the tile's valid tokens
+                uint32_t z = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
+                const int left = valid - lane * 4;
+                z = left >= 4 ? z : left <= 0 ? 0u : z & ((1u << (8 * left)) - 1u);
+                z = __vmaxu4(z, z >> 16);
+                const int top = int(__reduce_max_sync(0xffffffffu, max(z & 255u, z >> 8 & 255u)));
+                const int unit = max(min(max(top, 1), 253) - 127, -100);
+                uint4 q[2][2];
+                uint32_t f[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int tk = tok0 + k * 64;
+                    f[k] = half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
+#pragma unroll
+                    for (int h = 0; h < S::HALVES; ++h)
+                        q[k][h] = *reinterpret_cast<const uint4*>(raw + tk * 128 + (((x + h * 4) ^ (tk & 7)) << 4));
+                }
+                wait(&ve[st], (i >> 1) ^ 1u);
+                if (tid == 0) unit_v[st] = unit;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int h = 0; h < S::HALVES; ++h) {
+                        const int tk = tok0 + k * 64;
+                        const uint32_t u[4] = {q[k][h].x, q[k][h].y, q[k][h].z, q[k][h].w};
+                        uint32_t v[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v[2 * e] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e])), f[k]);
+                            v[2 * e + 1] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e] >> 16)), f[k]);
+                        }
+                        uint8_t* o = out + h * 16384 + tk * 128;
+                        const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
+                        // of the two tokens of 8 lanes one writes its even chunks
+                        // first and one its odd ones: all banks at once
+                        *reinterpret_cast<uint4*>(o + (((2 * x + odd) ^ (tk & 7)) << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(o + (((2 * x + 1 - odd) ^ (tk & 7)) << 4)) = odd ? lo : hi;
+                    }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    at_arrive(&vf[st]);
+                    at_arrive(&rve[rs]);
+                }
+            }
+        }
+    }
+
+    at_before();
+    __syncthreads();
+    at_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tbase) : "memory");
+    if (threadIdx.x == 0 && *gone && A.status) atomicOr(A.status, int(SPEC_BADBIT_TIMEOUT));
+}
+
+template <int DP>
+cudaError_t launch_tiles_e4m3(const AttnLaunch& L) {
+    using S = TilesE4Shape<DP>;
+    static bool ready[64] = {};  // per device; setting it twice does no harm
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(k_attn_tiles_e4m3<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM));
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    k_attn_tiles_e4m3<DP><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
+    return cudaGetLastError();
+}
+
+}  // namespace sv
