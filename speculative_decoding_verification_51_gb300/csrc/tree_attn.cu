@@ -55,7 +55,86 @@ constexpr int MAX_R = 128;  // rows of the largest tile
 // channels of a row as the kernels lay them out
 int width_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 
+// The parts that k_attn_tiles left: CTA (c, y) joins the item that starts in CTA
+// c's share and ends in another's, its y-th share of the channels.  One row a
+// thread (lanes side by side, so that reads are coalesced), 8 channels at most, up
+// to 8 parts' reads in flight.  Launched with programmatic dependent launch:
+// it finds its item while k_attn_tiles still runs.
+constexpr int JOIN_T = 256, JOIN_Y = 8;
+__global__ void __launch_bounds__(JOIN_T) k_attn_join(const __grid_constant__ AttnArgs A, int width) {
+    __shared__ PlanWindow window;
+    Share share;
+    if (!read_plan(A, window, share)) return;
+    const Lists L = {window, A.plan, window.b0};
+    const Segment s = segment_at(A, L, share, share.end - 1, window.b0);
+    const long long g0 = s.g - s.t0;
+    if (g0 < share.begin || s.t0 + 1 == s.tiles) return;  // begins before this share, or ends with it
+    const int c0 = blockIdx.x, parts = cta_of(share, g0 + s.tiles - 1) - c0 + 1;
+    const int r = threadIdx.x & 127, row = s.rt * 128 + r, quads = width / 4;
+    const int per = quads / JOIN_Y / (JOIN_T / 128);  // 2 (128 channels) or 1
+    const int q0 = (blockIdx.y * (JOIN_T / 128) + (threadIdx.x >> 7)) * per;
+    griddep_wait();
+    if (row >= A.rows) return;
+    auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
+    const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + r;
+    const float4* po = reinterpret_cast<const float4*>(A.part_o) + (long long)q0 * 128 + r;
+    float ref = -INFINITY, total = 0.f, o[2][4] = {};
+    for (int c = 0; c < parts; c += 8) {  // running sums, by the running reference
+        float2 z[8];
+        float4 x[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool on = c + i < parts;
+            z[i] = on ? __ldcg(ml + slot(c + i) * 128) : make_float2(-INFINITY, 0.f);
+            x[i] = on ? __ldcg(po + slot(c + i) * quads * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+            y[i] = on && per == 2 ? __ldcg(po + slot(c + i) * quads * 128 + 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float to = ref;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to = fmaxf(to, z[i].x);
+        const float at = to == -INFINITY ? 0.f : to, f = ex2_approx(ref - at);
+        ref = to;
+        total *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            o[0][e] *= f;
+            o[1][e] *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float w = ex2_approx(z[i].x - at);  // 0 for a part that is not there
+            total = fmaf(w, z[i].y, total);
+            o[0][0] = fmaf(w, x[i].x, o[0][0]);
+            o[0][1] = fmaf(w, x[i].y, o[0][1]);
+            o[0][2] = fmaf(w, x[i].z, o[0][2]);
+            o[0][3] = fmaf(w, x[i].w, o[0][3]);
+            o[1][0] = fmaf(w, y[i].x, o[1][0]);
+            o[1][1] = fmaf(w, y[i].y, o[1][1]);
+            o[1][2] = fmaf(w, y[i].z, o[1][2]);
+            o[1][3] = fmaf(w, y[i].w, o[1][3]);
+        }
+    }
+    put_row(A, s, row, q0 * 4, o[0], total);
+    if (per == 2) put_row(A, s, row, q0 * 4 + 4, o[1], total);
+    if (q0 == 0) put_lse(A, s, row, ref, total);
+}
+
 }  // namespace
+
+namespace sv {
+cudaError_t launch_attn_join(const AttnLaunch& L, int width) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(L.ctas), JOIN_Y);
+    cfg.blockDim = dim3(JOIN_T);
+    cfg.stream = L.st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_join, L.A, width);
+}
+}  // namespace sv
 
 extern "C" {
 

@@ -280,11 +280,12 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
     __shared__ __align__(8) uint64_t kf[ST], ke[ST], vf[ST], ve[ST];  // stages full and empty
     __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
     __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag, join_flag;
+    __shared__ int abort_flag;
     __shared__ uint32_t bad_nodes[2];
     __shared__ PlanWindow window;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_launch_dependents();  // k_attn_join waits for this grid's end by itself
     Share share;
     if (!read_plan(A, window, share)) return;  // the whole CTA
     const int first = window.b0;
@@ -454,6 +455,21 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
             if (row < A.rows && node < s.n)
                 mask = A.masks[(long long)s.b * A.N + node] & (0xffffffffu >> (32 - s.n));
             float ref = -INFINITY, tot = 0.f;
+            // the segment after this one; its query row comes to L2 meanwhile
+            const long long next = s.g + (s.t1 - s.t0);
+            const bool more = next < share.end;
+            Segment after = s;
+            if (more) {
+                after = segment_at(A, L, share, next, s.b);
+                const int nr = after.rt * 128 + r, nv = nr / A.G;
+                if (nr < A.rows && nv < after.n) {
+                    const uint16_t* src = static_cast<const uint16_t*>(A.q) + after.b * A.qb + nv * A.qn +
+                                          (after.h * A.G + nr - nv * A.G) * A.qh;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+                    if (A.D > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.masks + (long long)after.b * A.N + nv));
+                }
+            }
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const uint32_t sa = tbase + lanes + (i & 1) * 128;
                 const uint32_t pa = tbase + lanes + T_P + (i & 1) * 64;  // PV of tile i - 2 is done with it
@@ -461,7 +477,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
                 const bool tail = t0 + 128 > s.ctx;
                 wait(&sf[i & 1], i >> 1);
                 at_after();
-                if (tail) hide_unseen(sa, t0 - s.ctx, mask);
+                if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 - s.ctx, mask);
                 // One pass makes the weights by the reference as it is and finds the
                 // largest score; where some row's passes the reference by too
                 // much (seldom, but for a segment's first tile), the reference is
@@ -503,7 +519,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
                     f2_unpack(sum, s0, s1);
                     const float top = mx * c;
                     const bool raise = top > ref + AT_SLACK;
-                    if (!__any_sync(0xffffffffu, raise)) break;
+                    if (__builtin_expect(!__any_sync(0xffffffffu, raise), 1)) break;
                     const float to = raise ? top : ref;
                     const float f2 = ref == to ? 1.f : ex2_approx(ref - to);
                     ref = to;
@@ -514,7 +530,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
                     }
                 }
                 tot += s0 + s1;
-                if (tail) {
+                if (__builtin_expect(tail, 0)) {
                     const uint32_t st = i % ST;
                     wait(&vf[st], i / ST);
                     const uint32_t bad = clean_values<F16, DP>(sm_v + st * S::OPERAND, t0, s, tid);
@@ -528,15 +544,13 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
             }
             // the next segment's queries (every product of this one's is done)
             const Segment done = s;
-            const long long next = s.g + (s.t1 - s.t0);
-            const bool more = next < share.end;
             sync();  // every warp has marked its nodes
             const uint32_t nodes_bad = bad_nodes[seg & 1];
             // the other word is for the next segment, which starts when all
             // four warps have arrived at qf: nobody reads or marks it now
             if (tid == 0) bad_nodes[(seg & 1) ^ 1] = 0;
             if (more) {
-                s = segment_at(A, L, share, next, s.b);
+                s = after;
                 load_q(s);
             }
             // (the last scores say that all products but the last two are done,
@@ -547,7 +561,6 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
             at_before();
             __syncwarp();
             if (lane == 0) at_arrive(&of);
-            if (!(done.t0 == 0 && done.t1 == done.tiles)) join_parts<4>(A, share, done, 128, DP, &join_flag, tid, 128, 1);
             if (!more) break;
         }
     }
@@ -574,7 +587,8 @@ cudaError_t launch_tiles(const AttnLaunch& L) {
         ready[dev] = true;
     }
     k_attn_tiles<KIND, DP><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_attn_join(L, DP) : e;
 }
 
 }  // namespace sv

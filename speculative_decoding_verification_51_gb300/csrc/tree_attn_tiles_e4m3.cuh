@@ -87,11 +87,12 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     __shared__ __align__(8) uint64_t rkf[NR], rke[NR], rvf[NR], rve[NR], vf[2], ve[2], uk[8];
     __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
     __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag, join_flag, unit_v[2];
+    __shared__ int abort_flag, unit_v[2];
     __shared__ uint32_t bad_nodes[2];
     __shared__ PlanWindow window;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_launch_dependents();  // k_attn_join waits for this grid's end by itself
     Share share;
     if (!read_plan(A, window, share)) return;  // the whole CTA
     const int first = window.b0;
@@ -286,20 +287,21 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             auto pair = [&](uint32_t x) {
                 return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&x)) : make_float2(bf16_lo(x), bf16_hi(x));
             };
-            float m = 0.f;
+            float m = 0.f, odd = 0.f;  // odd: NaN where some value is not finite, and the row with it
 #pragma unroll
             for (int j = 0; j < DP / 8; ++j) {
                 const uint32_t x[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = pair(x[e]);
-                    m = fmaxf(m, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+                    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    odd = fmaf(f.x, 0.f, fmaf(f.y, 0.f, odd));
                 }
             }
-            const int ex = e4m3_exponent(m);
-            const float down = exp2_int(-ex) * sign, nan = __int_as_float(0x7fc00000);
+            const int ex = odd == 0.f ? e4m3_exponent(m) : 0;
+            const float down = exp2_int(-ex) * sign;
             // a factor of zero would make NaN of -inf; no score of this size counts
-            rc = fmaxf(c * exp2_int(ex), 1e-30f);
+            rc = fmaxf(c * exp2_int(ex), 1e-30f) + odd;
 #pragma unroll
             for (int j = 0; j < DP / 32; ++j) {
                 // as halves: 11 bits, and below 2^-14 of the scale steps of 2^-24
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 for (int e = 0; e < 16; ++e) {
                     const uint4& y = u[j * 4 + e / 4];
                     const float2 z = pair(e % 4 == 0 ? y.x : e % 4 == 1 ? y.y : e % 4 == 2 ? y.z : y.w);
-                    f[e] = pack16<true>(fabsf(z.x) < INFINITY ? z.x * down : nan, fabsf(z.y) < INFINITY ? z.y * down : nan);
+                    f[e] = pack16<true>(z.x * down, z.y * down);
                 }
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
@@ -336,13 +338,28 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             if (row < A.rows && node < s.n)
                 mask = A.masks[(long long)s.b * A.N + node] & (0xffffffffu >> (32 - s.n));
             float ref = -INFINITY, tot = 0.f;
+            // the segment after this one; its query row comes to L2 meanwhile
+            const long long next = s.g + (s.t1 - s.t0);
+            const bool more = next < share.end;
+            Segment after = s;
+            if (more) {
+                after = segment_at(A, L, share, next, s.b);
+                const int nr = after.rt * 128 + r, nv = nr / A.G;
+                if (nr < A.rows && nv < after.n) {
+                    const uint16_t* src = static_cast<const uint16_t*>(A.q) + after.b * A.qb + nv * A.qn +
+                                          (after.h * A.G + nr - nv * A.G) * A.qh;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+                    if (A.D > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.masks + (long long)after.b * A.N + nv));
+                }
+            }
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const uint32_t sa = tbase + lanes + (i & 1) * 128;
                 const int t0 = t * 128;
                 const bool tail = t0 + 128 > s.ctx;
                 wait(&sf[i & 1], i >> 1);
                 at_after();
-                if (tail) hide_unseen(sa, t0 - s.ctx, mask);
+                if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 - s.ctx, mask);
                 wait(&uk[i & 7], i >> 3);
                 wait(&vf[i & 1], i >> 1);
                 const float unit = float(unit_v[i & 1]);
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     }
                     mx = fmaxf(mx, m2);
                     const bool raise = mx > (ref == -INFINITY ? -INFINITY : AT_SLACK);
-                    if (__any_sync(0xffffffffu, raise)) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
                         const float d = raise ? mx : 0.f;
                         const float f = !raise ? 1.f : ref == -INFINITY ? 0.f : ex2_approx(-d);
                         if (raise) ref = base + d;
@@ -419,7 +436,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 float s0, s1;
                 f2_unpack(sum, s0, s1);
                 tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 1]), tot);
-                if (tail) {
+                if (__builtin_expect(tail, 0)) {
                     const uint32_t bad = clean_values<true, DP>(sm_v + (i & 1) * S::OPERAND, t0, s, tid);
                     if (bad) atomicOr(&bad_nodes[seg & 1], bad);
                     fence_proxy_async_smem();
@@ -431,15 +448,13 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             }
             // the next segment's queries (every product of this one's is done)
             const Segment done = s;
-            const long long next = s.g + (s.t1 - s.t0);
-            const bool more = next < share.end;
             sync();  // every warp has marked its nodes
             const uint32_t nodes_bad = bad_nodes[seg & 1];
             // the other word is for the next segment, which starts when all
             // four warps have arrived at qf: nobody reads or marks it now
             if (tid == 0) bad_nodes[(seg & 1) ^ 1] = 0;
             if (more) {
-                s = segment_at(A, L, share, next, s.b);
+                s = after;
                 load_q(s);
             }
             // (the last scores say that all products but the last two are done,
@@ -450,7 +465,6 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             at_before();
             __syncwarp();
             if (lane == 0) at_arrive(&of);
-            if (!(done.t0 == 0 && done.t1 == done.tiles)) join_parts<4>(A, share, done, 128, DP, &join_flag, tid, 128, 1);
             if (!more) break;
         }
     } else if (warp >= 8) {
@@ -542,7 +556,8 @@ cudaError_t launch_tiles_e4m3(const AttnLaunch& L) {
         ready[dev] = true;
     }
     k_attn_tiles_e4m3<DP><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_attn_join(L, DP) : e;
 }
 
 }  // namespace sv
