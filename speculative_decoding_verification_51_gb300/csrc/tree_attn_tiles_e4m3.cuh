@@ -357,11 +357,15 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 const uint32_t sa = tbase + lanes + (i & 1) * 128;
                 const int t0 = t * 128;
                 const bool tail = t0 + 128 > s.ctx;
-                wait(&sf[i & 1], i >> 1);
+                {   // three waits side by side: each costs some 100 cycles though it is over
+                    const bool w0 = mbar_try_wait(&sf[i & 1], i >> 1 & 1), w1 = mbar_try_wait(&uk[i & 7], i >> 3 & 1),
+                               w2 = mbar_try_wait(&vf[i & 1], i >> 1 & 1);
+                    if (!w0) wait(&sf[i & 1], i >> 1);
+                    if (!w1) wait(&uk[i & 7], i >> 3);
+                    if (!w2) wait(&vf[i & 1], i >> 1);
+                }
                 at_after();
                 if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 - s.ctx, mask);
-                wait(&uk[i & 7], i >> 3);
-                wait(&vf[i & 1], i >> 1);
                 const float unit = float(unit_v[i & 1]);
                 const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 7]);
                 // 32 tokens at a time: exponents relative to the reference, their
@@ -422,16 +426,12 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     }
                     at_st16(sa + j / 2, p);
                 };
-                uint32_t f[32], g[32];
-                at_ld32(sa, f);
 #pragma unroll 1
-                for (int j = 0; j < 128; j += 64) {
+                for (int j = 0; j < 128; j += 32) {
+                    uint32_t f[32];
+                    at_ld32(sa + j, f);
                     at_ld_wait(f);
-                    at_ld32(sa + j + 32, g);
                     piece(f, j);
-                    at_ld_wait(g);
-                    if (j == 0) at_ld32(sa + 64, f);
-                    piece(g, j + 32);
                 }
                 float s0, s1;
                 f2_unpack(sum, s0, s1);
