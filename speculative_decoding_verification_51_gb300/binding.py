@@ -584,20 +584,26 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _on:
-    """Makes `device` current for a call (nothing to do where it is)."""
-    __slots__ = ("guard",)
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    # the same handle without a Stream object around it (3 us a call on the
+    # machine's Arm cores, of the 25 that a small operator took)
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _call(fn, what: str, device: torch.device, *args) -> None:
+    """fn(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(index))
+    if rc != SPEC_OK:
+        raise SpecVerifyError(rc, what)
 
 
 def _streamed(fn):
@@ -620,18 +626,24 @@ def _raise(rc, what):
 def _heads(t, name, heads, D, dtype, device, tokens=None):
     """[..., heads, D] as (tokens, token stride, head stride): the leading
     dimensions must be one run of tokens."""
+    sh = t.shape
+    if len(sh) == 3 and sh[2] == D and t.dtype is dtype and t.device == device and \
+            (heads is None or sh[1] == heads) and (tokens is None or sh[0] == tokens):
+        st = t.stride()
+        if st[2] == 1:
+            return sh[0], st[0], st[1]
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() < 3 or t.shape[-1] != D or (heads is not None and t.shape[-2] != heads):
+    if t.dim() < 3 or sh[-1] != D or (heads is not None and sh[-2] != heads):
         raise ValueError(f"{name} must be [tokens, {heads if heads is not None else 'heads'}, {D}], "
-                         f"got {tuple(t.shape)}")
-    st, sh = t.stride(), t.shape
+                         f"got {tuple(sh)}")
+    st = t.stride()
     if sh[-1] > 1 and st[-1] != 1:
         raise ValueError(f"the channels of {name} must be contiguous")
     n, step = sh[-3], st[-3]
-    for i in range(t.dim() - 4, -1, -1):
+    for i in range(len(sh) - 4, -1, -1):
         if sh[i] != 1 and n != 1 and st[i] != n * step:
             raise ValueError(f"the leading dimensions of {name} must be one run of tokens")
         if n == 1:
@@ -640,6 +652,13 @@ def _heads(t, name, heads, D, dtype, device, tokens=None):
     if tokens is not None and n != tokens:
         raise ValueError(f"{name} has {n} tokens, expected {tokens}")
     return n, step, st[-2]
+
+
+def _flat(t, name, dtype, n, device):
+    """A contiguous tensor of n entries."""
+    if t.dtype is not dtype or t.device != device or t.numel() != n or not t.is_contiguous():
+        _check(t, name, dtype, device=device)
+        raise ValueError(f"{name} has {t.numel()} entries for {n} tokens")
 
 
 class RopeTable:
@@ -679,27 +698,25 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
     tensors, or given ones (q and k themselves: in place).  inverse=True turns
     back, which takes gradients of the outputs to gradients of the inputs.
     Returns (out_q, out_k), or out_q where k is None."""
-    dev, D = q.device, q.shape[-1]
-    T, qt, qh = _heads(q, "q", None, D, q.dtype, dev)
+    dev, dtype, D, hq = q.device, q.dtype, q.shape[-1], q.shape[-2]
+    T, qt, qh = _heads(q, "q", None, D, dtype, dev)
     dt = _dtype_code(q, "q")
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _, ot, oh = _heads(out_q, "out_q", q.shape[-2], D, q.dtype, dev, T)
+        out_q = torch.empty(q.shape, dtype=dtype, device=dev)
+    _, ot, oh = _heads(out_q, "out_q", hq, D, dtype, dev, T)
+    kp = okp = None
     kt = kh = okt = okh = hk = 0
     if k is not None:
         hk = k.shape[-2]
-        _, kt, kh = _heads(k, "k", hk, D, q.dtype, dev, T)
+        _, kt, kh = _heads(k, "k", hk, D, dtype, dev, T)
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        _, okt, okh = _heads(out_k, "out_k", hk, D, q.dtype, dev, T)
-    _check(positions, "positions", torch.int32, device=dev)
-    if positions.numel() != T:
-        raise ValueError(f"positions has {positions.numel()} entries for {T} tokens")
-    with _on(dev):
-        rc = lib().spec_rope(_ptr(q), q.shape[-2], qt, qh, _ptr(out_q), ot, oh, _ptr(k), hk, kt, kh,
-                             _ptr(out_k), okt, okh, dt, D, T, _ptr(positions), table._ref,
-                             int(inverse), _stream(None))
-    _raise(rc, "spec_rope")
+            out_k = torch.empty(k.shape, dtype=dtype, device=dev)
+        _, okt, okh = _heads(out_k, "out_k", hk, D, dtype, dev, T)
+        kp, okp = k.data_ptr(), out_k.data_ptr()
+    _flat(positions, "positions", torch.int32, T, dev)
+    _call((_LIB or lib()).spec_rope, "spec_rope", dev, q.data_ptr(), hq, qt, qh, out_q.data_ptr(), ot,
+          oh, kp, hk, kt, kh, okp, okt, okh, dt, D, T, positions.data_ptr(), table._ref,
+          1 if inverse else 0)
     return out_q if k is None else (out_q, out_k)
 
 
@@ -762,36 +779,32 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     `table` and `positions` the keys are rotated on the way, and q [...,
     q_heads, head_dim] into out_q (a new tensor by default), which is
     returned."""
-    dev, D = cache.device, cache.head_dim
-    T, kt, kh = _heads(k, "k", cache.heads, D, k.dtype, dev)
-    _, vt, vh = _heads(v, "v", cache.heads, D, k.dtype, dev, T)
+    dev, D, dtype = cache.device, cache.head_dim, k.dtype
+    T, kt, kh = _heads(k, "k", cache.heads, D, dtype, dev)
+    _, vt, vh = _heads(v, "v", cache.heads, D, dtype, dev, T)
     dt = _dtype_code(k, "k")
-    _check(slots, "slots", torch.int64, device=dev)
-    if slots.numel() != T:
-        raise ValueError(f"slots has {slots.numel()} entries for {T} tokens")
+    _flat(slots, "slots", torch.int64, T, dev)
     if (table is None) != (positions is None):
         raise ValueError("a rotation needs positions and a table")
-    if positions is not None:
-        _check(positions, "positions", torch.int32, device=dev)
-        if positions.numel() != T:
-            raise ValueError(f"positions has {positions.numel()} entries for {T} tokens")
+    pp = tp = qp = op = None
     qt = qh = ot = oh = hq = 0
+    if positions is not None:
+        _flat(positions, "positions", torch.int32, T, dev)
+        pp, tp = positions.data_ptr(), table._ref
     if q is not None:
         if table is None:
             raise ValueError("q is taken along only to be rotated")
         hq = q.shape[-2]
-        _, qt, qh = _heads(q, "q", hq, D, k.dtype, dev, T)
+        _, qt, qh = _heads(q, "q", hq, D, dtype, dev, T)
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _, ot, oh = _heads(out_q, "out_q", hq, D, k.dtype, dev, T)
+            out_q = torch.empty(q.shape, dtype=dtype, device=dev)
+        _, ot, oh = _heads(out_q, "out_q", hq, D, dtype, dev, T)
+        qp, op = q.data_ptr(), out_q.data_ptr()
     if dev_status is not None:
         _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    with _on(dev):
-        rc = lib().spec_kv_write(cache._ref, _ptr(k), kt, kh, _ptr(v), vt, vh, dt, T, _ptr(slots),
-                                 _ptr(positions), None if table is None else table._ref, _ptr(q),
-                                 hq, qt, qh, _ptr(out_q) if q is not None else None, ot, oh,
-                                 _ptr(dev_status), _stream(None))
-    _raise(rc, "spec_kv_write")
+    _call((_LIB or lib()).spec_kv_write, "spec_kv_write", dev, cache._ref, k.data_ptr(), kt, kh,
+          v.data_ptr(), vt, vh, dt, T, slots.data_ptr(), pp, tp, qp, hq, qt, qh, op, ot, oh,
+          _ptr(dev_status))
     return out_q if q is not None else None
 
 
@@ -802,20 +815,20 @@ def kv_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype | None = 
     head_dim] of `dtype` (the cache's own by default, bfloat16 for an 8-bit
     one); a slot outside the cache reads as zeros (spec_kv_read)."""
     dev = cache.device
-    _check(slots, "slots", torch.int64, device=dev)
+    _flat(slots, "slots", torch.int64, slots.numel(), dev)
     if dtype is None:
         dtype = torch.bfloat16 if cache.dtype == SPEC_E4M3 else cache.k.dtype
     shape = (*slots.shape, cache.heads, cache.head_dim)
     if out_k is None:
         out_k = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _check(out_k, "out_k", dtype, shape, dev)
     if out_v is None:
         out_v = torch.empty(shape, dtype=dtype, device=dev)
-    _check(out_k, "out_k", dtype, shape, dev)
-    _check(out_v, "out_v", dtype, shape, dev)
-    with _on(dev):
-        rc = lib().spec_kv_read(cache._ref, slots.numel(), _ptr(slots), _dtype_code(out_k, "dtype"),
-                                _ptr(out_k), _ptr(out_v), _stream(None))
-    _raise(rc, "spec_kv_read")
+    else:
+        _check(out_v, "out_v", dtype, shape, dev)
+    _call((_LIB or lib()).spec_kv_read, "spec_kv_read", dev, cache._ref, slots.numel(),
+          slots.data_ptr(), _dtype_code(out_k, "dtype"), out_k.data_ptr(), out_v.data_ptr())
     return out_k, out_v
 
 
@@ -844,24 +857,24 @@ def tree_plan(tree_parents: torch.Tensor, num_nodes: torch.Tensor, context_len: 
     if tree_parents.dim() != 2 or page_table.dim() != 2:
         raise ValueError("tree_parents must be [B, N] and page_table [B, max_pages]")
     B, N = tree_parents.shape
+    width = page_table.shape[1]
     dev = cache.device
-    _check(tree_parents, "tree_parents", torch.int32, device=dev)
+    _check(tree_parents, "tree_parents", torch.int32, None, dev)
     _check(num_nodes, "num_nodes", torch.int32, (B,), dev)
     _check(context_len, "context_len", torch.int32, (B,), dev)
-    _check(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    _check(page_table, "page_table", torch.int32, (B, width), dev)
     if dev_status is not None:
         _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    n = int(lib().spec_tree_plan_size(B))
+    L = _LIB or lib()
+    n = L.spec_tree_plan_size(B)
     buffer = torch.empty(n, dtype=torch.uint8, device=dev)
     positions = torch.empty((B, N), dtype=torch.int32, device=dev)
     masks = torch.empty((B, N), dtype=torch.int32, device=dev)
     slots = torch.empty((B, N), dtype=torch.int64, device=dev)
-    with _on(dev):
-        rc = lib().spec_tree_plan(_ptr(tree_parents), _ptr(num_nodes), _ptr(context_len),
-                                  _ptr(page_table), B, N, page_table.shape[1], cache.page_size,
-                                  cache.num_pages, _ptr(positions), _ptr(slots), _ptr(masks),
-                                  _ptr(buffer), n, _ptr(dev_status), _stream(None))
-    _raise(rc, "spec_tree_plan")
+    _call(L.spec_tree_plan, "spec_tree_plan", dev, tree_parents.data_ptr(), num_nodes.data_ptr(),
+          context_len.data_ptr(), page_table.data_ptr(), B, N, width, cache.page_size,
+          cache.num_pages, positions.data_ptr(), slots.data_ptr(), masks.data_ptr(),
+          buffer.data_ptr(), n, _ptr(dev_status))
     return TreePlan(positions, slots, masks, context_len, page_table, cache.page_size,
                     cache.num_pages, buffer, {})
 
@@ -901,21 +914,20 @@ def tree_attention(q: torch.Tensor, cache: KVCache, plan: TreePlan, *, scale: fl
         _check(lse, "lse", torch.float32, (B, N, Hq), dev)
     if dev_status is not None:
         _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    with _on(dev):
+    L = _LIB or lib()
+    if workspace is None:
+        workspace = plan.workspace.get((Hq, cache.heads, D))
         if workspace is None:
-            workspace = plan.workspace.get((Hq, cache.heads, D))
-            if workspace is None:
-                n = int(lib().spec_tree_attention_workspace_size(cache._ref, Hq))
-                if n == 0:
-                    raise ValueError(f"unsupported: {Hq} query heads over {cache.heads} of {D}")
-                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-                plan.workspace[(Hq, cache.heads, D)] = workspace
-        rc = lib().spec_tree_attention(
-            _ptr(q), st[0], st[1], st[2], dt, B, N, Hq, cache._ref, _ptr(plan.page_table),
-            plan.page_table.shape[1], _ptr(masks), _ptr(plan.buffer),
-            1.0 / math.sqrt(D) if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
-            workspace.numel(), _ptr(dev_status), _stream(None))
-    _raise(rc, "spec_tree_attention")
+            with torch.cuda.device(dev):
+                n = int(L.spec_tree_attention_workspace_size(cache._ref, Hq))
+            if n == 0:
+                raise ValueError(f"unsupported: {Hq} query heads over {cache.heads} of {D}")
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            plan.workspace[(Hq, cache.heads, D)] = workspace
+    _call(L.spec_tree_attention, "spec_tree_attention", dev, q.data_ptr(), st[0], st[1], st[2], dt, B,
+          N, Hq, cache._ref, plan.page_table.data_ptr(), plan.page_table.shape[1],
+          masks.data_ptr(), plan.buffer.data_ptr(), 1.0 / math.sqrt(D) if scale is None else scale,
+          out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _ptr(dev_status))
     return out
 
 
@@ -939,20 +951,17 @@ def kv_commit(caches: list, plan: TreePlan, last_node: torch.Tensor, *,
     if dev_status is not None:
         _check(dev_status, "dev_status", torch.int32, (1,), dev)
     for c in caches:
-        if (plan.page_size, plan.num_pages) != (c.page_size, c.num_pages) or c.device != dev:
+        if plan.page_size != c.page_size or plan.num_pages != c.num_pages or c.device != dev:
             raise ValueError("the plan was made for a cache of other pages")
-    with _on(dev):
-        st = _stream(None)
-        # the lengths are written once, by the last group of caches: it may be
-        # the plan's own context_len, which the earlier groups still read
-        scratch = new_context_len if len(caches) <= MAX_COMMIT_CACHES else torch.empty_like(new_context_len)
-        for i in range(0, len(caches), MAX_COMMIT_CACHES):
-            group = caches[i:i + MAX_COMMIT_CACHES]
-            arr = (_CCache * len(group))(*[c._c for c in group])
-            last = i + MAX_COMMIT_CACHES >= len(caches)
-            rc = lib().spec_kv_commit(ctypes.addressof(arr), len(group), _ptr(plan.masks),
-                                      _ptr(plan.slots), _ptr(last_node), _ptr(plan.context_len), B,
-                                      N, _ptr(new_context_len if last else scratch),
-                                      _ptr(dev_status), st)
-            _raise(rc, "spec_kv_commit")
+    fn = (_LIB or lib()).spec_kv_commit
+    # the lengths are written once, by the last group of caches: it may be the
+    # plan's own context_len, which the earlier groups still read
+    groups = [caches[i:i + MAX_COMMIT_CACHES] for i in range(0, len(caches), MAX_COMMIT_CACHES)]
+    scratch = torch.empty_like(new_context_len) if len(groups) > 1 else None
+    for i, group in enumerate(groups):
+        arr = group[0]._c if len(group) == 1 else (_CCache * len(group))(*[c._c for c in group])
+        to = new_context_len if i == len(groups) - 1 else scratch
+        _call(fn, "spec_kv_commit", dev, ctypes.addressof(arr), len(group), plan.masks.data_ptr(),
+              plan.slots.data_ptr(), last_node.data_ptr(), plan.context_len.data_ptr(), B, N,
+              to.data_ptr(), _ptr(dev_status))
     return new_context_len
