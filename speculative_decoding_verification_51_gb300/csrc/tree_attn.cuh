@@ -90,6 +90,19 @@ struct Lists {
 // on.  Call with the whole CTA; false (for all of it) where there is no share.
 __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Share& s) {
     const long long hr = (long long)A.Hkv * A.tiles_r;
+    if (A.B <= PLAN_WINDOW) {  // the window holds every request: one round of reads
+        if (int(threadIdx.x) <= A.B) {
+            w.tiles[threadIdx.x] = A.plan.tiles[threadIdx.x];
+            if (int(threadIdx.x) < A.B) {
+                w.ctx[threadIdx.x] = A.plan.ctx[threadIdx.x];
+                w.nodes[threadIdx.x] = A.plan.nodes[threadIdx.x];
+            }
+        }
+        if (threadIdx.x == 0) w.b0 = 0;
+        __syncthreads();
+        s = share_of(w.tiles[A.B] * hr);
+        return s.begin < s.end;
+    }
     const int last = A.plan.tiles[A.B];
     bool any = false;
     for (int i = threadIdx.x; i < A.B; i += blockDim.x) {
@@ -134,7 +147,7 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Lists& L,
     x.g = g;
     x.tiles = hi - lo;
     const long long r = g - lo * hr;
-    const int item = int(r / x.tiles);
+    const int item = r >> 31 ? int(r / x.tiles) : int(uint32_t(r) / uint32_t(x.tiles));
     x.t0 = int(r - (long long)item * x.tiles);
     x.t1 = int(min((long long)x.tiles, x.t0 + (s.end - g)));
     x.h = item / A.tiles_r;
@@ -233,57 +246,54 @@ __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, c
     if (!*flag) return;
     __threadfence();
     // A thread keeps one row (R divides the number of threads) and takes U groups
-    // of 4 channels at a time, up to 4 parts of each in flight; the lanes' rows lie
-    // side by side, so that every read is coalesced.
+    // of 4 channels at a time, 8 parts of each in flight; the lanes' rows lie side
+    // by side, so that every read is coalesced.
     const int r = tid % R, row = s.rt * R + r, parts = c1 - c0 + 1, step = threads / R;
     auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
     const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + r;
-    float ref = -INFINITY, total = 0.f;
-    for (int c = 0; c < parts; c += 4) {  // the running form of the total
-        float2 x[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) x[y] = c + y < parts ? __ldcg(ml + slot(c + y) * R) : make_float2(-INFINITY, 0.f);
-        const float to = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), ref);
-        const float at = to == -INFINITY ? 0.f : to;
-        total *= ex2_approx(ref - at);
-        ref = to;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) total = fmaf(ex2_approx(x[y].x - at), x[y].y, total);
-    }
-    const float at = ref == -INFINITY ? 0.f : ref;
     const int quads = width / 4;
     for (int q = tid / R; q < quads; q += U * step) {
-        float o[U][4] = {};
-        for (int c = 0; c < parts; c += 4) {
-            float4 x[4][U];
-            float f[4];
+        float ref = -INFINITY, total = 0.f, o[U][4] = {};
+        for (int c = 0; c < parts; c += 8) {  // running sums, by the running reference
+            float2 z[8];
+            float4 x[8][U];
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-                f[y] = c + y < parts ? __ldcg(reinterpret_cast<const float*>(ml + slot(c + y) * R)) : -INFINITY;
+            for (int y = 0; y < 8; ++y) {
+                z[y] = c + y < parts ? __ldcg(ml + slot(c + y) * R) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int z = 0; z < U; ++z)
-                    x[y][z] = c + y < parts && q + z * step < quads
-                                  ? __ldcg(reinterpret_cast<const float4*>(A.part_o) + (slot(c + y) * quads + q + z * step) * R + r)
+                for (int u = 0; u < U; ++u)
+                    x[y][u] = c + y < parts && q + u * step < quads
+                                  ? __ldcg(reinterpret_cast<const float4*>(A.part_o) + (slot(c + y) * quads + q + u * step) * R + r)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float to = ref;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float w = ex2_approx(f[y] - at);  // 0 for a part that is not there
+            for (int y = 0; y < 8; ++y) to = fmaxf(to, z[y].x);
+            const float at = to == -INFINITY ? 0.f : to, f = ex2_approx(ref - at);
+            ref = to;
+            total *= f;
 #pragma unroll
-                for (int z = 0; z < U; ++z) {
-                    o[z][0] = fmaf(w, x[y][z].x, o[z][0]);
-                    o[z][1] = fmaf(w, x[y][z].y, o[z][1]);
-                    o[z][2] = fmaf(w, x[y][z].z, o[z][2]);
-                    o[z][3] = fmaf(w, x[y][z].w, o[z][3]);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[u][e] *= f;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const float w = ex2_approx(z[y].x - at);  // 0 for a part that is not there
+                total = fmaf(w, z[y].y, total);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    o[u][0] = fmaf(w, x[y][u].x, o[u][0]);
+                    o[u][1] = fmaf(w, x[y][u].y, o[u][1]);
+                    o[u][2] = fmaf(w, x[y][u].z, o[u][2]);
+                    o[u][3] = fmaf(w, x[y][u].w, o[u][3]);
                 }
             }
         }
 #pragma unroll
-        for (int z = 0; z < U; ++z)
-            if (q + z * step < quads) put_row(A, s, row, (q + z * step) * 4, o[z], total);
+        for (int u = 0; u < U; ++u)
+            if (q + u * step < quads) put_row(A, s, row, (q + u * step) * 4, o[u], total);
+        if (q == 0) put_lse(A, s, row, ref, total);
     }
-    if (tid < R) put_lse(A, s, row, ref, total);
 }
 // the workspace slot of this CTA's part: the second where the item starts in
 // its share (join_parts)

@@ -47,7 +47,8 @@ struct RowsShape {
     static constexpr int BOXES = E4 ? (DP + 127) / 128 : (DP + 63) / 64;  // 128 bytes of a row each
     static constexpr int SIDE = BOXES * 2048;                             // K (or V) of a chunk
     static constexpr int STAGE = 2 * SIDE;
-    static constexpr int OB = R * (DP + 8) * 4;  // one warp's sums, at the join
+    // one warp's sums, at the join: pitches that spread 8 rows over all banks
+    static constexpr int OP = E4 ? DP + 16 : DP + 8, OB = R * OP * 4;
     static constexpr int FIXED = 4 * OB + R * (DP + 8) * 2 + (2 * WARPS + 4) * R * 4 + 4096;
     static constexpr int ROOM = (232448 - 1024 - int(sizeof(PlanWindow)) - FIXED) / (WARPS * STAGE);
     static constexpr int STAGES = ROOM < 6 ? ROOM : 6;
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                 const __grid_constant__ AttnArgs A) {
     using S = RowsShape<KIND, NK, MT>;
     constexpr bool E4 = S::E4, F16 = KIND != SPEC_BF16;
-    constexpr int DP = S::DP, R = S::R, OP = DP + 8, QP = DP + 8, AR_WARPS = S::WARPS, AR_THREADS = S::THREADS;
+    constexpr int DP = S::DP, R = S::R, OP = S::OP, QP = DP + 8, AR_WARPS = S::WARPS, AR_THREADS = S::THREADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -121,9 +122,34 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     if (threadIdx.x == 0) sm_flag[1] = 0;
     __syncwarp();
 
-    // ---- this warp's copies: the next chunk to load, a page index ahead
-    Segment ps = segment_at(A, L, share, share.begin, first);
-    int pc = ps.c0 + warp, page_at = 0, off_at = 0;
+    // ---- a segment's query rows: read while the segment before it is joined
+    constexpr int QV = R * DP / 8, QN = (QV + AR_THREADS - 1) / AR_THREADS;  // vectors of 8 channels
+    uint4 qn[QN];
+    uint32_t mask_n = 0;
+    auto fetch = [&](const Segment& s) {
+#pragma unroll
+        for (int k = 0; k < QN; ++k) {
+            const int i = threadIdx.x + k * AR_THREADS, r = i / (DP / 8), d = (i - r * (DP / 8)) * 8, row = s.rt * R + r;
+            const int v = row / A.G;
+            qn[k] = make_uint4(0, 0, 0, 0);
+            if (i < QV && row < A.rows && d < A.D && v < s.n)
+                qn[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
+                                                             (s.h * A.G + row - v * A.G) * A.qh + d));
+        }
+        const int row = s.rt * R + int(threadIdx.x), v = row / A.G;
+        mask_n = 0;
+        if (threadIdx.x < R && row < A.rows && v < s.n)
+            mask_n = __ldg(A.masks + (long long)s.b * A.N + v) & (0xffffffffu >> (32 - s.n));
+    };
+
+    const Segment ps0 = segment_at(A, L, share, share.begin, first);
+    fetch(ps0);  // before the copies, which would hold it up
+
+    // ---- this warp's copies.  Lane l holds the page of the l-th next chunk of the
+    // warp (one read every 32 chunks: read one by one, each would wait for L2 or
+    // HBM before its copies could start).
+    Segment ps = ps0;
+    int pc = ps.c0 + warp, page_at = 0, off_at = 0, pages = 0, ahead = 0;
     bool more = true;
     auto seek = [&]() {  // to the next chunk this warp has, if any
         while (pc >= ps.c1) {
@@ -134,10 +160,15 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
             }
             ps = segment_at(A, L, share, g, ps.b);
             pc = ps.c0 + warp;
+            ahead = 0;
         }
-        const int t = pc * 16, p = t / A.page;
-        off_at = t - p * A.page;
-        page_at = __ldg(A.table + (long long)ps.b * A.max_pages + p);
+        if ((ahead & 31) == 0) {
+            const int c = pc + lane * AR_WARPS;
+            pages = c < ps.c1 ? __ldg(A.table + (long long)ps.b * A.max_pages + c * 16 / A.page) : 0;
+        }
+        page_at = __shfl_sync(0xffffffffu, pages, ahead & 31);
+        ++ahead;
+        off_at = pc * 16 % A.page;
     };
     seek();
     uint32_t issued = 0, used = 0;
@@ -166,74 +197,59 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     for (int i = 0; i < S::STAGES; ++i) issue();
 
     bool dead = false;  // a copy did not arrive in time: no more waits, SPEC_BADBIT_TIMEOUT
-    int b_at = first;
-    for (long long g = share.begin; g < share.end;) {
-        const Segment s = segment_at(A, L, share, g, b_at);
-        b_at = s.b;
-        g += s.t1 - s.t0;
-
+    Segment s = ps0;
+    for (;;) {
         // ---- the query's rows to shared memory (e4m3: as f16, a power of two
         // a row bringing its largest value to [1, 2))
         if constexpr (E4) {
             for (int r = threadIdx.x; r < R; r += AR_THREADS) sm_qmax[r] = 0;
             __syncthreads();
-        }
-        constexpr int QV = R * DP / 8;  // vectors of 8 channels
-#pragma unroll 1
-        for (int pass = E4 ? 0 : 1; pass < 2; ++pass) {
-            for (int i = threadIdx.x; i < QV; i += AR_THREADS) {
-                const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8, row = s.rt * R + r;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                const int v = row / A.G;
-                if (row < A.rows && d < A.D && v < s.n)
-                    w = *reinterpret_cast<const uint4*>(
-                        static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
-                        (s.h * A.G + row - v * A.G) * A.qh + d);
-                if constexpr (!E4) {
-                    *reinterpret_cast<uint4*>(sm_q + r * QP + d) = w;
-                } else {
-                    float f[8];
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            auto pair = [&](uint32_t u) {
+                return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&u)) : make_float2(bf16_lo(u), bf16_hi(u));
+            };
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (A.q_f16) {
-                            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
-                            f[2 * e] = x.x;
-                            f[2 * e + 1] = x.y;
-                        } else {
-                            f[2 * e] = bf16_lo(u[e]);
-                            f[2 * e + 1] = bf16_hi(u[e]);
-                        }
-                    }
-                    if (pass == 0) {
-                        float m = 0.f;
+            for (int k = 0; k < QN; ++k) {
+                const int i = threadIdx.x + k * AR_THREADS;
+                const uint32_t u[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
+                float m = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[e]));
-                        atomicMax(&sm_qmax[r], __float_as_uint(m));
-                    } else {
-                        // 2^-e for the row's exponent e (its largest value >= 2^-126)
-                        const uint32_t ex = max(min(sm_qmax[r] >> 23, 253u), 1u);
-                        const float f2 = __uint_as_float((254u - ex) << 23);
-                        // channels d = 16 j + 4 t + e of a lane's K fragment go to
-                        // 2 t + e (e < 2) and 8 + 2 t + e - 2
-                        const int at = (d & ~15) + ((d & 8) ? 4 : 0);
-                        uint32_t* dst = reinterpret_cast<uint32_t*>(sm_q + r * QP + at);
-                        dst[0] = pack16<true>(f[0] * f2, f[1] * f2);
-                        dst[1] = pack16<true>(f[4] * f2, f[5] * f2);
-                        dst[4] = pack16<true>(f[2] * f2, f[3] * f2);
-                        dst[5] = pack16<true>(f[6] * f2, f[7] * f2);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = pair(u[e]);
+                    m = fmaxf(m, fmaxf(finite_abs(f.x), finite_abs(f.y)));
                 }
+                if (i < QV) atomicMax(&sm_qmax[i / (DP / 8)], __float_as_uint(m));
             }
-            if (pass == 0) __syncthreads();
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const int i = threadIdx.x + k * AR_THREADS, r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
+                if (i >= QV) break;
+                const uint32_t u[4] = {qn[k].x, qn[k].y, qn[k].z, qn[k].w};
+                // 2^-e for the row's exponent e (its largest value >= 2^-126)
+                const uint32_t ex = max(min(sm_qmax[r] >> 23, 253u), 1u);
+                const float f2 = __uint_as_float((254u - ex) << 23);
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = pair(u[e]);
+                    h[e] = pack16<true>(f.x * f2, f.y * f2);
+                }
+                // channels d = 16 j + 4 t + e of a lane's K fragment go to
+                // 2 t + e (e < 2) and 8 + 2 t + e - 2
+                uint32_t* dst = reinterpret_cast<uint32_t*>(sm_q + r * QP + (d & ~15) + ((d & 8) ? 4 : 0));
+                dst[0] = h[0];
+                dst[1] = h[2];
+                dst[4] = h[1];
+                dst[5] = h[3];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const int i = threadIdx.x + k * AR_THREADS, r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
+                if (i < QV) *reinterpret_cast<uint4*>(sm_q + r * QP + d) = qn[k];
+            }
         }
-        if (threadIdx.x < R) {
-            const int row = s.rt * R + threadIdx.x, v = row / A.G;
-            uint32_t m = 0;
-            if (row < A.rows && v < s.n)
-                m = A.masks[(long long)s.b * A.N + v] & (0xffffffffu >> (32 - s.n));
-            sm_mask[threadIdx.x] = m;
-        }
+        if (threadIdx.x < R) sm_mask[threadIdx.x] = mask_n;
         __syncthreads();
 
         // ---- this warp's chunks
@@ -499,6 +515,13 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
             issue();
         }
 
+        const long long next = s.g + (s.t1 - s.t0);
+        Segment after = s;
+        if (next < share.end) {
+            after = segment_at(A, L, share, next, s.b);
+            fetch(after);
+        }
+
         // ---- join the warps
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -527,10 +550,6 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
             sm_tot[threadIdx.x] = l;
         }
         float* ob = sm_o + (warp & 3) * R * OP;
-        auto col = [&](int n, int e) {
-            if constexpr (E4) return (n >> 1) * 16 + 4 * (lane & 3) + 2 * e + (n & 1);
-            else return n * 8 + 2 * (lane & 3) + e;
-        };
 #pragma unroll
         for (int half = AR_WARPS / 4 - 1; half >= 0; --half) {
             if ((warp >> 2) == half) {
@@ -543,14 +562,32 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
 #pragma unroll
                         for (int w = 0; w < AR_WARPS; ++w) mm = fmaxf(mm, sm_m[w * R + r]);
                         const float f = ref[m][x] == -INFINITY ? 0.f : ex2_approx(ref[m][x] - mm);
+                        float* z = ob + r * OP;
+                        const bool first_half = half == AR_WARPS / 4 - 1;
+                        if constexpr (E4) {  // accumulators 2 j and 2 j + 1: channels 16 j + 4 t + {0, 2}, {1, 3}
 #pragma unroll
-                        for (int n = 0; n < 2 * NK; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float* z = ob + r * OP + col(n, e);
-                                const float v = o[m][n][2 * x + e] * f;
-                                *z = half == AR_WARPS / 4 - 1 ? v : *z + v;
+                            for (int j = 0; j < NK; ++j) {
+                                float4* y = reinterpret_cast<float4*>(z + j * 16 + 4 * (lane & 3));
+                                float4 v = make_float4(o[m][2 * j][2 * x] * f, o[m][2 * j + 1][2 * x] * f,
+                                                       o[m][2 * j][2 * x + 1] * f, o[m][2 * j + 1][2 * x + 1] * f);
+                                if (!first_half) {
+                                    const float4 b = *y;
+                                    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+                                }
+                                *y = v;
                             }
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < 2 * NK; ++n) {
+                                float2* y = reinterpret_cast<float2*>(z + n * 8 + 2 * (lane & 3));
+                                float2 v = make_float2(o[m][n][2 * x] * f, o[m][n][2 * x + 1] * f);
+                                if (!first_half) {
+                                    const float2 b = *y;
+                                    v = make_float2(v.x + b.x, v.y + b.y);
+                                }
+                                *y = v;
+                            }
+                        }
                     }
             }
             __syncthreads();
@@ -589,7 +626,9 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
         }
         if (!whole) join_parts<2>(A, share, s, R, DP, sm_flag, threadIdx.x, AR_THREADS, 0);
         __syncthreads();
+        if (next >= share.end) break;
         if (threadIdx.x == 0) sm_flag[1] = 0;
+        s = after;
     }
 }
 
