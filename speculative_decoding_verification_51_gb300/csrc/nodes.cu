@@ -206,13 +206,13 @@ __global__ void __launch_bounds__(COMMIT_T) k_kv_commit(const __grid_constant__ 
         const int side = i >= per, j = side ? i - per : i;
         const int h = j / vecs, x = j - h * vecs;
         char* base = static_cast<char*>(side ? A.v[l] : A.k[l]) + h * A.c.head_stride * es + x * 16;
-        for (int r = 0; r < n; r += 4) {  // four rows in flight, stores in path order
-            uint4 w[4];
+        for (int r = 0; r < n; r += 8) {  // eight rows in flight, stores in path order
+            uint4 w[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 if (r + u < n) w[u] = *reinterpret_cast<const uint4*>(base + src[r + u] * es);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
                 if (r + u < n) *reinterpret_cast<uint4*>(base + dst[r + u] * es) = w[u];
         }
     }
@@ -220,7 +220,15 @@ __global__ void __launch_bounds__(COMMIT_T) k_kv_commit(const __grid_constant__ 
         for (int i = tid; i < 2 * A.c.heads; i += COMMIT_T) {
             const int side = i >= A.c.heads, h = side ? i - A.c.heads : i;
             uint8_t* base = (side ? A.vs[l] : A.ks[l]) + (long long)h * A.c.page;
-            for (int r = 0; r < n; ++r) base[sdst[r]] = base[ssrc[r]];
+            for (int r = 0; r < n; r += 8) {
+                uint8_t w[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (r + u < n) w[u] = base[ssrc[r + u]];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (r + u < n) base[sdst[r + u]] = w[u];
+            }
         }
 }
 

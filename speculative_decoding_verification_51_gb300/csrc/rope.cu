@@ -129,7 +129,8 @@ __device__ __forceinline__ void set2(Words<T, VEC>& x, int e, float a, float b) 
 }
 
 // T: element type of the tensors; VEC: elements of a vector; IP: lanes of a
-// token; E4: the cache is e4m3 (else of type T); PAIR: some item has two vectors.
+// token; E4: the cache is e4m3 (else of type T); PAIR: half layout (else
+// interleaved, or nothing turns).
 template <typename T, int VEC, int IP, bool E4, bool PAIR>
 __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant__ RotArgs A) {
     const int lane = threadIdx.x % IP;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
     // this lane's item of a head that turns, and of one that does not
     Place pt = {lane * VEC, 0, lane * VEC < A.D, false}, pp = pt;
     if (PAIR && (lane + IP) * VEC < A.D) pp.second = IP * VEC;
-    if (A.interleaved) {
+    if (!PAIR) {
         pt.turns = pt.off < 2 * hr;
     } else {
         const int r = hr / VEC;
@@ -155,14 +156,12 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
     float cs[NT], sn[NT];
     if (hr && pt.turns) {
         const int pos = __ldg(A.pos + t);
-        const int n = A.interleaved ? VEC / 2 : VEC;
 #pragma unroll
-        for (int e = 0; e < NT; ++e)
-            if (e < n) {
-                angle(__ldg(A.turns + lane * n + e), pos, cs[e], sn[e]);
-                cs[e] *= A.scale;
-                sn[e] *= A.scale * A.sign;
-            }
+        for (int e = 0; e < NT; ++e) {
+            angle(__ldg(A.turns + lane * NT + e), pos, cs[e], sn[e]);
+            cs[e] *= A.scale;
+            sn[e] *= A.scale * A.sign;
+        }
     }
 
     // heads [lo, hi) of one tensor: to `out`, or (bytes, scales) as e4m3
@@ -183,54 +182,77 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
 #pragma unroll
             for (int u = 0; u < UH; ++u) {
                 if (h + u >= hi) break;  // the same for the whole group
-                // elements 2 e and 2 e + 1 of the first vector and of the second
-                auto four = [&](int e, float (&f)[4]) {
-                    const float2 a2 = get2(x[u], e), b2 = PAIR ? get2(y[PAIR ? u : 0], e) : make_float2(0.f, 0.f);
-                    f[0] = a2.x;
-                    f[1] = a2.y;
-                    f[2] = b2.x;
-                    f[3] = b2.y;
-                    if (!p.turns) return;
-                    if (A.interleaved) {
-                        const float a = f[0], b = f[1];
-                        f[0] = a * cs[e] - b * sn[e];
-                        f[1] = a * sn[e] + b * cs[e];
-                    } else if (PAIR) {
+                float va[VEC], vb[PAIR ? VEC : 1];
 #pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int i = PAIR ? 2 * e + z : 0;
-                            const float a = f[z], b = f[2 + z];
-                            f[z] = a * cs[i] - b * sn[i];
-                            f[2 + z] = a * sn[i] + b * cs[i];
-                        }
+                for (int e = 0; e < VEC / 2; ++e) {
+                    const float2 a = get2(x[u], e);
+                    va[2 * e] = a.x;
+                    va[2 * e + 1] = a.y;
+                    if (PAIR) {
+                        const float2 b = get2(y[PAIR ? u : 0], e);
+                        vb[PAIR ? 2 * e : 0] = b.x;
+                        vb[PAIR ? 2 * e + 1 : 0] = b.y;
                     }
-                };
-                float f[4];
-                if (E4 && bytes) {
-                    float m = 0.f;
-                    if (p.on) {
+                }
+                if (p.turns) {
+                    if constexpr (PAIR) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const float a = va[e], b = vb[e];
+                            va[e] = a * cs[e] - b * sn[e];
+                            vb[e] = a * sn[e] + b * cs[e];
+                        }
+                    } else {
 #pragma unroll
                         for (int e = 0; e < VEC / 2; ++e) {
-                            four(e, f);
-                            m = fmaxf(m, fmaxf(finite_abs(f[0]), finite_abs(f[1])));
-                            if (PAIR && p.second) m = fmaxf(m, fmaxf(finite_abs(f[2]), finite_abs(f[3])));
+                            const float a = va[2 * e], b = va[2 * e + 1];
+                            va[2 * e] = a * cs[e] - b * sn[e];
+                            va[2 * e + 1] = a * sn[e] + b * cs[e];
                         }
                     }
+                }
+                if (E4 && bytes) {
+                    // (a maximum drops NaN, which converts to NaN; an infinity shows in it)
+                    auto widest = [&](auto&& size) {
+                        float m = 0.f;
+                        if (p.on) {
 #pragma unroll
-                    for (int o = IP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(gmask, m, o, IP));
+                            for (int e = 0; e < VEC; ++e) m = fmaxf(m, size(va[e]));
+                            if (PAIR && p.second) {
+#pragma unroll
+                                for (int e = 0; e < VEC; ++e) m = fmaxf(m, size(vb[PAIR ? e : 0]));
+                            }
+                        }
+#pragma unroll
+                        for (int o = IP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(gmask, m, o, IP));
+                        return m;
+                    };
+                    float m = widest([](float f) { return fabsf(f); });
+                    const bool odd = m == INFINITY;  // seldom: then finite values alone count
+                    if (odd) m = widest([](float f) { return finite_abs(f); });
                     const int ex = e4m3_exponent(m);
+                    const float down = exp2_int(-ex);
                     if (p.on) {
                         Words<uint8_t, VEC> a, b;
+                        auto pack = [&](auto&& two) {
 #pragma unroll
-                        for (int e = 0; e < VEC / 4; ++e) {
-                            float g[4];
-                            four(2 * e, f);
-                            four(2 * e + 1, g);
-                            a.w[e] = pack_e4m3x2(e4m3_scaled(f[0], ex), e4m3_scaled(f[1], ex)) |
-                                     uint32_t(pack_e4m3x2(e4m3_scaled(g[0], ex), e4m3_scaled(g[1], ex))) << 16;
-                            if (PAIR)
-                                b.w[e] = pack_e4m3x2(e4m3_scaled(f[2], ex), e4m3_scaled(f[3], ex)) |
-                                         uint32_t(pack_e4m3x2(e4m3_scaled(g[2], ex), e4m3_scaled(g[3], ex))) << 16;
+                            for (int e = 0; e < VEC / 4; ++e) {
+                                a.w[e] = two(va[4 * e] * down, va[4 * e + 1] * down) |
+                                         uint32_t(two(va[4 * e + 2] * down, va[4 * e + 3] * down)) << 16;
+                                if constexpr (PAIR)
+                                    b.w[e] = two(vb[4 * e] * down, vb[4 * e + 1] * down) |
+                                             uint32_t(two(vb[4 * e + 2] * down, vb[4 * e + 3] * down)) << 16;
+                                else b.w[e] = 0;
+                            }
+                        };
+                        if (__builtin_expect(odd, 0)) {
+                            pack([](float lo, float hi) { return pack_e4m3x2(lo, hi); });
+                        } else {
+                            pack([](float lo, float hi) {
+                                uint16_t r;
+                                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+                                return r;
+                            });
                         }
                         uint8_t* at = bytes + (h + u) * A.c.head_stride + p.off;
                         *reinterpret_cast<Words<uint8_t, VEC>*>(at) = a;
@@ -241,9 +263,9 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
                     Words<T, VEC> a, b;
 #pragma unroll
                     for (int e = 0; e < VEC / 2; ++e) {
-                        four(e, f);
-                        set2(a, e, f[0], f[1]);
-                        if (PAIR) set2(b, e, f[2], f[3]);
+                        set2(a, e, va[2 * e], va[2 * e + 1]);
+                        if constexpr (PAIR) set2(b, e, vb[2 * e], vb[2 * e + 1]);
+                        else set2(b, e, 0.f, 0.f);
                     }
                     T* at = out + (h + u) * oh + p.off;
                     *reinterpret_cast<Words<T, VEC>*>(at) = a;
@@ -333,54 +355,53 @@ __global__ void __launch_bounds__(ROT_THREADS) k_rotate_any(const __grid_constan
     }
 }
 
-// Rows of T slots: one thread per 8 channels of a (token, head).  I: the type
+// Rows of T slots: one thread per 16 bytes of a (token, head)'s row.  I: the type
 // of the indexes (32 bits where they are enough: a division of 64 costs more than
 // the copy).
 template <typename C, typename T, typename I>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ CacheView c, long long T_,
                                                  const long long* slots, T* out_k, T* out_v) {
-    const I vecs = c.D / 8, heads = c.heads, n = I(T_) * heads * vecs;
+    constexpr int VEC = 16 / sizeof(C);
+    const I vecs = c.D / VEC, heads = c.heads, n = I(T_) * heads * vecs;
     for (I i = blockIdx.x * I(256) + threadIdx.x; i < n; i += gridDim.x * I(256)) {
         const I th = i / vecs, t = th / heads;
-        const int d = int(i - th * vecs) * 8, h = int(th - t * heads);
+        const int d = int(i - th * vecs) * VEC, h = int(th - t * heads);
         const long long slot = slots[t];
-        Vec<T, 8> ok, ov;
+        Words<C, VEC> k, v;
+        float fk = 1.f, fv = 1.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ok.e[e] = ov.e[e] = from_f32<T>(0.f);
+        for (int e = 0; e < 4; ++e) k.w[e] = v.w[e] = 0;
         if (slot >= 0 && slot < c.slots) {
             const long long p = sizeof(I) == 4 ? (long long)(uint32_t(slot) / uint32_t(c.page)) : slot / c.page;
             const int o = int(slot - p * c.page);
             const long long at = p * c.page_stride + h * c.head_stride + o * c.token_stride + d;
+            k = *reinterpret_cast<const Words<C, VEC>*>(static_cast<const C*>(c.k) + at);
+            v = *reinterpret_cast<const Words<C, VEC>*>(static_cast<const C*>(c.v) + at);
             if constexpr (sizeof(C) == 1) {
                 const long long sr = (p * c.heads + h) * c.page + o;
-                const float fk = exp2_int(min(max(int(c.ks[sr]), 1), 253) - 127),
-                            fv = exp2_int(min(max(int(c.vs[sr]), 1), 253) - 127);
-                const Vec<uint16_t, 4> k = load_vec<uint16_t, 4>(
-                    reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(c.k) + at));
-                const Vec<uint16_t, 4> v = load_vec<uint16_t, 4>(
-                    reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(c.v) + at));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t wk = e4m3x2_to_f16x2(k.e[e]), wv = e4m3x2_to_f16x2(v.e[e]);
-                    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&wk));
-                    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&wv));
-                    ok.e[2 * e] = from_f32<T>(a.x * fk);
-                    ok.e[2 * e + 1] = from_f32<T>(a.y * fk);
-                    ov.e[2 * e] = from_f32<T>(b.x * fv);
-                    ov.e[2 * e + 1] = from_f32<T>(b.y * fv);
-                }
-            } else {
-                const Vec<C, 8> k = load_vec<C, 8>(static_cast<const C*>(c.k) + at);
-                const Vec<C, 8> v = load_vec<C, 8>(static_cast<const C*>(c.v) + at);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ok.e[e] = from_f32<T>(to_f32(k.e[e]));
-                    ov.e[e] = from_f32<T>(to_f32(v.e[e]));
-                }
+                fk = exp2_int(min(max(int(c.ks[sr]), 1), 253) - 127);
+                fv = exp2_int(min(max(int(c.vs[sr]), 1), 253) - 127);
             }
         }
-        store_vec<T, 8>(out_k + (long long)i * 8, ok);
-        store_vec<T, 8>(out_v + (long long)i * 8, ov);
+        auto write = [&](const Words<C, VEC>& x, float f, T* out) {
+            Words<T, VEC> w;
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) {
+                float2 a;
+                if constexpr (sizeof(C) == 1) {
+                    const uint32_t b = e4m3x2_to_f16x2(uint16_t(x.w[e / 2] >> (16 * (e & 1))));
+                    a = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                    a.x *= f;
+                    a.y *= f;
+                } else {
+                    a = get2(x, e);
+                }
+                set2(w, e, a.x, a.y);
+            }
+            *reinterpret_cast<Words<T, VEC>*>(out + (long long)i * VEC) = w;
+        };
+        write(k, fk, out_k);
+        write(v, fv, out_v);
     }
 }
 
@@ -397,14 +418,17 @@ cudaError_t launch_rotate(RotArgs A, cudaStream_t st) {
     const int H = A.q.n + A.k.n + A.v.n, sms = sm_count();
     if (sms <= 0) return cudaErrorUnknown;
     // A group takes all heads of its token, so that sines and cosines are computed
-    // once, where that leaves every SM 1536 lanes; with fewer tokens a share of the
-    // heads, four at least (whose loads are in flight together), and single heads
-    // where even that leaves SMs without work.
-    int shares = 1;
+    // once, where that leaves every SM 3072 lanes (four times what it holds); with
+    // fewer tokens a share of the heads, twice as many as have their loads in flight
+    // together (UH) while that leaves every SM 768 lanes, else UH, as where nothing
+    // turns, and single heads where even that leaves SMs without work.
+    constexpr int UH = 128 / (VEC * int(sizeof(T)) * (PAIR ? 2 : 1));
     const long long lanes = A.T * ip;
-    while (shares * 4 < H && lanes * shares < 1536ll * sms) ++shares;
-    if (shares * 4 >= H && lanes * shares < 256ll * sms) shares = H;
-    A.share = (H + shares - 1) / shares;
+    int share = A.half_rot ? (H + UH - 1) / UH * UH : UH;
+    while (share > 2 * UH && lanes * ((H + share - 1) / share) < 3072ll * sms) share -= UH;
+    while (share > UH && lanes * ((H + share - 1) / share) < 768ll * sms) share -= UH;
+    if (share == UH && lanes * ((H + UH - 1) / UH) < 256ll * sms) share = 1;
+    A.share = share;
     const long long gx = (A.T + ROT_THREADS / ip - 1) / (ROT_THREADS / ip);
     if (gx > 0x7fffffffll || (H + A.share - 1) / A.share > 65535) return cudaErrorInvalidValue;
     const dim3 grid(unsigned(gx), unsigned((H + A.share - 1) / A.share));
@@ -417,7 +441,7 @@ cudaError_t launch_rotate(RotArgs A, cudaStream_t st) {
 
 template <typename T, bool E4>
 cudaError_t launch_rotate_vec(const RotArgs& A, cudaStream_t st) {
-    // vectors of 8 elements or of 4, where every offset of the call is a
+    // vectors of 16 elements, 8 or 4, where every offset of the call is a
     // multiple of that; else one value at a time
     auto ok = [&](int vec) {
         const size_t a = std::min<size_t>(16, vec * sizeof(T));
@@ -430,6 +454,8 @@ cudaError_t launch_rotate_vec(const RotArgs& A, cudaStream_t st) {
         return side(A.q, true) && side(A.k, !A.slots) && side(A.v, false);
     };
     const bool pair = A.half_rot && !A.interleaved;
+    if constexpr (E4 && sizeof(T) == 2)  // bytes then go out 16 at a time too
+        if (!pair && ok(16)) return launch_rotate<T, 16, E4, false>(A, st);
     if (ok(8)) return pair ? launch_rotate<T, 8, E4, true>(A, st) : launch_rotate<T, 8, E4, false>(A, st);
     if (ok(4)) return pair ? launch_rotate<T, 4, E4, true>(A, st) : launch_rotate<T, 4, E4, false>(A, st);
     const long long warps = A.T * (A.q.n + A.k.n + A.v.n), grid = (warps + ROT_THREADS / 32 - 1) / (ROT_THREADS / 32);
@@ -578,7 +604,7 @@ namespace {
 template <typename C, typename T>
 cudaError_t launch_read_to(const CacheView& c, int64_t T_, const int64_t* slots, void* out_k, void* out_v,
                            cudaStream_t st) {
-    const long long n = T_ * c.heads * (c.D / 8);
+    const long long n = T_ * c.heads * (c.D / (16 / int(sizeof(C))));
     const unsigned grid = unsigned(std::min<long long>((n + 255) / 256, 1ll << 22));
     const long long* s = reinterpret_cast<const long long*>(slots);
     T *k = static_cast<T*>(out_k), *v = static_cast<T*>(out_v);
