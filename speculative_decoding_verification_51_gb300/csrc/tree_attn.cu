@@ -52,8 +52,9 @@ spec_status cache_map(CUtensorMap* map, const spec_kv_cache& c, void* base, int 
 
 constexpr int MAX_R = 128;  // rows of the largest tile
 
-// channels of a row as the kernels lay them out
-int width_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
+// channels of a part's row in the workspace, the most that a kernel lays out for D
+// (k_attn_tiles 64 or 128, k_attn_rows 64, 96, 128 or 256)
+int width_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // The parts that k_attn_tiles left: CTA (c, y) joins the item that starts in CTA
 // c's share and ends in another's, its y-th share of the channels.  One row a
