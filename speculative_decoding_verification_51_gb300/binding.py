@@ -4,13 +4,14 @@ Argument marshalling only: tensors are checked for device, dtype, shape and
 contiguity, their device pointers and the current CUDA stream are passed to
 the library, and a non-OK status raises.  Every step of verification runs in
 the library's kernels; there is no fallback.  torch is used for allocation
-(outputs, workspace) and for the stream handle.
+(outputs, workspace) and for the stream handle.  The operators around the
+verification do the same from C++ (csrc/torch_ops.cpp).
 """
 from __future__ import annotations
 
 import ctypes
-import functools
-import math
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -35,6 +36,7 @@ N_MARKS = 6  # events a profiled call records
 
 _LOCK = threading.Lock()
 _LIB = None
+_OPS = None
 
 
 class SpecVerifyError(RuntimeError):
@@ -556,8 +558,6 @@ def spec_verify_lmhead(hidden: torch.Tensor, lm_head: torch.Tensor, draft_probs:
 _DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
-MAX_NODES = 32
-MAX_COMMIT_CACHES = 64
 
 
 class _CCache(ctypes.Structure):
@@ -573,92 +573,33 @@ class _CTable(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
-def _dtype_code(t, name):
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return code
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(index: int) -> int:
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    # the same handle without a Stream object around it (3 us a call on the
-    # machine's Arm cores, of the 25 that a small operator took)
-    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
-
-
-def _call(fn, what: str, device: torch.device, *args) -> None:
-    """fn(*args, stream) with `device` current, on its current stream."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _raw_stream(index))
-    if rc != SPEC_OK:
-        raise SpecVerifyError(rc, what)
-
-
-def _streamed(fn):
-    """A call with stream=s runs with s current, so that what it allocates
-    (outputs, workspaces) belongs to the stream that its kernels run on."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+def _ops():
+    """The module that calls the library with torch tensors (csrc/torch_ops.cpp)."""
+    global _OPS
+    lib()  # raises if nothing has been built
+    with _LOCK:
+        if _OPS is None:
+            path = _build.ops_path()
+            if not os.path.exists(path):
+                raise RuntimeError(
+                    f"spec_verify torch module missing ({path}); build it with "
+                    "`python -m speculative_decoding_verification_51_gb300.build`")
+            loader = importlib.machinery.ExtensionFileLoader("specverify_torch", path)
+            spec = importlib.util.spec_from_file_location("specverify_torch", path, loader=loader)
+            mod = importlib.util.module_from_spec(spec)
+            loader.exec_module(mod)
+            mod.error_class(SpecVerifyError)
+            _OPS = mod
+        return _OPS
 
 
 def _raise(rc, what):
     if rc != SPEC_OK:
         raise SpecVerifyError(rc, what)
-
-
-def _heads(t, name, heads, D, dtype, device, tokens=None):
-    """[..., heads, D] as (tokens, token stride, head stride): the leading
-    dimensions must be one run of tokens."""
-    sh = t.shape
-    if len(sh) == 3 and sh[2] == D and t.dtype is dtype and t.device == device and \
-            (heads is None or sh[1] == heads) and (tokens is None or sh[0] == tokens):
-        st = t.stride()
-        if st[2] == 1:
-            return sh[0], st[0], st[1]
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() < 3 or sh[-1] != D or (heads is not None and sh[-2] != heads):
-        raise ValueError(f"{name} must be [tokens, {heads if heads is not None else 'heads'}, {D}], "
-                         f"got {tuple(sh)}")
-    st = t.stride()
-    if sh[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"the channels of {name} must be contiguous")
-    n, step = sh[-3], st[-3]
-    for i in range(len(sh) - 4, -1, -1):
-        if sh[i] != 1 and n != 1 and st[i] != n * step:
-            raise ValueError(f"the leading dimensions of {name} must be one run of tokens")
-        if n == 1:
-            step = st[i]
-        n *= sh[i]
-    if tokens is not None and n != tokens:
-        raise ValueError(f"{name} has {n} tokens, expected {tokens}")
-    return n, step, st[-2]
-
-
-def _flat(t, name, dtype, n, device):
-    """A contiguous tensor of n entries."""
-    if t.dtype is not dtype or t.device != device or t.numel() != n or not t.is_contiguous():
-        _check(t, name, dtype, device=device)
-        raise ValueError(f"{name} has {t.numel()} entries for {n} tokens")
 
 
 class RopeTable:
@@ -689,7 +630,6 @@ def rope_table(rot: int, *, base: float = 10000.0, layout: str = "half", scaling
     return RopeTable(turns.to(device), layout, scale.value)
 
 
-@_streamed
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: RopeTable, *,
          out_q: torch.Tensor | None = None, out_k: torch.Tensor | None = None,
          inverse: bool = False, stream=None):
@@ -698,26 +638,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
     tensors, or given ones (q and k themselves: in place).  inverse=True turns
     back, which takes gradients of the outputs to gradients of the inputs.
     Returns (out_q, out_k), or out_q where k is None."""
-    dev, dtype, D, hq = q.device, q.dtype, q.shape[-1], q.shape[-2]
-    T, qt, qh = _heads(q, "q", None, D, dtype, dev)
-    dt = _dtype_code(q, "q")
-    if out_q is None:
-        out_q = torch.empty(q.shape, dtype=dtype, device=dev)
-    _, ot, oh = _heads(out_q, "out_q", hq, D, dtype, dev, T)
-    kp = okp = None
-    kt = kh = okt = okh = hk = 0
-    if k is not None:
-        hk = k.shape[-2]
-        _, kt, kh = _heads(k, "k", hk, D, dtype, dev, T)
-        if out_k is None:
-            out_k = torch.empty(k.shape, dtype=dtype, device=dev)
-        _, okt, okh = _heads(out_k, "out_k", hk, D, dtype, dev, T)
-        kp, okp = k.data_ptr(), out_k.data_ptr()
-    _flat(positions, "positions", torch.int32, T, dev)
-    _call((_LIB or lib()).spec_rope, "spec_rope", dev, q.data_ptr(), hq, qt, qh, out_q.data_ptr(), ot,
-          oh, kp, hk, kt, kh, okp, okt, okh, dt, D, T, positions.data_ptr(), table._ref,
-          1 if inverse else 0)
-    return out_q if k is None else (out_q, out_k)
+    return (_OPS or _ops()).rope(q, k, positions, table, out_q, out_k, inverse, stream)
 
 
 class KVCache:
@@ -769,7 +690,6 @@ def new_kv_cache(num_pages: int, page_size: int, heads: int, head_dim: int, *,
     return KVCache(k, v, *sc)
 
 
-@_streamed
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
              positions: torch.Tensor | None = None, table: RopeTable | None = None,
              q: torch.Tensor | None = None, out_q: torch.Tensor | None = None,
@@ -779,57 +699,15 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     `table` and `positions` the keys are rotated on the way, and q [...,
     q_heads, head_dim] into out_q (a new tensor by default), which is
     returned."""
-    dev, D, dtype = cache.device, cache.head_dim, k.dtype
-    T, kt, kh = _heads(k, "k", cache.heads, D, dtype, dev)
-    _, vt, vh = _heads(v, "v", cache.heads, D, dtype, dev, T)
-    dt = _dtype_code(k, "k")
-    _flat(slots, "slots", torch.int64, T, dev)
-    if (table is None) != (positions is None):
-        raise ValueError("a rotation needs positions and a table")
-    pp = tp = qp = op = None
-    qt = qh = ot = oh = hq = 0
-    if positions is not None:
-        _flat(positions, "positions", torch.int32, T, dev)
-        pp, tp = positions.data_ptr(), table._ref
-    if q is not None:
-        if table is None:
-            raise ValueError("q is taken along only to be rotated")
-        hq = q.shape[-2]
-        _, qt, qh = _heads(q, "q", hq, D, dtype, dev, T)
-        if out_q is None:
-            out_q = torch.empty(q.shape, dtype=dtype, device=dev)
-        _, ot, oh = _heads(out_q, "out_q", hq, D, dtype, dev, T)
-        qp, op = q.data_ptr(), out_q.data_ptr()
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    _call((_LIB or lib()).spec_kv_write, "spec_kv_write", dev, cache._ref, k.data_ptr(), kt, kh,
-          v.data_ptr(), vt, vh, dt, T, slots.data_ptr(), pp, tp, qp, hq, qt, qh, op, ot, oh,
-          _ptr(dev_status))
-    return out_q if q is not None else None
+    return (_OPS or _ops()).kv_write(cache, k, v, slots, positions, table, q, out_q, dev_status, stream)
 
 
-@_streamed
 def kv_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype | None = None,
             out_k: torch.Tensor | None = None, out_v: torch.Tensor | None = None, stream=None):
     """The rows of `slots` (int64, any shape) as (k, v) [*slots.shape, heads,
     head_dim] of `dtype` (the cache's own by default, bfloat16 for an 8-bit
     one); a slot outside the cache reads as zeros (spec_kv_read)."""
-    dev = cache.device
-    _flat(slots, "slots", torch.int64, slots.numel(), dev)
-    if dtype is None:
-        dtype = torch.bfloat16 if cache.dtype == SPEC_E4M3 else cache.k.dtype
-    shape = (*slots.shape, cache.heads, cache.head_dim)
-    if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=dev)
-    else:
-        _check(out_k, "out_k", dtype, shape, dev)
-    if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=dev)
-    else:
-        _check(out_v, "out_v", dtype, shape, dev)
-    _call((_LIB or lib()).spec_kv_read, "spec_kv_read", dev, cache._ref, slots.numel(),
-          slots.data_ptr(), _dtype_code(out_k, "dtype"), out_k.data_ptr(), out_v.data_ptr())
-    return out_k, out_v
+    return (_OPS or _ops()).kv_read(cache, slots, dtype, out_k, out_v, stream)
 
 
 @dataclass
@@ -844,42 +722,21 @@ class TreePlan:
     page_size: int
     num_pages: int
     buffer: torch.Tensor       # the division of the attention's work
-    workspace: dict            # of tree_attention, by (device, bytes)
+    workspace: dict            # of tree_attention, by (stream, heads, head_dim)
 
 
-@_streamed
 def tree_plan(tree_parents: torch.Tensor, num_nodes: torch.Tensor, context_len: torch.Tensor,
               page_table: torch.Tensor, cache: KVCache, *, dev_status: torch.Tensor | None = None,
               stream=None) -> TreePlan:
     """Positions, cache slots and ancestor masks of the nodes [B, N] that
     follow each request's context (spec_tree_plan); `cache` gives the pages'
     size and number."""
-    if tree_parents.dim() != 2 or page_table.dim() != 2:
-        raise ValueError("tree_parents must be [B, N] and page_table [B, max_pages]")
-    B, N = tree_parents.shape
-    width = page_table.shape[1]
-    dev = cache.device
-    _check(tree_parents, "tree_parents", torch.int32, None, dev)
-    _check(num_nodes, "num_nodes", torch.int32, (B,), dev)
-    _check(context_len, "context_len", torch.int32, (B,), dev)
-    _check(page_table, "page_table", torch.int32, (B, width), dev)
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    L = _LIB or lib()
-    n = L.spec_tree_plan_size(B)
-    buffer = torch.empty(n, dtype=torch.uint8, device=dev)
-    positions = torch.empty((B, N), dtype=torch.int32, device=dev)
-    masks = torch.empty((B, N), dtype=torch.int32, device=dev)
-    slots = torch.empty((B, N), dtype=torch.int64, device=dev)
-    _call(L.spec_tree_plan, "spec_tree_plan", dev, tree_parents.data_ptr(), num_nodes.data_ptr(),
-          context_len.data_ptr(), page_table.data_ptr(), B, N, width, cache.page_size,
-          cache.num_pages, positions.data_ptr(), slots.data_ptr(), masks.data_ptr(),
-          buffer.data_ptr(), n, _ptr(dev_status))
+    positions, slots, masks, buffer = (_OPS or _ops()).tree_plan(
+        tree_parents, num_nodes, context_len, page_table, cache, dev_status, stream)
     return TreePlan(positions, slots, masks, context_len, page_table, cache.page_size,
                     cache.num_pages, buffer, {})
 
 
-@_streamed
 def tree_attention(q: torch.Tensor, cache: KVCache, plan: TreePlan, *, scale: float | None = None,
                    masks: torch.Tensor | None = None, out: torch.Tensor | None = None,
                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -888,50 +745,10 @@ def tree_attention(q: torch.Tensor, cache: KVCache, plan: TreePlan, *, scale: fl
     cache (spec_tree_attention).  scale: 1 / sqrt(head_dim) by default; masks
     [B, N] int32: the plan's by default; lse [B, N, q_heads] float32: written
     where given.  The workspace is kept with the plan unless one is given."""
-    if q.dim() != 4 or q.shape[3] != cache.head_dim:
-        raise ValueError("q must be [B, N, q_heads, head_dim]")
-    B, N, Hq, D = q.shape
-    dev = cache.device
-    if q.device != dev:
-        raise ValueError(f"q is on {q.device}, expected {dev}")
-    st = q.stride()
-    if st[3] != 1:
-        raise ValueError("the channels of q must be contiguous")
-    if plan.positions.shape != (B, N):
-        raise ValueError(f"the plan is for {tuple(plan.positions.shape)}, q for {(B, N)}")
-    if (plan.page_size, plan.num_pages) != (cache.page_size, cache.num_pages):
-        raise ValueError("the plan was made for a cache of other pages")
-    dt = _dtype_code(q, "q")
-    if masks is None:
-        masks = plan.masks
-    else:
-        _check(masks, "masks", torch.int32, (B, N), dev)
-    if out is None:
-        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
-    else:
-        _check(out, "out", q.dtype, (B, N, Hq, D), dev)
-    if lse is not None:
-        _check(lse, "lse", torch.float32, (B, N, Hq), dev)
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    L = _LIB or lib()
-    if workspace is None:
-        workspace = plan.workspace.get((Hq, cache.heads, D))
-        if workspace is None:
-            with torch.cuda.device(dev):
-                n = int(L.spec_tree_attention_workspace_size(cache._ref, Hq))
-            if n == 0:
-                raise ValueError(f"unsupported: {Hq} query heads over {cache.heads} of {D}")
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-            plan.workspace[(Hq, cache.heads, D)] = workspace
-    _call(L.spec_tree_attention, "spec_tree_attention", dev, q.data_ptr(), st[0], st[1], st[2], dt, B,
-          N, Hq, cache._ref, plan.page_table.data_ptr(), plan.page_table.shape[1],
-          masks.data_ptr(), plan.buffer.data_ptr(), 1.0 / math.sqrt(D) if scale is None else scale,
-          out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _ptr(dev_status))
-    return out
+    return (_OPS or _ops()).tree_attention(q, cache, plan, scale, masks, out, lse, workspace, dev_status,
+                                           stream)
 
 
-@_streamed
 def kv_commit(caches: list, plan: TreePlan, last_node: torch.Tensor, *,
               new_context_len: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
@@ -940,28 +757,4 @@ def kv_commit(caches: list, plan: TreePlan, last_node: torch.Tensor, *,
     context lengths (spec_kv_commit).  last_node: spec_verify_tree's third
     result, or spec_verify's second for a chain.  new_context_len may be the
     plan's context_len itself."""
-    B, N = plan.positions.shape
-    if not caches:
-        raise ValueError("no caches")
-    dev = caches[0].device
-    _check(last_node, "last_node", torch.int32, (B,), dev)
-    if new_context_len is None:
-        new_context_len = torch.empty((B,), dtype=torch.int32, device=dev)
-    _check(new_context_len, "new_context_len", torch.int32, (B,), dev)
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, (1,), dev)
-    for c in caches:
-        if plan.page_size != c.page_size or plan.num_pages != c.num_pages or c.device != dev:
-            raise ValueError("the plan was made for a cache of other pages")
-    fn = (_LIB or lib()).spec_kv_commit
-    # the lengths are written once, by the last group of caches: it may be the
-    # plan's own context_len, which the earlier groups still read
-    groups = [caches[i:i + MAX_COMMIT_CACHES] for i in range(0, len(caches), MAX_COMMIT_CACHES)]
-    scratch = torch.empty_like(new_context_len) if len(groups) > 1 else None
-    for i, group in enumerate(groups):
-        arr = group[0]._c if len(group) == 1 else (_CCache * len(group))(*[c._c for c in group])
-        to = new_context_len if i == len(groups) - 1 else scratch
-        _call(fn, "spec_kv_commit", dev, ctypes.addressof(arr), len(group), plan.masks.data_ptr(),
-              plan.slots.data_ptr(), last_node.data_ptr(), plan.context_len.data_ptr(), B, N,
-              to.data_ptr(), _ptr(dev_status))
-    return new_context_len
+    return (_OPS or _ops()).kv_commit(caches, plan, last_node, new_context_len, dev_status, stream)

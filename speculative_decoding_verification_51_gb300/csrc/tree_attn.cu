@@ -197,6 +197,7 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.D = cache->head_dim;
     A.page = cache->page_size;
     A.max_pages = max_pages;
+    A.num_pages = cache->num_pages;
     A.rows = N * A.G;
     A.c = scale * 1.4426950408889634f;
     A.q_f16 = dtype == SPEC_F16;

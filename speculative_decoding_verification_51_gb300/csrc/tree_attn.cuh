@@ -29,7 +29,7 @@ struct AttnArgs {
     const uint8_t* ks;
     const uint8_t* vs;
     long long v_page, v_head, v_token;
-    int B, N, Hq, Hkv, G, D, page, max_pages;
+    int B, N, Hq, Hkv, G, D, page, max_pages, num_pages;
     int rows, tiles_r;  // rows of a (request, key head), row tiles of them
     int box;            // tokens of one copy (k_attn_tiles)
     float c;            // scale * log2(e): scores are exponents of two
@@ -47,6 +47,12 @@ struct Segment {
     int ctx, n;
     long long g;       // the piece's first tile in the list of all
 };
+
+// A page of the table, which spec_tree_plan found to be in the cache; one that was
+// changed since then does not lead out of it.
+__device__ __forceinline__ int page_in(const AttnArgs& A, int p) {
+    return int(min(unsigned(p), unsigned(A.num_pages - 1)));
+}
 
 struct Share {
     long long total, begin, end;
@@ -183,7 +189,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // head h, channel d), or 0 where it is finite.
 template <int KIND>
 __device__ __forceinline__ float not_finite_v(const AttnArgs& A, int b, int h, int t, int d) {
-    const int p = A.table[(long long)b * A.max_pages + t / A.page];
+    const int p = page_in(A, A.table[(long long)b * A.max_pages + t / A.page]);
     const long long at = p * A.v_page + h * A.v_head + (t % A.page) * A.v_token + d;
     float x;
     if constexpr (KIND == SPEC_E4M3) {

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 if (t >= s.t1 || chunk >= boxes || tok >= len) return -1;
                 const int p = tok / A.page;
                 off = tok - p * A.page;
-                return __ldg(table + p);
+                return page_in(A, __ldg(table + p));
             };
             int off = 0, page = page_of(s.t0, off);
             for (int t = s.t0; t < s.t1; ++t, ++i) {
