@@ -45,6 +45,7 @@ __device__ __forceinline__ bool length_ok(const PlanArgs& A, int ctx, int n) {
 }
 
 __global__ void __launch_bounds__(PLAN_T) k_tree_plan(const __grid_constant__ PlanArgs A) {
+    begin_after_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x == 0) {
         __shared__ int sums[PLAN_T / 32];
@@ -153,6 +154,7 @@ struct CommitArgs {
 constexpr int COMMIT_T = 128;
 
 __global__ void __launch_bounds__(COMMIT_T) k_kv_commit(const __grid_constant__ CommitArgs A) {
+    begin_after_previous();
     const int b = blockIdx.x, l = blockIdx.y, tid = threadIdx.x;
     const int last = A.last[b];
     const long long* slots = A.slots + (long long)b * A.N;
@@ -277,8 +279,7 @@ spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes
     A.status = dev_status;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dev_status && cudaMemsetAsync(dev_status, 0, 4, st) != cudaSuccess) return SPEC_ERR_CUDA;
-    k_tree_plan<<<unsigned(B) + 1, PLAN_T, 0, st>>>(A);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_behind(k_tree_plan, dim3(unsigned(B) + 1), PLAN_T, 0, st, A) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status spec_kv_commit(const spec_kv_cache* caches, int num_caches, const uint32_t* masks,
@@ -314,9 +315,10 @@ spec_status spec_kv_commit(const spec_kv_cache* caches, int num_caches, const ui
     A.N = N;
     A.new_ctx = new_context_len;
     A.status = dev_status;
-    k_kv_commit<<<dim3(unsigned(B), unsigned(num_caches)), COMMIT_T, 0,
-                  reinterpret_cast<cudaStream_t>(stream)>>>(A);
-    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return launch_behind(k_kv_commit, dim3(unsigned(B), unsigned(num_caches)), COMMIT_T, 0,
+                         reinterpret_cast<cudaStream_t>(stream), A) == cudaSuccess
+               ? SPEC_OK
+               : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"

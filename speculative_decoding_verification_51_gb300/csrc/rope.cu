@@ -133,6 +133,7 @@ __device__ __forceinline__ void set2(Words<T, VEC>& x, int e, float a, float b) 
 // interleaved, or nothing turns).
 template <typename T, int VEC, int IP, bool E4, bool PAIR>
 __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant__ RotArgs A) {
+    begin_after_previous();
     const int lane = threadIdx.x % IP;
     const long long t = blockIdx.x * (long long)(ROT_THREADS / IP) + threadIdx.x / IP;
     if (t >= A.T) return;
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
 // or one value that does not turn at a time; an e4m3 row is read twice.
 template <typename T, bool E4>
 __global__ void __launch_bounds__(ROT_THREADS) k_rotate_any(const __grid_constant__ RotArgs A) {
+    begin_after_previous();
     const int lane = threadIdx.x & 31, H = A.q.n + A.k.n + A.v.n, hr = A.half_rot;
     const long long w = blockIdx.x * (long long)(ROT_THREADS / 32) + (threadIdx.x >> 5);
     if (w >= A.T * H) return;
@@ -361,6 +363,7 @@ __global__ void __launch_bounds__(ROT_THREADS) k_rotate_any(const __grid_constan
 template <typename C, typename T, typename I>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ CacheView c, long long T_,
                                                  const long long* slots, T* out_k, T* out_v) {
+    begin_after_previous();
     constexpr int VEC = 16 / sizeof(C);
     const I vecs = c.D / VEC, heads = c.heads, n = I(T_) * heads * vecs;
     for (I i = blockIdx.x * I(256) + threadIdx.x; i < n; i += gridDim.x * I(256)) {
@@ -432,11 +435,11 @@ cudaError_t launch_rotate(RotArgs A, cudaStream_t st) {
     const long long gx = (A.T + ROT_THREADS / ip - 1) / (ROT_THREADS / ip);
     if (gx > 0x7fffffffll || (H + A.share - 1) / A.share > 65535) return cudaErrorInvalidValue;
     const dim3 grid(unsigned(gx), unsigned((H + A.share - 1) / A.share));
-    if (ip == 4) k_rotate<T, VEC, 4, E4, PAIR><<<grid, ROT_THREADS, 0, st>>>(A);
-    else if (ip == 8) k_rotate<T, VEC, 8, E4, PAIR><<<grid, ROT_THREADS, 0, st>>>(A);
-    else if (ip == 16) k_rotate<T, VEC, 16, E4, PAIR><<<grid, ROT_THREADS, 0, st>>>(A);
-    else k_rotate<T, VEC, 32, E4, PAIR><<<grid, ROT_THREADS, 0, st>>>(A);
-    return cudaGetLastError();
+    auto* kernel = ip == 4    ? k_rotate<T, VEC, 4, E4, PAIR>
+                   : ip == 8  ? k_rotate<T, VEC, 8, E4, PAIR>
+                   : ip == 16 ? k_rotate<T, VEC, 16, E4, PAIR>
+                              : k_rotate<T, VEC, 32, E4, PAIR>;
+    return launch_behind(kernel, grid, ROT_THREADS, 0, st, A);
 }
 
 template <typename T, bool E4>
@@ -460,8 +463,7 @@ cudaError_t launch_rotate_vec(const RotArgs& A, cudaStream_t st) {
     if (ok(4)) return pair ? launch_rotate<T, 4, E4, true>(A, st) : launch_rotate<T, 4, E4, false>(A, st);
     const long long warps = A.T * (A.q.n + A.k.n + A.v.n), grid = (warps + ROT_THREADS / 32 - 1) / (ROT_THREADS / 32);
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    k_rotate_any<T, E4><<<unsigned(grid), ROT_THREADS, 0, st>>>(A);
-    return cudaGetLastError();
+    return launch_behind(k_rotate_any<T, E4>, dim3(unsigned(grid)), ROT_THREADS, 0, st, A);
 }
 
 spec_status check_table(const spec_rope_table* t, int D) {
@@ -608,9 +610,8 @@ cudaError_t launch_read_to(const CacheView& c, int64_t T_, const int64_t* slots,
     const unsigned grid = unsigned(std::min<long long>((n + 255) / 256, 1ll << 22));
     const long long* s = reinterpret_cast<const long long*>(slots);
     T *k = static_cast<T*>(out_k), *v = static_cast<T*>(out_v);
-    if (n < (1ll << 31) && c.slots < (1ll << 32)) k_kv_read<C, T, uint32_t><<<grid, 256, 0, st>>>(c, T_, s, k, v);
-    else k_kv_read<C, T, long long><<<grid, 256, 0, st>>>(c, T_, s, k, v);
-    return cudaGetLastError();
+    auto* kernel = n < (1ll << 31) && c.slots < (1ll << 32) ? k_kv_read<C, T, uint32_t> : k_kv_read<C, T, long long>;
+    return launch_behind(kernel, dim3(grid), 256, 0, st, c, (long long)T_, s, k, v);
 }
 template <typename C>
 cudaError_t launch_read(const CacheView& c, int64_t T, const int64_t* slots, int dtype,

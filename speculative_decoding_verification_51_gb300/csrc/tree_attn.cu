@@ -59,22 +59,27 @@ int width_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // The parts that k_attn_tiles left: CTA (c, y) joins the item that starts in CTA
 // c's share and ends in another's, its y-th share of the channels.  One row a
 // thread (lanes side by side, so that reads are coalesced), 8 channels at most, up
-// to 8 parts' reads in flight.  Launched with programmatic dependent launch:
-// it finds its item while k_attn_tiles still runs.
+// to 8 parts' reads in flight.  It finds its item while k_attn_tiles still runs
+// (the plan was there before that began).
 constexpr int JOIN_T = 256, JOIN_Y = 8;
 __global__ void __launch_bounds__(JOIN_T) k_attn_join(const __grid_constant__ AttnArgs A, int width) {
     __shared__ PlanWindow window;
     Share share;
-    if (!read_plan(A, window, share)) return;
-    const Lists L = {window, A.plan, window.b0};
-    const Segment s = segment_at(A, L, share, share.end - 1, window.b0);
-    const long long g0 = s.g - s.t0;
-    if (g0 < share.begin || s.t0 + 1 == s.tiles) return;  // begins before this share, or ends with it
+    Segment s = {};
+    long long g0 = 0;
+    bool mine = read_plan(A, window, share);
+    if (mine) {
+        const Lists L = {window, A.plan, window.b0};
+        s = segment_at(A, L, share, share.end - 1, window.b0);
+        g0 = s.g - s.t0;
+        mine = g0 >= share.begin && s.t0 + 1 != s.tiles;  // not begun before this share, nor ended with it
+    }
+    griddep_wait();
+    if (!mine) return;
     const int c0 = blockIdx.x, parts = cta_of(share, g0 + s.tiles - 1) - c0 + 1;
     const int r = threadIdx.x & 127, row = s.rt * 128 + r, quads = width / 4;
     const int per = quads / JOIN_Y / (JOIN_T / 128);  // 2 (128 channels) or 1
     const int q0 = (blockIdx.y * (JOIN_T / 128) + (threadIdx.x >> 7)) * per;
-    griddep_wait();
     if (row >= A.rows) return;
     auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
     const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + r;
@@ -124,16 +129,7 @@ __global__ void __launch_bounds__(JOIN_T) k_attn_join(const __grid_constant__ At
 
 namespace sv {
 cudaError_t launch_attn_join(const AttnLaunch& L, int width) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(L.ctas), JOIN_Y);
-    cfg.blockDim = dim3(JOIN_T);
-    cfg.stream = L.st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join, L.A, width);
+    return launch_behind(k_attn_join, dim3(unsigned(L.ctas), JOIN_Y), JOIN_T, 0, L.st, L.A, width);
 }
 }  // namespace sv
 

@@ -111,16 +111,17 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     uint8_t* sc = sm_sc + warp * S::STAGES * 32;
 
     __shared__ PlanWindow window;
-    Share share;
-    if (!read_plan(A, window, share)) return;  // the whole CTA
-    const int first = window.b0;
-    const Lists L = {window, A.plan, first};
     if (lane == 0) {
         for (int i = 0; i < S::STAGES; ++i) mbar_init(&bar[i], 1);
         fence_mbarrier_init();
     }
     if (threadIdx.x == 0) sm_flag[1] = 0;
     __syncwarp();
+    begin_after_previous();
+    Share share;
+    if (!read_plan(A, window, share)) return;  // the whole CTA
+    const int first = window.b0;
+    const Lists L = {window, A.plan, first};
 
     // ---- a segment's query rows: read while the segment before it is joined
     constexpr int QV = R * DP / 8, QN = (QV + AR_THREADS - 1) / AR_THREADS;  // vectors of 8 channels
@@ -645,8 +646,7 @@ cudaError_t launch_rows(const AttnLaunch& L) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    k_attn_rows<KIND, NK, MT><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
-    return cudaGetLastError();
+    return launch_behind(k_attn_rows<KIND, NK, MT>, dim3(unsigned(L.ctas)), S::THREADS, S::SMEM, L.st, L.mk, L.mv, L.A);
 }
 
 template <int KIND>

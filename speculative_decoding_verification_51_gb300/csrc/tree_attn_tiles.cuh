@@ -285,7 +285,9 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
     __shared__ PlanWindow window;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_launch_dependents();  // k_attn_join waits for this grid's end by itself
+    // in this order: k_attn_join, which begins next, reads the plan before its own wait
+    griddep_wait();
+    griddep_launch_dependents();
     Share share;
     if (!read_plan(A, window, share)) return;  // the whole CTA
     const int first = window.b0;
@@ -586,8 +588,7 @@ cudaError_t launch_tiles(const AttnLaunch& L) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    k_attn_tiles<KIND, DP><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
-    e = cudaGetLastError();
+    e = launch_behind(k_attn_tiles<KIND, DP>, dim3(unsigned(L.ctas)), S::THREADS, S::SMEM, L.st, L.mk, L.mv, L.A);
     return e == cudaSuccess ? launch_attn_join(L, DP) : e;
 }
 

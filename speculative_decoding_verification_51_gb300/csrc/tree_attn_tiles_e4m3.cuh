@@ -92,7 +92,9 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     __shared__ PlanWindow window;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_launch_dependents();  // k_attn_join waits for this grid's end by itself
+    // in this order: k_attn_join, which begins next, reads the plan before its own wait
+    griddep_wait();
+    griddep_launch_dependents();
     Share share;
     if (!read_plan(A, window, share)) return;  // the whole CTA
     const int first = window.b0;
@@ -555,8 +557,7 @@ cudaError_t launch_tiles_e4m3(const AttnLaunch& L) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    k_attn_tiles_e4m3<DP><<<L.ctas, S::THREADS, S::SMEM, L.st>>>(L.mk, L.mv, L.A);
-    e = cudaGetLastError();
+    e = launch_behind(k_attn_tiles_e4m3<DP>, dim3(unsigned(L.ctas)), S::THREADS, S::SMEM, L.st, L.mk, L.mv, L.A);
     return e == cudaSuccess ? launch_attn_join(L, DP) : e;
 }
 
