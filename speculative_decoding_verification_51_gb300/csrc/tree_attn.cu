@@ -209,6 +209,12 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.tiles_r = (A.rows + R - 1) / R;
     // A copy lies in one page: k_attn_rows takes chunks of 16 tokens,
     // k_attn_tiles the longest power of two up to a tile that divides a page.
+    // What another item costs a CTA of the tile kernels, in tiles: its queries, and
+    // a pipeline that runs dry and fills again.  Measured (us without a lead / with
+    // 3 / 6 / 9 for 8 bits, 2 / 5 / 9 for 16): 32 trees of 32 over 1000 to 16384 tokens
+    // 263 / 234 / 223 / 225 and 241 / 228 / 214 / 215, 200 such trees over 30 to 3000
+    // tokens of 16 bits 289 / 271 / 260 / 265.  k_attn_rows reads HBM meanwhile.
+    A.lead = !tiles ? 0 : e4 ? 6 : 5;
     A.box = tiles ? std::min(TREE_TILE, A.page & -A.page) : 16;
     spec_status r = cache_map(&L.mk, *cache, cache->k, A.box);
     if (r == SPEC_OK) r = cache_map(&L.mv, *cache, cache->v, A.box);

@@ -32,6 +32,7 @@ struct AttnArgs {
     int B, N, Hq, Hkv, G, D, page, max_pages, num_pages;
     int rows, tiles_r;  // rows of a (request, key head), row tiles of them
     int box;            // tokens of one copy (k_attn_tiles)
+    int lead;           // what an item costs beyond its tiles, in tiles
     float c;            // scale * log2(e): scores are exponents of two
     int q_f16;          // q and out are f16 (else bf16)
     float* part_o;      // [2 * CTAs][width / 4][R][4] unnormalised sums
@@ -45,7 +46,7 @@ struct Segment {
     int c0, c1;  // chunks of 16 tokens
     int t0, t1, tiles;  // tiles of the item: this piece's, and all
     int ctx, n;
-    long long g;       // the piece's first tile in the list of all
+    long long g;       // the piece's first tile's place in the list of all
 };
 
 // A page of the table, which spec_tree_plan found to be in the cache; one that was
@@ -54,19 +55,26 @@ __device__ __forceinline__ int page_in(const AttnArgs& A, int p) {
     return int(min(unsigned(p), unsigned(A.num_pages - 1)));
 }
 
+// A share is a stretch [begin, end) of the list of all items.  In the list an item
+// takes its tiles' places and `lead` places before them: what it costs a CTA to
+// turn to another item, in tiles (A.lead), so that CTAs with many short items get
+// fewer tiles.  Nothing happens in a lead: a share's ends that fall into one are
+// moved to its end and its beginning.  With few tiles a CTA (8) there is none.
 struct Share {
     long long total, begin, end;
-    int ctas;
+    int ctas, lead;
 };
 
-__device__ __forceinline__ Share share_of(long long total) {
+__device__ __forceinline__ Share share_of(const AttnArgs& A, int tiles) {
+    const long long hr = (long long)A.Hkv * A.tiles_r;
     Share s;
-    s.total = total;
-    s.ctas = int(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+    s.lead = tiles * hr >= 8ll * gridDim.x ? A.lead : 0;
+    s.total = (tiles + (long long)s.lead * A.B) * hr;
+    s.ctas = int(s.total < (long long)gridDim.x ? s.total : (long long)gridDim.x);
     s.begin = s.end = 0;
     if ((int)blockIdx.x < s.ctas) {
-        s.begin = total * blockIdx.x / s.ctas;
-        s.end = total * (blockIdx.x + 1) / s.ctas;
+        s.begin = s.total * blockIdx.x / s.ctas;
+        s.end = s.total * (blockIdx.x + 1) / s.ctas;
     }
     return s;
 }
@@ -76,6 +84,7 @@ __device__ __forceinline__ Share share_of(long long total) {
 // past the window are read where they lie.
 constexpr int PLAN_WINDOW = 32;
 struct PlanWindow {
+    long long begin, end;  // the share's, moved out of leads
     int b0;
     int tiles[PLAN_WINDOW + 1], ctx[PLAN_WINDOW], nodes[PLAN_WINDOW];
 };
@@ -92,10 +101,26 @@ struct Lists {
     }
 };
 
+// What request b (tiles lo to hi of the plan's list) says of a share: whether it
+// holds its first place, and where its ends are moved to.
+__device__ __forceinline__ void find_ends(const AttnArgs& A, PlanWindow& w, const Share& s, int b, int lo, int hi) {
+    const long long hr = (long long)A.Hkv * A.tiles_r, from = (lo + (long long)s.lead * b) * hr;
+    const int each = hi - lo + s.lead;
+    const long long to = from + each * hr;
+    if (from <= s.begin && s.begin < to) {
+        w.b0 = b;
+        const long long into = (s.begin - from) % each;
+        w.begin = s.begin + max(s.lead - into, 0ll);
+    }
+    if (from < s.end && s.end <= to) {  // (the end of an item is one already)
+        const long long into = (s.end - from) % each;
+        w.end = s.end - (into <= s.lead ? into : 0ll);
+    }
+}
+
 // This CTA's share, and the window from the request that holds its first tile
 // on.  Call with the whole CTA; false (for all of it) where there is no share.
 __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Share& s) {
-    const long long hr = (long long)A.Hkv * A.tiles_r;
     if (A.B <= PLAN_WINDOW) {  // the window holds every request: one round of reads
         if (int(threadIdx.x) <= A.B) {
             w.tiles[threadIdx.x] = A.plan.tiles[threadIdx.x];
@@ -104,9 +129,18 @@ __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Shar
                 w.nodes[threadIdx.x] = A.plan.nodes[threadIdx.x];
             }
         }
+        __syncthreads();
+        s = share_of(A, w.tiles[A.B]);
+        if (s.begin >= s.end) return false;
+        if (s.lead) {
+            if (int(threadIdx.x) < A.B) find_ends(A, w, s, threadIdx.x, w.tiles[threadIdx.x], w.tiles[threadIdx.x + 1]);
+            __syncthreads();
+            s.begin = w.begin;
+            s.end = w.end;
+            __syncthreads();
+        }
         if (threadIdx.x == 0) w.b0 = 0;
         __syncthreads();
-        s = share_of(w.tiles[A.B] * hr);
         return s.begin < s.end;
     }
     const int last = A.plan.tiles[A.B];
@@ -114,14 +148,16 @@ __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Shar
     for (int i = threadIdx.x; i < A.B; i += blockDim.x) {
         const int lo = A.plan.tiles[i], hi = A.plan.tiles[i + 1];
         if (!any) {
-            s = share_of(last * hr);
+            s = share_of(A, last);
             any = true;
         }
-        if (lo * hr <= s.begin && s.begin < hi * hr) w.b0 = i;
+        find_ends(A, w, s, i, lo, hi);
     }
-    s = share_of(last * hr);
+    s = share_of(A, last);
     if (s.begin >= s.end) return false;
     __syncthreads();
+    s.begin = w.begin;
+    s.end = w.end;
     const int b0 = w.b0;
     for (int i = threadIdx.x; i <= PLAN_WINDOW && b0 + i <= A.B; i += blockDim.x) {
         w.tiles[i] = A.plan.tiles[b0 + i];
@@ -131,31 +167,34 @@ __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Shar
         }
     }
     __syncthreads();
-    return true;
+    return s.begin < s.end;
 }
 
-// the CTA whose share holds tile g
+// the CTA whose share holds place g
 __device__ __forceinline__ int cta_of(const Share& s, long long g) {
     return int(((g + 1) * s.ctas - 1) / s.total);
 }
 
-// The segment that starts at tile g; b is the request that holds g or one before.
+// The segment that starts at place g (a tile, or the lead before an item's first
+// one); b is the request that holds g or one before.
 __device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Lists& L, const Share& s, long long g, int b) {
     const long long hr = (long long)A.Hkv * A.tiles_r;
     Segment x;
     int lo = L.tiles(b), hi = L.tiles(b + 1);
-    while (hi * hr <= g) {
+    while ((hi + (long long)s.lead * (b + 1)) * hr <= g) {
         ++b;
         lo = hi;
         hi = L.tiles(b + 1);
     }
     x.b = b;
-    x.g = g;
     x.tiles = hi - lo;
-    const long long r = g - lo * hr;
-    const int item = r >> 31 ? int(r / x.tiles) : int(uint32_t(r) / uint32_t(x.tiles));
-    x.t0 = int(r - (long long)item * x.tiles);
-    x.t1 = int(min((long long)x.tiles, x.t0 + (s.end - g)));
+    const int each = x.tiles + s.lead;
+    const long long r = g - (lo + (long long)s.lead * b) * hr;
+    const int item = r >> 31 ? int(r / each) : int(uint32_t(r) / uint32_t(each));
+    const int at = int(r - (long long)item * each) - s.lead;
+    x.t0 = max(at, 0);
+    x.g = g + (x.t0 - at);
+    x.t1 = int(min((long long)x.tiles, x.t0 + (s.end - x.g)));
     x.h = item / A.tiles_r;
     x.rt = item - x.h * A.tiles_r;
     x.ctx = L.ctx(b);

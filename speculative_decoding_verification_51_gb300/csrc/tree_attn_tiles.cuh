@@ -138,11 +138,11 @@ __device__ __forceinline__ void at_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// S in place: what the row does not see becomes -inf.  u0: node index of the
-// tile's first token (negative: within the context).
-__device__ __forceinline__ void hide_unseen(uint32_t sa, int u0, uint32_t mask) {
+// `tokens` columns of S in place: what the row does not see becomes -inf.  u0: node
+// index of the first one's token (negative: within the context).
+__device__ __forceinline__ void hide_unseen(uint32_t sa, int u0, uint32_t mask, int tokens) {
 #pragma unroll 1
-    for (int j = 0; j < 128; j += 32) {
+    for (int j = 0; j < tokens; j += 32) {
         const int u = u0 + j;
         const uint32_t on = u <= -32 ? 0xffffffffu
                             : u < 0  ? (0xffffffffu >> (32 + u)) | (mask << -u)
@@ -215,12 +215,13 @@ __device__ __forceinline__ uint32_t clean_values(uint8_t* tile, int t0, const Se
     return bad;
 }
 
-// A thread's finished row (r of the tile; its sums in TMEM at o): to the output
-// where the segment is the whole item, else to the workspace.  `bad`: the
+// Channels [from, to) of a thread's finished row (r of the tile; its sums in TMEM
+// at o): to the output where the segment is the whole item, else to the workspace.  `bad`: the
 // nodes it sees that have values which are not finite.
 template <int KIND, int DP>
 __device__ __forceinline__ void put_tile(const AttnArgs& A, const Share& share, const Segment& s, uint32_t o,
-                                         int r, int node, uint32_t bad, float ref, float tot) {
+                                         int r, int node, uint32_t bad, float ref, float tot, int from,
+                                         int to) {
     const bool whole = s.t0 == 0 && s.t1 == s.tiles;
     const long long slot = part_slot(share, s);
     const int row = s.rt * 128 + r;
@@ -228,7 +229,7 @@ __device__ __forceinline__ void put_tile(const AttnArgs& A, const Share& share, 
     const bool none = inv == 0.f && tot == tot;
     const long long at = (((long long)s.b * A.N + node) * A.Hq + s.h * A.G + row - node * A.G) * A.D;
 #pragma unroll 1
-    for (int j = 0; j < DP; j += 32) {
+    for (int j = from; j < to; j += 32) {
         uint32_t u0[32];
         at_ld32(o + j, u0);
         at_ld_wait(u0);
@@ -260,6 +261,7 @@ __device__ __forceinline__ void put_tile(const AttnArgs& A, const Share& share, 
         }
         __syncwarp();
     }
+    if (from) return;
     if (whole) put_lse(A, s, row, ref, tot);
     else if (row < A.rows) *reinterpret_cast<float2*>(A.part_ml + (slot * 128 + r) * 2) = make_float2(ref, tot);
 }
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
         for (long long g = share.begin; g < share.end;) {
             const Segment s = segment_at(A, L, share, g, b_at);
             b_at = s.b;
-            g += s.t1 - s.t0;
+            g = s.g + s.t1 - s.t0;
             const int len = s.ctx + s.n;
             const int32_t* table = A.table + (long long)s.b * A.max_pages;
             auto page_of = [&](int t, int& off) {
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
             for (long long g = share.begin; g < share.end; ++seg) {
                 const Segment s = segment_at(A, L, share, g, b_at);
                 b_at = s.b;
-                g += s.t1 - s.t0;
+                g = s.g + s.t1 - s.t0;
                 wait(&qf, seg);
                 at_after();
                 scores(i);
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
                 const bool tail = t0 + 128 > s.ctx;
                 wait(&sf[i & 1], i >> 1);
                 at_after();
-                if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 - s.ctx, mask);
+                if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 - s.ctx, mask, 128);
                 // One pass makes the weights by the reference as it is and finds the
                 // largest score; where some row's passes the reference by too
                 // much (seldom, but for a segment's first tile), the reference is
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
             // so that of either barrier only the last phase can be open)
             wait(&pv[(i - 1) & 1], (i - 1) >> 1);
             at_after();
-            put_tile<KIND, DP>(A, share, done, tbase + lanes + T_O, r, node, nodes_bad & mask, ref, tot);
+            put_tile<KIND, DP>(A, share, done, tbase + lanes + T_O, r, node, nodes_bad & mask, ref, tot, 0, DP);
             at_before();
             __syncwarp();
             if (lane == 0) at_arrive(&of);

@@ -21,8 +21,14 @@
 // tile's weights.  E is taken as -100 or more, so that a tile of zeros does not
 // push the total out of float32.
 //
-// Warps: 0 copies; 1 products; 2 K's factors; 4..7 softmax (as in
-// k_attn_tiles, but P lies over S, since TMEM holds the queries); 8..15 V.
+// Softmax.  Two threads a row, each half of the tile's tokens, since one warp a
+// scheduler leaves it idle most of the time.  They keep one reference: each raises its
+// own where it has to, a vote of the two warps says whether any has, and only then
+// do they agree on the larger one and bring weights and sums to it.  References are
+// whole exponents, so that this is exact.
+//
+// Warps: 0 copies; 1 products with K; 2 K's factors; 3 products with V; 4..7 and
+// 8..11 softmax; 12..19 V.
 #pragma once
 
 #include "tree_attn_tiles.cuh"
@@ -33,24 +39,31 @@ template <int DP>
 struct TilesE4Shape {
     static constexpr int HALVES = DP / 64;
     static constexpr int OPERAND = HALVES * 16384;  // 128 tokens of f16 channels
-    static constexpr int RAW = 16384, RAWS = 4;     // 128 tokens of 128 bytes
-    static constexpr size_t SMEM = 1024 + size_t(RAWS) * 2 * RAW + 2 * OPERAND;
-    static constexpr int THREADS = 512;
+    static constexpr int RAW = 16384, RAWS = 3;     // 128 tokens (or rows) of 128 bytes
+    static constexpr size_t SMEM = 1024 + size_t(RAWS) * 2 * RAW + 2 * OPERAND + 3 * RAW;
+    static_assert(SMEM + 12288 <= 232448, "shared memory");
+    static constexpr int THREADS = 640;
 };
 
 // D f32, A and B e4m3, both K-major, M = N = 128
 constexpr uint32_t AT_ID_E4 = (1u << 4) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-__device__ __forceinline__ void at_mma_e4(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void at_mma_e4(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(AT_ID_E4), "r"(acc)
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(AT_ID_E4), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void at_st8(uint32_t t, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// 16 columns of this thread's lane, waited for
+__device__ __forceinline__ void at_ld16_now(uint32_t t, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
 }
 // 2^d as two halves (d <= 0; 0 below f16's least subnormal)
 __device__ __forceinline__ uint32_t half2_exp2(int d) {
@@ -62,6 +75,8 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// 2^-d for a whole d >= 0 (0 where it is no normal float)
+__device__ __forceinline__ float exp2_down(float d) { return d < 127.f ? exp2_int(-int(d)) : 0.f; }
 // The next term of two halves: their e4m3 bytes; the halves keep what is left
 // (a difference of neighbours, so exact).
 __device__ __forceinline__ uint32_t e4m3_term(uint32_t& x) {
@@ -82,13 +97,16 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                                                ~uintptr_t(1023));
     uint8_t* sm_raw = smem;                     // [raws][K, V][128 tokens][128]
     uint8_t* sm_v = smem + NR * 2 * S::RAW;     // [2] f16 values
+    uint8_t* sm_q = sm_v + 2 * S::OPERAND;      // [terms][128 rows][128] queries
     __shared__ __align__(16) uint8_t sm_sc[NR * 256];     // scale bytes
     __shared__ __align__(16) float sm_ck[8][128];         // K's factors
     __shared__ __align__(8) uint64_t rkf[NR], rke[NR], rvf[NR], rve[NR], vf[2], ve[2], uk[8];
-    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin;
+    __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, unit_v[2];
     __shared__ uint32_t bad_nodes[2];
+    __shared__ float2 sm_max[2][128];          // what the halves of a row exchange: queries,
+    __shared__ float sm_ref[2][128], sm_tot[2][128];  // references, totals
     __shared__ PlanWindow window;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -110,13 +128,14 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             mbar_init(&vf[i], 8);
             mbar_init(&ve[i], 1);
             mbar_init(&sf[i], 1);
-            mbar_init(&pf[i], 4);
+            mbar_init(&pf[i], 8);
             mbar_init(&pv[i], 1);
         }
         for (int i = 0; i < 8; ++i) mbar_init(&uk[i], 1);
-        mbar_init(&qf, 4);
-        mbar_init(&of, 4);
-        mbar_init(&fin, 1);
+        mbar_init(&qf, 8);
+        mbar_init(&of, 8);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         abort_flag = 0;
         bad_nodes[0] = bad_nodes[1] = 0;
         fence_mbarrier_init();
@@ -131,8 +150,8 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     __syncthreads();
     at_after();
     const uint32_t tbase = tmem_base;
-    // S (then P in its first 64 columns) at 0 and 128, O, the queries' terms
-    constexpr uint32_t T_O = 256, T_Q = 384, TERM = DP / 4;
+    // S at 0 and 128, O, P at 384 and 448
+    constexpr uint32_t T_O = 256, T_P = 384;
     const int terms = A.q_f16 ? 3 : 2;
     volatile int* gone = &abort_flag;
     // a bounded wait; once one has run out nobody waits any more
@@ -141,9 +160,10 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
         if (!at_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
     };
 
-    // registers from the other warpgroups to softmax (232 + 3 * 88 <= 4 * 128): in
-    // 128 its columns spill, to an L1 that shared memory has left little of
-    if (warp < 4 || warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // registers from the other warpgroups to softmax (64 + 2 * 136 + 2 * 72 <= 5 * 96):
+    // in 96 its columns spill, to an L1 that shared memory has left little of
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
         // ---- copies: lane = (rows or scales, box of A.box tokens)
         const int chunk = lane & 7, part = lane >> 3, boxes = 128 / A.box;
@@ -153,7 +173,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
         for (long long g = share.begin; g < share.end;) {
             const Segment s = segment_at(A, L, share, g, b_at);
             b_at = s.b;
-            g += s.t1 - s.t0;
+            g = s.g + s.t1 - s.t0;
             const int len = s.ctx + s.n;
             const int32_t* table = A.table + (long long)s.b * A.max_pages;
             auto page_of = [&](int t, int& off) {
@@ -198,34 +218,45 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        // ---- products
+        // ---- products with K
+        if (lane == 0) {
+            uint32_t j = 0, seg = 0;
+            int b_at = first;
+            for (long long g = share.begin; g < share.end; ++seg) {
+                const Segment s = segment_at(A, L, share, g, b_at);
+                b_at = s.b;
+                g = s.g + s.t1 - s.t0;
+                wait(&qf, seg);
+                for (int t = s.t0; t < s.t1; ++t, ++j) {
+                    const uint32_t rs = j % NR;
+                    wait(&rkf[rs], j / NR);
+                    if (j >= 2) wait(&pf[j & 1], (j - 2) >> 1);  // those of tile j - 2 are weights
+                    at_after();
+                    const uint32_t ka = smem_u32(sm_raw) + rs * 2 * S::RAW, qa = smem_u32(sm_q);
+                    for (int x = 0; x < terms; ++x)
+#pragma unroll
+                        for (int k = 0; k < DP / 32; ++k)
+                            at_mma_e4(tbase + (j & 1) * 128, at_desc_k(qa + x * S::RAW + k * 32), at_desc_k(ka + k * 32),
+                                      x > 0 || k > 0);
+                    at_commit(&sf[j & 1]);
+                    at_commit(&rke[rs]);
+                }
+            }
+            at_commit(&fin[0]);  // every product is done before TMEM is freed
+            at_wait_bounded(&fin[0], 0, AT_WAIT_NS);
+        }
+    } else if (warp == 3) {
+        // ---- products with V, from a thread of their own: either's waits and commits
+        // (some 100 cycles each) would keep the other's products from being issued
         if (lane == 0) {
             constexpr uint32_t id_o = at_idesc<true>(DP, true);
             uint32_t i = 0, seg = 0;
             int b_at = first;
-            auto scores = [&](uint32_t j) {
-                const uint32_t rs = j % NR;
-                wait(&rkf[rs], j / NR);
-                if (j >= 2) wait(&pv[j & 1], (j - 2) >> 1);  // P of tile j - 2 lies there
-                at_after();
-                const uint32_t ka = smem_u32(sm_raw) + rs * 2 * S::RAW;
-                for (int x = 0; x < terms; ++x)
-#pragma unroll
-                    for (int k = 0; k < DP / 32; ++k)
-                        at_mma_e4(tbase + (j & 1) * 128, tbase + T_Q + x * TERM + k * 8, at_desc_k(ka + k * 32),
-                                  x > 0 || k > 0);
-                at_commit(&rke[rs]);
-                at_commit(&sf[j & 1]);
-            };
             for (long long g = share.begin; g < share.end; ++seg) {
                 const Segment s = segment_at(A, L, share, g, b_at);
                 b_at = s.b;
-                g += s.t1 - s.t0;
-                wait(&qf, seg);
-                at_after();
-                scores(i);
+                g = s.g + s.t1 - s.t0;
                 for (int t = s.t0; t < s.t1; ++t, ++i) {
-                    if (t + 1 < s.t1) scores(i + 1);
                     wait(&vf[i & 1], i >> 1);
                     wait(&pf[i & 1], i >> 1);
                     if (t == s.t0) wait(&of, seg ^ 1u);  // the last segment's rows have been read
@@ -233,25 +264,25 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     const uint32_t va = smem_u32(sm_v) + (i & 1) * S::OPERAND;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        at_mma_ts(tbase + T_O, tbase + (i & 1) * 128 + k * 8, at_desc_mn(va + k * 2048), id_o,
+                        at_mma_ts(tbase + T_O, tbase + T_P + (i & 1) * 64 + k * 8, at_desc_mn(va + k * 2048), id_o,
                                   t > s.t0 || k > 0);
-                    at_commit(&ve[i & 1]);
                     at_commit(&pv[i & 1]);
+                    at_commit(&ve[i & 1]);
                 }
             }
-            at_commit(&fin);  // every product is done before TMEM is freed
-            at_wait_bounded(&fin, 0, AT_WAIT_NS);
+            at_commit(&fin[1]);
+            at_wait_bounded(&fin[1], 0, AT_WAIT_NS);
         }
     } else if (warp == 2) {
         // ---- K's factors, 4 tokens a lane (1 past the request's end).  A slot is
         // written again 8 tiles on, when the scores of tile i + 4 are done, which
-        // take the place of the weights of tile i + 2: softmax is through with i.
+        // take the place of those of tile i + 2: softmax is through with i.
         uint32_t i = 0;
         int b_at = first;
         for (long long g = share.begin; g < share.end;) {
             const Segment s = segment_at(A, L, share, g, b_at);
             b_at = s.b;
-            g += s.t1 - s.t0;
+            g = s.g + s.t1 - s.t0;
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const uint32_t rs = i % NR;
                 wait(&rkf[rs], i / NR);
@@ -269,29 +300,42 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 }
             }
         }
-    } else if (warp >= 4 && warp < 8) {
-        // ---- softmax: row = this thread's TMEM lane
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int w = warp - 4, r = w * 32 + lane, tid = r;
+    } else if (warp >= 4 && warp < 12) {
+        // ---- softmax: row = this thread's TMEM lane, tokens (and channels) of one half
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        const int half = (warp - 4) >> 2, w = warp & 3, r = w * 32 + lane, tid = r;
         const uint32_t lanes = uint32_t(w * 32) << 16;
+        constexpr int CH = DP / 2;  // channels of a half
         const float c = fabsf(A.c), sign = A.c < 0.f ? -1.f : 1.f;
-        auto sync = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        auto sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        // the two warps of 32 rows
+        auto sync_rows = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(2 + w) : "memory"); };
+        auto any_of_rows = [&](bool p) {
+            uint32_t any;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(any)
+                : "r"(uint32_t(p)), "r"(2 + w)
+                : "memory");
+            return any != 0;
+        };
         float rc = 0.f;  // the row's factor on scores
         auto load_q = [&](const Segment& s) {
             const int row = s.rt * 128 + r, v = row / A.G;
             const bool on = row < A.rows && v < s.n;
             const uint16_t* src = static_cast<const uint16_t*>(A.q) + s.b * A.qb + v * A.qn +
-                                  (s.h * A.G + row - v * A.G) * A.qh;
-            uint4 u[DP / 8];  // every load in flight at once
+                                  (s.h * A.G + row - v * A.G) * A.qh + half * CH;
+            uint4 u[CH / 8];  // every load in flight at once
 #pragma unroll
-            for (int j = 0; j < DP / 8; ++j)
-                u[j] = on && j * 8 < A.D ? __ldg(reinterpret_cast<const uint4*>(src + j * 8)) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < CH / 8; ++j)
+                u[j] = on && half * CH + j * 8 < A.D ? __ldg(reinterpret_cast<const uint4*>(src + j * 8)) : make_uint4(0, 0, 0, 0);
             auto pair = [&](uint32_t x) {
                 return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&x)) : make_float2(bf16_lo(x), bf16_hi(x));
             };
             float m = 0.f, odd = 0.f;  // odd: NaN where some value is not finite, and the row with it
 #pragma unroll
-            for (int j = 0; j < DP / 8; ++j) {
+            for (int j = 0; j < CH / 8; ++j) {
                 const uint32_t x[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -300,12 +344,16 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     odd = fmaf(f.x, 0.f, fmaf(f.y, 0.f, odd));
                 }
             }
+            sm_max[half][r] = make_float2(m, odd);
+            sync_rows();
+            m = fmaxf(m, sm_max[half ^ 1][r].x);
+            odd += sm_max[half ^ 1][r].y;
             const int ex = odd == 0.f ? e4m3_exponent(m) : 0;
             const float down = exp2_int(-ex) * sign;
             // a factor of zero would make NaN of -inf; no score of this size counts
             rc = fmaxf(c * exp2_int(ex), 1e-30f) + odd;
 #pragma unroll
-            for (int j = 0; j < DP / 32; ++j) {
+            for (int j = 0; j < CH / 32; ++j) {
                 // as halves: 11 bits, and below 2^-14 of the scale steps of 2^-24
                 uint32_t f[16];
 #pragma unroll
@@ -323,11 +371,13 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                         o[e] = e4m3_term(f[2 * e]);
                         o[e] |= e4m3_term(f[2 * e + 1]) << 16;
                     }
-                    at_st8(tbase + lanes + T_Q + x * TERM + j * 8, o);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint4*>(sm_q + x * S::RAW + r * 128 + ((((half * CH + j * 32) / 16 + e) ^ (r & 7)) << 4)) =
+                            make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            at_st_wait();
-            at_before();
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) at_arrive(&qf);
         };
@@ -356,25 +406,41 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 }
             }
             for (int t = s.t0; t < s.t1; ++t, ++i) {
-                const uint32_t sa = tbase + lanes + (i & 1) * 128;
+                const uint32_t sa = tbase + lanes + (i & 1) * 128 + half * 64;
+                const uint32_t pa = tbase + lanes + T_P + (i & 1) * 64 + half * 32;
                 const int t0 = t * 128;
                 const bool tail = t0 + 128 > s.ctx;
-                {   // three waits side by side: each costs some 100 cycles though it is over
+                {   // waits side by side: each costs some 100 cycles though it is over
                     const bool w0 = mbar_try_wait(&sf[i & 1], i >> 1 & 1), w1 = mbar_try_wait(&uk[i & 7], i >> 3 & 1),
-                               w2 = mbar_try_wait(&vf[i & 1], i >> 1 & 1);
+                               w2 = mbar_try_wait(&vf[i & 1], i >> 1 & 1),
+                               w3 = i < 2 || mbar_try_wait(&pv[i & 1], (i >> 1 & 1) ^ 1);  // P of tile i - 2 lies there
                     if (!w0) wait(&sf[i & 1], i >> 1);
                     if (!w1) wait(&uk[i & 7], i >> 3);
                     if (!w2) wait(&vf[i & 1], i >> 1);
+                    if (!w3) wait(&pv[i & 1], (i - 2) >> 1);
                 }
                 at_after();
-                if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 - s.ctx, mask);
+                if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 + half * 64 - s.ctx, mask, 64);
                 const float unit = float(unit_v[i & 1]);
-                const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 7]);
+                const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 7] + half * 64);
+                const float ref0 = ref;
                 // 32 tokens at a time: exponents relative to the reference, their
                 // largest, the weights.  Where a row's largest is too far above the
                 // reference (seldom, but for a segment's first tokens), the
-                // reference is raised and what was made by the old one rescaled.
+                // reference is raised and the weights made by the old one rescaled.
                 uint64_t sum = f2_pack(0.f, 0.f);
+                // 32 weights (16 columns) times 2^-d (d whole): a weight is 2^8 at most,
+                // and 2^-d alone may be less than f16 holds, so in two factors
+                auto scale_weights = [&](uint32_t at, float d) {
+                    const int n = int(fminf(d, 64.f));
+                    const uint32_t h1 = half2_exp2(-(n / 2)), h2 = half2_exp2(n / 2 - n);
+                    uint32_t x[16];
+                    at_st_wait();
+                    at_ld16_now(at, x);  // (16 and no more: P may lie at the end of TMEM)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = half2_mul(half2_mul(x[e], h1), h2);
+                    at_st16(at, x);
+                };
                 auto piece = [&](uint32_t (&x)[32], int j) {
                     const float base = ref == -INFINITY ? 0.f : ref;
                     const uint64_t rc2 = f2_pack(rc, rc), at2 = f2_pack(unit - base, unit - base);
@@ -397,27 +463,14 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     mx = fmaxf(mx, m2);
                     const bool raise = mx > (ref == -INFINITY ? -INFINITY : AT_SLACK);
                     if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-                        const float d = raise ? mx : 0.f;
-                        const float f = !raise ? 1.f : ref == -INFINITY ? 0.f : ex2_approx(-d);
+                        const float d = raise ? ceilf(mx) : 0.f;  // whole, so that weights are rescaled exactly
+                        const float f = !raise ? 1.f : ref == -INFINITY ? 0.f : exp2_down(d);
                         if (raise) ref = base + d;
                         tot *= f;
                         sum = f2_mul(sum, f2_pack(f, f));
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - d);
-                        const uint32_t h = pack16<true>(f, f);
-#pragma unroll 1
-                        for (int y = 0; y < j; y += 32) {
-                            uint32_t old[32], to[16];
-                            at_ld32(sa + y / 2, old);
-                            at_ld_wait(old);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) to[e] = half2_mul(old[e], h);
-                            at_st16(sa + y / 2, to);
-                        }
-                        if (t > s.t0) {  // O holds sums by the old reference
-                            wait(&pv[(i - 1) & 1], (i - 1) >> 1);
-                            scale_rows<DP>(tbase + lanes + T_O, f);
-                        }
+                        if (j) scale_weights(pa, d);
                     }
                     uint32_t p[16];
 #pragma unroll
@@ -426,19 +479,36 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                         sum = f2_add(sum, f2_pack(a, b));
                         p[e] = pack16<true>(a, b);
                     }
-                    at_st16(sa + j / 2, p);
+                    at_st16(pa + j / 2, p);
                 };
 #pragma unroll 1
-                for (int j = 0; j < 128; j += 32) {
+                for (int j = 0; j < 64; j += 32) {
                     uint32_t f[32];
                     at_ld32(sa + j, f);
                     at_ld_wait(f);
                     piece(f, j);
                 }
+                if (__builtin_expect(any_of_rows(ref != ref0), 0)) {
+                    sm_ref[half][r] = ref;
+                    sync_rows();  // (the next write is behind the next vote)
+                    const float to = fmaxf(ref, sm_ref[half ^ 1][r]);
+                    const float d = ref == to ? 0.f : to - ref, f = exp2_down(d);
+                    if (__any_sync(0xffffffffu, ref != to)) {
+                        tot *= f;
+                        sum = f2_mul(sum, f2_pack(f, f));
+                        scale_weights(pa, d);
+                        scale_weights(pa + 16, d);
+                    }
+                    if (t > s.t0) {  // O holds sums by the old reference
+                        wait(&pv[(i - 1) & 1], (i - 1) >> 1);
+                        scale_rows<CH>(tbase + lanes + T_O + half * CH, ref0 == to ? 1.f : exp2_down(to - ref0));
+                    }
+                    ref = to;
+                }
                 float s0, s1;
                 f2_unpack(sum, s0, s1);
                 tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 1]), tot);
-                if (__builtin_expect(tail, 0)) {
+                if (__builtin_expect(tail && half == 0, 0)) {
                     const uint32_t bad = clean_values<true, DP>(sm_v + (i & 1) * S::OPERAND, t0, s, tid);
                     if (bad) atomicOr(&bad_nodes[seg & 1], bad);
                     fence_proxy_async_smem();
@@ -450,11 +520,13 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             }
             // the next segment's queries (every product of this one's is done)
             const Segment done = s;
+            sm_tot[half][r] = tot;
             sync();  // every warp has marked its nodes
+            tot += sm_tot[half ^ 1][r];
             const uint32_t nodes_bad = bad_nodes[seg & 1];
             // the other word is for the next segment, which starts when all
-            // four warps have arrived at qf: nobody reads or marks it now
-            if (tid == 0) bad_nodes[(seg & 1) ^ 1] = 0;
+            // eight warps have arrived at qf: nobody reads or marks it now
+            if (tid == 0 && half == 0) bad_nodes[(seg & 1) ^ 1] = 0;
             if (more) {
                 s = after;
                 load_q(s);
@@ -463,24 +535,26 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             // so that of either barrier only the last phase can be open)
             wait(&pv[(i - 1) & 1], (i - 1) >> 1);
             at_after();
-            put_tile<SPEC_E4M3, DP>(A, share, done, tbase + lanes + T_O, r, node, nodes_bad & mask, ref, tot);
+            put_tile<SPEC_E4M3, DP>(A, share, done, tbase + lanes + T_O, r, node, nodes_bad & mask, ref, tot, half * CH,
+                                     half * CH + CH);
             at_before();
             __syncwarp();
             if (lane == 0) at_arrive(&of);
             if (!more) break;
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 12) {
         // ---- V to f16: 4 lanes a token, two 16-byte chunks (16 channels each) a
-        // lane, 2 tokens a thread.  Eight lanes take tokens 4 apart, whose
-        // swizzles differ in their top bit.
-        const int tid = threadIdx.x - 256, x = lane & 3, odd = lane >> 2 & 1;
-        const int tok0 = (warp - 8) * 8 + odd * 4 + (lane >> 3);
+        // lane, 2 tokens a thread.  Eight lanes take tokens t and t ^ 5: their
+        // swizzles differ in the top bit, so that reads are from all banks at once,
+        // and in the lowest, so that writes are.
+        const int tid = threadIdx.x - 384, x = lane & 3, odd = lane >> 2 & 1;
+        const int tok0 = (warp - 12) * 8 + ((lane >> 3) ^ (odd * 5));
         uint32_t i = 0;
         int b_at = first;
         for (long long g = share.begin; g < share.end;) {
             const Segment s = segment_at(A, L, share, g, b_at);
             b_at = s.b;
-            g += s.t1 - s.t0;
+            g = s.g + s.t1 - s.t0;
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int valid = s.ctx + s.n - t * 128;
                 const uint32_t rs = i % NR, st = i & 1;
@@ -520,11 +594,8 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                             v[2 * e + 1] = half2_mul(e4m3x2_to_f16x2(uint16_t(u[e] >> 16)), f[k]);
                         }
                         uint8_t* o = out + h * 16384 + tk * 128;
-                        const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-                        // of the two tokens of 8 lanes one writes its even chunks
-                        // first and one its odd ones: all banks at once
-                        *reinterpret_cast<uint4*>(o + (((2 * x + odd) ^ (tk & 7)) << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(o + (((2 * x + 1 - odd) ^ (tk & 7)) << 4)) = odd ? lo : hi;
+                        *reinterpret_cast<uint4*>(o + (((2 * x) ^ (tk & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4*>(o + (((2 * x + 1) ^ (tk & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
                     }
                 fence_proxy_async_smem();
                 __syncwarp();
