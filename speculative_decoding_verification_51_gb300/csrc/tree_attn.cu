@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(JOIN_T) k_attn_join(const __grid_constant__ At
         g0 = s.g - s.t0;
         mine = g0 >= share.begin && s.t0 + 1 != s.tiles;  // not begun before this share, nor ended with it
     }
+    // one CTA at least ends after k_attn_tiles, and so does this grid
+    if (!mine && (blockIdx.x || blockIdx.y)) return;
     griddep_wait();
     if (!mine) return;
     const int c0 = blockIdx.x, parts = cta_of(share, g0 + s.tiles - 1) - c0 + 1;

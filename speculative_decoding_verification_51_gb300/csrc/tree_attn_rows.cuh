@@ -165,9 +165,9 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
         }
         if ((ahead & 31) == 0) {
             const int c = pc + lane * AR_WARPS;
-            pages = c < ps.c1 ? page_in(A, __ldg(A.table + (long long)ps.b * A.max_pages + c * 16 / A.page)) : 0;
+            pages = c < ps.c1 ? __ldg(A.table + (long long)ps.b * A.max_pages + c * 16 / A.page) : 0;
         }
-        page_at = __shfl_sync(0xffffffffu, pages, ahead & 31);
+        page_at = page_in(A, __shfl_sync(0xffffffffu, pages, ahead & 31));
         ++ahead;
         off_at = pc * 16 % A.page;
     };

@@ -11,7 +11,7 @@
 // 2^-a), h2 = e4m3(q 2^-a - h1), .., a power of two a row that brings the largest
 // to 448 or less.  Two terms hold bf16's 8 bits and three f16's 11, down to
 // 2^-18 of the row's largest value; the terms' products add up in one
-// accumulator.  K's scale comes afterwards: a warp turns a tile's scale bytes to
+// accumulator.  K's scale comes afterwards: a tile's scale bytes are turned to
 // factors, and the exponent of a weight is (s rc) ck[t] - m.
 //
 // Values.  v 2^e is stored as f16 v 2^(e - E), E the largest exponent of the
@@ -22,13 +22,12 @@
 // push the total out of float32.
 //
 // Softmax.  Two threads a row, each half of the tile's tokens, since one warp a
-// scheduler leaves it idle most of the time.  They keep one reference: each raises its
-// own where it has to, a vote of the two warps says whether any has, and only then
-// do they agree on the larger one and bring weights and sums to it.  References are
-// whole exponents, so that this is exact.
+// scheduler leaves it idle most of the time.  They keep one reference, which is
+// raised seldom: a vote of the two warps says whether any row's weights are too
+// large, and only then are its largest exponent found and the weights made again.
 //
-// Warps: 0 copies; 1 products with K; 2 K's factors; 3 products with V; 4..7 and
-// 8..11 softmax; 12..19 V.
+// Warps: 0 and 2 copies; 1 products with K; 3 products with V; 4..7 and 8..11 softmax;
+// 12..19 V, and K's factors.
 #pragma once
 
 #include "tree_attn_tiles.cuh"
@@ -52,17 +51,6 @@ __device__ __forceinline__ void at_mma_e4(uint32_t d, uint64_t a, uint64_t b, ui
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(AT_ID_E4), "r"(acc)
-        : "memory");
-}
-// 16 columns of this thread's lane, waited for
-__device__ __forceinline__ void at_ld16_now(uint32_t t, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(t)
         : "memory");
 }
 // 2^d as two halves (d <= 0; 0 below f16's least subnormal)
@@ -99,8 +87,8 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     uint8_t* sm_v = smem + NR * 2 * S::RAW;     // [2] f16 values
     uint8_t* sm_q = sm_v + 2 * S::OPERAND;      // [terms][128 rows][128] queries
     __shared__ __align__(16) uint8_t sm_sc[NR * 256];     // scale bytes
-    __shared__ __align__(16) float sm_ck[8][128];         // K's factors
-    __shared__ __align__(8) uint64_t rkf[NR], rke[NR], rvf[NR], rve[NR], vf[2], ve[2], uk[8];
+    __shared__ __align__(16) float sm_ck[2][128];         // K's factors
+    __shared__ __align__(8) uint64_t rkf[NR], rke[NR], rvf[NR], rve[NR], vf[2], ve[2];
     __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag, unit_v[2];
@@ -120,7 +108,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
             mbar_init(&rkf[i], 1);
-            mbar_init(&rke[i], 2);  // the products, and the factors' warp
+            mbar_init(&rke[i], 2);  // the products, and the factors
             mbar_init(&rvf[i], 1);
             mbar_init(&rve[i], 8);
         }
@@ -131,7 +119,6 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             mbar_init(&pf[i], 8);
             mbar_init(&pv[i], 1);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&uk[i], 1);
         mbar_init(&qf, 8);
         mbar_init(&of, 8);
         mbar_init(&fin[0], 1);
@@ -164,8 +151,13 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     // in 96 its columns spill, to an L1 that shared memory has left little of
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0) {
-        // ---- copies: lane = (rows or scales, box of A.box tokens)
+    if (warp == 0 || warp == 2) {
+        // ---- copies of K (warp 0) and V (warp 2; together they would be late: a copy
+        // takes some 100 cycles to issue): lane = (rows or scales, box of A.box tokens)
+        const int side = warp >> 1;
+        uint64_t *full = side ? rvf : rkf, *empty = side ? rve : rke;
+        const CUtensorMap* map = side ? &mv : &mk;
+        const uint8_t* scales = side ? A.vs : A.ks;
         const int chunk = lane & 7, part = lane >> 3, boxes = 128 / A.box;
         const uint32_t box_bytes = uint32_t(A.box) * 128;
         uint32_t i = 0;  // tiles so far
@@ -178,33 +170,30 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             const int32_t* table = A.table + (long long)s.b * A.max_pages;
             auto page_of = [&](int t, int& off) {
                 const int tok = t * 128 + chunk * A.box;
-                if (t >= s.t1 || chunk >= boxes || tok >= len) return -1;
+                off = -1;  // no box for this lane
+                if (t >= s.t1 || chunk >= boxes || tok >= len) return 0;
                 const int p = tok / A.page;
                 off = tok - p * A.page;
-                return page_in(A, __ldg(table + p));
+                return __ldg(table + p);  // (nothing is done with it before the next tile: it takes long)
             };
-            int off = 0, page = page_of(s.t0, off);
+            int off, page = page_of(s.t0, off);
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int nv = min(boxes, max(0, (len - t * 128 + A.box - 1) / A.box));
-                int off2 = 0;
+                int off2;
                 const int page2 = page_of(t + 1, off2);
                 const uint32_t st = i % NR, ph = i / NR;
-                uint8_t* raw = sm_raw + st * 2 * S::RAW;
-                const long long sc = ((long long)page * A.Hkv + s.h) * A.page + off;
-#pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    uint64_t* full = side ? &rvf[st] : &rkf[st];
-                    if (lane == 0) {
-                        wait(side ? &rve[st] : &rke[st], ph ^ 1u);
-                        if (!*gone) mbar_arrive_expect_tx(full, nv * (box_bytes + A.box));
-                    }
-                    __syncwarp();
-                    if (page >= 0 && !*gone) {
-                        if (part == 0)
-                            tma_load_4d(raw + side * S::RAW + chunk * box_bytes, side ? &mv : &mk, 0, off, s.h, page, full);
-                        if (part == 1)
-                            bulk_g2s(sm_sc + st * 256 + side * 128 + chunk * A.box, (side ? A.vs : A.ks) + sc, A.box, full);
-                    }
+                const int in = page_in(A, page);
+                if (lane == 0) {
+                    wait(&empty[st], ph ^ 1u);
+                    if (!*gone) mbar_arrive_expect_tx(&full[st], nv * (box_bytes + A.box));
+                }
+                __syncwarp();
+                if (off >= 0 && !*gone) {
+                    if (part == 0)
+                        tma_load_4d(sm_raw + (st * 2 + side) * S::RAW + chunk * box_bytes, map, 0, off, s.h, in, &full[st]);
+                    if (part == 1)
+                        bulk_g2s(sm_sc + st * 256 + side * 128 + chunk * A.box,
+                                 scales + ((long long)in * A.Hkv + s.h) * A.page + off, A.box, &full[st]);
                 }
                 page = page2;
                 off = off2;
@@ -212,10 +201,8 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
         }
         // every copy has landed before the CTA leaves (they have, unless a wait ran out)
         if (lane == 0 && *gone) {
-            for (uint32_t j = i > NR ? i - NR : 0; j < i; ++j) {
-                at_wait_bounded(&rkf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
-                at_wait_bounded(&rvf[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
-            }
+            for (uint32_t j = i > NR ? i - NR : 0; j < i; ++j)
+                at_wait_bounded(&full[j % NR], (j / NR) & 1u, AT_WAIT_NS / 8);
         }
     } else if (warp == 1) {
         // ---- products with K
@@ -272,33 +259,6 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             }
             at_commit(&fin[1]);
             at_wait_bounded(&fin[1], 0, AT_WAIT_NS);
-        }
-    } else if (warp == 2) {
-        // ---- K's factors, 4 tokens a lane (1 past the request's end).  A slot is
-        // written again 8 tiles on, when the scores of tile i + 4 are done, which
-        // take the place of those of tile i + 2: softmax is through with i.
-        uint32_t i = 0;
-        int b_at = first;
-        for (long long g = share.begin; g < share.end;) {
-            const Segment s = segment_at(A, L, share, g, b_at);
-            b_at = s.b;
-            g = s.g + s.t1 - s.t0;
-            for (int t = s.t0; t < s.t1; ++t, ++i) {
-                const uint32_t rs = i % NR;
-                wait(&rkf[rs], i / NR);
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(sm_sc + rs * 256 + lane * 4);
-                const int left = s.ctx + s.n - t * 128 - lane * 4;
-                float f[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    f[e] = e < left ? exp2_int(min(max(int(w >> (8 * e) & 255u), 1), 253) - 127) : 1.f;
-                *reinterpret_cast<float4*>(&sm_ck[i & 7][lane * 4]) = make_float4(f[0], f[1], f[2], f[3]);
-                __syncwarp();
-                if (lane == 0) {
-                    at_arrive(&uk[i & 7]);
-                    at_arrive(&rke[rs]);
-                }
-            }
         }
     } else if (warp >= 4 && warp < 12) {
         // ---- softmax: row = this thread's TMEM lane, tokens (and channels) of one half
@@ -410,103 +370,78 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 const uint32_t pa = tbase + lanes + T_P + (i & 1) * 64 + half * 32;
                 const int t0 = t * 128;
                 const bool tail = t0 + 128 > s.ctx;
-                {   // waits side by side: each costs some 100 cycles though it is over
-                    const bool w0 = mbar_try_wait(&sf[i & 1], i >> 1 & 1), w1 = mbar_try_wait(&uk[i & 7], i >> 3 & 1),
-                               w2 = mbar_try_wait(&vf[i & 1], i >> 1 & 1),
-                               w3 = i < 2 || mbar_try_wait(&pv[i & 1], (i >> 1 & 1) ^ 1);  // P of tile i - 2 lies there
+                {   // waits side by side: each costs some 100 cycles though it is over.
+                    // (V being there says that the products of tile i - 2, whose
+                    // weights lay where this one's will, are done)
+                    const bool w0 = mbar_try_wait(&sf[i & 1], i >> 1 & 1), w1 = mbar_try_wait(&vf[i & 1], i >> 1 & 1);
                     if (!w0) wait(&sf[i & 1], i >> 1);
-                    if (!w1) wait(&uk[i & 7], i >> 3);
-                    if (!w2) wait(&vf[i & 1], i >> 1);
-                    if (!w3) wait(&pv[i & 1], (i - 2) >> 1);
+                    if (!w1) wait(&vf[i & 1], i >> 1);
                 }
                 at_after();
                 if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 + half * 64 - s.ctx, mask, 64);
                 const float unit = float(unit_v[i & 1]);
-                const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 7] + half * 64);
-                const float ref0 = ref;
-                // 32 tokens at a time: exponents relative to the reference, their
-                // largest, the weights.  Where a row's largest is too far above the
-                // reference (seldom, but for a segment's first tokens), the
-                // reference is raised and the weights made by the old one rescaled.
-                uint64_t sum = f2_pack(0.f, 0.f);
-                // 32 weights (16 columns) times 2^-d (d whole): a weight is 2^8 at most,
-                // and 2^-d alone may be less than f16 holds, so in two factors
-                auto scale_weights = [&](uint32_t at, float d) {
-                    const int n = int(fminf(d, 64.f));
-                    const uint32_t h1 = half2_exp2(-(n / 2)), h2 = half2_exp2(n / 2 - n);
-                    uint32_t x[16];
-                    at_st_wait();
-                    at_ld16_now(at, x);  // (16 and no more: P may lie at the end of TMEM)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = half2_mul(half2_mul(x[e], h1), h2);
-                    at_st16(at, x);
-                };
-                auto piece = [&](uint32_t (&x)[32], int j) {
-                    const float base = ref == -INFINITY ? 0.f : ref;
-                    const uint64_t rc2 = f2_pack(rc, rc), at2 = f2_pack(unit - base, unit - base);
-                    float mx = -INFINITY, m2 = -INFINITY;
+                const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 1] + half * 64);
+                const uint64_t rc2 = f2_pack(rc, rc);
+                // exponents of tokens j .. j + 31 by `base`, in place of their scores
+                auto exponents = [&](uint32_t (&x)[32], int j, float base) {
+                    at_ld32(sa + j, x);
+                    const uint64_t at2 = f2_pack(unit - base, unit - base);
+                    at_ld_wait(x);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 k4 = ck[j / 4 + e];
-                        float a0, b0, a1, b1;
+                        float a, b;
                         f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), rc2),
-                                         f2_pack(k4.x, k4.y), at2), a0, b0);
+                                         f2_pack(k4.x, k4.y), at2), a, b);
+                        x[4 * e] = __float_as_uint(a);
+                        x[4 * e + 1] = __float_as_uint(b);
                         f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), rc2),
-                                         f2_pack(k4.z, k4.w), at2), a1, b1);
-                        mx = fmaxf(fmaxf(a0, b0), mx);
-                        m2 = fmaxf(fmaxf(a1, b1), m2);
-                        x[4 * e] = __float_as_uint(a0);
-                        x[4 * e + 1] = __float_as_uint(b0);
-                        x[4 * e + 2] = __float_as_uint(a1);
-                        x[4 * e + 3] = __float_as_uint(b1);
+                                         f2_pack(k4.z, k4.w), at2), a, b);
+                        x[4 * e + 2] = __float_as_uint(a);
+                        x[4 * e + 3] = __float_as_uint(b);
                     }
-                    mx = fmaxf(mx, m2);
-                    const bool raise = mx > (ref == -INFINITY ? -INFINITY : AT_SLACK);
-                    if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-                        const float d = raise ? ceilf(mx) : 0.f;  // whole, so that weights are rescaled exactly
-                        const float f = !raise ? 1.f : ref == -INFINITY ? 0.f : exp2_down(d);
-                        if (raise) ref = base + d;
-                        tot *= f;
-                        sum = f2_mul(sum, f2_pack(f, f));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - d);
-                        if (j) scale_weights(pa, d);
-                    }
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float a = ex2_approx(__uint_as_float(x[2 * e])), b = ex2_approx(__uint_as_float(x[2 * e + 1]));
-                        sum = f2_add(sum, f2_pack(a, b));
-                        p[e] = pack16<true>(a, b);
-                    }
-                    at_st16(pa + j / 2, p);
                 };
+                // The weights by the reference as it is.  None is above 2^8 where their
+                // sum is not; where some row's sum is (or it has no reference yet), its
+                // reference is raised to the largest exponent and they are made again.
+                float s0, s1;
+                for (bool again = false;; again = true) {
+                    const float base = ref == -INFINITY ? 0.f : ref;
+                    uint64_t sum = f2_pack(0.f, 0.f);
 #pragma unroll 1
-                for (int j = 0; j < 64; j += 32) {
-                    uint32_t f[32];
-                    at_ld32(sa + j, f);
-                    at_ld_wait(f);
-                    piece(f, j);
-                }
-                if (__builtin_expect(any_of_rows(ref != ref0), 0)) {
-                    sm_ref[half][r] = ref;
-                    sync_rows();  // (the next write is behind the next vote)
-                    const float to = fmaxf(ref, sm_ref[half ^ 1][r]);
-                    const float d = ref == to ? 0.f : to - ref, f = exp2_down(d);
-                    if (__any_sync(0xffffffffu, ref != to)) {
-                        tot *= f;
-                        sum = f2_mul(sum, f2_pack(f, f));
-                        scale_weights(pa, d);
-                        scale_weights(pa + 16, d);
+                    for (int j = 0; j < 64; j += 32) {
+                        uint32_t x[32], p[16];
+                        exponents(x, j, base);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float a = ex2_approx(__uint_as_float(x[2 * e])), b = ex2_approx(__uint_as_float(x[2 * e + 1]));
+                            sum = f2_add(sum, f2_pack(a, b));
+                            p[e] = pack16<true>(a, b);
+                        }
+                        at_st16(pa + j / 2, p);
                     }
+                    f2_unpack(sum, s0, s1);
+                    if (again || __builtin_expect(!any_of_rows(!(s0 + s1 <= 256.f) || ref == -INFINITY), 1)) break;
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int j = 0; j < 64; j += 32) {
+                        uint32_t x[32];
+                        exponents(x, j, base);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+                    }
+                    sm_ref[half][r] = mx;
+                    sync_rows();  // (the next write is behind the next vote)
+                    mx = fmaxf(mx, sm_ref[half ^ 1][r]);
+                    const float to = fmaxf(ref, base + ceilf(mx));  // whole, so that sums are rescaled exactly
+                    const float f = ref == to ? 1.f : exp2_down(to - ref);
+                    tot *= f;
                     if (t > s.t0) {  // O holds sums by the old reference
                         wait(&pv[(i - 1) & 1], (i - 1) >> 1);
-                        scale_rows<CH>(tbase + lanes + T_O + half * CH, ref0 == to ? 1.f : exp2_down(to - ref0));
+                        scale_rows<CH>(tbase + lanes + T_O + half * CH, f);
                     }
                     ref = to;
                 }
-                float s0, s1;
-                f2_unpack(sum, s0, s1);
                 tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 1]), tot);
                 if (__builtin_expect(tail && half == 0, 0)) {
                     const uint32_t bad = clean_values<true, DP>(sm_v + (i & 1) * S::OPERAND, t0, s, tid);
@@ -581,6 +516,17 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 }
                 wait(&ve[st], (i >> 1) ^ 1u);
                 if (tid == 0) unit_v[st] = unit;
+                if (warp == 12) {  // K's factors, 4 tokens a lane (1 past the request's end)
+                    wait(&rkf[rs], i / NR);
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(sm_sc + rs * 256 + lane * 4);
+                    float c4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c4[e] = e < left ? exp2_int(min(max(int(w >> (8 * e) & 255u), 1), 253) - 127) : 1.f;
+                    *reinterpret_cast<float4*>(&sm_ck[st][lane * 4]) = make_float4(c4[0], c4[1], c4[2], c4[3]);
+                    __syncwarp();
+                    if (lane == 0) at_arrive(&rke[rs]);
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
