@@ -139,8 +139,6 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
     if (t >= A.T) return;
     const unsigned gmask = IP == 32 ? 0xffffffffu : ((1u << IP) - 1u) << (((threadIdx.x & 31) / IP) * IP);
     const int hr = A.half_rot, h0 = blockIdx.y * A.share, h1 = h0 + A.share;
-    const SlotRow sr = slot_row(A, t, lane == 0 && blockIdx.y == 0);
-
     // this lane's item of a head that turns, and of one that does not
     Place pt = {lane * VEC, 0, lane * VEC < A.D, false}, pp = pt;
     if (PAIR && (lane + IP) * VEC < A.D) pp.second = IP * VEC;
@@ -153,6 +151,43 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
         else pt.off = 2 * hr + (lane - r) * VEC;
         pt.on = pt.off < A.D;
     }
+    // UH heads' items from `in`, as many as there are
+    constexpr int UH = 128 / (VEC * int(sizeof(T)) * (PAIR ? 2 : 1));
+    Words<T, VEC> x[UH], y[PAIR ? UH : 1];
+    auto load = [&](const T* in, long long ih, const Place& p, int n) {
+#pragma unroll
+        for (int u = 0; u < UH; ++u)
+            if (p.on && u < n) {
+                x[u] = *reinterpret_cast<const Words<T, VEC>*>(in + u * ih);
+                if (PAIR && p.second) y[u] = *reinterpret_cast<const Words<T, VEC>*>(in + u * ih + p.second);
+            }
+    };
+    // The share's heads of each tensor, and where they go.  Nothing turns, or pairs lie
+    // side by side: one flat loop, whose first loads are under way while the slot is
+    // read and the angles are made (20011 tokens' keys and values to 8 bits and back 57
+    // -> 50 us).  Pairs half a head apart: nested loops that load as they go, since
+    // angles and two vectors an item together would spill (11128 tokens of narrow
+    // heads 52 us, by the flat loop 65).
+    auto tensor = [&](int kind) -> const Heads& { return kind == 0 ? A.q : kind == 1 ? A.k : A.v; };
+    int kind = 0, h = 0, hi = 0;
+    auto first_of = [&]() {  // of `kind` or the next that has some
+        for (; kind < 3; ++kind) {
+            const int base = kind == 0 ? 0 : kind == 1 ? A.q.n : A.q.n + A.k.n;
+            h = max(h0 - base, 0);
+            hi = min(h1 - base, tensor(kind).n);
+            if (h < hi) break;
+        }
+    };
+    auto load_here = [&]() {
+        const Heads& X = tensor(kind);
+        const Place& p = kind != 2 && hr ? pt : pp;
+        load(static_cast<const T*>(X.in) + t * X.it + h * X.ih + p.off, X.ih, p, hi - h);
+    };
+    if constexpr (!PAIR) {
+        first_of();
+        load_here();
+    }
+    const SlotRow sr = slot_row(A, t, lane == 0 && blockIdx.y == 0);
     constexpr int NT = PAIR ? VEC : VEC / 2;  // angles of an item, at most
     float cs[NT], sn[NT];
     if (hr && pt.turns) {
@@ -165,131 +200,143 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
         }
     }
 
-    // heads [lo, hi) of one tensor: to `out`, or (bytes, scales) as e4m3
-    auto heads = [&](const Heads& X, int lo, int hi, const Place& p, T* out, long long oh, uint8_t* bytes,
-                     uint8_t* scales) {
-        const T* in = static_cast<const T*>(X.in) + t * X.it + lo * X.ih + p.off;
-        constexpr int UH = 128 / (VEC * int(sizeof(T)) * (PAIR ? 2 : 1));
-#pragma unroll 1
-        for (int h = lo; h < hi; h += UH) {
-            Words<T, VEC> x[UH], y[PAIR ? UH : 1];
+    // UH heads from h on: to `out`, or (bytes, scales) as e4m3
+    auto put = [&](int h, int hi, const Place& p, T* out, long long oh, uint8_t* bytes, uint8_t* scales) {
 #pragma unroll
-            for (int u = 0; u < UH; ++u)
-                if (p.on && h + u < hi) {
-                    x[u] = *reinterpret_cast<const Words<T, VEC>*>(in + u * X.ih);
-                    if (PAIR && p.second) y[u] = *reinterpret_cast<const Words<T, VEC>*>(in + u * X.ih + p.second);
+        for (int u = 0; u < UH; ++u) {
+            if (h + u >= hi) break;  // the same for the whole group
+            float va[VEC], vb[PAIR ? VEC : 1];
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) {
+                const float2 a = get2(x[u], e);
+                va[2 * e] = a.x;
+                va[2 * e + 1] = a.y;
+                if (PAIR) {
+                    const float2 b = get2(y[PAIR ? u : 0], e);
+                    vb[PAIR ? 2 * e : 0] = b.x;
+                    vb[PAIR ? 2 * e + 1 : 0] = b.y;
                 }
-            in += UH * X.ih;
+            }
+            if (p.turns) {
+                if constexpr (PAIR) {
 #pragma unroll
-            for (int u = 0; u < UH; ++u) {
-                if (h + u >= hi) break;  // the same for the whole group
-                float va[VEC], vb[PAIR ? VEC : 1];
-#pragma unroll
-                for (int e = 0; e < VEC / 2; ++e) {
-                    const float2 a = get2(x[u], e);
-                    va[2 * e] = a.x;
-                    va[2 * e + 1] = a.y;
-                    if (PAIR) {
-                        const float2 b = get2(y[PAIR ? u : 0], e);
-                        vb[PAIR ? 2 * e : 0] = b.x;
-                        vb[PAIR ? 2 * e + 1 : 0] = b.y;
+                    for (int e = 0; e < VEC; ++e) {
+                        const float a = va[e], b = vb[e];
+                        va[e] = a * cs[e] - b * sn[e];
+                        vb[e] = a * sn[e] + b * cs[e];
                     }
-                }
-                if (p.turns) {
-                    if constexpr (PAIR) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float a = va[e], b = vb[e];
-                            va[e] = a * cs[e] - b * sn[e];
-                            vb[e] = a * sn[e] + b * cs[e];
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VEC / 2; ++e) {
-                            const float a = va[2 * e], b = va[2 * e + 1];
-                            va[2 * e] = a * cs[e] - b * sn[e];
-                            va[2 * e + 1] = a * sn[e] + b * cs[e];
-                        }
-                    }
-                }
-                if (E4 && bytes) {
-                    // (a maximum drops NaN, which converts to NaN; an infinity shows in it)
-                    auto widest = [&](auto&& size) {
-                        float m = 0.f;
-                        if (p.on) {
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) m = fmaxf(m, size(va[e]));
-                            if (PAIR && p.second) {
-#pragma unroll
-                                for (int e = 0; e < VEC; ++e) m = fmaxf(m, size(vb[PAIR ? e : 0]));
-                            }
-                        }
-#pragma unroll
-                        for (int o = IP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(gmask, m, o, IP));
-                        return m;
-                    };
-                    float m = widest([](float f) { return fabsf(f); });
-                    const bool odd = m == INFINITY;  // seldom: then finite values alone count
-                    if (odd) m = widest([](float f) { return finite_abs(f); });
-                    const int ex = e4m3_exponent(m);
-                    const float down = exp2_int(-ex);
-                    if (p.on) {
-                        Words<uint8_t, VEC> a, b;
-                        auto pack = [&](auto&& two) {
-#pragma unroll
-                            for (int e = 0; e < VEC / 4; ++e) {
-                                a.w[e] = two(va[4 * e] * down, va[4 * e + 1] * down) |
-                                         uint32_t(two(va[4 * e + 2] * down, va[4 * e + 3] * down)) << 16;
-                                if constexpr (PAIR)
-                                    b.w[e] = two(vb[4 * e] * down, vb[4 * e + 1] * down) |
-                                             uint32_t(two(vb[4 * e + 2] * down, vb[4 * e + 3] * down)) << 16;
-                                else b.w[e] = 0;
-                            }
-                        };
-                        if (__builtin_expect(odd, 0)) {
-                            pack([](float lo, float hi) { return pack_e4m3x2(lo, hi); });
-                        } else {
-                            pack([](float lo, float hi) {
-                                uint16_t r;
-                                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-                                return r;
-                            });
-                        }
-                        uint8_t* at = bytes + (h + u) * A.c.head_stride + p.off;
-                        *reinterpret_cast<Words<uint8_t, VEC>*>(at) = a;
-                        if (PAIR && p.second) *reinterpret_cast<Words<uint8_t, VEC>*>(at + p.second) = b;
-                    }
-                    if (lane == 0) scales[(long long)(h + u) * A.c.page] = uint8_t(ex + 127);
-                } else if (p.on) {
-                    Words<T, VEC> a, b;
+                } else {
 #pragma unroll
                     for (int e = 0; e < VEC / 2; ++e) {
-                        set2(a, e, va[2 * e], va[2 * e + 1]);
-                        if constexpr (PAIR) set2(b, e, vb[2 * e], vb[2 * e + 1]);
-                        else set2(b, e, 0.f, 0.f);
+                        const float a = va[2 * e], b = va[2 * e + 1];
+                        va[2 * e] = a * cs[e] - b * sn[e];
+                        va[2 * e + 1] = a * sn[e] + b * cs[e];
                     }
-                    T* at = out + (h + u) * oh + p.off;
-                    *reinterpret_cast<Words<T, VEC>*>(at) = a;
-                    if (PAIR && p.second) *reinterpret_cast<Words<T, VEC>*>(at + p.second) = b;
                 }
+            }
+            if (E4 && bytes) {
+                // (a maximum drops NaN, which converts to NaN; an infinity shows in it)
+                auto widest = [&](auto&& size) {
+                    float m = 0.f;
+                    if (p.on) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) m = fmaxf(m, size(va[e]));
+                        if (PAIR && p.second) {
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e) m = fmaxf(m, size(vb[PAIR ? e : 0]));
+                        }
+                    }
+#pragma unroll
+                    for (int o = IP / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(gmask, m, o, IP));
+                    return m;
+                };
+                float m = widest([](float f) { return fabsf(f); });
+                const bool odd = m == INFINITY;  // seldom: then finite values alone count
+                if (odd) m = widest([](float f) { return finite_abs(f); });
+                const int ex = e4m3_exponent(m);
+                const float down = exp2_int(-ex);
+                if (p.on) {
+                    Words<uint8_t, VEC> a, b;
+                    auto pack = [&](auto&& two) {
+#pragma unroll
+                        for (int e = 0; e < VEC / 4; ++e) {
+                            a.w[e] = two(va[4 * e] * down, va[4 * e + 1] * down) |
+                                     uint32_t(two(va[4 * e + 2] * down, va[4 * e + 3] * down)) << 16;
+                            if constexpr (PAIR)
+                                b.w[e] = two(vb[4 * e] * down, vb[4 * e + 1] * down) |
+                                         uint32_t(two(vb[4 * e + 2] * down, vb[4 * e + 3] * down)) << 16;
+                            else b.w[e] = 0;
+                        }
+                    };
+                    if (__builtin_expect(odd, 0)) {
+                        pack([](float lo, float hi) { return pack_e4m3x2(lo, hi); });
+                    } else {
+                        pack([](float lo, float hi) {
+                            uint16_t r;
+                            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+                            return r;
+                        });
+                    }
+                    uint8_t* at = bytes + (h + u) * A.c.head_stride + p.off;
+                    *reinterpret_cast<Words<uint8_t, VEC>*>(at) = a;
+                    if (PAIR && p.second) *reinterpret_cast<Words<uint8_t, VEC>*>(at + p.second) = b;
+                }
+                if (lane == 0) scales[(long long)(h + u) * A.c.page] = uint8_t(ex + 127);
+            } else if (p.on) {
+                Words<T, VEC> a, b;
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    set2(a, e, va[2 * e], va[2 * e + 1]);
+                    if constexpr (PAIR) set2(b, e, vb[2 * e], vb[2 * e + 1]);
+                    else set2(b, e, 0.f, 0.f);
+                }
+                T* at = out + (h + u) * oh + p.off;
+                *reinterpret_cast<Words<T, VEC>*>(at) = a;
+                if (PAIR && p.second) *reinterpret_cast<Words<T, VEC>*>(at + p.second) = b;
             }
         }
     };
-    // one loop over the three tensors, so that its code is there once
-#pragma unroll 1
-    for (int kind = 0; kind < 3; ++kind) {
-        const Heads& X = kind == 0 ? A.q : kind == 1 ? A.k : A.v;
-        const int base = kind == 0 ? 0 : kind == 1 ? A.q.n : A.q.n + A.k.n;
-        const int lo = max(h0 - base, 0), hi = min(h1 - base, X.n);
+    // the tensor `kind`: f(its heads, an item's place, where they go)
+    auto with = [&](int kind, auto&& f) {
         const bool cached = A.slots && kind;
-        if (lo >= hi || (cached && sr.row < 0)) continue;
-        const bool turning = kind != 2 && hr;
-        const Place p = turning ? pt : pp;
+        if (cached && sr.row < 0) return;
+        const Heads& X = tensor(kind);
+        const Place p = kind != 2 && hr ? pt : pp;
         T* out = cached ? static_cast<T*>(kind == 1 ? A.c.k : A.c.v) + (E4 ? 0 : sr.row)
                         : static_cast<T*>(X.out) + t * X.ot;
         uint8_t* bytes = E4 && cached ? static_cast<uint8_t*>(kind == 1 ? A.c.k : A.c.v) + sr.row : nullptr;
-        heads(X, lo, hi, p, out, cached ? A.c.head_stride : X.oh, bytes,
-              E4 && cached ? (kind == 1 ? A.c.ks : A.c.vs) + sr.scale : nullptr);
+        f(X, p, out, cached ? A.c.head_stride : X.oh, bytes,
+          E4 && cached ? (kind == 1 ? A.c.ks : A.c.vs) + sr.scale : nullptr);
+    };
+    if constexpr (PAIR) {
+#pragma unroll 1
+        for (int k = 0; k < 3; ++k) {
+            const int base = k == 0 ? 0 : k == 1 ? A.q.n : A.q.n + A.k.n;
+            const int lo = max(h0 - base, 0), end = min(h1 - base, tensor(k).n);
+            if (lo >= end) continue;
+            with(k, [&](const Heads& X, const Place& p, T* out, long long oh, uint8_t* bytes, uint8_t* scales) {
+                const T* in = static_cast<const T*>(X.in) + t * X.it + lo * X.ih + p.off;
+#pragma unroll 1
+                for (int i = lo; i < end; i += UH) {
+                    load(in, X.ih, p, end - i);
+                    in += UH * X.ih;
+                    put(i, end, p, out, oh, bytes, scales);
+                }
+            });
+        }
+    } else {
+#pragma unroll 1
+        while (kind < 3) {
+            with(kind, [&](const Heads&, const Place& p, T* out, long long oh, uint8_t* bytes, uint8_t* scales) {
+                put(h, hi, p, out, oh, bytes, scales);
+            });
+            h += UH;
+            if (h >= hi) {
+                ++kind;
+                first_of();
+            }
+            if (kind < 3) load_here();
+        }
     }
 }
 
@@ -357,14 +404,15 @@ __global__ void __launch_bounds__(ROT_THREADS) k_rotate_any(const __grid_constan
     }
 }
 
-// Rows of T slots: one thread per 16 bytes of a (token, head)'s row.  I: the type
+// Rows of T slots: one thread per 16 bytes of a (token, head)'s row as it is
+// written, so that a warp's stores leave no gaps.  I: the type
 // of the indexes (32 bits where they are enough: a division of 64 costs more than
 // the copy).
 template <typename C, typename T, typename I>
 __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ CacheView c, long long T_,
                                                  const long long* slots, T* out_k, T* out_v) {
     begin_after_previous();
-    constexpr int VEC = 16 / sizeof(C);
+    constexpr int VEC = 16 / sizeof(T);
     const I vecs = c.D / VEC, heads = c.heads, n = I(T_) * heads * vecs;
     for (I i = blockIdx.x * I(256) + threadIdx.x; i < n; i += gridDim.x * I(256)) {
         const I th = i / vecs, t = th / heads;
@@ -373,7 +421,7 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ CacheVi
         Words<C, VEC> k, v;
         float fk = 1.f, fv = 1.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) k.w[e] = v.w[e] = 0;
+        for (int e = 0; e < VEC * int(sizeof(C)) / 4; ++e) k.w[e] = v.w[e] = 0;
         if (slot >= 0 && slot < c.slots) {
             const long long p = sizeof(I) == 4 ? (long long)(uint32_t(slot) / uint32_t(c.page)) : slot / c.page;
             const int o = int(slot - p * c.page);
@@ -606,7 +654,7 @@ namespace {
 template <typename C, typename T>
 cudaError_t launch_read_to(const CacheView& c, int64_t T_, const int64_t* slots, void* out_k, void* out_v,
                            cudaStream_t st) {
-    const long long n = T_ * c.heads * (c.D / (16 / int(sizeof(C))));
+    const long long n = T_ * c.heads * (c.D / (16 / int(sizeof(T))));
     const unsigned grid = unsigned(std::min<long long>((n + 255) / 256, 1ll << 22));
     const long long* s = reinterpret_cast<const long long*>(slots);
     T *k = static_cast<T*>(out_k), *v = static_cast<T*>(out_v);
