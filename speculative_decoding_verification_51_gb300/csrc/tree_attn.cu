@@ -211,12 +211,14 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.tiles_r = (A.rows + R - 1) / R;
     // A copy lies in one page: k_attn_rows takes chunks of 16 tokens,
     // k_attn_tiles the longest power of two up to a tile that divides a page.
-    // What another item costs a CTA of the tile kernels, in tiles: its queries, and
-    // a pipeline that runs dry and fills again.  Measured (us without a lead / with
-    // 3 / 6 / 9 for 8 bits, 2 / 5 / 9 for 16): 32 trees of 32 over 1000 to 16384 tokens
-    // 263 / 234 / 223 / 225 and 241 / 228 / 214 / 215, 200 such trees over 30 to 3000
-    // tokens of 16 bits 289 / 271 / 260 / 265.  k_attn_rows reads HBM meanwhile.
-    A.lead = !tiles ? 0 : e4 ? 6 : 5;
+    // What another item costs a CTA, in tiles: its queries, a pipeline that runs dry
+    // and fills again, the join of the warps.  Measured (us without a lead / with 2 /
+    // 4 / 8, or for the tile kernels 3 / 6 / 9 and 2 / 5 / 9):
+    //   k_attn_rows, 256 chains over 64 to 4096 tokens 352 / 337 / 330 / 344, 64 over
+    //     20 to 2000 tokens 87 / 66 / 56 / 60, heads of 256 178 / 147 / 153 / 165
+    //   8 bits, 32 trees of 32 over 1000 to 16384 tokens 263 / 234 / 223 / 225
+    //   16 bits, the same 241 / 228 / 214 / 215
+    A.lead = !tiles ? (A.D > 128 ? 2 : 4) : e4 ? 6 : 5;
     A.box = tiles ? std::min(TREE_TILE, A.page & -A.page) : 16;
     spec_status r = cache_map(&L.mk, *cache, cache->k, A.box);
     if (r == SPEC_OK) r = cache_map(&L.mv, *cache, cache->v, A.box);
