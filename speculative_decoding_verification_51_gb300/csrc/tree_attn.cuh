@@ -65,6 +65,14 @@ struct Share {
     int ctas, lead;
 };
 
+// a / b and a % b, in 32 bits where they are enough
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)(uint32_t(a) / uint32_t(b));
+}
+__device__ __forceinline__ long long remainder(long long a, long long b) {
+    return (a | b) >> 32 ? a % b : (long long)(uint32_t(a) % uint32_t(b));
+}
+
 __device__ __forceinline__ Share share_of(const AttnArgs& A, int tiles) {
     const long long hr = (long long)A.Hkv * A.tiles_r;
     Share s;
@@ -73,8 +81,8 @@ __device__ __forceinline__ Share share_of(const AttnArgs& A, int tiles) {
     s.ctas = int(s.total < (long long)gridDim.x ? s.total : (long long)gridDim.x);
     s.begin = s.end = 0;
     if ((int)blockIdx.x < s.ctas) {
-        s.begin = s.total * blockIdx.x / s.ctas;
-        s.end = s.total * (blockIdx.x + 1) / s.ctas;
+        s.begin = quotient(s.total * blockIdx.x, s.ctas);
+        s.end = quotient(s.total * (blockIdx.x + 1), s.ctas);
     }
     return s;
 }
@@ -102,18 +110,20 @@ struct Lists {
 };
 
 // What request b (tiles lo to hi of the plan's list) says of a share: whether it
-// holds its first place, and where its ends are moved to.
-__device__ __forceinline__ void find_ends(const AttnArgs& A, PlanWindow& w, const Share& s, int b, int lo, int hi) {
+// holds its first place (then the window begins with request `b0`), and where its ends
+// are moved to.
+__device__ __forceinline__ void find_ends(const AttnArgs& A, PlanWindow& w, const Share& s, int b, int lo, int hi,
+                                          int b0) {
     const long long hr = (long long)A.Hkv * A.tiles_r, from = (lo + (long long)s.lead * b) * hr;
     const int each = hi - lo + s.lead;
     const long long to = from + each * hr;
     if (from <= s.begin && s.begin < to) {
-        w.b0 = b;
-        const long long into = (s.begin - from) % each;
+        w.b0 = b0;
+        const long long into = remainder(s.begin - from, each);
         w.begin = s.begin + max(s.lead - into, 0ll);
     }
     if (from < s.end && s.end <= to) {  // (the end of an item is one already)
-        const long long into = (s.end - from) % each;
+        const long long into = remainder(s.end - from, each);
         w.end = s.end - (into <= s.lead ? into : 0ll);
     }
 }
@@ -129,18 +139,14 @@ __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Shar
                 w.nodes[threadIdx.x] = A.plan.nodes[threadIdx.x];
             }
         }
-        __syncthreads();
-        s = share_of(A, w.tiles[A.B]);
-        if (s.begin >= s.end) return false;
-        if (s.lead) {
-            if (int(threadIdx.x) < A.B) find_ends(A, w, s, threadIdx.x, w.tiles[threadIdx.x], w.tiles[threadIdx.x + 1]);
-            __syncthreads();
-            s.begin = w.begin;
-            s.end = w.end;
-            __syncthreads();
-        }
         if (threadIdx.x == 0) w.b0 = 0;
         __syncthreads();
+        s = share_of(A, w.tiles[A.B]);
+        if (s.begin >= s.end || !s.lead) return s.begin < s.end;
+        if (int(threadIdx.x) < A.B) find_ends(A, w, s, threadIdx.x, w.tiles[threadIdx.x], w.tiles[threadIdx.x + 1], 0);
+        __syncthreads();
+        s.begin = w.begin;
+        s.end = w.end;
         return s.begin < s.end;
     }
     const int last = A.plan.tiles[A.B];
@@ -151,7 +157,7 @@ __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Shar
             s = share_of(A, last);
             any = true;
         }
-        find_ends(A, w, s, i, lo, hi);
+        find_ends(A, w, s, i, lo, hi, i);
     }
     s = share_of(A, last);
     if (s.begin >= s.end) return false;
@@ -172,7 +178,7 @@ __device__ __forceinline__ bool read_plan(const AttnArgs& A, PlanWindow& w, Shar
 
 // the CTA whose share holds place g
 __device__ __forceinline__ int cta_of(const Share& s, long long g) {
-    return int(((g + 1) * s.ctas - 1) / s.total);
+    return int(quotient((g + 1) * s.ctas - 1, s.total));
 }
 
 // The segment that starts at place g (a tile, or the lead before an item's first
@@ -190,7 +196,7 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Lists& L,
     x.tiles = hi - lo;
     const int each = x.tiles + s.lead;
     const long long r = g - (lo + (long long)s.lead * b) * hr;
-    const int item = r >> 31 ? int(r / each) : int(uint32_t(r) / uint32_t(each));
+    const int item = int(quotient(r, each));
     const int at = int(r - (long long)item * each) - s.lead;
     x.t0 = max(at, 0);
     x.g = g + (x.t0 - at);
