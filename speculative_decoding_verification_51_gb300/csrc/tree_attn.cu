@@ -203,11 +203,15 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                          align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
     A.status = dev_status;
-    // Many rows go to the tcgen05 kernel (128 a tile), which takes up to 128 channels.
+    // More than 16 rows go to the tcgen05 kernels (128 a tile, heads of up to 128),
+    // since k_attn_rows reads the cache again for every 16.  Measured (us, k_attn_rows /
+    // tiles; 32 requests of 1000 to 16384 tokens, 200 of 30 to 1000):
+    //   16 rows, 16 bits 178 / 200 and 107 / 122, 8 bits 166 / 198 and 116 / 181
+    //   20 to 32 rows in tiles of 32, 16 bits 212 / 202 and 148 / 122, 8 bits 233 / 199
+    //     and 164 / 185
     const bool e4 = cache->dtype == SPEC_E4M3;
-    const bool tiles = A.rows > 32 && A.D <= 128;
-    const int mt = tiles ? 0 : A.rows <= 16 || A.D > 128 ? 1 : 2;
-    const int R = tiles ? 128 : mt * 16;
+    const bool tiles = A.rows > 16 && A.D <= 128;
+    const int R = tiles ? 128 : 16;
     A.tiles_r = (A.rows + R - 1) / R;
     // A copy lies in one page: k_attn_rows takes chunks of 16 tokens,
     // k_attn_tiles the longest power of two up to a tile that divides a page.
@@ -225,9 +229,9 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     if (r != SPEC_OK) return r;
     L.ctas = sms;
     L.st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = e4                         ? launch_attn_e4m3(L, mt)
-                          : cache->dtype == SPEC_F16 ? launch_attn_f16(L, mt)
-                                                     : launch_attn_bf16(L, mt);
+    const cudaError_t e = e4                         ? launch_attn_e4m3(L, tiles)
+                          : cache->dtype == SPEC_F16 ? launch_attn_f16(L, tiles)
+                                                     : launch_attn_bf16(L, tiles);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -362,9 +362,9 @@ struct AttnLaunch {
 // k_attn_tiles leaves the parts of items to k_attn_join, launched behind it
 // (tree_attn.cu); rows of `width` channels.
 cudaError_t launch_attn_join(const AttnLaunch& L, int width);
-// mt: row tiles of 16 of k_attn_rows (1 or 2), or 0 for k_attn_tiles
-cudaError_t launch_attn_bf16(const AttnLaunch& L, int mt);
-cudaError_t launch_attn_f16(const AttnLaunch& L, int mt);
-cudaError_t launch_attn_e4m3(const AttnLaunch& L, int mt);
+// by k_attn_tiles, or k_attn_rows
+cudaError_t launch_attn_bf16(const AttnLaunch& L, bool tiles);
+cudaError_t launch_attn_f16(const AttnLaunch& L, bool tiles);
+cudaError_t launch_attn_e4m3(const AttnLaunch& L, bool tiles);
 
 }  // namespace sv

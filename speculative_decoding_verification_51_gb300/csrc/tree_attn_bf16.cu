@@ -3,8 +3,8 @@
 #include "tree_attn_tiles.cuh"
 
 namespace sv {
-cudaError_t launch_attn_bf16(const AttnLaunch& L, int mt) {
-    if (mt == 0) return L.A.D <= 64 ? launch_tiles<SPEC_BF16, 64>(L) : launch_tiles<SPEC_BF16, 128>(L);
-    return launch_rows_any<SPEC_BF16>(L, mt);
+cudaError_t launch_attn_bf16(const AttnLaunch& L, bool tiles) {
+    if (tiles) return L.A.D <= 64 ? launch_tiles<SPEC_BF16, 64>(L) : launch_tiles<SPEC_BF16, 128>(L);
+    return launch_rows_any<SPEC_BF16>(L);
 }
 }  // namespace sv

@@ -3,8 +3,8 @@
 #include "tree_attn_tiles_e4m3.cuh"
 
 namespace sv {
-cudaError_t launch_attn_e4m3(const AttnLaunch& L, int mt) {
-    if (mt == 0) return L.A.D <= 64 ? launch_tiles_e4m3<64>(L) : launch_tiles_e4m3<128>(L);
-    return launch_rows_any<SPEC_E4M3>(L, mt);
+cudaError_t launch_attn_e4m3(const AttnLaunch& L, bool tiles) {
+    if (tiles) return L.A.D <= 64 ? launch_tiles_e4m3<64>(L) : launch_tiles_e4m3<128>(L);
+    return launch_rows_any<SPEC_E4M3>(L);
 }
 }  // namespace sv

@@ -38,10 +38,12 @@ namespace sv {
 
 constexpr float AR_SLACK = 6.f;
 
-template <int KIND, int NK, int MT>
+constexpr int AR_MT = 1;  // row tiles of 16: a thread has no registers for two of wide heads
+
+template <int KIND, int NK>
 struct RowsShape {
     static constexpr bool E4 = KIND == SPEC_E4M3;
-    static constexpr int DP = NK * 16, R = MT * 16;
+    static constexpr int DP = NK * 16, R = AR_MT * 16;
     // eight warps, or four where the stages of eight would not fit
     static constexpr int WARPS = !E4 && NK > 8 ? 4 : 8, THREADS = WARPS * 32;
     static constexpr int BOXES = E4 ? (DP + 127) / 128 : (DP + 63) / 64;  // 128 bytes of a row each
@@ -55,7 +57,7 @@ struct RowsShape {
     static_assert(STAGES >= 2, "no room for a ring");
     static constexpr size_t SMEM = 1024 + size_t(WARPS) * STAGES * STAGE + FIXED;
     // the query's fragments stay in registers where they are few
-    static constexpr bool QREG = MT * NK <= 8;
+    static constexpr bool QREG = AR_MT * NK <= 8;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -84,11 +86,11 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int KIND, int NK, int MT>
-__global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
+template <int KIND, int NK>
+__global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
     k_attn_rows(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                 const __grid_constant__ AttnArgs A) {
-    using S = RowsShape<KIND, NK, MT>;
+    using S = RowsShape<KIND, NK>;
     constexpr bool E4 = S::E4, F16 = KIND != SPEC_BF16;
     constexpr int DP = S::DP, R = S::R, OP = S::OP, QP = DP + 8, AR_WARPS = S::WARPS, AR_THREADS = S::THREADS;
     extern __shared__ uint8_t smem_raw[];
@@ -255,17 +257,17 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
 
         // ---- this warp's chunks
         const uint32_t qa = smem_u32(sm_q) + (((lane & 7) + ((lane >> 3) & 1) * 8) * QP + (lane >> 4) * 8) * 2;
-        uint32_t qf[S::QREG ? MT : 1][S::QREG ? NK : 1][4];
+        uint32_t qf[S::QREG ? AR_MT : 1][S::QREG ? NK : 1][4];
         if constexpr (S::QREG) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < AR_MT; ++m)
 #pragma unroll
                 for (int k = 0; k < NK; ++k) ldsm4(qa + (m * 16 * QP + k * 16) * 2, qf[m][k]);
         }
-        float o[MT][2 * NK][4], ref[MT][2], tot[MT][2], rc[MT][2];
-        uint32_t mask[MT][2];
+        float o[AR_MT][2 * NK][4], ref[AR_MT][2], tot[AR_MT][2], rc[AR_MT][2];
+        uint32_t mask[AR_MT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < AR_MT; ++m) {
 #pragma unroll
             for (int n = 0; n < 2 * NK; ++n)
 #pragma unroll
@@ -294,9 +296,9 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
             const bool tail = t0 + 16 > s.ctx;
 
             // scores
-            float p[MT][2][4];
+            float p[AR_MT][2][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < AR_MT; ++m)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                                        b10 = e4m3x2_to_f16x2(uint16_t(w[2 * i + 1])),
                                        b11 = e4m3x2_to_f16x2(uint16_t(w[2 * i + 1] >> 16));
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
+                        for (int m = 0; m < AR_MT; ++m) {
                             uint32_t a[4];
                             if constexpr (S::QREG) {
 #pragma unroll
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                     const int j = 2 * k + ((lane >> 3) & 1);
                     ldsm4(ka + (j >> 3) * 2048 + tk * 128 + (((j & 7) ^ (tk & 7)) << 4), w);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
+                    for (int m = 0; m < AR_MT; ++m) {
                         uint32_t a[4];
                         if constexpr (S::QREG) {
 #pragma unroll
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                 }
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int m = 0; m < AR_MT; ++m) {
                 bool raise = false;
                 float top[2];
 #pragma unroll
@@ -469,9 +471,9 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
             }
             // sums
             const uint32_t va = smem_u32(vp);
-            uint32_t a[MT][4];
+            uint32_t a[AR_MT][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int m = 0; m < AR_MT; ++m) {
                 a[m][0] = pack16<F16>(p[m][0][0], p[m][0][1]);
                 a[m][1] = pack16<F16>(p[m][0][2], p[m][0][3]);
                 a[m][2] = pack16<F16>(p[m][1][0], p[m][1][1]);
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                                        e1 = e4m3x2_to_f16x2(uint16_t(hi)),
                                        o1 = e4m3x2_to_f16x2(uint16_t(hi >> 16));
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
+                        for (int m = 0; m < AR_MT; ++m) {
                             mma16<true>(o[m][2 * (k + i)], a[m], e0, e1);
                             mma16<true>(o[m][2 * (k + i) + 1], a[m], o0, o1);
                         }
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
                     const int j = 2 * k + (lane >> 4);
                     ldsm4t(va + (j >> 3) * 2048 + tv * 128 + (((j & 7) ^ (tv & 7)) << 4), w);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
+                    for (int m = 0; m < AR_MT; ++m) {
                         mma16<F16>(o[m][2 * k], a[m], w[0], w[1]);
                         mma16<F16>(o[m][2 * k + 1], a[m], w[2], w[3]);
                     }
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
 
         // ---- join the warps
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < AR_MT; ++m)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float l = tot[m][x];
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
         for (int half = AR_WARPS / 4 - 1; half >= 0; --half) {
             if ((warp >> 2) == half) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < AR_MT; ++m)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int r = m * 16 + x * 8 + (lane >> 2);
@@ -633,29 +635,29 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK, MT>::THREADS, 1)
     }
 }
 
-template <int KIND, int NK, int MT>
+template <int KIND, int NK>
 cudaError_t launch_rows(const AttnLaunch& L) {
-    using S = RowsShape<KIND, NK, MT>;
+    using S = RowsShape<KIND, NK>;
     static bool ready[64] = {};  // per device; setting it twice does no harm
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(k_attn_rows<KIND, NK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM));
+        e = cudaFuncSetAttribute(k_attn_rows<KIND, NK>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::SMEM));
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    return launch_behind(k_attn_rows<KIND, NK, MT>, dim3(unsigned(L.ctas)), S::THREADS, S::SMEM, L.st, L.mk, L.mv, L.A);
+    return launch_behind(k_attn_rows<KIND, NK>, dim3(unsigned(L.ctas)), S::THREADS, S::SMEM, L.st, L.mk, L.mv, L.A);
 }
 
 template <int KIND>
-cudaError_t launch_rows_any(const AttnLaunch& L, int mt) {
+cudaError_t launch_rows_any(const AttnLaunch& L) {
     const int D = L.A.D;
-    if (D > 128) return launch_rows<KIND, 16, 1>(L);
-    if (mt == 1)
-        return D <= 64 ? launch_rows<KIND, 4, 1>(L) : D <= 96 ? launch_rows<KIND, 6, 1>(L) : launch_rows<KIND, 8, 1>(L);
-    return D <= 64 ? launch_rows<KIND, 4, 2>(L) : D <= 96 ? launch_rows<KIND, 6, 2>(L) : launch_rows<KIND, 8, 2>(L);
+    return D <= 64    ? launch_rows<KIND, 4>(L)
+           : D <= 96  ? launch_rows<KIND, 6>(L)
+           : D <= 128 ? launch_rows<KIND, 8>(L)
+                      : launch_rows<KIND, 16>(L);
 }
 
 }  // namespace sv
