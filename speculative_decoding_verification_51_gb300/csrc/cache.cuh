@@ -55,21 +55,6 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
-// N consecutive elements as one vector access of N * sizeof(T) bytes (16 at a
-// time where that is more); the address is aligned to the access.
-template <typename T, int N>
-struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
-    T e[N];
-};
-template <typename T, int N>
-__device__ __forceinline__ Vec<T, N> load_vec(const T* p) {
-    return *reinterpret_cast<const Vec<T, N>*>(p);
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_vec(T* p, const Vec<T, N>& v) {
-    *reinterpret_cast<Vec<T, N>*>(p) = v;
-}
-
 // ---------------------------------------------------------------- e4m3 rows
 // An e4m3 row holds x 2^-e with e the least integer for which max |x| <= 448
 // 2^e.  A power of two shifts the exponent alone, so x 2^-e is exact and the

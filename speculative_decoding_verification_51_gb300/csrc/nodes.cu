@@ -15,6 +15,10 @@
 // d.  Its index is d or more, so that a row is always read before a row with a
 // greater d is written over it: a thread keeps its 16 bytes of the row
 // through the whole path, in order, and no thread waits for another.
+//
+// Both are bound by latency: 256 trees of 32 nodes over up to 4000 tokens take
+// 3.7 us of device time, the commit of their paths in one 8-bit cache 4.5 (a table
+// entry, a slot and a row have to be read one after the other).
 #include <algorithm>
 #include <cfloat>
 

@@ -12,6 +12,9 @@
 //                 between segments the next rows of Q, and the finished rows of O
 // S of tile i + 1 is computed while the weights of tile i are made.
 //
+// Two requests of 9 nodes and 8 query heads a key head over 131 K tokens take 167 us:
+// 0.95 of the measured copy rate, a quarter of the tensor rate.
+//
 // As in k_attn_rows the reference of a row is raised only when a score passes
 // it by 2^8, so that O in TMEM is seldom rescaled; a weight is then at most
 // 2^8, which bf16 and f16 hold and whose rounding is relative.
