@@ -257,13 +257,15 @@ __device__ __forceinline__ void store4(const AttnArgs& A, long long at, const fl
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + at) = w;
 }
 
-// One row's finished values: 4 channels from d on.
+// One row's finished values: 4 channels from d on.  Zeros for a node past the
+// tree (its row ran over the context too, so that its sums and total may be NaN)
+// and for a row that saw nothing; NaN where the total is.
 __device__ __forceinline__ void put_row(const AttnArgs& A, const Segment& s, int row, int d,
                                         const float (&o)[4], float total) {
     if (row >= A.rows || d >= A.D) return;
     const int v = row / A.G, g = row - v * A.G;
-    const float f = v < s.n && total != 0.f ? 1.f / total : 0.f;
-    const bool none = f == 0.f && !(total != total);
+    const bool none = v >= s.n || total == 0.f;
+    const float f = none ? 0.f : 1.f / total;
     float x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = none ? 0.f : o[e] * f;

@@ -228,8 +228,8 @@ __device__ __forceinline__ void put_tile(const AttnArgs& A, const Share& share, 
     const bool whole = s.t0 == 0 && s.t1 == s.tiles;
     const long long slot = part_slot(share, s);
     const int row = s.rt * 128 + r;
-    const float inv = node < s.n && tot != 0.f ? 1.f / tot : 0.f;
-    const bool none = inv == 0.f && tot == tot;
+    const bool none = node >= s.n || tot == 0.f;  // as in put_row
+    const float inv = none ? 0.f : 1.f / tot;
     const long long at = (((long long)s.b * A.N + node) * A.Hq + s.h * A.G + row - node * A.G) * A.D;
 #pragma unroll 1
     for (int j = from; j < to; j += 32) {
