@@ -1,6 +1,6 @@
 // tree_attn_tiles_e4m3.cuh -- k_attn_tiles_e4m3: k_attn_tiles over an 8-bit cache.
 //
-// 32 trees of 32 nodes (128 rows a key head) over 1000 to 16384 tokens take 210 us: 0.43
+// 32 trees of 32 nodes (128 rows a key head) over 1000 to 16384 tokens take 214 us: 0.42
 // of the measured copy rate and 0.28 of the tensor rate.  What bounds it is a
 // tile's softmax, some 2450 cycles of which HBM would need 1050.
 //
@@ -19,12 +19,20 @@
 // accumulator.  K's scale comes afterwards: a tile's scale bytes are turned to
 // factors, and the exponent of a weight is (s rc) ck[t] - m.
 //
-// Values.  v 2^e is stored as f16 v 2^(e - E), E the largest exponent of the
-// tile's rows: exact for rows within 2^15 of the largest, and off by 2^-33 of the
-// largest below.  2^E joins the exponents of the tile's weights, w_t = 2^(s_t + E -
-// m), so that all tiles' sums are in one unit; the total takes 2^-E times the
-// tile's weights.  E is taken as -100 or more, so that a tile of zeros does not
-// push the total out of float32.
+// Values.  Where the exponents of a tile's rows lie within 8 of one another, v 2^e is
+// stored as f16 v 2^(e - E), E the largest of them: exact.  2^E joins the exponents of the
+// tile's weights, w_t = 2^(s_t + E - m), so that all tiles' sums are in one unit; the
+// total takes 2^-E times the tile's weights.  In any other tile (rows of zeros have
+// the least exponent there is, so theirs are such tiles) E could be one that a row
+// does not see, or that of a token of no weight, and would take the bits of all the
+// others: there the values stay as they lie and w_t = 2^(s_t + e_t - m), with a second
+// exponential for the total.  (That path for every tile takes the trees above 254 us
+// instead of 214.)  E and e_t are taken as -92 or more in m, so that zeros do not push
+// the total out of float32.
+//
+// Weights are f16.  A raised reference leaves the largest at 2^8 or less, and they
+// may grow to 2^15: so 8 octaves that E may exceed a row's own exponents by, or the
+// tail of a long context 2^25 times below its largest weight, still count.
 //
 // Softmax.  Two threads a row, each half of the tile's tokens, since one warp a
 // scheduler leaves it idle most of the time.  They keep one reference, which is
@@ -50,6 +58,9 @@ struct TilesE4Shape {
 };
 
 // D f32, A and B e4m3, both K-major, M = N = 128
+constexpr int AT_SPREAD = 8;               // exponents of one tile's values that one unit serves
+constexpr int AT_WIDE = 1 << 20;           // in place of the unit: the values have exponents of their own
+constexpr float AT_TOP = 8.f, AT_LEAST = -92.f;
 constexpr uint32_t AT_ID_E4 = (1u << 4) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 __device__ __forceinline__ void at_mma_e4(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
     asm volatile(
@@ -93,6 +104,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
     uint8_t* sm_q = sm_v + 2 * S::OPERAND;      // [terms][128 rows][128] queries
     __shared__ __align__(16) uint8_t sm_sc[NR * 256];     // scale bytes
     __shared__ __align__(16) float sm_ck[2][128];         // K's factors
+    __shared__ __align__(16) float sm_ve[2][128];         // V's exponents, in a tile that has no unit
     __shared__ __align__(8) uint64_t rkf[NR], rke[NR], rvf[NR], rve[NR], vf[2], ve[2];
     __shared__ __align__(8) uint64_t sf[2], pf[2], pv[2], qf, of, fin[2];
     __shared__ uint32_t tmem_base;
@@ -384,7 +396,10 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 }
                 at_after();
                 if (__builtin_expect(tail, 0)) hide_unseen(sa, t0 + half * 64 - s.ctx, mask, 64);
-                const float unit = float(unit_v[i & 1]);
+                const int unit_i = unit_v[i & 1];
+                const bool wide = unit_i == AT_WIDE;
+                const float unit = wide ? 0.f : float(unit_i);
+                const float* ve = sm_ve[i & 1] + half * 64;
                 const float4* ck = reinterpret_cast<const float4*>(sm_ck[i & 1] + half * 64);
                 const uint64_t rc2 = f2_pack(rc, rc);
                 // exponents of tokens j .. j + 31 by `base`, in place of their scores
@@ -406,39 +421,64 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                         x[4 * e + 3] = __float_as_uint(b);
                     }
                 };
-                // The weights by the reference as it is.  None is above 2^8 where their
+                // The weights by the reference as it is.  None is above 2^15 where their
                 // sum is not; where some row's sum is (or it has no reference yet), its
-                // reference is raised to the largest exponent and they are made again.
-                float s0, s1;
+                // reference is raised to the largest exponent less 8 and they are made again.
+                // (So also where 2^(s_t - m), of which a tile without a unit has the sum `all`,
+                // nears float32's limit: zeros with all the weight.)
+                float s0, s1, all = 0.f;
                 for (bool again = false;; again = true) {
                     const float base = ref == -INFINITY ? 0.f : ref;
                     uint64_t sum = f2_pack(0.f, 0.f);
+                    if (__builtin_expect(!wide, 1)) {
 #pragma unroll 1
-                    for (int j = 0; j < 64; j += 32) {
-                        uint32_t x[32], p[16];
-                        exponents(x, j, base);
+                        for (int j = 0; j < 64; j += 32) {
+                            uint32_t x[32], p[16];
+                            exponents(x, j, base);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float a = ex2_approx(__uint_as_float(x[2 * e])), b = ex2_approx(__uint_as_float(x[2 * e + 1]));
-                            sum = f2_add(sum, f2_pack(a, b));
-                            p[e] = pack16<true>(a, b);
+                            for (int e = 0; e < 16; ++e) {
+                                const float a = ex2_approx(__uint_as_float(x[2 * e])), b = ex2_approx(__uint_as_float(x[2 * e + 1]));
+                                sum = f2_add(sum, f2_pack(a, b));
+                                p[e] = pack16<true>(a, b);
+                            }
+                            at_st16(pa + j / 2, p);
                         }
-                        at_st16(pa + j / 2, p);
+                    } else {
+                        all = 0.f;
+#pragma unroll 1
+                        for (int j = 0; j < 64; j += 32) {
+                            uint32_t x[32], p[16];
+                            exponents(x, j, base);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float a = __uint_as_float(x[2 * e]), b = __uint_as_float(x[2 * e + 1]);
+                                all += ex2_approx(a) + ex2_approx(b);
+                                const float wa = ex2_approx(a + ve[j + 2 * e]), wb = ex2_approx(b + ve[j + 2 * e + 1]);
+                                sum = f2_add(sum, f2_pack(wa, wb));
+                                p[e] = pack16<true>(wa, wb);
+                            }
+                            at_st16(pa + j / 2, p);
+                        }
                     }
                     f2_unpack(sum, s0, s1);
-                    if (again || __builtin_expect(!any_of_rows(!(s0 + s1 <= 256.f) || ref == -INFINITY), 1)) break;
+                    if (again || __builtin_expect(!any_of_rows(!(s0 + s1 <= 32768.f && all <= 0x1p107f) || ref == -INFINITY), 1)) break;
                     float mx = -INFINITY;
 #pragma unroll 1
                     for (int j = 0; j < 64; j += 32) {
                         uint32_t x[32];
                         exponents(x, j, base);
+                        if (wide) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = __float_as_uint(__uint_as_float(x[e]) + fmaxf(ve[j + e], AT_LEAST));
+                        }
 #pragma unroll
                         for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
                     }
                     sm_ref[half][r] = mx;
                     sync_rows();  // (the next write is behind the next vote)
                     mx = fmaxf(mx, sm_ref[half ^ 1][r]);
-                    const float to = fmaxf(ref, base + ceilf(mx));  // whole, so that sums are rescaled exactly
+                    const float to = fmaxf(ref, base + ceilf(mx) - AT_TOP);  // whole, so that sums are rescaled exactly
                     const float f = ref == to ? 1.f : exp2_down(to - ref);
                     tot *= f;
                     if (t > s.t0) {  // O holds sums by the old reference
@@ -447,7 +487,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     }
                     ref = to;
                 }
-                tot = fmaf(s0 + s1, exp2_int(-unit_v[i & 1]), tot);
+                tot = wide ? tot + all : fmaf(s0 + s1, exp2_int(-unit_i), tot);
                 if (__builtin_expect(tail && half == 0, 0)) {
                     const uint32_t bad = clean_values<true, DP>(sm_v + (i & 1) * S::OPERAND, t0, s, tid);
                     if (bad) atomicOr(&bad_nodes[seg & 1], bad);
@@ -502,25 +542,33 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 const uint8_t* sc = sm_sc + rs * 256 + 128;
                 uint8_t* out = sm_v + st * S::OPERAND;
                 wait(&rvf[rs], i / NR);
-                // the largest scale byte of the tile's valid tokens
-                uint32_t z = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
+                // the largest and the least scale byte of the tile's valid tokens
+                const uint32_t bytes = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
                 const int left = valid - lane * 4;
-                z = left >= 4 ? z : left <= 0 ? 0u : z & ((1u << (8 * left)) - 1u);
+                const uint32_t past = left >= 4 ? 0u : left <= 0 ? ~0u : ~0u << (8 * left);
+                uint32_t z = bytes & ~past, y = bytes | past;
                 z = __vmaxu4(z, z >> 16);
+                y = __vminu4(y, y >> 16);
                 const int top = int(__reduce_max_sync(0xffffffffu, max(z & 255u, z >> 8 & 255u)));
-                const int unit = max(min(max(top, 1), 253) - 127, -100);
+                const int low = int(__reduce_min_sync(0xffffffffu, min(y & 255u, y >> 8 & 255u)));
+                const bool wide = min(max(top, 1), 253) - min(max(low, 1), 253) > AT_SPREAD;
+                const int unit = wide ? AT_WIDE : max(min(max(top, 1), 253) - 127, int(AT_LEAST));
                 uint4 q[2][2];
                 uint32_t f[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int tk = tok0 + k * 64;
-                    f[k] = half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
+                    f[k] = wide ? 0x3c003c00u : half2_exp2(min(min(max(int(sc[tk]), 1), 253) - 127 - unit, 0));
 #pragma unroll
                     for (int h = 0; h < S::HALVES; ++h)
                         q[k][h] = *reinterpret_cast<const uint4*>(raw + tk * 128 + (((x + h * 4) ^ (tk & 7)) << 4));
                 }
                 wait(&ve[st], (i >> 1) ^ 1u);
                 if (tid == 0) unit_v[st] = unit;
+                if (wide && warp == 13)
+                    *reinterpret_cast<float4*>(&sm_ve[st][lane * 4]) =
+                        make_float4(float(min(max(int(bytes & 255u), 1), 253) - 127), float(min(max(int(bytes >> 8 & 255u), 1), 253) - 127),
+                                    float(min(max(int(bytes >> 16 & 255u), 1), 253) - 127), float(min(max(int(bytes >> 24), 1), 253) - 127));
                 if (warp == 12) {  // K's factors, 4 tokens a lane (1 past the request's end)
                     wait(&rkf[rs], i / NR);
                     const uint32_t w = *reinterpret_cast<const uint32_t*>(sm_sc + rs * 256 + lane * 4);

@@ -61,3 +61,138 @@ def test_nodes_past_the_tree_are_zero_whatever_the_context_holds(ctx, N, Hq, qdt
     fin = torch.isfinite(ref)
     assert torch.equal(torch.isnan(out.double()), torch.isnan(ref))
     assert bool(((out.double() - ref).abs()[fin] <= bound[fin]).all())
+
+
+# ---------------------------------------------------------------- values of very different sizes
+
+@pytest.mark.parametrize("kind,power", [(BF, 40), (HF, 9), (E4, 7), (E4, 12), (E4, 17), (E4, 40), (E4, 90)])
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+@pytest.mark.parametrize("ctx", [[0, 40], [101, 300], [2000, 21000]])
+def test_unseen_nodes_of_large_values_have_no_effect(ctx, N, Hq, kind, power):
+    """A sibling's values 2^power times the others': the nodes that do not see it
+    lose nothing by it."""
+    qdt = BF if kind == E4 else kind
+    D, page = 128, 16
+    q, cache, p, table, ctx, nodes = attn_case(2, N, Hq, 2, D, page, qdt, kind, ctx, [N, N - 1], 17)
+    src = FL if kind == E4 else kind
+    g = gen(power)
+    for b in range(2):
+        for u in (4, int(nodes[b]) - 1):
+            s = slots_of(table, ctx, page, b, [int(ctx[b]) + u])
+            big = randn((1, 2, D), FL, g) * 2.0 ** power
+            binding.kv_write(cache, randn((1, 2, D), src, g), big.to(src), s)
+    check_attention(q, cache, p, table, ctx, nodes, masks=star_masks(2, N, nodes))
+
+
+@pytest.mark.parametrize("kind,power", [(BF, 30), (HF, 9), (E4, 6), (E4, 10), (E4, 16), (E4, 30), (E4, 80)])
+@pytest.mark.parametrize("qdt", [BF, HF])
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+def test_large_values_of_little_weight(N, Hq, qdt, kind, power):
+    """Early tokens with values 2^power times the others' and scores some 90 octaves
+    or more below: what they add is 2^(power - 90) at most, and the others keep their bits."""
+    if kind != E4 and kind != qdt:
+        pytest.skip("a 16-bit cache takes queries of its own type")
+    D, page = 64, 16
+    ctx, nodes = [700, 16000], [N, N - 1]
+    q, cache, p, table, ctx, nodes = attn_case(2, N, Hq, 2, D, page, qdt, kind, ctx, nodes, 23)
+    # all queries share a direction: + 8 in channel 0; the tokens have - 128 there
+    # (score - 128 exp(-128) against scores of size 2 to 10)
+    q[..., 0] = 8.0
+    src = FL if kind == E4 else kind
+    g = gen(power)
+    for b in range(2):
+        for t in (3, 130, 401):
+            k = randn((1, 2, D), FL, g)
+            k[..., 0] = -128.0
+            v = randn((1, 2, D), FL, g) * 2.0 ** power
+            binding.kv_write(cache, k.to(src), v.to(src), slots_of(table, ctx, page, b, [t]))
+    check_attention(q, cache, p, table, ctx, nodes)
+
+
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+@pytest.mark.parametrize("D", [48, 128])
+def test_rows_of_zeros_among_values_of_every_size(D, N, Hq):
+    """8 bits: rows of zeros, tiny ones and large ones side by side, in tiles of their
+    own and mixed, the zeros with much of the weight."""
+    ctx, nodes = [130, 1500], [N, N]
+    q, cache, p, table, ctx, nodes = attn_case(2, N, Hq, 2, D, 16, BF, E4, ctx, nodes, 31)
+    g = gen(3)
+    for b in range(2):
+        n = int(ctx[b]) + N
+        k, v = randn((n, 2, D), FL, g), randn((n, 2, D), FL, g)
+        v *= torch.exp2(torch.randint(-30, 31, (n, 1, 1), generator=g, device="cuda").float())
+        v[::3] = 0
+        if n > 600:
+            v[:128] = 0                                   # whole tiles of zeros, first and later
+            v[384:512] = 0
+            v[256:384] *= 2.0 ** -60
+        k[17] = q[b, 0, 0].float() * 2
+        v[17] = 0
+        binding.kv_write(cache, k, v, slots_of(table, ctx, 16, b, np.arange(n)))
+    check_attention(q, cache, p, table, ctx, nodes)
+
+
+@pytest.mark.parametrize("octave", [64, 72, 80, 88, 96, 104])
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+def test_zeros_with_all_the_weight(N, Hq, octave):
+    """8 bits: a row of zeros `octave` (in e) above all others' scores, 92 to 150 octaves
+    of two: what is left of the others is 0 in every type, and the total is the zeros'."""
+    D = 64
+    q, cache, p, table, ctx, nodes = attn_case(1, N, Hq, 2, D, 16, BF, E4, [400], [N], 53)
+    q[..., 0] = 8.0
+    g = gen(2)
+    n = 400 + N
+    k, v = randn((n, 2, D), FL, g), randn((n, 2, D), FL, g)
+    k[..., 0] = 0
+    k[300], v[300] = 0, 0
+    k[300, :, 0] = octave
+    binding.kv_write(cache, k, v, slots_of(table, ctx, 16, 0, np.arange(n)))
+    lse = torch.zeros((1, N, Hq), device="cuda")
+    out = binding.tree_attention(q, cache, p, lse=lse)
+    ref, rl, bound = NC.attention(q, cache, table, ctx, nodes, p.masks.cpu().numpy().view(np.uint32), 1 / 8)
+    assert float((out.double() - ref).abs().max()) < 2.0 ** -80
+    assert float((lse.double() - rl).abs().max()) < 2.0 ** -13      # scores within 2^-22 of sums below 250
+
+
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+def test_all_values_zero(N, Hq):
+    """8 bits, nothing but zeros over a long context: zeros, and the total still counts."""
+    q, cache, p, table, ctx, nodes = attn_case(1, N, Hq, 2, 64, 64, BF, E4, [70000], [N], 37, vscale=0.0)
+    assert not check_attention(q, cache, p, table, ctx, nodes).any()
+
+
+@pytest.mark.parametrize("qdt,kind", [(BF, E4), (HF, E4)])
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+@pytest.mark.parametrize("dominant_at", [0, 59990])
+def test_long_flat_tail(dominant_at, N, Hq, qdt, kind):
+    """One token with nearly all the weight, 60000 with 2^-25.97 of it each: 9.1e-4 in all.
+    f16 weights relative to the largest would be zero, all of them."""
+    D, n = 64, 60000
+    q, cache, p, table, ctx, nodes = attn_case(1, N, Hq, 2, D, 64, qdt, kind, [n], [N], 41)
+    q = torch.zeros_like(q)
+    q[..., 0] = 1.0
+    src = FL if kind == E4 else kind
+    k, v = torch.zeros((n + N, 2, D), device="cuda"), torch.zeros((n + N, 2, D), device="cuda")
+    k[dominant_at, :, 0] = 18.0                            # 18 log2(e) = 25.97 octaves
+    v[:, :, 1] = 1.0
+    v[dominant_at, :, 0], v[dominant_at, :, 1] = 1.0, 0.0
+    binding.kv_write(cache, k.to(src), v.to(src), slots_of(table, ctx, 64, 0, np.arange(n + N)))
+    out = binding.tree_attention(q, cache, p, scale=1.0).double()
+    m = p.masks.cpu().numpy().view(np.uint32)
+    ref, _, _ = NC.attention(q, cache, table, ctx, nodes, m, 1.0)
+    # a weight of 2^(8 - 25.97) of f16's steps of 2^-24 is off by 2^-7.03 of itself at
+    # most, the output's rounding by 2^-9: 0.0096
+    assert float(((out - ref).abs() / ref)[..., :2].max()) < 0.01
+    assert not out[..., 2:].any()
+
+
+@pytest.mark.parametrize("qdt", [BF, HF])
+def test_many_rows_zero_values_dominate(qdt):
+    q, cache, p, table, ctx, nodes = attn_case(1, 12, 24, 2, 64, 16, qdt, E4, [400], [12], 51)
+    g = gen(1)
+    n = 412
+    k, v = randn((n, 2, 64), FL, g), randn((n, 2, 64), FL, g)
+    k[17], v[17] = q[0, 0, 0].float(), 0
+    k[300], v[300] = q[0, 3, 20].float(), 0
+    binding.kv_write(cache, k, v, slots_of(table, ctx, 16, 0, np.arange(n)))
+    check_attention(q, cache, p, table, ctx, nodes)
