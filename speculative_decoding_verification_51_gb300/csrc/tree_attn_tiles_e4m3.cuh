@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             auto pair = [&](uint32_t x) {
                 return A.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&x)) : make_float2(bf16_lo(x), bf16_hi(x));
             };
-            float m = 0.f, odd = 0.f;  // odd: NaN where some value is not finite, and the row with it
+            float m = 0.f, odd = 0.f;  // odd: NaN where some value is not finite
 #pragma unroll
             for (int j = 0; j < CH / 8; ++j) {
                 const uint32_t x[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
@@ -325,10 +325,13 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             sync_rows();
             m = fmaxf(m, sm_max[half ^ 1][r].x);
             odd += sm_max[half ^ 1][r].y;
-            const int ex = odd == 0.f ? e4m3_exponent(m) : 0;
+            // (then the row's scores are NaN, by its operand: a factor would make NaN of the
+            // -inf of what it does not see, too)
+            const bool bad = !(odd == 0.f);
+            const int ex = bad ? 0 : e4m3_exponent(m);
             const float down = exp2_int(-ex) * sign;
             // a factor of zero would make NaN of -inf; no score of this size counts
-            rc = fmaxf(c * exp2_int(ex), 1e-30f) + odd;
+            rc = fmaxf(c * exp2_int(ex), 1e-30f);
 #pragma unroll
             for (int j = 0; j < CH / 32; ++j) {
                 // as halves: 11 bits, and below 2^-14 of the scale steps of 2^-24
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 for (int e = 0; e < 16; ++e) {
                     const uint4& y = u[j * 4 + e / 4];
                     const float2 z = pair(e % 4 == 0 ? y.x : e % 4 == 1 ? y.y : e % 4 == 2 ? y.z : y.w);
-                    f[e] = pack16<true>(z.x * down, z.y * down);
+                    f[e] = bad ? 0x7fff7fffu : pack16<true>(z.x * down, z.y * down);
                 }
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {

@@ -196,3 +196,25 @@ def test_many_rows_zero_values_dominate(qdt):
     k[300], v[300] = q[0, 3, 20].float(), 0
     binding.kv_write(cache, k, v, slots_of(table, ctx, 16, 0, np.arange(n)))
     check_attention(q, cache, p, table, ctx, nodes)
+
+
+# ---------------------------------------------------------------- queries
+
+@pytest.mark.parametrize("qdt,kind", KINDS)
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+def test_a_bad_query_that_sees_nothing_gives_zeros(N, Hq, qdt, kind):
+    q, cache, p, table, ctx, nodes = attn_case(3, N, Hq, 2, 64, 16, qdt, kind, [0, 50, 0], [N, N, N - 1], 43)
+    masks = p.masks.clone()
+    masks[0, 1] = masks[0, 3] = masks[2, 2] = 0
+    q[0, 1, 1, 5], q[0, 3, 0, 60], q[2, 2, :, 0] = math.nan, math.inf, -math.inf
+    lse = torch.zeros((3, N, Hq), device="cuda")
+    out = binding.tree_attention(q, cache, p, masks=masks, lse=lse)
+    for b, v in ((0, 1), (0, 3), (2, 2)):
+        assert not out[b, v].any() and bool((lse[b, v] == -math.inf).all())
+    good = torch.ones((3, N), dtype=torch.bool, device="cuda")
+    good[0, 1] = good[0, 3] = good[2, 2] = False
+    ref, _, bound = NC.attention(q.nan_to_num(0, 0, 0), cache, table, ctx, nodes, masks.cpu().numpy().view(np.uint32), 1 / 8)
+    assert bool(((out.double() - ref).abs() <= bound)[good].all())
+    # a node past the tree, with such a query
+    q[2, N - 1] = math.nan
+    assert not binding.tree_attention(q, cache, p, masks=masks)[2, N - 1].any()
