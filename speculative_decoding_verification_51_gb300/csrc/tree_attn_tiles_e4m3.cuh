@@ -11,12 +11,15 @@
 // 64-96 + 32).  Weights are an operand in TMEM; queries lie in shared memory, since TMEM
 // has room for two tiles' scores and weights and the sums, and no more.
 //
-// Scores.  Products of 8-bit types (kind::f8f6f4) take e4m3 queries, 4
-// significant bits each.  A query is split: q 2^-a = h1 + h2 (+ h3), h1 = e4m3(q
-// 2^-a), h2 = e4m3(q 2^-a - h1), .., a power of two a row that brings the largest
-// to 448 or less.  Two terms hold bf16's 8 bits and three f16's 11, down to
-// 2^-18 of the row's largest value; the terms' products add up in one
-// accumulator.  K's scale comes afterwards: a tile's scale bytes are turned to
+// Scores.  Products of 8-bit types (kind::f8f6f4) take queries of 8 bits, split: q 2^-a
+// = h1 + h2 (+ h3), h1 = e4m3(q 2^-a) with 4 significant bits, then e5m2 terms of what
+// is left, with 3 (the remainder's sign gives one more), a power of two a row that
+// brings the largest to 448 or less.  Two terms hold bf16's 8 bits, three f16's 11.
+// A value so small that h1 falls among e4m3's last steps of 2^-9 leaves a remainder
+// of 2^-10 at most, of which e5m2 (steps down to 2^-16) keeps 3 bits: two terms
+// are off by 2^-14 and three by 2^-17, 2^-21.8 and 2^-24.8 of the row's largest value.
+// (e4m3 terms throughout: 2^-17.8.)  The terms' products add up in one accumulator.
+// K's scale comes afterwards: a tile's scale bytes are turned to
 // factors, and the exponent of a weight is (s rc) ck[t] - m.
 //
 // Values.  Where the exponents of a tile's rows lie within 8 of one another, v 2^e is
@@ -57,16 +60,16 @@ struct TilesE4Shape {
     static constexpr int THREADS = 640;
 };
 
-// D f32, A and B e4m3, both K-major, M = N = 128
+// D f32, A e4m3 (or e5m2: bit 7), B e4m3, both K-major, M = N = 128
 constexpr int AT_SPREAD = 8;               // exponents of one tile's values that one unit serves
 constexpr int AT_WIDE = 1 << 20;           // in place of the unit: the values have exponents of their own
 constexpr float AT_TOP = 8.f, AT_LEAST = -92.f;
 constexpr uint32_t AT_ID_E4 = (1u << 4) | (uint32_t(128 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-__device__ __forceinline__ void at_mma_e4(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void at_mma_e4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(AT_ID_E4), "r"(acc)
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 // 2^d as two halves (d <= 0; 0 below f16's least subnormal)
@@ -81,12 +84,20 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
 }
 // 2^-d for a whole d >= 0 (0 where it is no normal float)
 __device__ __forceinline__ float exp2_down(float d) { return d < 127.f ? exp2_int(-int(d)) : 0.f; }
-// The next term of two halves: their e4m3 bytes; the halves keep what is left
-// (a difference of neighbours, so exact).
-__device__ __forceinline__ uint32_t e4m3_term(uint32_t& x) {
+// The first or a later term of two halves: their e4m3 or e5m2 bytes; the halves keep
+// what is left (a difference of neighbours, so exact).
+template <bool FIRST>
+__device__ __forceinline__ uint32_t query_term(uint32_t& x) {
     uint16_t w;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(w) : "r"(x));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(e4m3x2_to_f16x2(w)));
+    uint32_t h;
+    if constexpr (FIRST) {
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(w) : "r"(x));
+        h = e4m3x2_to_f16x2(w);
+    } else {
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(w) : "r"(x));
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(w));
+    }
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(h));
     return w;
 }
 
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < DP / 32; ++k)
                             at_mma_e4(tbase + (j & 1) * 128, at_desc_k(qa + x * S::RAW + k * 32), at_desc_k(ka + k * 32),
-                                      x > 0 || k > 0);
+                                      AT_ID_E4 | (x ? 1u << 7 : 0u), x > 0 || k > 0);
                     at_commit(&sf[j & 1]);
                     at_commit(&rke[rs]);
                 }
@@ -348,8 +359,8 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     uint32_t o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        o[e] = e4m3_term(f[2 * e]);
-                        o[e] |= e4m3_term(f[2 * e + 1]) << 16;
+                        if (x == 0) o[e] = query_term<true>(f[2 * e]) | query_term<true>(f[2 * e + 1]) << 16;
+                        else o[e] = query_term<false>(f[2 * e]) | query_term<false>(f[2 * e + 1]) << 16;
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e)

@@ -218,3 +218,49 @@ def test_a_bad_query_that_sees_nothing_gives_zeros(N, Hq, qdt, kind):
     # a node past the tree, with such a query
     q[2, N - 1] = math.nan
     assert not binding.tree_attention(q, cache, p, masks=masks)[2, N - 1].any()
+
+
+@pytest.mark.parametrize("qdt", [BF, HF])
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+def test_outlier_channel_of_the_queries(N, Hq, qdt):
+    """8 bits: one channel of the queries 300 times the others, on which the keys have
+    nothing, so that the scores are the others'.  A query's channel is held to 2^-21.8
+    of the row's largest (bf16 queries, many rows) or 2^-24, so a score to that times
+    the sum of |k|."""
+    D = 64
+    q, cache, p, table, ctx, nodes = attn_case(2, N, Hq, 2, D, 16, qdt, E4, [333, 9000], [N, N], 47)
+    g = gen(9)
+    for b in range(2):
+        n = int(ctx[b]) + N
+        k = randn((n, 2, D), FL, g)
+        k[..., 7] = 0
+        binding.kv_write(cache, k, randn((n, 2, D), FL, g), slots_of(table, ctx, 16, b, np.arange(n)))
+    q[..., 7] = 300 * (1 + q[..., 7].abs())
+    held = 2.0 ** -21.8 if qdt == BF and N * Hq // 2 > 16 else 2.0 ** -24
+    lse = torch.zeros((2, N, Hq), device="cuda")
+    out = binding.tree_attention(q, cache, p, lse=lse).double()
+    ref, rl, bound = NC.attention(q, cache, table, ctx, nodes, p.masks.cpu().numpy().view(np.uint32), 1 / 8)
+    assert bool(((out - ref).abs() <= bound).all())
+    for b in range(2):
+        K, _ = NC.cache_rows(cache, table[b, :-(-(int(ctx[b]) + N) // 16)].long(), int(ctx[b]) + N)
+        big = K.abs().sum(-1).amax(0)                                     # the largest sum of |k|, by key head
+        off = q[b].double().abs().amax(-1) * big.repeat_interleave(Hq // 2) / 8 * (held + 2.0 ** -24)
+        # scores' own sums (the seen channels' are below 200) to 2^-22, the total's to 2^-20
+        assert bool(((lse[b].double() - rl[b]).abs() <= off + 200 * 2.0 ** -22 + 2.0 ** -20).all())
+
+
+# ---------------------------------------------------------------- many rows: what few rows are tested for elsewhere
+
+@pytest.mark.parametrize("qdt,kind", KINDS)
+def test_many_rows_large_scores_and_scales_of_any_sign(qdt, kind):
+    N, Hq = 12, 24
+    case = attn_case(2, N, Hq, 2, 128, 16, qdt, kind, [300, 40], [N, N - 1], 7)
+    q, rest = case[0], case[1:]
+    check_attention(q * 40, *rest)
+    check_attention(torch.zeros_like(q), *rest)
+    check_attention(q, *rest, scale=0.0)
+    check_attention(q, *rest, scale=-0.3)
+    check_attention(q * 40, *rest, scale=-0.1)
+    check_attention(q, *rest, scale=1e-6)
+    check_attention(*attn_case(2, N, Hq, 2, 64, 16, qdt, kind, [300, 4000], [N, N], 8,
+                               vscale=2.0 ** -40 if kind == E4 else 2.0 ** -6))
