@@ -16,8 +16,11 @@
 // 0.95 of the measured copy rate, a quarter of the tensor rate.
 //
 // As in k_attn_rows the reference of a row is raised only when a score passes
-// it by 2^8, so that O in TMEM is seldom rescaled; a weight is then at most
-// 2^8, which bf16 and f16 hold and whose rounding is relative.
+// it by some octaves, so that O in TMEM is seldom rescaled; a weight is then at most
+// 2^8 (bf16) or 2^15 (f16), which the types hold and whose rounding is relative.  f16
+// ends at 2^-24, and a long context can have much of its weight in a flat tail below: so
+// a raised reference leaves the largest f16 weight at 2^8, and the tail counts down to
+// 2^-33 of it.
 //
 // The loops over a tile's columns are rolled where they can be: the roles' code
 // together has to stay in the SM's instruction cache.  (Unrolled, the stall
@@ -29,7 +32,11 @@
 
 namespace sv {
 
-constexpr float AT_SLACK = 8.f;
+// what a score may pass the reference by, and where a raised one leaves the largest
+template <bool F16>
+struct TilesRange {
+    static constexpr float SLACK = F16 ? 15.f : 8.f, TOP = F16 ? 8.f : 0.f;
+};
 constexpr uint64_t AT_WAIT_NS = 200000000ull;
 
 // As mbar_wait_bounded, for warps that wait long: the hint lets the hardware suspend
@@ -529,9 +536,9 @@ __global__ void __launch_bounds__(TilesShape<DP>::THREADS, 1)
                     }
                     f2_unpack(sum, s0, s1);
                     const float top = mx * c;
-                    const bool raise = top > ref + AT_SLACK;
+                    const bool raise = top > ref + TilesRange<F16>::SLACK;
                     if (__builtin_expect(!__any_sync(0xffffffffu, raise), 1)) break;
-                    const float to = raise ? top : ref;
+                    const float to = raise ? top - TilesRange<F16>::TOP : ref;
                     const float f2 = ref == to ? 1.f : ex2_approx(ref - to);
                     ref = to;
                     tot *= f2;

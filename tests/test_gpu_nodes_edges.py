@@ -161,7 +161,7 @@ def test_all_values_zero(N, Hq):
     assert not check_attention(q, cache, p, table, ctx, nodes).any()
 
 
-@pytest.mark.parametrize("qdt,kind", [(BF, E4), (HF, E4)])
+@pytest.mark.parametrize("qdt,kind", [(HF, HF), (BF, E4), (HF, E4)])
 @pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
 @pytest.mark.parametrize("dominant_at", [0, 59990])
 def test_long_flat_tail(dominant_at, N, Hq, qdt, kind):
