@@ -34,6 +34,7 @@
 // of zeros (e = -126) does not push the total out of float32.
 #pragma once
 
+#include "ring.cuh"
 #include "tree_attn.cuh"
 
 namespace sv {
@@ -176,10 +177,10 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
         off_at = pc * 16 % A.page;
     };
     seek();
-    uint32_t issued = 0, used = 0;
+    CopyRing<S::STAGES> copies;
     auto issue = [&]() {
-        if (!more) return;
-        const uint32_t st = issued % S::STAGES;
+        if (!more || !copies.alive()) return;
+        const uint32_t st = copies.begin();
         if (lane == 0) {
             uint8_t* d = ring + st * S::STAGE;
             mbar_arrive_expect_tx(&bar[st], uint32_t(S::STAGE) + (E4 ? 32u : 0u));
@@ -195,13 +196,11 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
                 bulk_g2s(sc + st * 32 + 16, A.vs + at, 16, &bar[st]);
             }
         }
-        ++issued;
         pc += AR_WARPS;
         seek();
     };
     for (int i = 0; i < S::STAGES; ++i) issue();
 
-    bool dead = false;  // a copy did not arrive in time: no more waits, SPEC_BADBIT_TIMEOUT
     Segment s = ps0;
     for (;;) {
         // ---- the query's rows to shared memory (e4m3: as f16, a power of two
@@ -286,14 +285,15 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
         }
         uint32_t v_bad = 0;  // nodes of which some value is not finite
         for (int c = s.c0 + warp; c < s.c1; c += AR_WARPS) {
-            const uint32_t st = used % S::STAGES;
+            const uint32_t st = copies.stage();
             uint8_t* kp = ring + st * S::STAGE;
             uint8_t* vp = kp + S::SIDE;
-            if (!dead && __any_sync(0xffffffffu, !mbar_wait_bounded(&bar[st], (used / S::STAGES) & 1u))) {
-                dead = true;
+            // (where a copy did not arrive in time: no more copies and waits)
+            if (copies.alive() && __any_sync(0xffffffffu, !mbar_wait_bounded(&bar[st], copies.parity()))) {
+                copies.lose();
                 if (lane == 0 && A.status) atomicOr(A.status, int(SPEC_BADBIT_TIMEOUT));
             }
-            ++used;
+            copies.next();
             const int t0 = c * 16;
             const bool tail = t0 + 16 > s.ctx;
 
@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
         if (threadIdx.x == 0) sm_flag[1] = 0;
         s = after;
     }
+    copies.drain([&](uint32_t st, uint32_t parity) { mbar_wait_bounded(&bar[st], parity, 100000000ull); });
 }
 
 template <int KIND, int NK>
