@@ -659,8 +659,8 @@ spec_status spec_kv_read(const spec_kv_cache* cache, int64_t T, const int64_t* s
  * earlier node: SPEC_BADBIT_TREE; a negative context, one past its page table, or
  * a page outside the cache: SPEC_BADBIT_PAGE) gets that for all of its nodes:
  * nothing of it is written or read.
- * One plan serves every layer of the step; the calls that use it must not
- * overlap on the GPU.
+ * One plan serves every layer of the step, on any number of streams: nothing
+ * else writes to it.
  */
 size_t spec_tree_plan_size(int B);
 spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes,
@@ -687,7 +687,8 @@ spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes
  *                sum_t exp(scale q . K[t]); -inf for a row that sees nothing.
  *   plan         of spec_tree_plan, with the same B, N and page table.
  *   workspace    at least spec_tree_attention_workspace_size(...) bytes,
- *                256-byte aligned, no initialisation.
+ *                256-byte aligned, no initialisation; one call's at a time
+ *                (calls that may overlap on the GPU need one each).
  *   dev_status   NULL or one device int32, or-ed into (SPEC_BADBIT_TIMEOUT).
  * Scores and sums are float32; weights are rounded to q's type (or, over an
  * e4m3 cache, to f16) before they meet V.  What a row does not see has no effect on it,

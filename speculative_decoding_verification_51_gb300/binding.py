@@ -713,7 +713,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, *, dtype: torch.dtype | None = 
 @dataclass
 class TreePlan:
     """Where the nodes of a step stand (spec_tree_plan).  One plan serves every
-    layer of the step; calls that use it must not overlap on the GPU."""
+    layer of the step, on any number of streams."""
     positions: torch.Tensor    # [B, N] int32
     slots: torch.Tensor        # [B, N] int64
     masks: torch.Tensor        # [B, N] int32: bit u: node u is this one or above it

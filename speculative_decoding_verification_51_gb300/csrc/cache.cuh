@@ -166,28 +166,20 @@ inline spec_status check_cache(const spec_kv_cache* c) {
 //   tiles[B + 1]       tiles of TREE_TILE tokens of the requests before b (a
 //                      request has one tile at least, so that its rows are
 //                      written)
-//   arrived[PLAN_PARTS] per CTA: arrivals of the parts of the item that starts
-//                      in its share and ends in another's (all zero between
-//                      calls: whoever joins the parts puts it back)
+// and zeros up to its end.  spec_tree_plan alone writes it.
 constexpr int TREE_TILE = 128;
-constexpr int PLAN_PARTS = 1024;  // >= CTAs of an attention launch
 
-struct PlanView {
-    int* ctx;
-    int* nodes;
-    int* tiles;
-    int* arrived;
+template <class I>
+struct PlanLists {
+    I* ctx;
+    I* nodes;
+    I* tiles;
 };
-inline __host__ __device__ size_t plan_words(int B) {
-    return size_t(B) * 3 + 1 + PLAN_PARTS;
-}
-inline PlanView plan_view(void* plan, int B) {
-    PlanView v;
-    v.ctx = static_cast<int*>(plan);
-    v.nodes = v.ctx + B;
-    v.tiles = v.nodes + B;
-    v.arrived = v.tiles + B + 1;
-    return v;
+using PlanView = PlanLists<const int>;
+inline size_t plan_words(int B) { return size_t(B) * 3 + 1; }
+template <class I>
+inline PlanLists<I> plan_lists(I* plan, int B) {
+    return {plan, plan + B, plan + 2 * size_t(B)};
 }
 
 // The device's SM count, read once per device.

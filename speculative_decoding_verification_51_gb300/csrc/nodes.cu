@@ -38,7 +38,8 @@ struct PlanArgs {
     int32_t* positions;
     long long* slots;
     uint32_t* masks;
-    PlanView plan;
+    PlanLists<int> plan;
+    int rest;  // words of the plan after its lists
     int32_t* status;
 };
 
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(PLAN_T) k_tree_plan(const __grid_constant__ Pl
             carry += all;
         }
         if (tid == 0) A.plan.tiles[A.B] = carry;
-        for (int i = tid; i < PLAN_PARTS; i += PLAN_T) A.plan.arrived[i] = 0;
+        if (tid < A.rest) A.plan.tiles[A.B + 1 + tid] = 0;  // (less than 256 bytes)
         return;
     }
     const int b = blockIdx.x - 1;
@@ -279,7 +280,8 @@ spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes
     A.positions = positions;
     A.slots = reinterpret_cast<long long*>(slots);
     A.masks = masks;
-    A.plan = plan_view(plan, B);
+    A.plan = plan_lists(static_cast<int*>(plan), B);
+    A.rest = int(spec_tree_plan_size(B) / 4 - plan_words(B));
     A.status = dev_status;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dev_status && cudaMemsetAsync(dev_status, 0, 4, st) != cudaSuccess) return SPEC_ERR_CUDA;

@@ -141,7 +141,7 @@ size_t spec_tree_attention_workspace_size(const spec_kv_cache* cache, int q_head
     if (check_cache(cache) != SPEC_OK || q_heads < 1 || q_heads % cache->heads) return 0;
     const int sms = sm_count();
     if (sms <= 0) return 0;
-    return align256(size_t(2) * sms * MAX_R * width_of(cache->head_dim) * 4) +
+    return align256(size_t(sms) * 8) + align256(size_t(2) * sms * MAX_R * width_of(cache->head_dim) * 4) +
            align256(size_t(2) * sms * MAX_R * 2 * 4);
 }
 
@@ -168,7 +168,7 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
         workspace_bytes < spec_tree_attention_workspace_size(cache, q_heads))
         return SPEC_ERR_WORKSPACE;
     const int sms = sm_count();
-    if (sms <= 0 || sms > PLAN_PARTS) return SPEC_ERR_CUDA;
+    if (sms <= 0) return SPEC_ERR_CUDA;
 
     AttnLaunch L;
     AttnArgs& A = L.A;
@@ -180,7 +180,7 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.lse = lse;
     A.table = page_table;
     A.masks = masks;
-    A.plan = plan_view(const_cast<void*>(plan), B);
+    A.plan = plan_lists(static_cast<const int*>(plan), B);
     A.v = cache->v;
     A.ks = cache->k_scale;
     A.vs = cache->v_scale;
@@ -199,9 +199,10 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.rows = N * A.G;
     A.c = scale * 1.4426950408889634f;
     A.q_f16 = dtype == SPEC_F16;
-    A.part_o = static_cast<float*>(workspace);
-    A.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                         align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
+    char* room = static_cast<char*>(workspace) + align256(size_t(sms) * 8);
+    A.arrived = static_cast<unsigned long long*>(workspace);
+    A.part_o = reinterpret_cast<float*>(room);
+    A.part_ml = reinterpret_cast<float*>(room + align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
     A.status = dev_status;
     // More than 16 rows go to the tcgen05 kernels (128 a tile, heads of up to 128),
     // since k_attn_rows reads the cache again for every 16.  Measured (us, k_attn_rows /

@@ -35,6 +35,7 @@ struct AttnArgs {
     int lead;           // what an item costs beyond its tiles, in tiles
     float c;            // scale * log2(e): scores are exponents of two
     int q_f16;          // q and out are f16 (else bf16)
+    unsigned long long* arrived;  // [CTAs] arrivals of the parts of the item that starts in a share (arrive)
     float* part_o;      // [2 * CTAs][width / 4][R][4] unnormalised sums
     float* part_ml;     // [2 * CTAs][R][2] reference and total
     int32_t* status;
@@ -279,6 +280,30 @@ __device__ __forceinline__ void put_lse(const AttnArgs& A, const Segment& s, int
         v < s.n && total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Counts an arrival at `w` and says whether it is the last of `parts`.  The workspace may
+// hold anything before its first use, so that a count is one only beneath a mark of
+// 48 bits (memory that holds the mark by chance would be taken for a count).  An
+// arrival that finds no mark has not counted: it puts the mark there with itself as the
+// first, or counts beneath the one that another put there meanwhile; every retry means
+// that another arrival went on.  Whoever is last puts the count back to zero, so that
+// later calls need one atomic.
+constexpr unsigned long long ARRIVED = 0x51c2e98a437dull << 16;
+__device__ __forceinline__ bool arrive(unsigned long long* w, int parts) {
+    constexpr unsigned long long COUNT = 0xffff;
+    unsigned long long old = atomicAdd(w, 1ull);
+    while ((old & ~COUNT) != ARRIVED) {
+        const unsigned long long now = atomicAdd(w, 0ull);
+        if ((now & ~COUNT) == ARRIVED) {
+            old = atomicAdd(w, 1ull);
+        } else if (atomicCAS(w, now, ARRIVED | 1ull) == now) {
+            old = ARRIVED;
+        }
+    }
+    const bool last = int(old & COUNT) + 1 == parts;
+    if (last) *w = ARRIVED;
+    return last;
+}
+
 // After this CTA's part of an item lies in the workspace: the CTA that
 // arrives last joins the parts (R rows of `width` channels each).
 // `threads` threads call it together (tid their index, `bar` their barrier) and
@@ -292,11 +317,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& A, const Share& sh, c
     const int c0 = cta_of(sh, g0), c1 = cta_of(sh, g0 + s.tiles - 1);
     __threadfence();
     sync();
-    if (tid == 0) {
-        const int last = atomicAdd(&A.plan.arrived[c0], 1) == c1 - c0;
-        if (last) A.plan.arrived[c0] = 0;  // as the next call finds it
-        *flag = last;
-    }
+    if (tid == 0) *flag = arrive(A.arrived + c0, c1 - c0 + 1);
     sync();
     if (!*flag) return;
     __threadfence();
