@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(PLAN_T) k_tree_plan(const __grid_constant__ Pl
     if (n < 1 || n > A.N) bad = SPEC_BADBIT_NUM_DRAFT;
     else if (!fits) bad = SPEC_BADBIT_PAGE;
     if (fits) {
-        const int used = (ctx + n + A.page - 1) / A.page;
+        const int used = (ctx + n - 1) / A.page + 1;
         for (int i = tid; i < used; i += PLAN_T) {
             const int p = table[i];
             if (p < 0 || p >= A.num_pages) bad |= SPEC_BADBIT_PAGE;
