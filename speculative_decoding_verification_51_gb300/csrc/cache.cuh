@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <initializer_list>
 #include <utility>
 
 #include "common.cuh"
@@ -120,6 +121,12 @@ inline int dtype_bytes(int dt) {
 }
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// (a null pointer is aligned)
+inline bool all_aligned(size_t a, std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!aligned(p, a)) return false;
+    return true;
+}
 
 inline CacheView view_of(const spec_kv_cache& c) {
     CacheView v;

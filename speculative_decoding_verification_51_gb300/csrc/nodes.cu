@@ -266,6 +266,8 @@ spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes
     if (!tree_parents || !num_nodes || !context_len || !page_table || !positions || !slots ||
         !masks || !plan)
         return SPEC_ERR_INVALID_ARG;
+    if (!all_aligned(4, {tree_parents, num_nodes, context_len, page_table, positions, masks, dev_status}) || !aligned(slots, 8))
+        return SPEC_ERR_UNSUPPORTED;
     if (!aligned(plan, 256) || plan_bytes < spec_tree_plan_size(B)) return SPEC_ERR_WORKSPACE;
     PlanArgs A;
     A.parents = tree_parents;
@@ -313,6 +315,8 @@ spec_status spec_kv_commit(const spec_kv_cache* caches, int num_caches, const ui
     if (B == 0) return SPEC_OK;
     if (!masks || !slots || !last_node || !context_len || !new_context_len)
         return SPEC_ERR_INVALID_ARG;
+    if (!all_aligned(4, {masks, last_node, context_len, new_context_len, dev_status}) || !aligned(slots, 8))
+        return SPEC_ERR_UNSUPPORTED;
     A.c = view_of(caches[0]);
     A.masks = masks;
     A.slots = reinterpret_cast<const long long*>(slots);

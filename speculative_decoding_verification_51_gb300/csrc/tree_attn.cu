@@ -162,7 +162,7 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     if (B == 0) return SPEC_OK;
     if (!q || !page_table || !masks || !plan || !out || !workspace) return SPEC_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || q_batch_stride % 8 || q_node_stride % 8 ||
-        q_head_stride % 8)
+        q_head_stride % 8 || !all_aligned(4, {page_table, masks, lse, dev_status}))
         return SPEC_ERR_UNSUPPORTED;
     if (!aligned(workspace, 256) || !aligned(plan, 256) ||
         workspace_bytes < spec_tree_attention_workspace_size(cache, q_heads))
