@@ -9,6 +9,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -70,11 +72,20 @@ int64_t int_attr(PyObject* o, PyObject* name) {
     return integer(a.p);
 }
 
+// The calls have no backward: a tensor whose history they would drop is refused.
+void without_history(const Tensor& t, const char* name) {
+    if ((t.requires_grad() && c10::GradMode::is_enabled()) ||
+        (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode()))
+        bad(std::string(name) + " carries a gradient, which this call would drop: detach it, or call under torch.no_grad()");
+}
+
 // None: not given
 const Tensor* maybe(PyObject* o, const char* name) {
     if (o == Py_None) return nullptr;
     if (!THPVariable_Check(o)) bad_type(std::string(name) + " must be a tensor");
-    return &THPVariable_Unpack(o);
+    const Tensor& t = THPVariable_Unpack(o);
+    without_history(t, name);
+    return &t;
 }
 const Tensor& tensor(PyObject* o, const char* name) {
     const Tensor* t = maybe(o, name);
