@@ -11,6 +11,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -19,6 +20,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "spec_verify.h"
@@ -49,7 +52,7 @@ struct Ref {  // an owned reference
 };
 
 // Attribute names, made once.
-#define NAMES(X) X(_ref) X(k) X(positions) X(slots) X(masks) X(context_len) X(page_table) X(page_size) \
+#define NAMES(X) X(_ref) X(k) X(v) X(k_scale) X(v_scale) X(turns) X(positions) X(slots) X(masks) X(context_len) X(page_table) X(page_size) \
     X(num_pages) X(buffer) X(workspace) X(stream_id) X(device_index) X(device_type)
 struct Names {
 #define X(n) PyObject* n = nullptr;
@@ -175,15 +178,31 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType ty, c10::Device dev) {
 }
 
 // The call's stream: `stream` (a torch.cuda.Stream) is made current for its duration, so
-// that what is allocated belongs to the stream that the kernels run on.
+// that what is allocated belongs to the stream that the kernels run on, and the
+// allocator is told of every other tensor the call uses there (`uses`), so that the
+// memory of one that is dropped meanwhile is not given away before they ran.
 struct OnStream {
     c10::cuda::OptionalCUDAStreamGuard guard;
+    std::optional<c10::cuda::CUDAStream> given;
     explicit OnStream(PyObject* s) {
         if (s == Py_None) return;
-        guard.reset_stream(c10::cuda::CUDAStream::unpack3(
-            int_attr(s, N.stream_id), c10::DeviceIndex(int_attr(s, N.device_index)),
-            c10::DeviceType(int_attr(s, N.device_type))));
+        given = c10::cuda::CUDAStream::unpack3(int_attr(s, N.stream_id), c10::DeviceIndex(int_attr(s, N.device_index)),
+                                               c10::DeviceType(int_attr(s, N.device_type)));
+        guard.reset_stream(*given);
     }
+    void uses(std::initializer_list<const Tensor*> ts) const {
+        if (!given) return;
+        for (const Tensor* t : ts)
+            if (t && t->defined()) c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), *given);
+    }
+    void uses_attrs(PyObject* o, std::initializer_list<PyObject*> names) const {
+        if (!given) return;
+        for (PyObject* n : names) {
+            Ref a(attr(o, n));
+            uses({maybe(a.p, "tensor")});
+        }
+    }
+    void uses_cache(PyObject* o) const { uses_attrs(o, {N.k, N.v, N.k_scale, N.v_scale}); }
 };
 
 // f(stream) with the device current, without the interpreter's lock
@@ -240,6 +259,8 @@ PyObject* rope(PyObject* const* a) {
     }
     flat(pos, "positions", at::kInt, rq.n, dev);
     const auto* pp = static_cast<const int32_t*>(pos.data_ptr());
+    on.uses({&q, k, &pos, &oq, &ok});
+    on.uses_attrs(a[3], {N.turns});
     run("spec_rope", dev, [&](spec_stream_t st) {
         return spec_rope(rq.p, rq.heads, rq.step, rq.head, ro.p, ro.step, ro.head, rk.p, rk.heads, rk.step, rk.head,
                          rp.p, rp.step, rp.head, dt, int(D), rq.n, pp, table, inverse, st);
@@ -279,6 +300,9 @@ PyObject* kv_write(PyObject* const* a) {
     }
     int32_t* st_word = status_word(a[8], dev);
     const auto* sp = static_cast<const int64_t*>(slots.data_ptr());
+    on.uses({&k, &v, &slots, pos, q, &oq, maybe(a[8], "dev_status")});
+    on.uses_cache(a[0]);
+    if (table) on.uses_attrs(a[5], {N.turns});
     run("spec_kv_write", dev, [&](spec_stream_t st) {
         return spec_kv_write(c.c, rk.p, rk.step, rk.head, rv.p, rv.step, rv.head, dt, rk.n, sp, pp, table, rq.p, rq.heads,
                              rq.step, rq.head, ro.p, ro.step, ro.head, st_word, st);
@@ -313,6 +337,8 @@ PyObject* kv_read(PyObject* const* a) {
         }
     }
     const spec_dtype dt = dtype_of(out[0], "dtype");
+    on.uses({&slots, &out[0], &out[1]});
+    on.uses_cache(a[0]);
     run("spec_kv_read", dev, [&](spec_stream_t st) {
         return spec_kv_read(c.c, slots.numel(), static_cast<const int64_t*>(slots.data_ptr()), dt, out[0].data_ptr(),
                             out[1].data_ptr(), st);
@@ -340,6 +366,7 @@ PyObject* tree_plan(PyObject* const* a) {
     const size_t n = spec_tree_plan_size(int(B));
     const Tensor buffer = empty({int64_t(n)}, at::kByte, dev), positions = empty({B, NN}, at::kInt, dev),
                  masks = empty({B, NN}, at::kInt, dev), slots = empty({B, NN}, at::kLong, dev);
+    on.uses({&par, &nodes, &ctx, &table, maybe(a[5], "dev_status")});
     run("spec_tree_plan", dev, [&](spec_stream_t st) {
         return spec_tree_plan(static_cast<const int32_t*>(par.data_ptr()), static_cast<const int32_t*>(nodes.data_ptr()),
                               static_cast<const int32_t*>(ctx.data_ptr()), static_cast<const int32_t*>(table.data_ptr()),
@@ -425,6 +452,8 @@ PyObject* tree_attention(PyObject* const* a) {
             if (PyDict_SetItem(kept.p, key.p, t.p)) throw Raised();
         }
     }
+    on.uses({&q, &buffer, &table, &masks, &out, lse, &ws, maybe(a[8], "dev_status")});
+    on.uses_cache(a[1]);
     run("spec_tree_attention", dev, [&](spec_stream_t st) {
         return spec_tree_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), dt, int(B), int(NN), int(Hq), c.c,
                                    static_cast<const int32_t*>(table.data_ptr()), int(table.size(1)),
@@ -455,7 +484,11 @@ PyObject* kv_commit(PyObject* const* a) {
         check(len, "new_context_len", at::kInt, {B}, dev);
     }
     int32_t* st_word = status_word(a[4], dev);
-    for (Py_ssize_t i = 0; i < count; ++i) check_pages(plan, Cache(PySequence_Fast_GET_ITEM(list.p, i)), dev);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        check_pages(plan, Cache(PySequence_Fast_GET_ITEM(list.p, i)), dev);
+        on.uses_cache(PySequence_Fast_GET_ITEM(list.p, i));
+    }
+    on.uses({&last, &masks, &slots, &ctx, &len, maybe(a[4], "dev_status")});
     // the lengths are written once, by the last group of caches: it may be the
     // plan's own context_len, which the earlier groups still read
     Tensor scratch;

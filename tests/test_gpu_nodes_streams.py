@@ -47,3 +47,55 @@ def test_workspace_of_any_content(N, Hq):
             room.fill_(fill)
         for _ in range(3):
             assert torch.equal(binding.tree_attention(q, cache, p, workspace=room), want)
+
+
+@pytest.mark.parametrize("kind", [BF, E4])
+def test_tensors_of_another_stream_outlive_the_call(kind):
+    """`stream=` behind a stream that is busy: what a call uses is dropped at once, and its
+    memory is not given to anybody else before the call has run."""
+    B, N, Hq, Hkv, D, page = 3, 4, 8, 2, 64, 16
+    q, cache, p, table, ctx, nodes = attn_case(B, N, Hq, Hkv, D, page, BF, kind, [1000, 40, 300], [N] * 3, 9)
+    side, g = torch.cuda.Stream(), gen(1)
+    t = lambda *s: randn(s, BF, g)  # noqa: E731
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots = p.slots.view(-1)
+    par = i([[-1, 0, 0, 1]] * B)
+
+    def check(call, make):
+        """`make`: the call's tensors, dropped after it."""
+        want = call(*[x.clone() for x in make], stream=None)
+        want = [x.clone() for x in want]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)                  # some 50 ms
+        args = [x.clone() for x in make]
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(*args, stream=side)
+        held = {x.data_ptr() for x in args}
+        sizes = [(x.shape, x.dtype) for x in args]
+        del args
+        assert not side.query()                             # the call has not run yet
+        other = [torch.empty(s, dtype=d, device="cuda") for s, d in sizes for _ in range(3)]
+        assert not held & {x.data_ptr() for x in other}
+        for x in other:
+            x.fill_(-1)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+    def table_of(turns):
+        return binding.RopeTable(turns, "half", 1.0)
+
+    turns = binding.rope_table(64).turns
+    check(lambda a, b, c, d, stream: binding.rope(a, b, c, table_of(d), stream=stream), [t(12, 8, 64), t(12, 2, 64), i([5] * 12), turns])
+    check(lambda a, b, c, d, e, f, stream: (binding.kv_write(cache, a, b, c, positions=d, table=table_of(e), q=f, stream=stream),),
+          [t(12, 2, 64), t(12, 2, 64), slots, i([5] * 12), turns, t(12, 8, 64)])
+    check(lambda a, stream: binding.kv_read(cache, a, stream=stream), [slots])
+
+    def plan(a, b, c, d, stream):
+        x = binding.tree_plan(a, b, c, d, cache, stream=stream)
+        return x.positions, x.slots, x.masks
+
+    check(plan, [par, i(nodes.tolist()), i(ctx.tolist()), table])
+    check(lambda a, b, stream: (binding.tree_attention(a, cache, p, masks=b, stream=stream),), [q, p.masks])
+    check(lambda a, stream: (binding.kv_commit([cache], p, a, stream=stream),), [i([-1, -1, -1])])
