@@ -3,9 +3,9 @@
 Each translation unit under ``csrc/`` is compiled in parallel, then linked
 into ``_build/libspecverify_<machine>.so`` (CUDA runtime linked statically).
 ``csrc/torch_ops.cpp`` becomes ``_build/specverify_torch_<machine>.so``, the
-Python module that calls the library with torch tensors.  Both are rebuilt
-when any source or header is newer than they are, the module also for
-another torch.
+Python module that calls the library with torch tensors; without torch there
+is the library alone.  Either is rebuilt when one of its sources or headers is
+newer than it is, the module also for another torch.
 """
 from __future__ import annotations
 
@@ -43,9 +43,8 @@ def ops_path() -> str:
     return os.path.join(BUILD, f"specverify_torch_{platform.machine()}.so")
 
 
-def _inputs() -> list[str]:
-    return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+def _inputs(*endings: str) -> list[str]:
+    return [p for e in endings for p in glob.glob(os.path.join(CSRC, "*." + e))] + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def extra_flags() -> list[str]:
@@ -53,23 +52,38 @@ def extra_flags() -> list[str]:
     return os.environ.get("SPEC_VERIFY_NVCC_EXTRA", "").split()
 
 
-def _stamp() -> str:
-    return lib_path() + ".flags"
+def _torch_version() -> str | None:
+    """None without torch: then there is the library alone."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch.__version__
 
 
-def _made_with() -> str:
-    """What the library and the module depend on besides their sources."""
-    import torch
-    return " ".join([*extra_flags(), "torch", torch.__version__])
+def _fresh(out: str, made_with: str, inputs: list[str]) -> bool:
+    """Whether `out` is there, made with the same as now and newer than its inputs."""
+    stamp = out + ".flags"
+    if not os.path.exists(out) or not os.path.exists(stamp) or open(stamp).read() != made_with:
+        return False
+    return os.path.getmtime(out) >= max(os.path.getmtime(p) for p in inputs)
+
+
+def _put(tmp: str, out: str, made_with: str) -> None:
+    os.replace(tmp, out)
+    with open(out + ".flags", "w") as f:
+        f.write(made_with)
+
+
+def _stale() -> tuple[bool, bool]:
+    """Whether the library, and the module, have to be made."""
+    torch_version = _torch_version()
+    return (not _fresh(lib_path(), " ".join(extra_flags()), _inputs("cu", "cuh")),
+            torch_version is not None and not _fresh(ops_path(), torch_version, _inputs("cpp")))
 
 
 def up_to_date() -> bool:
-    outs = [lib_path(), ops_path()]
-    if not all(os.path.exists(p) for p in (*outs, _stamp())):
-        return False
-    if open(_stamp()).read() != _made_with():
-        return False
-    return min(os.path.getmtime(p) for p in outs) >= max(os.path.getmtime(p) for p in _inputs())
+    return not any(_stale())
 
 
 def _torch_flags() -> tuple[list[str], list[str]]:
@@ -87,9 +101,12 @@ def _torch_flags() -> tuple[list[str], list[str]]:
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
-    """Build the library if needed; return its path."""
-    out = lib_path()
-    if not force and up_to_date():
+    """Build what is needed of the library and the module; return the library's path."""
+    out, module = lib_path(), ops_path()
+    make_lib, make_module = _stale()
+    if force:
+        make_lib, make_module = True, _torch_version() is not None
+    if not make_lib and not make_module:
         return out
     objdir = os.path.join(BUILD, f"obj_{platform.machine()}")
     os.makedirs(objdir, exist_ok=True)
@@ -103,33 +120,32 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    flags, libs = _torch_flags()
-    ops_obj = os.path.join(objdir, "torch_ops.o")
+    cxx, ops_obj = os.environ.get("CXX", "g++"), os.path.join(objdir, "torch_ops.o")
 
-    def compile_ops() -> None:
-        r = subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *flags, "-c",
-                            os.path.join(CSRC, "torch_ops.cpp"), "-o", ops_obj], capture_output=True, text=True)
+    def compile_ops() -> list[str]:
+        flags, libs = _torch_flags()
+        r = subprocess.run([cxx, "-O2", "-std=c++17", "-fPIC", *flags, "-c", os.path.join(CSRC, "torch_ops.cpp"),
+                            "-o", ops_obj], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on torch_ops.cpp:\n{r.stderr}")
+        return libs
+
+    def link(cmd: list[str], to: str, made_with: str) -> None:
+        tmp = f"{to}.{os.getpid()}.tmp"
+        r = subprocess.run([*cmd, "-shared", "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        _put(tmp, to, made_with)
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ops = ex.submit(compile_ops)
-        results = list(ex.map(compile_one, SOURCES))
-        ops.result()
-    tmp = f"{out}.{os.getpid()}.tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, out)
-    tmp = f"{ops_path()}.{os.getpid()}.tmp"
-    r = subprocess.run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, ops_obj, f"-L{BUILD}",
-                        f"-l:{os.path.basename(out)}", "-Wl,-rpath,$ORIGIN", *libs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, ops_path())
-    with open(_stamp(), "w") as f:
-        f.write(_made_with())
+        ops = ex.submit(compile_ops) if make_module else None
+        results = list(ex.map(compile_one, SOURCES)) if make_lib else []
+        if make_lib:  # whatever becomes of the module
+            link([nvcc(), *ARCH, *[o for o, _ in results]], out, " ".join(extra_flags()))
+        if make_module:
+            libs = ops.result()
+            link([cxx, ops_obj, f"-L{BUILD}", f"-l:{os.path.basename(out)}", "-Wl,-rpath,$ORIGIN", *libs], module,
+                 _torch_version())
     if ptxas_verbose:
         for (_, log), src in zip(results, SOURCES):
             print(f"== {src}\n{log}")
