@@ -482,9 +482,9 @@ cudaError_t launch_rotate(RotArgs A, cudaStream_t st) {
     while (share > 2 * UH && lanes * ((H + share - 1) / share) < 3072ll * sms) share -= UH;
     while (share > UH && lanes * ((H + share - 1) / share) < 768ll * sms) share -= UH;
     if (share == UH && lanes * ((H + UH - 1) / UH) < 256ll * sms) share = 1;
-    A.share = share;
+    A.share = std::max(share, (H + 65534) / 65535);  // blockIdx.y ends at 65534
     const long long gx = (A.T + ROT_THREADS / ip - 1) / (ROT_THREADS / ip);
-    if (gx > 0x7fffffffll || (H + A.share - 1) / A.share > 65535) return cudaErrorInvalidValue;
+    if (gx > 0x7fffffffll) return cudaErrorInvalidValue;
     const dim3 grid(unsigned(gx), unsigned((H + A.share - 1) / A.share));
     auto* kernel = ip == 4    ? k_rotate<T, VEC, 4, E4, PAIR>
                    : ip == 8  ? k_rotate<T, VEC, 8, E4, PAIR>

@@ -1,11 +1,13 @@
 """The operators around the verification at the ends of their ranges: page tables
-near 2^31 tokens."""
+near 2^31 tokens, as many heads as the calls take."""
 import numpy as np
 import pytest
 import torch
 
+import nodes_common as NC
 from gpu_common import ensure_built
 from speculative_decoding_verification_51_gb300 import binding
+from test_gpu_nodes import BF, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,20 @@ def test_plan_of_the_longest_tables(page, pages):
     assert p.slots.tolist() == [[page - 2, page - 1], [-1, -1], [-1, -1]]
     assert p.positions.tolist() == [[longest - 2, longest - 1], [0, 0], [0, 0]]
     assert p.masks.tolist() == [[1, 3], [0, 0], [0, 0]]
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("T", [1, 3])
+def test_rotation_of_the_most_heads(T, layout):
+    """65536 query heads and as many key heads, and one more than a refusal names."""
+    D, most = 8, 65536
+    g, table = gen(T), binding.rope_table(D, layout=layout)
+    th, _ = NC.thetas(D)
+    pos = ints(np.arange(T) + 7)
+    q, k = randn((T, most, D), BF, g), randn((T, most, D), BF, g)
+    for x, y in zip((q, k), binding.rope(q, k, pos, table)):
+        d = (y.cpu().double() - NC.rotate(x, pos, th, layout)).abs()
+        assert bool((d <= NC.rotate_bound(x, th, layout, BF) + 2e-6 * x.cpu().double().abs().amax()).all())
+    with pytest.raises(binding.SpecVerifyError) as e:
+        binding.rope(randn((T, most + 1, D), BF, g), None, pos, table)
+    assert e.value.status == binding.SPEC_ERR_INVALID_ARG
