@@ -40,14 +40,15 @@ def test_plan_of_the_longest_tables(page, pages):
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
-@pytest.mark.parametrize("T", [1, 3])
-def test_rotation_of_the_most_heads(T, layout):
-    """65536 query heads and as many key heads, and one more than a refusal names."""
+@pytest.mark.parametrize("T,Hkv", [(1, 1000), (1, 65536), (3, 65536)])
+def test_rotation_of_the_most_heads(T, Hkv, layout):
+    """65536 query heads, 1000 key heads (a block takes one head then) or as many again, and
+    one more than the calls take."""
     D, most = 8, 65536
     g, table = gen(T), binding.rope_table(D, layout=layout)
     th, _ = NC.thetas(D)
     pos = ints(np.arange(T) + 7)
-    q, k = randn((T, most, D), BF, g), randn((T, most, D), BF, g)
+    q, k = randn((T, most, D), BF, g), randn((T, Hkv, D), BF, g)
     for x, y in zip((q, k), binding.rope(q, k, pos, table)):
         d = (y.cpu().double() - NC.rotate(x, pos, th, layout)).abs()
         assert bool((d <= NC.rotate_bound(x, th, layout, BF) + 2e-6 * x.cpu().double().abs().amax()).all())
