@@ -186,18 +186,6 @@ def test_long_flat_tail(dominant_at, N, Hq, qdt, kind):
     assert not out[..., 2:].any()
 
 
-@pytest.mark.parametrize("qdt", [BF, HF])
-def test_many_rows_zero_values_dominate(qdt):
-    q, cache, p, table, ctx, nodes = attn_case(1, 12, 24, 2, 64, 16, qdt, E4, [400], [12], 51)
-    g = gen(1)
-    n = 412
-    k, v = randn((n, 2, 64), FL, g), randn((n, 2, 64), FL, g)
-    k[17], v[17] = q[0, 0, 0].float(), 0
-    k[300], v[300] = q[0, 3, 20].float(), 0
-    binding.kv_write(cache, k, v, slots_of(table, ctx, 16, 0, np.arange(n)))
-    check_attention(q, cache, p, table, ctx, nodes)
-
-
 # ---------------------------------------------------------------- queries
 
 @pytest.mark.parametrize("qdt,kind", KINDS)
@@ -264,3 +252,107 @@ def test_many_rows_large_scores_and_scales_of_any_sign(qdt, kind):
     check_attention(q, *rest, scale=1e-6)
     check_attention(*attn_case(2, N, Hq, 2, 64, 16, qdt, kind, [300, 4000], [N, N], 8,
                                vscale=2.0 ** -40 if kind == E4 else 2.0 ** -6))
+
+
+@pytest.mark.parametrize("qdt", [BF, HF])
+def test_many_rows_zero_values_dominate(qdt):
+    q, cache, p, table, ctx, nodes = attn_case(1, 12, 24, 2, 64, 16, qdt, E4, [400], [12], 51)
+    g = gen(1)
+    n = 412
+    k, v = randn((n, 2, 64), FL, g), randn((n, 2, 64), FL, g)
+    k[17], v[17] = q[0, 0, 0].float(), 0
+    k[300], v[300] = q[0, 3, 20].float(), 0
+    binding.kv_write(cache, k, v, slots_of(table, ctx, 16, 0, np.arange(n)))
+    check_attention(q, cache, p, table, ctx, nodes)
+
+
+@pytest.mark.parametrize("kind,pages", [(BF, 140000), (E4, 270000)])
+@pytest.mark.parametrize("N,Hq", [(3, 8), (12, 24)])
+def test_strides_stream_and_pages_past_32_bits(N, Hq, kind, pages):
+    """Tokens before heads in the cache, queries inside a projection's output, the pages
+    in use past 2^31 elements and 2^32 bytes of it, and a stream of its own."""
+    g = gen(4)
+    B, Hkv, D, page = 2, 2, 128, 64
+    dt = torch.uint8 if kind == E4 else kind
+    assert pages * page * Hkv * D > 2 ** 31 and pages * page * Hkv * D * dt.itemsize > 2 ** 32
+    base = torch.empty((pages, page, Hkv, D), dtype=dt, device="cuda")
+    both = base.transpose(1, 2)                                   # one tensor: keys equal values
+    scales = [torch.full((pages, Hkv, page), 127, dtype=torch.uint8, device="cuda")] * 2 if kind == E4 else []
+    cache = binding.KVCache(both, both, *scales)
+    ctx, nodes = np.array([150, 511], np.int32), np.array([N, N - 1], np.int32)
+    par = np.zeros((B, N), np.int32)
+    par[:, 0] = -1
+    table = (pages - 1 - np.arange(18, dtype=np.int32)).reshape(2, 9)
+    p = binding.tree_plan(dev(par), dev(nodes), dev(ctx), dev(table), cache)
+    for b in range(B):
+        t = np.arange(int(ctx[b] + nodes[b]))
+        x = randn((len(t), Hkv, D), BF, g)
+        binding.kv_write(cache, x, x, slots_of(dev(table), ctx, page, b, t))
+    q = randn((B, N, Hq + 4, D), BF, g)[:, :, 2:2 + Hq]
+    want = check_attention(q, cache, p, dev(table), ctx, nodes)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = binding.tree_attention(q, cache, p, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- a step in a CUDA graph
+
+@pytest.mark.parametrize("qdt,kind", KINDS)
+@pytest.mark.parametrize("N,Hq", FEW_AND_MANY)
+def test_step_in_a_graph(N, Hq, qdt, kind):
+    """Plan, write, attention and commit of two layers captured once and replayed over
+    changing lengths: the same bits as the calls themselves."""
+    B, Hkv, D, page = 3, 2, 64, 16
+    g = gen(6)
+    rng = np.random.default_rng(6)
+    top = np.array([900, 8000, 60])
+    table, pages = NC.make_table(rng, top, [N] * B, page)
+    table = dev(table.clip(0))
+    caches = [binding.new_kv_cache(pages, page, Hkv, D, dtype=kind) for _ in range(4)]
+    src = qdt if kind == E4 else kind
+    every = torch.arange(pages * page, device="cuda")
+    for a, b in zip(caches[:2], caches[2:]):
+        x, y = randn((pages * page, Hkv, D), src, g), randn((pages * page, Hkv, D), src, g)
+        binding.kv_write(a, x, y, every)
+        binding.kv_write(b, x, y, every)
+    rot = binding.rope_table(D)
+    ctx = torch.zeros(B, dtype=torch.int32, device="cuda")
+    par = dev(NC.random_tree(rng, B, N))
+    nodes = torch.zeros(B, dtype=torch.int32, device="cuda")
+    last = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q, k, v = randn((B, N, Hq, D), src, g), randn((B, N, Hkv, D), src, g), randn((B, N, Hkv, D), src, g)
+
+    def step(caches):
+        p = binding.tree_plan(par, nodes, ctx, table, caches[0])
+        outs = []
+        for c in caches:
+            t = binding.kv_write(c, k, v, p.slots.view(-1), positions=p.positions.view(-1), table=rot, q=q)
+            outs.append(binding.tree_attention(t.view(B, N, Hq, D), c, p))
+        return outs + [binding.kv_commit(caches, p, last)]
+
+    def lengths(i):
+        ctx.copy_(dev((top * [0.1, 1.0, 0.5][i]).astype(np.int32)))
+        nodes.copy_(dev(np.array([[N, 1, N - 1], [N, N, N], [1, N, 2]][i], np.int32)))
+        last.copy_(nodes - 1)
+
+    lengths(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(caches[:2])
+    torch.cuda.current_stream().wait_stream(side)
+    step(caches[2:])                                            # both sets of caches alike again
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(caches[:2])
+    for i in (1, 0, 2, 1):
+        lengths(i)
+        graph.replay()
+        got = [o.clone() for o in outs]
+        want = step(caches[2:])
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    for a, b in zip(caches[:2], caches[2:]):
+        assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
