@@ -41,12 +41,10 @@ namespace sv {
 
 constexpr float AR_SLACK = 6.f;
 
-constexpr int AR_MT = 1;  // row tiles of 16
-
 template <int KIND, int NK>
 struct RowsShape {
     static constexpr bool E4 = KIND == SPEC_E4M3;
-    static constexpr int DP = NK * 16, R = AR_MT * 16;
+    static constexpr int DP = NK * 16, R = 16;
     // eight warps, or four where the stages of eight would not fit
     static constexpr int WARPS = !E4 && NK > 8 ? 4 : 8, THREADS = WARPS * 32;
     static constexpr int BOXES = E4 ? (DP + 127) / 128 : (DP + 63) / 64;  // 128 bytes of a row each
@@ -60,7 +58,7 @@ struct RowsShape {
     static_assert(STAGES >= 2, "no room for a ring");
     static constexpr size_t SMEM = 1024 + size_t(WARPS) * STAGES * STAGE + FIXED;
     // the query's fragments stay in registers where they are few
-    static constexpr bool QREG = AR_MT * NK <= 8;
+    static constexpr bool QREG = NK <= 8;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -258,30 +256,25 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
 
         // ---- this warp's chunks
         const uint32_t qa = smem_u32(sm_q) + (((lane & 7) + ((lane >> 3) & 1) * 8) * QP + (lane >> 4) * 8) * 2;
-        uint32_t qf[S::QREG ? AR_MT : 1][S::QREG ? NK : 1][4];
+        uint32_t qf[S::QREG ? NK : 1][4];
         if constexpr (S::QREG) {
 #pragma unroll
-            for (int m = 0; m < AR_MT; ++m)
-#pragma unroll
-                for (int k = 0; k < NK; ++k) ldsm4(qa + (m * 16 * QP + k * 16) * 2, qf[m][k]);
+            for (int k = 0; k < NK; ++k) ldsm4(qa + k * 32, qf[k]);
         }
-        float o[AR_MT][2 * NK][4], ref[AR_MT][2], tot[AR_MT][2], rc[AR_MT][2];
-        uint32_t mask[AR_MT][2];
+        float o[2 * NK][4], ref[2], tot[2], rc[2];
+        uint32_t mask[2];
 #pragma unroll
-        for (int m = 0; m < AR_MT; ++m) {
+        for (int n = 0; n < 2 * NK; ++n)
 #pragma unroll
-            for (int n = 0; n < 2 * NK; ++n)
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[m][n][e] = 0.f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = m * 16 + x * 8 + (lane >> 2);
-                ref[m][x] = -INFINITY;
-                tot[m][x] = 0.f;
-                mask[m][x] = sm_mask[r];
-                rc[m][x] = A.c;
-                if constexpr (E4) rc[m][x] = A.c * exp2_int(int(max(min(sm_qmax[r] >> 23, 253u), 1u)) - 127);
-            }
+        for (int x = 0; x < 2; ++x) {
+            const int r = x * 8 + (lane >> 2);
+            ref[x] = -INFINITY;
+            tot[x] = 0.f;
+            mask[x] = sm_mask[r];
+            rc[x] = A.c;
+            if constexpr (E4) rc[x] = A.c * exp2_int(int(max(min(sm_qmax[r] >> 23, 253u), 1u)) - 127);
         }
         uint32_t v_bad = 0;  // nodes of which some value is not finite
         for (int c = s.c0 + warp; c < s.c1; c += AR_WARPS) {
@@ -298,13 +291,11 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
             const bool tail = t0 + 16 > s.ctx;
 
             // scores
-            float p[AR_MT][2][4];
+            float p[2][4];
 #pragma unroll
-            for (int m = 0; m < AR_MT; ++m)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[m][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) p[n][e] = 0.f;
             const uint32_t ka = smem_u32(kp);
             if constexpr (E4) {
                 const int tk = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -319,18 +310,15 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
                                        b01 = e4m3x2_to_f16x2(uint16_t(w[2 * i] >> 16)),
                                        b10 = e4m3x2_to_f16x2(uint16_t(w[2 * i + 1])),
                                        b11 = e4m3x2_to_f16x2(uint16_t(w[2 * i + 1] >> 16));
+                        uint32_t a[4];
+                        if constexpr (S::QREG) {
 #pragma unroll
-                        for (int m = 0; m < AR_MT; ++m) {
-                            uint32_t a[4];
-                            if constexpr (S::QREG) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) a[e] = qf[m][k + i][e];
-                            } else {
-                                ldsm4(qa + (m * 16 * QP + (k + i) * 16) * 2, a);
-                            }
-                            mma16<true>(p[m][0], a, b00, b01);
-                            mma16<true>(p[m][1], a, b10, b11);
+                            for (int e = 0; e < 4; ++e) a[e] = qf[k + i][e];
+                        } else {
+                            ldsm4(qa + (k + i) * 32, a);
                         }
+                        mma16<true>(p[0], a, b00, b01);
+                        mma16<true>(p[1], a, b10, b11);
                     }
                 }
             } else {
@@ -340,18 +328,15 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
                     uint32_t w[4];
                     const int j = 2 * k + ((lane >> 3) & 1);
                     ldsm4(ka + (j >> 3) * 2048 + tk * 128 + (((j & 7) ^ (tk & 7)) << 4), w);
+                    uint32_t a[4];
+                    if constexpr (S::QREG) {
 #pragma unroll
-                    for (int m = 0; m < AR_MT; ++m) {
-                        uint32_t a[4];
-                        if constexpr (S::QREG) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) a[e] = qf[m][k][e];
-                        } else {
-                            ldsm4(qa + (m * 16 * QP + k * 16) * 2, a);
-                        }
-                        mma16<F16>(p[m][0], a, w[0], w[1]);
-                        mma16<F16>(p[m][1], a, w[2], w[3]);
+                        for (int e = 0; e < 4; ++e) a[e] = qf[k][e];
+                    } else {
+                        ldsm4(qa + k * 32, a);
                     }
+                    mma16<F16>(p[0], a, w[0], w[1]);
+                    mma16<F16>(p[1], a, w[2], w[3]);
                 }
             }
             // this lane's tokens: t0 + 8 n + 2 (lane % 4) + e
@@ -369,65 +354,62 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
                     }
                 }
             }
+            bool raise = false;
+            float top[2];
 #pragma unroll
-            for (int m = 0; m < AR_MT; ++m) {
-                bool raise = false;
-                float top[2];
+            for (int x = 0; x < 2; ++x) {
+                top[x] = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = p[n][2 * x + e] * rc[x];
+                        if constexpr (E4) v *= kf[n][e];
+                        if (tail) {
+                            const int u = t0 + n * 8 + 2 * (lane & 3) + e - s.ctx;
+                            if (u >= 0 && (u >= 32 || !(mask[x] >> u & 1u))) v = -INFINITY;
+                        }
+                        p[n][2 * x + e] = v;
+                        if constexpr (E4) v += fmaxf(ve[n][e], -100.f);
+                        top[x] = fmaxf(top[x], v);
+                    }
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+                raise |= top[x] > ref[x] + AR_SLACK;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    top[x] = -INFINITY;
+                    const float to = top[x] > ref[x] + AR_SLACK ? top[x] : ref[x];
+                    // a reference of -inf has sums of zero
+                    const float f = ref[x] == to ? 1.f : ex2_approx(ref[x] - to);
+                    ref[x] = to;
+                    tot[x] *= f;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float v = p[m][n][2 * x + e] * rc[m][x];
-                            if constexpr (E4) v *= kf[n][e];
-                            if (tail) {
-                                const int u = t0 + n * 8 + 2 * (lane & 3) + e - s.ctx;
-                                if (u >= 0 && (u >= 32 || !(mask[m][x] >> u & 1u))) v = -INFINITY;
-                            }
-                            p[m][n][2 * x + e] = v;
-                            if constexpr (E4) v += fmaxf(ve[n][e], -100.f);
-                            top[x] = fmaxf(top[x], v);
-                        }
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-                    raise |= top[x] > ref[m][x] + AR_SLACK;
-                }
-                if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float to = top[x] > ref[m][x] + AR_SLACK ? top[x] : ref[m][x];
-                        // a reference of -inf has sums of zero
-                        const float f = ref[m][x] == to ? 1.f : ex2_approx(ref[m][x] - to);
-                        ref[m][x] = to;
-                        tot[m][x] *= f;
-#pragma unroll
-                        for (int n = 0; n < 2 * NK; ++n) {
-                            o[m][n][2 * x] *= f;
-                            o[m][n][2 * x + 1] *= f;
-                        }
+                    for (int n = 0; n < 2 * NK; ++n) {
+                        o[n][2 * x] *= f;
+                        o[n][2 * x + 1] *= f;
                     }
                 }
-                // weights
+            }
+            // weights
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float at = ref[m][x] == -INFINITY ? 0.f : ref[m][x];
+            for (int x = 0; x < 2; ++x) {
+                const float at = ref[x] == -INFINITY ? 0.f : ref[x];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float v = p[m][n][2 * x + e] - at;
-                            if constexpr (E4) {
-                                tot[m][x] += ex2_approx(v);
-                                v = ex2_approx(v + ve[n][e]);
-                            } else {
-                                v = ex2_approx(v);
-                                tot[m][x] += v;
-                            }
-                            p[m][n][2 * x + e] = v;
+                    for (int e = 0; e < 2; ++e) {
+                        float v = p[n][2 * x + e] - at;
+                        if constexpr (E4) {
+                            tot[x] += ex2_approx(v);
+                            v = ex2_approx(v + ve[n][e]);
+                        } else {
+                            v = ex2_approx(v);
+                            tot[x] += v;
                         }
-                }
+                        p[n][2 * x + e] = v;
+                    }
             }
             // values of tokens past the request's end, and values of nodes
             // that are not finite, must not meet a weight of zero
@@ -473,14 +455,11 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
             }
             // sums
             const uint32_t va = smem_u32(vp);
-            uint32_t a[AR_MT][4];
-#pragma unroll
-            for (int m = 0; m < AR_MT; ++m) {
-                a[m][0] = pack16<F16>(p[m][0][0], p[m][0][1]);
-                a[m][1] = pack16<F16>(p[m][0][2], p[m][0][3]);
-                a[m][2] = pack16<F16>(p[m][1][0], p[m][1][1]);
-                a[m][3] = pack16<F16>(p[m][1][2], p[m][1][3]);
-            }
+            uint32_t a[4];
+            a[0] = pack16<F16>(p[0][0], p[0][1]);
+            a[1] = pack16<F16>(p[0][2], p[0][3]);
+            a[2] = pack16<F16>(p[1][0], p[1][1]);
+            a[3] = pack16<F16>(p[1][2], p[1][3]);
             const int tv = (lane & 7) + ((lane >> 3) & 1) * 8;
             if constexpr (E4) {
 #pragma unroll
@@ -496,11 +475,8 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
                                        o0 = e4m3x2_to_f16x2(uint16_t(lo >> 16)),
                                        e1 = e4m3x2_to_f16x2(uint16_t(hi)),
                                        o1 = e4m3x2_to_f16x2(uint16_t(hi >> 16));
-#pragma unroll
-                        for (int m = 0; m < AR_MT; ++m) {
-                            mma16<true>(o[m][2 * (k + i)], a[m], e0, e1);
-                            mma16<true>(o[m][2 * (k + i) + 1], a[m], o0, o1);
-                        }
+                        mma16<true>(o[2 * (k + i)], a, e0, e1);
+                        mma16<true>(o[2 * (k + i) + 1], a, o0, o1);
                     }
                 }
             } else {
@@ -509,11 +485,8 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
                     uint32_t w[4];
                     const int j = 2 * k + (lane >> 4);
                     ldsm4t(va + (j >> 3) * 2048 + tv * 128 + (((j & 7) ^ (tv & 7)) << 4), w);
-#pragma unroll
-                    for (int m = 0; m < AR_MT; ++m) {
-                        mma16<F16>(o[m][2 * k], a[m], w[0], w[1]);
-                        mma16<F16>(o[m][2 * k + 1], a[m], w[2], w[3]);
-                    }
+                    mma16<F16>(o[2 * k], a, w[0], w[1]);
+                    mma16<F16>(o[2 * k + 1], a, w[2], w[3]);
                 }
             }
             __syncwarp();  // every lane is done with the stage
@@ -529,18 +502,16 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
 
         // ---- join the warps
 #pragma unroll
-        for (int m = 0; m < AR_MT; ++m)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float l = tot[m][x];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                if ((lane & 3) == 0) {
-                    const int r = m * 16 + x * 8 + (lane >> 2);
-                    sm_m[warp * R + r] = ref[m][x];
-                    sm_l[warp * R + r] = l;
-                }
+        for (int x = 0; x < 2; ++x) {
+            float l = tot[x];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if ((lane & 3) == 0) {
+                const int r = x * 8 + (lane >> 2);
+                sm_m[warp * R + r] = ref[x];
+                sm_l[warp * R + r] = l;
             }
+        }
         if (lane == 0 && v_bad) atomicOr(reinterpret_cast<unsigned*>(&sm_flag[1]), v_bad);
         __syncthreads();
         if (threadIdx.x < R) {
@@ -559,41 +530,39 @@ __global__ void __launch_bounds__(RowsShape<KIND, NK>::THREADS, 1)
         for (int half = AR_WARPS / 4 - 1; half >= 0; --half) {
             if ((warp >> 2) == half) {
 #pragma unroll
-                for (int m = 0; m < AR_MT; ++m)
+                for (int x = 0; x < 2; ++x) {
+                    const int r = x * 8 + (lane >> 2);
+                    float mm = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int r = m * 16 + x * 8 + (lane >> 2);
-                        float mm = -INFINITY;
+                    for (int w = 0; w < AR_WARPS; ++w) mm = fmaxf(mm, sm_m[w * R + r]);
+                    const float f = ref[x] == -INFINITY ? 0.f : ex2_approx(ref[x] - mm);
+                    float* z = ob + r * OP;
+                    const bool first_half = half == AR_WARPS / 4 - 1;
+                    if constexpr (E4) {  // accumulators 2 j and 2 j + 1: channels 16 j + 4 t + {0, 2}, {1, 3}
 #pragma unroll
-                        for (int w = 0; w < AR_WARPS; ++w) mm = fmaxf(mm, sm_m[w * R + r]);
-                        const float f = ref[m][x] == -INFINITY ? 0.f : ex2_approx(ref[m][x] - mm);
-                        float* z = ob + r * OP;
-                        const bool first_half = half == AR_WARPS / 4 - 1;
-                        if constexpr (E4) {  // accumulators 2 j and 2 j + 1: channels 16 j + 4 t + {0, 2}, {1, 3}
-#pragma unroll
-                            for (int j = 0; j < NK; ++j) {
-                                float4* y = reinterpret_cast<float4*>(z + j * 16 + 4 * (lane & 3));
-                                float4 v = make_float4(o[m][2 * j][2 * x] * f, o[m][2 * j + 1][2 * x] * f,
-                                                       o[m][2 * j][2 * x + 1] * f, o[m][2 * j + 1][2 * x + 1] * f);
-                                if (!first_half) {
-                                    const float4 b = *y;
-                                    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
-                                }
-                                *y = v;
+                        for (int j = 0; j < NK; ++j) {
+                            float4* y = reinterpret_cast<float4*>(z + j * 16 + 4 * (lane & 3));
+                            float4 v = make_float4(o[2 * j][2 * x] * f, o[2 * j + 1][2 * x] * f,
+                                                   o[2 * j][2 * x + 1] * f, o[2 * j + 1][2 * x + 1] * f);
+                            if (!first_half) {
+                                const float4 b = *y;
+                                v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
                             }
-                        } else {
+                            *y = v;
+                        }
+                    } else {
 #pragma unroll
-                            for (int n = 0; n < 2 * NK; ++n) {
-                                float2* y = reinterpret_cast<float2*>(z + n * 8 + 2 * (lane & 3));
-                                float2 v = make_float2(o[m][n][2 * x] * f, o[m][n][2 * x + 1] * f);
-                                if (!first_half) {
-                                    const float2 b = *y;
-                                    v = make_float2(v.x + b.x, v.y + b.y);
-                                }
-                                *y = v;
+                        for (int n = 0; n < 2 * NK; ++n) {
+                            float2* y = reinterpret_cast<float2*>(z + n * 8 + 2 * (lane & 3));
+                            float2 v = make_float2(o[n][2 * x] * f, o[n][2 * x + 1] * f);
+                            if (!first_half) {
+                                const float2 b = *y;
+                                v = make_float2(v.x + b.x, v.y + b.y);
                             }
+                            *y = v;
                         }
                     }
+                }
             }
             __syncthreads();
         }
