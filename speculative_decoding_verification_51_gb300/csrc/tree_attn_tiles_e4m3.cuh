@@ -1,8 +1,8 @@
 // tree_attn_tiles_e4m3.cuh -- k_attn_tiles_e4m3: k_attn_tiles over an 8-bit cache.
 //
-// 32 trees of 32 nodes (128 rows a key head) over 1000 to 16384 tokens take 214 us: 0.42
-// of the measured copy rate and 0.28 of the tensor rate.  What bounds it is a
-// tile's softmax, some 2450 cycles of which HBM would need 1050.
+// 32 trees of 32 nodes (128 rows a key head) over 1000 to 16384 tokens take 197 us: 0.45
+// of the measured copy rate and 0.30 of the tensor rate.  What bounds it is a
+// tile's softmax, some twice the 1050 cycles that HBM would need.
 //
 // An SM's shared memory moves 128 bytes a cycle, and over an 8-bit cache that is
 // what runs out first: a tile of 128 tokens (32 KB) has some 1400 cycles to
@@ -29,8 +29,8 @@
 // the least exponent there is, so theirs are such tiles) E could be one that a row
 // does not see, or that of a token of no weight, and would take the bits of all the
 // others: there the values stay as they lie and w_t = 2^(s_t + e_t - m), with a second
-// exponential for the total.  (That path for every tile takes the trees above 254 us
-// instead of 214.)  E and e_t are taken as -92 or more in m, so that zeros do not push
+// exponential for the total.  (That path for every tile takes the trees above 293 us
+// instead of 197.)  E and e_t are taken as -92 or more in m, so that zeros do not push
 // the total out of float32.
 //
 // Weights are f16.  A raised reference leaves the largest at 2^8 or less, and they
@@ -81,6 +81,16 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+// 4 columns of this thread's lane, and 2 of them written
+__device__ __forceinline__ void at_ld4(uint32_t t, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(t));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
+}
+__device__ __forceinline__ void at_st2(uint32_t t, const uint32_t (&r)[2]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(t), "r"(r[0]), "r"(r[1]) : "memory");
 }
 // 2^-d for a whole d >= 0 (0 where it is no normal float)
 __device__ __forceinline__ float exp2_down(float d) { return d < 127.f ? exp2_int(-int(d)) : 0.f; }
@@ -336,11 +346,11 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
             sync_rows();
             m = fmaxf(m, sm_max[half ^ 1][r].x);
             odd += sm_max[half ^ 1][r].y;
-            // (then the row's scores are NaN, by its operand: a factor would make NaN of the
-            // -inf of what it does not see, too)
+            // (then the row's scores are NaN, by its operand: by its factor the -inf of what it
+            // does not see would be, too)
             const bool bad = !(odd == 0.f);
             const int ex = bad ? 0 : e4m3_exponent(m);
-            const float down = exp2_int(-ex) * sign;
+            const float down = bad ? __int_as_float(0x7fc00000) : exp2_int(-ex) * sign;
             // a factor of zero would make NaN of -inf; no score of this size counts
             rc = fmaxf(c * exp2_int(ex), 1e-30f);
 #pragma unroll
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 for (int e = 0; e < 16; ++e) {
                     const uint4& y = u[j * 4 + e / 4];
                     const float2 z = pair(e % 4 == 0 ? y.x : e % 4 == 1 ? y.y : e % 4 == 2 ? y.z : y.w);
-                    f[e] = bad ? 0x7fff7fffu : pack16<true>(z.x * down, z.y * down);
+                    f[e] = pack16<true>(z.x * down, z.y * down);
                 }
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
@@ -435,6 +445,12 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                         x[4 * e + 3] = __float_as_uint(b);
                     }
                 };
+                // (a tile without a unit, 4 tokens at a time: as many as above would take so much of the
+                // instruction cache that all tiles wait; 32 rows over 1000 to 16384 tokens 185 us
+                // instead of 195)
+                auto exponent = [&](uint32_t x, const float4& k4, int e, float base) {
+                    return fmaf(__uint_as_float(x) * rc, e == 0 ? k4.x : e == 1 ? k4.y : e == 2 ? k4.z : k4.w, -base);
+                };
                 // The weights by the reference as it is.  None is above 2^15 where their
                 // sum is not; where some row's sum is (or it has no reference yet), its
                 // reference is raised to the largest exponent less 8 and they are made again.
@@ -460,34 +476,44 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                     } else {
                         all = 0.f;
 #pragma unroll 1
-                        for (int j = 0; j < 64; j += 32) {
-                            uint32_t x[32], p[16];
-                            exponents(x, j, base);
+                        for (int j = 0; j < 64; j += 4) {
+                            uint32_t x[4], p[2];
+                            at_ld4(sa + j, x);
+                            const float4 k4 = ck[j / 4];
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float a = __uint_as_float(x[2 * e]), b = __uint_as_float(x[2 * e + 1]);
-                                all += ex2_approx(a) + ex2_approx(b);
-                                const float wa = ex2_approx(a + ve[j + 2 * e]), wb = ex2_approx(b + ve[j + 2 * e + 1]);
-                                sum = f2_add(sum, f2_pack(wa, wb));
-                                p[e] = pack16<true>(wa, wb);
+                            for (int e = 0; e < 4; ++e) {
+                                const float a = exponent(x[e], k4, e, base);
+                                all += ex2_approx(a);
+                                const float w = ex2_approx(a + ve[j + e]);
+                                sum = f2_add(sum, f2_pack(w, 0.f));
+                                x[e] = __float_as_uint(w);
                             }
-                            at_st16(pa + j / 2, p);
+                            p[0] = pack16<true>(__uint_as_float(x[0]), __uint_as_float(x[1]));
+                            p[1] = pack16<true>(__uint_as_float(x[2]), __uint_as_float(x[3]));
+                            at_st2(pa + j / 2, p);
                         }
                     }
                     f2_unpack(sum, s0, s1);
                     if (again || __builtin_expect(!any_of_rows(!(s0 + s1 <= 32768.f && all <= 0x1p107f) || ref == -INFINITY), 1)) break;
                     float mx = -INFINITY;
+                    if (__builtin_expect(!wide, 1)) {
 #pragma unroll 1
-                    for (int j = 0; j < 64; j += 32) {
-                        uint32_t x[32];
-                        exponents(x, j, base);
-                        if (wide) {
+                        for (int j = 0; j < 64; j += 32) {
+                            uint32_t x[32];
+                            exponents(x, j, base);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[e] = __float_as_uint(__uint_as_float(x[e]) + fmaxf(ve[j + e], AT_LEAST));
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
                         }
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < 64; j += 4) {
+                            uint32_t x[4];
+                            at_ld4(sa + j, x);
+                            const float4 k4 = ck[j / 4];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+                            for (int e = 0; e < 4; ++e)
+                                mx = fmaxf(mx, exponent(x[e], k4, e, base) + fmaxf(ve[j + e], AT_LEAST));
+                        }
                     }
                     sm_ref[half][r] = mx;
                     sync_rows();  // (the next write is behind the next vote)
@@ -556,16 +582,15 @@ __global__ void __launch_bounds__(TilesE4Shape<DP>::THREADS, 1)
                 const uint8_t* sc = sm_sc + rs * 256 + 128;
                 uint8_t* out = sm_v + st * S::OPERAND;
                 wait(&rvf[rs], i / NR);
-                // the largest and the least scale byte of the tile's valid tokens
+                // the largest scale byte of the tile's valid tokens, and whether some is far below
                 const uint32_t bytes = *reinterpret_cast<const uint32_t*>(sc + lane * 4);
                 const int left = valid - lane * 4;
-                const uint32_t past = left >= 4 ? 0u : left <= 0 ? ~0u : ~0u << (8 * left);
-                uint32_t z = bytes & ~past, y = bytes | past;
+                const uint32_t there = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                uint32_t z = bytes & there;
                 z = __vmaxu4(z, z >> 16);
-                y = __vminu4(y, y >> 16);
                 const int top = int(__reduce_max_sync(0xffffffffu, max(z & 255u, z >> 8 & 255u)));
-                const int low = int(__reduce_min_sync(0xffffffffu, min(y & 255u, y >> 8 & 255u)));
-                const bool wide = min(max(top, 1), 253) - min(max(low, 1), 253) > AT_SPREAD;
+                const uint32_t least = uint32_t(max(min(top, 253) - AT_SPREAD, 0)) * 0x01010101u;
+                const bool wide = __any_sync(0xffffffffu, __vcmpltu4(bytes, least) & there);
                 const int unit = wide ? AT_WIDE : max(min(max(top, 1), 253) - 127, int(AT_LEAST));
                 uint4 q[2][2];
                 uint32_t f[2];
