@@ -691,8 +691,11 @@ spec_status spec_tree_plan(const int32_t* tree_parents, const int32_t* num_nodes
  *                (calls that may overlap on the GPU need one each).
  *   dev_status   NULL or one device int32, or-ed into (SPEC_BADBIT_TIMEOUT).
  * Scores and sums are float32; weights are rounded to q's type (or, over an
- * e4m3 cache, to f16) before they meet V.  What a row does not see has no effect on it,
- * whatever it holds (infinities and NaN too).
+ * e4m3 cache, to f16) before they meet V, and of f16 weights those below 2^-25 of the
+ * row's largest (which V's scale counts into over an e4m3 cache) may add nothing, though
+ * the total has them.  Over an e4m3 cache a query's channels are held to 2^-21 of the
+ * row's largest, and rows of values below 2^-100 may add nothing.  What a row does
+ * not see has no effect on it, whatever it holds (infinities and NaN too).
  * SPEC_ERR_UNSUPPORTED: N > 32, q_heads not a multiple of the cache's heads,
  * misaligned pointers or strides.
  */

@@ -617,7 +617,9 @@ def rope_table(rot: int, *, base: float = 10000.0, layout: str = "half", scaling
                slow: float = 1.0, device="cuda") -> RopeTable:
     """The frequencies of `rot` rotated channels (spec_rope_turns): `layout`
     "half" or "interleaved"; `scaling` "none", "linear", "ntk" or "by_parts"
-    (which needs the original context's length) by `factor`."""
+    (which needs the original context's length; its ramp is over a pair's turns within
+    that) by `factor`.  "by_parts" puts 0.1 ln(factor) + 1 on the rotated channels:
+    RopeTable(t.turns, t.layout, scale) takes another."""
     if layout not in ROPE_LAYOUT:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUT)}")
     if scaling not in ROPE_SCALING:
@@ -635,8 +637,10 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
          inverse: bool = False, stream=None):
     """Rotary positions (spec_rope): q [..., q_heads, D] and k [..., k_heads,
     D] (or None) turned by positions [tokens] int32.  out_q / out_k: new
-    tensors, or given ones (q and k themselves: in place).  inverse=True turns
-    back, which takes gradients of the outputs to gradients of the inputs.
+    tensors, or given ones (q and k themselves: in place).  inverse=True is the
+    transpose, which takes gradients of the outputs to gradients of the inputs: it
+    turns by the negative angles with the table's factor on the rotated channels
+    (1 but for "by_parts"), so that it is the inverse where that is 1.
     Returns (out_q, out_k), or out_q where k is None."""
     return (_OPS or _ops()).rope(q, k, positions, table, out_q, out_k, inverse, stream)
 

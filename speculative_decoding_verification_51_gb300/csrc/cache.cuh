@@ -14,12 +14,15 @@ namespace sv {
 
 // ---------------------------------------------------------------- launches
 // The operators' kernels are launched with programmatic dependent launch: a kernel's
-// CTAs may take their SMs while the kernel before it in the stream ends.  Every
+// CTAs may take their SMs while the kernel before it in the stream ends.  A
 // kernel lets the next one begin at once and waits for the end of the one before
-// before it touches memory, in every CTA (of k_attn_join: in one at least), so that
-// ends follow in order.  What one
-// costs behind another fell by 1.1 to 2.2 us: a step's four kernels for 256 trees
-// took 41.0 us and take 32.2, one token's attention 10.3 and 8.5.
+// before it touches memory, in every CTA, so that ends follow in order.  Two differ:
+// k_attn_join reads the plan ahead of its wait, lets nothing begin early and waits in
+// one CTA at least; so the tile kernels, which it is launched behind, wait first and let
+// it begin only then (were they to do as the others, it could read a plan that
+// spec_tree_plan is still writing).  What one kernel costs behind another fell by 1.1 to
+// 2.2 us: a step's four kernels for 256 trees took 41.0 us and take 32.2, one token's
+// attention 10.3 and 8.5.
 __device__ __forceinline__ void begin_after_previous() {
     griddep_launch_dependents();
     griddep_wait();

@@ -24,8 +24,10 @@
 //
 // The kernels are bound by memory: every byte is read and written once.  32771 tokens
 // of 40 heads of 128 channels, half of them turned, take 99 us (1.00 of the measured
-// copy rate); 4608 tokens of 48 heads, keys and values to 8 bits, 21 (0.7); reading
-// these back 8.
+// copy rate), all of them turned in half layout 103 (0.96); 4608 tokens of 48 heads, keys
+// and values to 8 bits, 21 (0.7); reading these back 8.  80 registers a thread (three CTAs an
+// SM) are not enough for pairs half a head apart in vectors of 8, nor for e4m3 rows in
+// vectors of 16: they spill 48 to 112 bytes a thread.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -169,8 +171,8 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) k_rotate(const __grid_constant
     // side by side: one flat loop, whose first loads are under way while the slot is
     // read and the angles are made (20011 tokens' keys and values to 8 bits and back 57
     // -> 50 us).  Pairs half a head apart: nested loops that load as they go, since
-    // angles and two vectors an item together would spill (11128 tokens of narrow
-    // heads 52 us, by the flat loop 65).
+    // angles and two vectors an item together would spill still more (11128 tokens of
+    // narrow heads 52 us, by the flat loop 65).
     auto tensor = [&](int kind) -> const Heads& { return kind == 0 ? A.q : kind == 1 ? A.k : A.v; };
     int kind = 0, h = 0, hi = 0;
     auto first_of = [&]() {  // of `kind` or the next that has some

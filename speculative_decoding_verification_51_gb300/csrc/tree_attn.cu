@@ -207,9 +207,10 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     // More than 16 rows go to the tcgen05 kernels (128 a tile, heads of up to 128),
     // since k_attn_rows reads the cache again for every 16.  Measured (us, k_attn_rows /
     // tiles; 32 requests of 1000 to 16384 tokens, 200 of 30 to 1000):
-    //   16 rows, 16 bits 178 / 200 and 107 / 122, 8 bits 166 / 198 and 116 / 181
-    //   20 to 32 rows in tiles of 32, 16 bits 212 / 202 and 148 / 122, 8 bits 233 / 199
-    //     and 164 / 185
+    //   16 rows, 16 bits 177 / 198 and 106 / 121, 8 bits 166 / 184 and 115 / 182
+    //   32 rows, 16 bits 342 / 201 and 206 / 124, 8 bits 322 / 184 and 223 / 184
+    // (A form of k_attn_rows with 32 rows a tile took 212 and 148, 8 bits 233 and 164: over
+    // short contexts of 8 bits it was the fastest, and over no others.)
     const bool e4 = cache->dtype == SPEC_E4M3;
     const bool tiles = A.rows > 16 && A.D <= 128;
     const int R = tiles ? 128 : 16;
@@ -221,7 +222,8 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     // 4 / 8, or for the tile kernels 3 / 6 / 9 and 2 / 5 / 9):
     //   k_attn_rows, 256 chains over 64 to 4096 tokens 352 / 337 / 330 / 344, 64 over
     //     20 to 2000 tokens 87 / 66 / 56 / 60, heads of 256 178 / 147 / 153 / 165
-    //   8 bits, 32 trees of 32 over 1000 to 16384 tokens 263 / 234 / 223 / 225
+    //   8 bits, 32 trees of 32 over 1000 to 16384 tokens 247 / 218 / 196 / 193, 32 rows over
+    //     30 to 1000 223 / 190 / 184 / 185
     //   16 bits, the same 241 / 228 / 214 / 215
     A.lead = !tiles ? (A.D > 128 ? 2 : 4) : e4 ? 6 : 5;
     A.box = tiles ? std::min(TREE_TILE, A.page & -A.page) : 16;

@@ -1,7 +1,7 @@
 // tree_attn_rows.cuh -- k_attn_rows: the attention for few rows a key head
 // (16 a tile), where the cache's bytes are what counts: 256 chains of 4 nodes and 4
 // query heads a key head over 64 to 4096 tokens of 16 bits take 330 us, 0.99 of the
-// measured copy rate; one token over 777 tokens 8.4 us, which is latency.
+// measured copy rate; one token over 777 tokens 8.5 us, which is latency.
 //
 // A CTA (one per SM) has 8 warps, and every warp is a pipeline of its own: it
 // takes every eighth chunk of 16 tokens of the segment, loads the chunk's K
