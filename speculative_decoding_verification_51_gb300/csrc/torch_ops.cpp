@@ -378,6 +378,24 @@ PyObject* tree_plan(PyObject* const* a) {
     return PyTuple_Pack(4, x.p, y.p, z.p, w.p);
 }
 
+// The plan's tensors, whose fields a caller can set: as spec_tree_plan left them, for B
+// requests of N nodes.
+struct Plan {
+    Tensor slots, masks, ctx, table, buffer;
+    Plan(PyObject* o, int64_t B, int64_t NN, c10::Device dev)
+        : slots(tensor_attr(o, N.slots, "plan.slots")), masks(tensor_attr(o, N.masks, "plan.masks")),
+          ctx(tensor_attr(o, N.context_len, "plan.context_len")), table(tensor_attr(o, N.page_table, "plan.page_table")),
+          buffer(tensor_attr(o, N.buffer, "plan.buffer")) {
+        check(slots, "plan.slots", at::kLong, {B, NN}, dev);
+        check(masks, "plan.masks", at::kInt, {B, NN}, dev);
+        check(ctx, "plan.context_len", at::kInt, {B}, dev);
+        if (table.dim() != 2) bad("plan.page_table must be [B, max_pages]");
+        check(table, "plan.page_table", at::kInt, {B, table.size(1)}, dev);
+        on_device(buffer, "plan.buffer", dev);
+        if (!buffer.is_contiguous() || buffer.nbytes() < spec_tree_plan_size(int(B))) bad("plan.buffer is not the plan's");
+    }
+};
+
 void check_pages(PyObject* plan, const Cache& c, c10::Device dev) {
     if (int_attr(plan, N.page_size) != c.c->page_size || int_attr(plan, N.num_pages) != c.c->num_pages ||
         c.device() != dev)
@@ -395,16 +413,14 @@ PyObject* tree_attention(PyObject* const* a) {
     const int64_t B = q.size(0), NN = q.size(1), Hq = q.size(2), D = q.size(3);
     on_device(q, "q", dev);
     if (q.stride(3) != 1) bad("the channels of q must be contiguous");
-    const Tensor positions = tensor_attr(plan, N.positions, "plan.positions"), buffer = tensor_attr(plan, N.buffer, "plan.buffer"),
-                 table = tensor_attr(plan, N.page_table, "plan.page_table");
+    const Tensor positions = tensor_attr(plan, N.positions, "plan.positions");
     if (positions.dim() != 2 || positions.size(0) != B || positions.size(1) != NN)
         bad("the plan is for " + shape_str(positions.sizes()) + ", q for " + shape_str({B, NN}));
     check_pages(plan, c, positions.device());
+    const Plan P(plan, B, NN, dev);
     const spec_dtype dt = dtype_of(q, "q");
-    Tensor masks;
-    if (a[4] == Py_None) {
-        masks = tensor_attr(plan, N.masks, "plan.masks");
-    } else {
+    Tensor masks = P.masks;
+    if (a[4] != Py_None) {
         masks = tensor(a[4], "masks");
         check(masks, "masks", at::kInt, {B, NN}, dev);
     }
@@ -452,12 +468,12 @@ PyObject* tree_attention(PyObject* const* a) {
             if (PyDict_SetItem(kept.p, key.p, t.p)) throw Raised();
         }
     }
-    on.uses({&q, &buffer, &table, &masks, &out, lse, &ws, maybe(a[8], "dev_status")});
+    on.uses({&q, &P.buffer, &P.table, &masks, &out, lse, &ws, maybe(a[8], "dev_status")});
     on.uses_cache(a[1]);
     run("spec_tree_attention", dev, [&](spec_stream_t st) {
         return spec_tree_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), dt, int(B), int(NN), int(Hq), c.c,
-                                   static_cast<const int32_t*>(table.data_ptr()), int(table.size(1)),
-                                   static_cast<const uint32_t*>(masks.data_ptr()), buffer.data_ptr(), float(scale),
+                                   static_cast<const int32_t*>(P.table.data_ptr()), int(P.table.size(1)),
+                                   static_cast<const uint32_t*>(masks.data_ptr()), P.buffer.data_ptr(), float(scale),
                                    out.data_ptr(), lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(),
                                    ws.nbytes(), st_word, st);
     });
@@ -471,10 +487,11 @@ PyObject* kv_commit(PyObject* const* a) {
     const Py_ssize_t count = PySequence_Fast_GET_SIZE(list.p);
     if (count == 0) bad("no caches");
     PyObject* plan = a[1];
-    const Tensor &last = tensor(a[2], "last_node"), masks = tensor_attr(plan, N.masks, "plan.masks"),
-                 slots = tensor_attr(plan, N.slots, "plan.slots"), ctx = tensor_attr(plan, N.context_len, "plan.context_len");
-    const int64_t B = masks.size(0), NN = masks.size(1);
-    const c10::Device dev = masks.device();
+    const Tensor &last = tensor(a[2], "last_node"), positions = tensor_attr(plan, N.positions, "plan.positions");
+    if (positions.dim() != 2) bad("plan.positions must be [B, N]");
+    const int64_t B = positions.size(0), NN = positions.size(1);
+    const c10::Device dev = positions.device();
+    const Plan P(plan, B, NN, dev);
     check(last, "last_node", at::kInt, {B}, dev);
     Tensor len;
     if (a[3] == Py_None) {
@@ -488,7 +505,7 @@ PyObject* kv_commit(PyObject* const* a) {
         check_pages(plan, Cache(PySequence_Fast_GET_ITEM(list.p, i)), dev);
         on.uses_cache(PySequence_Fast_GET_ITEM(list.p, i));
     }
-    on.uses({&last, &masks, &slots, &ctx, &len, maybe(a[4], "dev_status")});
+    on.uses({&last, &P.masks, &P.slots, &P.ctx, &len, maybe(a[4], "dev_status")});
     // the lengths are written once, by the last group of caches: it may be the
     // plan's own context_len, which the earlier groups still read
     Tensor scratch;
@@ -499,9 +516,9 @@ PyObject* kv_commit(PyObject* const* a) {
         for (int j = 0; j < n; ++j) group[j] = *Cache(PySequence_Fast_GET_ITEM(list.p, i + j)).c;
         const Tensor& to = i + n == count ? len : scratch;
         run("spec_kv_commit", dev, [&](spec_stream_t st) {
-            return spec_kv_commit(group, n, static_cast<const uint32_t*>(masks.data_ptr()),
-                                  static_cast<const int64_t*>(slots.data_ptr()), static_cast<const int32_t*>(last.data_ptr()),
-                                  static_cast<const int32_t*>(ctx.data_ptr()), int(B), int(NN),
+            return spec_kv_commit(group, n, static_cast<const uint32_t*>(P.masks.data_ptr()),
+                                  static_cast<const int64_t*>(P.slots.data_ptr()), static_cast<const int32_t*>(last.data_ptr()),
+                                  static_cast<const int32_t*>(P.ctx.data_ptr()), int(B), int(NN),
                                   static_cast<int32_t*>(to.data_ptr()), st_word, st);
         });
     }
