@@ -77,6 +77,7 @@ int64_t int_attr(PyObject* o, PyObject* name) {
 
 // The calls have no backward: a tensor whose history they would drop is refused.
 void without_history(const Tensor& t, const char* name) {
+    if (!t.unsafeGetTensorImpl()->autograd_meta()) return;  // (most tensors, and every one of integers)
     if ((t.requires_grad() && c10::GradMode::is_enabled()) ||
         (t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode()))
         bad(std::string(name) + " carries a gradient, which this call would drop: detach it, or call under torch.no_grad()");
@@ -378,21 +379,28 @@ PyObject* tree_plan(PyObject* const* a) {
     return PyTuple_Pack(4, x.p, y.p, z.p, w.p);
 }
 
-// The plan's tensors, whose fields a caller can set: as spec_tree_plan left them, for B
-// requests of N nodes.
-struct Plan {
-    Tensor slots, masks, ctx, table, buffer;
-    Plan(PyObject* o, int64_t B, int64_t NN, c10::Device dev)
-        : slots(tensor_attr(o, N.slots, "plan.slots")), masks(tensor_attr(o, N.masks, "plan.masks")),
-          ctx(tensor_attr(o, N.context_len, "plan.context_len")), table(tensor_attr(o, N.page_table, "plan.page_table")),
+// The tensors of a plan that a call reads, for B requests of N nodes: a caller can set the
+// plan's fields.
+struct AttentionPlan {
+    Tensor masks, table, buffer;
+    AttentionPlan(PyObject* o, int64_t B, int64_t NN, c10::Device dev)
+        : masks(tensor_attr(o, N.masks, "plan.masks")), table(tensor_attr(o, N.page_table, "plan.page_table")),
           buffer(tensor_attr(o, N.buffer, "plan.buffer")) {
-        check(slots, "plan.slots", at::kLong, {B, NN}, dev);
         check(masks, "plan.masks", at::kInt, {B, NN}, dev);
-        check(ctx, "plan.context_len", at::kInt, {B}, dev);
         if (table.dim() != 2) bad("plan.page_table must be [B, max_pages]");
         check(table, "plan.page_table", at::kInt, {B, table.size(1)}, dev);
         on_device(buffer, "plan.buffer", dev);
         if (!buffer.is_contiguous() || buffer.nbytes() < spec_tree_plan_size(int(B))) bad("plan.buffer is not the plan's");
+    }
+};
+struct CommitPlan {
+    Tensor masks, slots, ctx;
+    CommitPlan(PyObject* o, int64_t B, int64_t NN, c10::Device dev)
+        : masks(tensor_attr(o, N.masks, "plan.masks")), slots(tensor_attr(o, N.slots, "plan.slots")),
+          ctx(tensor_attr(o, N.context_len, "plan.context_len")) {
+        check(masks, "plan.masks", at::kInt, {B, NN}, dev);
+        check(slots, "plan.slots", at::kLong, {B, NN}, dev);
+        check(ctx, "plan.context_len", at::kInt, {B}, dev);
     }
 };
 
@@ -417,7 +425,7 @@ PyObject* tree_attention(PyObject* const* a) {
     if (positions.dim() != 2 || positions.size(0) != B || positions.size(1) != NN)
         bad("the plan is for " + shape_str(positions.sizes()) + ", q for " + shape_str({B, NN}));
     check_pages(plan, c, positions.device());
-    const Plan P(plan, B, NN, dev);
+    const AttentionPlan P(plan, B, NN, dev);
     const spec_dtype dt = dtype_of(q, "q");
     Tensor masks = P.masks;
     if (a[4] != Py_None) {
@@ -491,7 +499,7 @@ PyObject* kv_commit(PyObject* const* a) {
     if (positions.dim() != 2) bad("plan.positions must be [B, N]");
     const int64_t B = positions.size(0), NN = positions.size(1);
     const c10::Device dev = positions.device();
-    const Plan P(plan, B, NN, dev);
+    const CommitPlan P(plan, B, NN, dev);
     check(last, "last_node", at::kInt, {B}, dev);
     Tensor len;
     if (a[3] == Py_None) {

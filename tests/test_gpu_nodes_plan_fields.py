@@ -29,9 +29,11 @@ def test_changed_fields_are_refused(field, change):
     q = torch.randn(2, 3, 4, 64, device="cuda").to(torch.bfloat16)
     good = binding.tree_attention(q, cache, p)
     bad = dataclasses.replace(p, **{field: change(getattr(p, field))})
-    with pytest.raises(ValueError):
-        binding.tree_attention(q, cache, bad)
-    with pytest.raises(ValueError):
-        binding.kv_commit([cache], bad, i([1, 2]))
+    if field in ("masks", "page_table", "buffer"):
+        with pytest.raises(ValueError):
+            binding.tree_attention(q, cache, bad)
+    if field in ("masks", "slots", "context_len"):
+        with pytest.raises(ValueError):
+            binding.kv_commit([cache], bad, i([1, 2]))
     assert torch.equal(binding.tree_attention(q, cache, p), good)
     assert binding.kv_commit([cache], p, i([1, 2])).tolist() == [7, 23]
