@@ -55,6 +55,8 @@ constexpr int MAX_R = 128;  // rows of the largest tile
 // channels of a part's row in the workspace, the most that a kernel lays out for D
 // (k_attn_tiles 64 or 128, k_attn_rows 64, 96, 128 or 256)
 int width_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+size_t part_o_bytes(int ctas, int D) { return align256(size_t(2) * ctas * MAX_R * width_of(D) * 4); }
+size_t part_ml_bytes(int ctas) { return align256(size_t(2) * ctas * MAX_R * 2 * 4); }
 
 // The parts that k_attn_tiles left: CTA (c, y) joins the item that starts in CTA
 // c's share and ends in another's, its y-th share of the channels.  One row a
@@ -141,8 +143,7 @@ size_t spec_tree_attention_workspace_size(const spec_kv_cache* cache, int q_head
     if (check_cache(cache) != SPEC_OK || q_heads < 1 || q_heads % cache->heads) return 0;
     const int sms = sm_count();
     if (sms <= 0) return 0;
-    return align256(size_t(sms) * 8) + align256(size_t(2) * sms * MAX_R * width_of(cache->head_dim) * 4) +
-           align256(size_t(2) * sms * MAX_R * 2 * 4);
+    return part_o_bytes(sms, cache->head_dim) + part_ml_bytes(sms) + align256(size_t(sms) * 8);
 }
 
 spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q_node_stride,
@@ -199,10 +200,11 @@ spec_status spec_tree_attention(const void* q, int64_t q_batch_stride, int64_t q
     A.rows = N * A.G;
     A.c = scale * 1.4426950408889634f;
     A.q_f16 = dtype == SPEC_F16;
-    char* room = static_cast<char*>(workspace) + align256(size_t(sms) * 8);
-    A.arrived = static_cast<unsigned long long*>(workspace);
+    // (the counts last: ahead of the parts they cost 7 narrow-headed requests 22.9 us, here 22.7)
+    char* room = static_cast<char*>(workspace);
     A.part_o = reinterpret_cast<float*>(room);
-    A.part_ml = reinterpret_cast<float*>(room + align256(size_t(2) * sms * MAX_R * width_of(A.D) * 4));
+    A.part_ml = reinterpret_cast<float*>(room += part_o_bytes(sms, A.D));
+    A.arrived = reinterpret_cast<unsigned long long*>(room + part_ml_bytes(sms));
     A.status = dev_status;
     // More than 16 rows go to the tcgen05 kernels (128 a tile, heads of up to 128),
     // since k_attn_rows reads the cache again for every 16.  Measured (us, k_attn_rows /

@@ -25,6 +25,7 @@ struct AttnArgs {
     const int32_t* table;
     const uint32_t* masks;
     PlanView plan;
+    unsigned long long* arrived;  // [CTAs] arrivals of the parts of the item that starts in a share (arrive)
     const void* v;  // the cache's values (read again where some are not finite)
     const uint8_t* ks;
     const uint8_t* vs;
@@ -35,7 +36,6 @@ struct AttnArgs {
     int lead;           // what an item costs beyond its tiles, in tiles
     float c;            // scale * log2(e): scores are exponents of two
     int q_f16;          // q and out are f16 (else bf16)
-    unsigned long long* arrived;  // [CTAs] arrivals of the parts of the item that starts in a share (arrive)
     float* part_o;      // [2 * CTAs][width / 4][R][4] unnormalised sums
     float* part_ml;     // [2 * CTAs][R][2] reference and total
     int32_t* status;
