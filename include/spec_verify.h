@@ -67,6 +67,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2, SPEC_E4M3 = 3 } spec_d
 #define SPEC_BADBIT_TIMEOUT 32u    /* an internal bounded wait gave up (never expected) */
 #define SPEC_BADBIT_TREE 64u       /* a tree node whose parent is not an earlier node */
 #define SPEC_BADBIT_PAGE 128u      /* a context past its page table, a page or a slot outside the cache */
+#define SPEC_BADBIT_OFFSETS 256u   /* offsets of packed prompts that fall, or leave their tensor */
+#define SPEC_BADBIT_TOKEN 512u     /* a token outside [0, V), or a row outside the logits */
 
 /* Human-readable name of a status code (static string). */
 const char* spec_status_str(spec_status s);
@@ -727,6 +729,154 @@ spec_status spec_kv_commit(const spec_kv_cache* caches, int num_caches, const ui
                            const int64_t* slots, const int32_t* last_node,
                            const int32_t* context_len, int B, int N, int32_t* new_context_len,
                            int32_t* dev_status, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The prompt's pass, ahead of the first decoding step, and the probabilities that
+ * an answer comes with.  The prompts of a batch lie packed one behind the other:
+ *   spec_prompt_plan       once: positions and cache slots of the tokens, and the
+ *                          pieces of the attention's work
+ *   per layer:
+ *     spec_norm_kv_write   norms and rotation of queries and keys; the rows to
+ *                          their slots, and the keys to a tensor
+ *     spec_prompt_attention
+ *   spec_token_logprobs    of the prompt's tokens, or of those that a step kept.
+ */
+
+/*
+ * The norm of each head: y = x / sqrt(mean(x^2) + eps) * weight over the head's
+ * channels, ahead of the rotation.  Squares, sums and products are float32 (so that
+ * |x| has to stay below 2^63 or so), the result of norm and rotation is rounded once.
+ *   q_weight, k_weight  [head_dim] of `dtype` (f32, bf16 or f16), device; NULL: ones.
+ *   eps                 finite and at least 0.  With 0 a head of zeros gives NaN.
+ */
+typedef struct {
+    const void* q_weight;
+    const void* k_weight;
+    int dtype; /* spec_dtype */
+    float eps;
+} spec_head_norm;
+
+/*
+ * spec_norm_rope -- spec_rope with the norm of each head ahead of the rotation.
+ * Arguments as there; table NULL: no rotation (positions is not read).
+ */
+spec_status spec_norm_rope(const spec_head_norm* norm, const void* q, int q_heads,
+                           int64_t q_token_stride, int64_t q_head_stride, void* out_q,
+                           int64_t oq_token_stride, int64_t oq_head_stride, const void* k,
+                           int k_heads, int64_t k_token_stride, int64_t k_head_stride, void* out_k,
+                           int64_t ok_token_stride, int64_t ok_head_stride, spec_dtype dtype, int D,
+                           int64_t T, const int32_t* positions, const spec_rope_table* table,
+                           spec_stream_t stream);
+
+/*
+ * spec_norm_kv_write -- spec_kv_write with the norm of each head of keys and queries
+ * ahead of the rotation (norm NULL: none), and the keys as the cache gets them, in their
+ * own type, to a tensor as well (out_k NULL: not).
+ *   out_k   [T, heads, head_dim] of `dtype`, strides of its own; k itself with equal
+ *           strides: in place.  A token whose slot is negative, or outside the cache, is
+ *           written all the same (as out_q is).
+ * The other arguments as there; q needs a norm or a table.
+ */
+spec_status spec_norm_kv_write(const spec_kv_cache* cache, const spec_head_norm* norm,
+                               const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                               void* out_k, int64_t ok_token_stride, int64_t ok_head_stride,
+                               const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                               spec_dtype dtype, int64_t T, const int64_t* slots,
+                               const int32_t* positions, const spec_rope_table* table,
+                               const void* q, int q_heads, int64_t q_token_stride,
+                               int64_t q_head_stride, void* out_q, int64_t oq_token_stride,
+                               int64_t oq_head_stride, int32_t* dev_status, spec_stream_t stream);
+
+/*
+ * spec_prompt_plan -- where the tokens of B packed prompts stand, and the pieces of their
+ * attention.
+ *   offsets    [B + 1] int32: prompt b's new tokens are rows offsets[b] .. offsets[b + 1] - 1
+ *              of the packed queries.  Rows before offsets[0] and from offsets[B] on belong to
+ *              no prompt.
+ *   k_offsets  NULL (the keys lie as the queries do, and M == T), or [B + 1] int32: its
+ *              keys' rows.  With more keys than queries the queries are the last ones; with
+ *              fewer the first queries see nothing.
+ *   T, M       rows of the packed queries and keys (at most 2^30).
+ *   positions  NULL or [T] int32 (written): the token's place among its prompt's keys
+ *              (negative for a query that sees nothing; 0 for a row of no prompt).
+ *   page_table, max_pages, page_size, num_pages  NULL, or the prompts' pages [B, max_pages]
+ *              as in spec_tree_plan.
+ *   slots      NULL or [T] int64 (written; with a page table): the slot of the token's
+ *              position, or -1: a row of no prompt, a negative position, a page past the
+ *              table or outside the cache (SPEC_BADBIT_PAGE).
+ *   plan       at least spec_prompt_plan_size(...) bytes, 256-byte aligned (written).
+ *   dev_status NULL or one device int32, or-ed into (not zeroed).
+ * Offsets that fall, are negative or pass T or M set SPEC_BADBIT_OFFSETS: then no prompt
+ * of the batch has tokens.  One plan serves every layer, on any number of streams.
+ * SPEC_ERR_UNSUPPORTED: more than 128 query heads a key head.
+ */
+size_t spec_prompt_plan_size(int B, int64_t T, int q_heads, int kv_heads);
+spec_status spec_prompt_plan(const int32_t* offsets, const int32_t* k_offsets, int B, int64_t T,
+                             int64_t M, int q_heads, int kv_heads, const int32_t* page_table,
+                             int max_pages, int page_size, int num_pages, int32_t* positions,
+                             int64_t* slots, void* plan, size_t plan_bytes, int32_t* dev_status,
+                             spec_stream_t stream);
+
+/*
+ * spec_prompt_attention -- causal attention within each prompt: query i of n over m keys
+ * sees keys j <= i + m - n, with a window the last `window` of those,
+ *   out[i, h] = sum_j softmax_j(scale q[i, h] . k[j, h / G]) v[j, h / G], G = q_heads / kv_heads.
+ *   q, k, v    [T, q_heads, D] and [M, kv_heads, D], bf16 or f16, 16-byte aligned, token and
+ *              head strides in elements, multiples of 8; channels contiguous; D a multiple of
+ *              8 in [8, 256].
+ *   plan       of spec_prompt_plan, with the same B, T, M and heads.  (One of other T, M
+ *              or group is not used: nothing is written.)
+ *   scale      positive and finite.
+ *   window     0: none.
+ *   out        [T, q_heads, D] of q's type, dense, 16-byte aligned (written for the rows of
+ *              prompts; others are left as they were).  A query that sees nothing gets zeros.
+ *   lse        NULL or [T, q_heads] f32: the natural logarithm of sum_j exp(scale q . k[j]),
+ *              -inf for a query that sees nothing; rows as in out.
+ *   dev_status NULL or one device int32, or-ed into (SPEC_BADBIT_TIMEOUT).
+ * Scores and sums are float32; weights are rounded to q's type before they meet v, and of
+ * f16 weights those below 2^-33 of the row's largest may add nothing, though the total
+ * has them.  What a query does not see has no effect on it, whatever it holds (infinities and
+ * NaN too).
+ */
+spec_status spec_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                  const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                  const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                                  spec_dtype dtype, int B, int64_t T, int64_t M, int q_heads,
+                                  int kv_heads, int D, const void* plan, float scale, int window,
+                                  void* out, float* lse, int32_t* dev_status,
+                                  spec_stream_t stream);
+
+/*
+ * spec_token_logprobs -- of E given tokens: the log probability under the target, the entropy
+ * of its distribution, and the most probable alternatives.
+ *   logits     [R, V] f32, bf16 or f16, row stride in elements (any, at least V where R > 1),
+ *              aligned to an element; 1 <= V <= 2^24.
+ *   rows       NULL (entry e reads row e, and E <= R) or [E] int32: the row that entry e reads.
+ *   tokens     [E] int32; a negative one: the entry is left out (zeros, and -1 as ids).
+ *   temperature NULL or [E] f32: probabilities are softmax(l / T); 0 stands for 1.
+ *   top        alternatives an entry, 0 to SPEC_MAX_TOP.
+ *   logprobs   [E] f32 (written).
+ *   entropy    NULL or [E] f32 (written): -sum p ln p, in nats.
+ *   top_ids, top_logprobs  [E, top] (written where top > 0): the tokens of the largest
+ *              logits, largest first, of equal ones the lowest index first.  Where a row has
+ *              fewer that are not -inf: -1 and -inf.
+ *   workspace  at least spec_token_logprobs_workspace_size(E, V) bytes, 256-byte aligned, no
+ *              initialisation; one call's at a time.
+ *   dev_status NULL or one device int32, or-ed into.
+ * A masked (-inf) logit has probability 0: a masked token's log probability is -inf.  A row of
+ * which nothing is left (SPEC_BADBIT_EMPTY_ROW) gives -inf and entropy 0; a token at or past V,
+ * or a row outside [0, R) (SPEC_BADBIT_TOKEN), and a temperature that is negative or not finite
+ * (SPEC_BADBIT_TEMPERATURE) give what a negative token does.  With +inf or NaN among a row's
+ * logits its log probabilities and entropy are NaN and its ids unspecified.
+ */
+#define SPEC_MAX_TOP 32
+size_t spec_token_logprobs_workspace_size(int64_t E, int V);
+spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int64_t R, int64_t row_stride,
+                                int V, const int32_t* rows, const int32_t* tokens,
+                                const float* temperature, int64_t E, int top, float* logprobs,
+                                float* entropy, int32_t* top_ids, float* top_logprobs,
+                                void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,7 +23,7 @@ from . import build as _build
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA, SPEC_ERR_WORKSPACE = range(5)
 SPEC_F32, SPEC_BF16, SPEC_F16, SPEC_E4M3 = 0, 1, 2, 3
 BADBIT = {"num_draft": 1, "temperature": 2, "draft_id": 4, "empty_row": 8, "no_probs": 16,
-          "timeout": 32, "tree": 64, "page": 128}
+          "timeout": 32, "tree": 64, "page": 128, "offsets": 256, "token": 512}
 MODE_BAD, MODE_GREEDY, MODE_RESIDUAL, MODE_BONUS, MODE_FALLBACK, MODE_TYPICAL = -1, 0, 1, 2, 3, 4
 MAX_K = 31
 # kernels of one call, in launch order: the request-by-request verifier
@@ -115,6 +115,22 @@ def _declare(lib):
     lib.spec_tree_attention.restype = i32
     lib.spec_tree_attention.argtypes = [vp, i64, i64, i64, i32, i32, i32, i32, vp, vp, i32, vp, vp,
                                         f32, vp, vp, vp, sz, vp, vp]
+    lib.spec_norm_rope.restype = i32
+    lib.spec_norm_rope.argtypes = [vp] + 2 * (side + [vp, i64, i64]) + [i32, i32, i64, vp, vp, vp]
+    lib.spec_norm_kv_write.restype = i32
+    lib.spec_norm_kv_write.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i64, vp, vp, vp] + side + \
+        [vp, i64, i64, vp, vp]
+    lib.spec_prompt_plan_size.restype = sz
+    lib.spec_prompt_plan_size.argtypes = [i32, i64, i32, i32]
+    lib.spec_prompt_plan.restype = i32
+    lib.spec_prompt_plan.argtypes = [vp, vp, i32, i64, i64, i32, i32, vp, i32, i32, i32, vp, vp, vp, sz, vp, vp]
+    lib.spec_prompt_attention.restype = i32
+    lib.spec_prompt_attention.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i32, i64, i64, i32, i32, i32, vp,
+                                          f32, i32, vp, vp, vp, vp]
+    lib.spec_token_logprobs_workspace_size.restype = sz
+    lib.spec_token_logprobs_workspace_size.argtypes = [i64, i32]
+    lib.spec_token_logprobs.restype = i32
+    lib.spec_token_logprobs.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp, i64, i32, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.spec_kv_commit.restype = i32
     lib.spec_kv_commit.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp]
     return lib
@@ -573,6 +589,11 @@ class _CTable(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class _CNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -632,16 +653,46 @@ def rope_table(rot: int, *, base: float = 10000.0, layout: str = "half", scaling
     return RopeTable(turns.to(device), layout, scale.value)
 
 
-def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: RopeTable, *,
+class HeadNorm:
+    """The norm of each head of queries and keys ahead of the rotation (spec_head_norm):
+    x / sqrt(mean(x^2) + eps) * weight.  Weights [head_dim], float32, bfloat16 or
+    float16, the same type for both; None: ones.  The tensors stay the caller's."""
+
+    def __init__(self, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, *,
+                 eps: float = 1e-6):
+        dtype = torch.float32
+        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if t is None:
+                continue
+            if t.dtype not in _DTYPES:
+                raise ValueError(f"{n} must be float32, bfloat16 or float16, got {t.dtype}")
+            _check(t, n, t.dtype)
+            dtype = t.dtype
+        if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise ValueError("q_weight and k_weight must have one type")
+        if not 0 <= eps < 3.4e38:
+            raise ValueError("eps must be finite and at least 0")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        self._c = _CNorm(_ptr(q_weight), _ptr(k_weight), _DTYPES[dtype], eps)
+        self._ref = ctypes.addressof(self._c)
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, table: RopeTable | None, *,
          out_q: torch.Tensor | None = None, out_k: torch.Tensor | None = None,
-         inverse: bool = False, stream=None):
+         inverse: bool = False, norm: HeadNorm | None = None, stream=None):
     """Rotary positions (spec_rope): q [..., q_heads, D] and k [..., k_heads,
     D] (or None) turned by positions [tokens] int32.  out_q / out_k: new
     tensors, or given ones (q and k themselves: in place).  inverse=True is the
     transpose, which takes gradients of the outputs to gradients of the inputs: it
     turns by the negative angles with the table's factor on the rotated channels
     (1 but for "by_parts"), so that it is the inverse where that is 1.
+    norm: each head's norm ahead of the rotation, in the same pass (spec_norm_rope); then
+    positions and table may be None: the norm alone.
     Returns (out_q, out_k), or out_q where k is None."""
+    if norm is not None:
+        if inverse:
+            raise ValueError("inverse is the rotation's, which has no norm")
+        return (_OPS or _ops()).norm_rope(q, k, positions, table, norm, out_q, out_k, stream)
     return (_OPS or _ops()).rope(q, k, positions, table, out_q, out_k, inverse, stream)
 
 
@@ -697,12 +748,18 @@ def new_kv_cache(num_pages: int, page_size: int, heads: int, head_dim: int, *,
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
              positions: torch.Tensor | None = None, table: RopeTable | None = None,
              q: torch.Tensor | None = None, out_q: torch.Tensor | None = None,
+             out_k: torch.Tensor | None = None, norm: HeadNorm | None = None,
              dev_status: torch.Tensor | None = None, stream=None):
     """Write key and value rows [..., heads, head_dim] to their cache slots
     (spec_kv_write); slots [tokens] int64, negative: not written.  With
     `table` and `positions` the keys are rotated on the way, and q [...,
     q_heads, head_dim] into out_q (a new tensor by default), which is
-    returned."""
+    returned.  norm: each head of keys and queries is normalised ahead of that (a
+    rotation is not needed then); out_k [..., heads, head_dim]: gets the keys as well, in
+    their own type (k itself: in place), those of negative slots too (spec_norm_kv_write)."""
+    if norm is not None or out_k is not None:
+        return (_OPS or _ops()).norm_kv_write(cache, k, v, slots, positions, table, q, out_q, out_k, norm, dev_status,
+                                              stream)
     return (_OPS or _ops()).kv_write(cache, k, v, slots, positions, table, q, out_q, dev_status, stream)
 
 
@@ -762,3 +819,67 @@ def kv_commit(caches: list, plan: TreePlan, last_node: torch.Tensor, *,
     result, or spec_verify's second for a chain.  new_context_len may be the
     plan's context_len itself."""
     return (_OPS or _ops()).kv_commit(caches, plan, last_node, new_context_len, dev_status, stream)
+
+
+# ---------------------------------------------------------------- the prompt's pass
+
+@dataclass
+class PromptPlan:
+    """Where the tokens of packed prompts stand (spec_prompt_plan).  One plan serves every
+    layer, on any number of streams."""
+    positions: torch.Tensor        # [T] int32
+    slots: torch.Tensor | None     # [T] int64, where a page table was given
+    prompts: int
+    num_tokens: int
+    num_keys: int
+    q_heads: int
+    kv_heads: int
+    buffer: torch.Tensor           # the pieces of the attention's work
+
+
+def prompt_plan(offsets: torch.Tensor, num_tokens: int, q_heads: int, kv_heads: int, *,
+                k_offsets: torch.Tensor | None = None, num_keys: int | None = None,
+                page_table: torch.Tensor | None = None, cache: KVCache | None = None,
+                dev_status: torch.Tensor | None = None, stream=None) -> PromptPlan:
+    """The pieces, positions and cache slots of packed prompts (spec_prompt_plan): prompt b's
+    new tokens are rows offsets[b] .. offsets[b + 1] - 1 of num_tokens; offsets [prompts + 1]
+    int32 on the device.  k_offsets and num_keys: its keys' rows where they are others (the
+    rest of a prompt whose beginning is there already).  Slots need page_table [prompts,
+    max_pages] int32 and a cache, which gives the pages' size and number."""
+    positions, slots, buffer = (_OPS or _ops()).prompt_plan(offsets, num_tokens, q_heads, kv_heads, k_offsets, num_keys,
+                                                            page_table, cache, dev_status, stream)
+    return PromptPlan(positions, slots, offsets.shape[0] - 1, num_tokens, num_tokens if num_keys is None else num_keys,
+                      q_heads, kv_heads, buffer)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: PromptPlan, *,
+                     scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Causal attention within each of the plan's prompts (spec_prompt_attention): q [T,
+    q_heads, head_dim], k and v [keys, kv_heads, head_dim], bfloat16 or float16.  scale: 1 /
+    sqrt(head_dim) by default; window: how many keys a query sees at most (0: all); lse [T,
+    q_heads] float32: written where given.  Rows of no prompt are left as they were (in a new
+    tensor: whatever its memory holds)."""
+    return (_OPS or _ops()).prompt_attention(q, k, v, plan, scale, window, out, lse, dev_status, stream)
+
+
+@dataclass
+class TokenLogprobs:
+    logprobs: torch.Tensor             # [...] float32, the shape of the tokens
+    entropy: torch.Tensor | None       # [...] float32
+    top_ids: torch.Tensor | None       # [..., top] int32
+    top_logprobs: torch.Tensor | None  # [..., top] float32
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, rows: torch.Tensor | None = None,
+                   temperature: torch.Tensor | None = None, top: int = 0, entropy: bool = False,
+                   workspace: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                   stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens (spec_token_logprobs): logits [..., V] float32, bfloat16
+    or float16, tokens int32, one a row of logits, a negative one left out (spec_verify's out_ids
+    fit as they are); or rows int32 of the tokens' shape says which row each reads (a kept path
+    in a tree's logits).  temperature float32 of the tokens' shape (0: 1).  top: the most
+    probable alternatives, at most 32; entropy: of each row's distribution."""
+    return TokenLogprobs(*(_OPS or _ops()).token_logprobs(logits, tokens, rows, temperature, top, entropy, workspace,
+                                                          dev_status, stream))

@@ -53,7 +53,7 @@ struct Ref {  // an owned reference
 
 // Attribute names, made once.
 #define NAMES(X) X(_ref) X(k) X(v) X(k_scale) X(v_scale) X(turns) X(positions) X(slots) X(masks) X(context_len) X(page_table) X(page_size) \
-    X(num_pages) X(buffer) X(workspace) X(stream_id) X(device_index) X(device_type)
+    X(num_pages) X(buffer) X(workspace) X(q_weight) X(k_weight) X(num_tokens) X(num_keys) X(q_heads) X(kv_heads) X(prompts) X(stream_id) X(device_index) X(device_type)
 struct Names {
 #define X(n) PyObject* n = nullptr;
     NAMES(X)
@@ -233,6 +233,24 @@ struct Cache {
     explicit Cache(PyObject* o)
         : c(reinterpret_cast<const spec_kv_cache*>(int_attr(o, N._ref))), k(tensor_attr(o, N.k, "cache")) {}
     c10::Device device() const { return k.device(); }
+};
+
+struct Norm {
+    const spec_head_norm* n;
+    Tensor q, k;  // weights, where there are some
+    explicit Norm(PyObject* o) : n(reinterpret_cast<const spec_head_norm*>(int_attr(o, N._ref))) {
+        Ref x(attr(o, N.q_weight)), y(attr(o, N.k_weight));
+        if (const Tensor* t = maybe(x.p, "q_weight")) q = *t;
+        if (const Tensor* t = maybe(y.p, "k_weight")) k = *t;
+    }
+    void fits(int64_t D, c10::Device dev) const {
+        if (q.defined()) flat_of(q, "q_weight", D, dev);
+        if (k.defined()) flat_of(k, "k_weight", D, dev);
+    }
+    static void flat_of(const Tensor& t, const char* name, int64_t D, c10::Device dev) {
+        on_device(t, name, dev);
+        if (t.numel() != D) bad(std::string(name) + " has " + std::to_string(t.numel()) + " entries for heads of " + std::to_string(D));
+    }
 };
 
 // rope(q, k, positions, table, out_q, out_k, inverse, stream)
@@ -533,6 +551,258 @@ PyObject* kv_commit(PyObject* const* a) {
     return same(a[3], len);
 }
 
+// norm_rope(q, k, positions, table, norm, out_q, out_k, stream)
+PyObject* norm_rope(PyObject* const* a) {
+    OnStream on(a[7]);
+    const Tensor& q = tensor(a[0], "q");
+    const Tensor *k = maybe(a[1], "k"), *pos = maybe(a[2], "positions");
+    const Norm norm(a[4]);
+    if (!pos != (a[3] == Py_None)) bad("a rotation needs positions and a table");
+    const spec_rope_table* table = nullptr;
+    if (pos) table = reinterpret_cast<const spec_rope_table*>(int_attr(a[3], N._ref));
+    const c10::Device dev = q.device();
+    const at::ScalarType ty = q.scalar_type();
+    const int64_t D = q.dim() ? q.size(-1) : 0;
+    norm.fits(D, dev);
+    const Rows rq = rows(q, "q", -1, D, ty, dev, -1);
+    const spec_dtype dt = dtype_of(q, "q");
+    const Tensor oq = a[5] == Py_None ? empty(q.sizes(), ty, dev) : tensor(a[5], "out_q");
+    const Rows ro = rows(oq, "out_q", rq.heads, D, ty, dev, rq.n);
+    Rows rk, rp;
+    Tensor ok;
+    if (k) {
+        rk = rows(*k, "k", -1, D, ty, dev, rq.n);
+        ok = a[6] == Py_None ? empty(k->sizes(), ty, dev) : tensor(a[6], "out_k");
+        rp = rows(ok, "out_k", rk.heads, D, ty, dev, rq.n);
+    }
+    const int32_t* pp = nullptr;
+    if (pos) {
+        flat(*pos, "positions", at::kInt, rq.n, dev);
+        pp = static_cast<const int32_t*>(pos->data_ptr());
+    }
+    on.uses({&q, k, pos, &oq, &ok, &norm.q, &norm.k});
+    if (pos) on.uses_attrs(a[3], {N.turns});
+    run("spec_norm_rope", dev, [&](spec_stream_t st) {
+        return spec_norm_rope(norm.n, rq.p, rq.heads, rq.step, rq.head, ro.p, ro.step, ro.head, rk.p, rk.heads, rk.step,
+                              rk.head, rp.p, rp.step, rp.head, dt, int(D), rq.n, pp, table, st);
+    });
+    if (!k) return same(a[5], oq);
+    Ref x(same(a[5], oq)), y(same(a[6], ok));
+    return PyTuple_Pack(2, x.p, y.p);
+}
+
+// norm_kv_write(cache, k, v, slots, positions, table, q, out_q, out_k, norm, dev_status, stream)
+PyObject* norm_kv_write(PyObject* const* a) {
+    OnStream on(a[11]);
+    const Cache c(a[0]);
+    const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &slots = tensor(a[3], "slots");
+    const Tensor *pos = maybe(a[4], "positions"), *q = maybe(a[6], "q"), *ok = maybe(a[8], "out_k");
+    std::optional<Norm> norm;
+    if (a[9] != Py_None) norm.emplace(a[9]);
+    const c10::Device dev = c.device();
+    const at::ScalarType ty = k.scalar_type();
+    const int64_t D = c.c->head_dim;
+    if (norm) norm->fits(D, dev);
+    const Rows rk = rows(k, "k", c.c->heads, D, ty, dev, -1), rv = rows(v, "v", c.c->heads, D, ty, dev, rk.n);
+    const spec_dtype dt = dtype_of(k, "k");
+    flat(slots, "slots", at::kLong, rk.n, dev);
+    if (!pos != (a[5] == Py_None)) bad("a rotation needs positions and a table");
+    const spec_rope_table* table = nullptr;
+    const int32_t* pp = nullptr;
+    if (pos) {
+        flat(*pos, "positions", at::kInt, rk.n, dev);
+        table = reinterpret_cast<const spec_rope_table*>(int_attr(a[5], N._ref));
+        pp = static_cast<const int32_t*>(pos->data_ptr());
+    }
+    Rows rq, ro, rp;
+    Tensor oq;
+    if (ok) rp = rows(*ok, "out_k", c.c->heads, D, ty, dev, rk.n);
+    if (q) {
+        if (!table && !norm) bad("q is taken along only to be normalised or rotated");
+        rq = rows(*q, "q", -1, D, ty, dev, rk.n);
+        oq = a[7] == Py_None ? empty(q->sizes(), ty, dev) : tensor(a[7], "out_q");
+        ro = rows(oq, "out_q", rq.heads, D, ty, dev, rk.n);
+    }
+    int32_t* st_word = status_word(a[10], dev);
+    const auto* sp = static_cast<const int64_t*>(slots.data_ptr());
+    on.uses({&k, &v, &slots, pos, q, &oq, ok, maybe(a[10], "dev_status")});
+    if (norm) on.uses({&norm->q, &norm->k});
+    on.uses_cache(a[0]);
+    if (table) on.uses_attrs(a[5], {N.turns});
+    run("spec_norm_kv_write", dev, [&](spec_stream_t st) {
+        return spec_norm_kv_write(c.c, norm ? norm->n : nullptr, rk.p, rk.step, rk.head, rp.p, rp.step, rp.head, rv.p, rv.step,
+                                  rv.head, dt, rk.n, sp, pp, table, rq.p, rq.heads, rq.step, rq.head, ro.p, ro.step,
+                                  ro.head, st_word, st);
+    });
+    if (!q) Py_RETURN_NONE;
+    return same(a[7], oq);
+}
+
+// prompt_plan(offsets, num_tokens, q_heads, kv_heads, k_offsets, num_keys, page_table, cache, dev_status, stream):
+// (positions, slots, buffer)
+PyObject* prompt_plan(PyObject* const* a) {
+    OnStream on(a[9]);
+    const Tensor& off = tensor(a[0], "offsets");
+    const Tensor *koff = maybe(a[4], "k_offsets"), *table = maybe(a[6], "page_table");
+    const int64_t T = integer(a[1]), Hq = integer(a[2]), Hkv = integer(a[3]), M = a[5] == Py_None ? T : integer(a[5]);
+    const c10::Device dev = off.device();
+    if (off.dim() != 1 || off.size(0) < 1) bad("offsets must be [prompts + 1]");
+    const int64_t B = off.size(0) - 1;
+    check(off, "offsets", at::kInt, {B + 1}, dev);
+    if (koff) check(*koff, "k_offsets", at::kInt, {B + 1}, dev);
+    if (!koff && M != T) bad("num_keys differs from num_tokens without k_offsets");
+    if (!table != (a[7] == Py_None)) bad("slots need a page table and a cache");
+    std::optional<Cache> c;
+    if (table) {
+        c.emplace(a[7]);
+        if (table->dim() != 2 || table->size(1) > INT32_MAX) bad("page_table must be [prompts, max_pages]");
+        check(*table, "page_table", at::kInt, {B, table->size(1)}, dev);
+        if (c->device() != dev) bad("the cache is on another device than the offsets");
+    }
+    if (B > INT32_MAX || Hq < 1 || Hq > INT32_MAX || Hkv < 1 || Hkv > INT32_MAX || T < 0 || M < 0) bad("sizes out of range");
+    int32_t* st_word = status_word(a[8], dev);
+    const size_t n = spec_prompt_plan_size(int(B), T, int(Hq), int(Hkv));
+    if (n == 0)
+        bad("unsupported: " + std::to_string(B) + " prompts of " + std::to_string(T) + " tokens, " + std::to_string(Hq) +
+            " query heads over " + std::to_string(Hkv));
+    const Tensor buffer = empty({int64_t(n)}, at::kByte, dev), positions = empty({T}, at::kInt, dev);
+    Tensor slots;
+    if (table) slots = empty({T}, at::kLong, dev);
+    on.uses({&off, koff, table, maybe(a[8], "dev_status")});
+    run("spec_prompt_plan", dev, [&](spec_stream_t st) {
+        return spec_prompt_plan(static_cast<const int32_t*>(off.data_ptr()),
+                                koff ? static_cast<const int32_t*>(koff->data_ptr()) : nullptr, int(B), T, M, int(Hq), int(Hkv),
+                                table ? static_cast<const int32_t*>(table->data_ptr()) : nullptr, table ? int(table->size(1)) : 0,
+                                table ? c->c->page_size : 0, table ? c->c->num_pages : 0,
+                                static_cast<int32_t*>(positions.data_ptr()),
+                                table ? static_cast<int64_t*>(slots.data_ptr()) : nullptr, buffer.data_ptr(), n, st_word, st);
+    });
+    Ref x(THPVariable_Wrap(positions)), w(THPVariable_Wrap(buffer));
+    if (!table) return PyTuple_Pack(3, x.p, Py_None, w.p);
+    Ref y(THPVariable_Wrap(slots));
+    return PyTuple_Pack(3, x.p, y.p, w.p);
+}
+
+// prompt_attention(q, k, v, plan, scale, window, out, lse, dev_status, stream)
+PyObject* prompt_attention(PyObject* const* a) {
+    OnStream on(a[9]);
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    PyObject* plan = a[3];
+    const c10::Device dev = q.device();
+    const at::ScalarType ty = q.scalar_type();
+    const int64_t B = int_attr(plan, N.prompts), T = int_attr(plan, N.num_tokens), M = int_attr(plan, N.num_keys),
+                  Hq = int_attr(plan, N.q_heads), Hkv = int_attr(plan, N.kv_heads);
+    if (q.dim() != 3) bad("q must be [tokens, q_heads, head_dim]");
+    if (k.dim() != 3 || v.dim() != 3) bad("k and v must be [keys, kv_heads, head_dim]");
+    const int64_t D = q.size(2);
+    const Rows rq = rows(q, "q", Hq, D, ty, dev, T), rk = rows(k, "k", Hkv, D, ty, dev, M), rv = rows(v, "v", Hkv, D, ty, dev, M);
+    const spec_dtype dt = dtype_of(q, "q");
+    const Tensor buffer = tensor_attr(plan, N.buffer, "plan.buffer");
+    on_device(buffer, "plan.buffer", dev);
+    if (B < 0 || B > INT32_MAX || Hq > INT32_MAX || Hkv > INT32_MAX || D > INT32_MAX || !buffer.is_contiguous() ||
+        buffer.nbytes() < spec_prompt_plan_size(int(B), T, int(Hq), int(Hkv)))
+        bad("plan.buffer is not the plan's");
+    double scale = 1.0 / std::sqrt(double(D));
+    if (a[4] != Py_None) {
+        scale = PyFloat_AsDouble(a[4]);
+        if (scale == -1.0 && PyErr_Occurred()) throw Raised();
+    }
+    const int64_t window = integer(a[5]);
+    if (window < 0 || window > INT32_MAX) bad("window must be a number of tokens, or 0");
+    Tensor out;
+    if (a[6] == Py_None) {
+        out = empty({T, Hq, D}, ty, dev);
+    } else {
+        out = tensor(a[6], "out");
+        check(out, "out", ty, {T, Hq, D}, dev);
+    }
+    const Tensor* lse = maybe(a[7], "lse");
+    if (lse) check(*lse, "lse", at::kFloat, {T, Hq}, dev);
+    int32_t* st_word = status_word(a[8], dev);
+    on.uses({&q, &k, &v, &buffer, &out, lse, maybe(a[8], "dev_status")});
+    run("spec_prompt_attention", dev, [&](spec_stream_t st) {
+        return spec_prompt_attention(rq.p, rq.step, rq.head, rk.p, rk.step, rk.head, rv.p, rv.step, rv.head, dt, int(B), T, M,
+                                     int(Hq), int(Hkv), int(D), buffer.data_ptr(), float(scale), int(window), out.data_ptr(),
+                                     lse ? static_cast<float*>(lse->data_ptr()) : nullptr, st_word, st);
+    });
+    return same(a[6], out);
+}
+
+// token_logprobs(logits, tokens, rows, temperature, top, entropy, workspace, dev_status, stream):
+// (logprobs, entropy, top_ids, top_logprobs)
+PyObject* token_logprobs(PyObject* const* a) {
+    OnStream on(a[8]);
+    const Tensor &logits = tensor(a[0], "logits"), &tokens = tensor(a[1], "tokens");
+    const Tensor *row = maybe(a[2], "rows"), *temp = maybe(a[3], "temperature");
+    const int64_t top = integer(a[4]);
+    const int ent = PyObject_IsTrue(a[5]);
+    if (ent < 0) throw Raised();
+    const c10::Device dev = logits.device();
+    const int64_t d = logits.dim();
+    if (d < 1 || logits.size(-1) < 1) bad("logits must be [..., V]");
+    on_device(logits, "logits", dev);
+    const spec_dtype dt = dtype_of(logits, "logits");
+    const int64_t V = logits.size(-1);
+    if (V > 1 && logits.stride(-1) != 1) bad("the vocabulary of logits must be contiguous");
+    // the leading dimensions are one run of rows
+    int64_t R = 1, step = V;
+    for (int64_t i = d - 2; i >= 0; --i) {
+        const int64_t n = logits.size(i), s = logits.stride(i);
+        if (n != 1 && R > 1 && s != R * step) bad("the leading dimensions of logits must be one run of rows");
+        if (R == 1 && n != 1) step = s;
+        R *= n;
+    }
+    if (R <= 1) step = V;
+    const int64_t E = tokens.numel();
+    check(tokens, "tokens", at::kInt, tokens.sizes(), dev);
+    if (row) check(*row, "rows", at::kInt, tokens.sizes(), dev);
+    else if (E != R) bad("tokens are " + std::to_string(E) + " for " + std::to_string(R) + " rows of logits");
+    if (temp) check(*temp, "temperature", at::kFloat, tokens.sizes(), dev);
+    if (top < 0 || top > SPEC_MAX_TOP) bad("top must be 0 to " + std::to_string(SPEC_MAX_TOP));
+    if (V > (1 << 24)) bad("unsupported: a vocabulary of " + std::to_string(V));
+    int32_t* st_word = status_word(a[7], dev);
+    size_t n = 0;
+    {
+        c10::cuda::OptionalCUDAGuard guard;
+        if (c10::cuda::current_device() != dev.index()) guard.set_index(dev.index());
+        n = spec_token_logprobs_workspace_size(E, int(V));
+    }
+    if (n == 0) bad("unsupported: " + std::to_string(E) + " tokens");
+    Tensor ws;
+    if (a[6] != Py_None) {
+        ws = tensor(a[6], "workspace");
+        on_device(ws, "workspace", dev);
+        if (!ws.is_contiguous()) bad("workspace must be contiguous");
+    } else {  // of the stream's own pool, so that nothing else has it before the kernels have run
+        ws = empty({int64_t(n)}, at::kByte, dev);
+    }
+    c10::SmallVector<int64_t, 6> shape(tokens.sizes().begin(), tokens.sizes().end());
+    const Tensor lp = empty(shape, at::kFloat, dev);
+    Tensor h, ids, lps;
+    if (ent) h = empty(shape, at::kFloat, dev);
+    if (top) {
+        shape.push_back(top);
+        ids = empty(shape, at::kInt, dev);
+        lps = empty(shape, at::kFloat, dev);
+    }
+    on.uses({&logits, &tokens, row, temp, &ws, maybe(a[7], "dev_status")});
+    auto ptr = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    run("spec_token_logprobs", dev, [&](spec_stream_t st) {
+        return spec_token_logprobs(logits.data_ptr(), dt, R, step, int(V), row ? static_cast<const int32_t*>(row->data_ptr()) : nullptr,
+                                   static_cast<const int32_t*>(tokens.data_ptr()),
+                                   temp ? static_cast<const float*>(temp->data_ptr()) : nullptr, E, int(top),
+                                   static_cast<float*>(lp.data_ptr()), static_cast<float*>(ptr(h)), static_cast<int32_t*>(ptr(ids)),
+                                   static_cast<float*>(ptr(lps)), ws.data_ptr(), ws.nbytes(), st_word, st);
+    });
+    auto wrap = [](const Tensor& t) {
+        if (t.defined()) return THPVariable_Wrap(t);
+        Py_INCREF(Py_None);
+        return Py_None;
+    };
+    Ref x(wrap(lp)), y(wrap(h)), z(wrap(ids)), w(wrap(lps));
+    return PyTuple_Pack(4, x.p, y.p, z.p, w.p);
+}
+
 template <PyObject* (*F)(PyObject* const*), int COUNT>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (n != COUNT) {
@@ -559,7 +829,9 @@ PyObject* error_class(PyObject*, PyObject* cls) {
 #define ENTRY(name, count) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<name, count>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(rope, 8),           ENTRY(kv_write, 10),  ENTRY(kv_read, 6), ENTRY(tree_plan, 7),
-                         ENTRY(tree_attention, 10), ENTRY(kv_commit, 6), {"error_class", error_class, METH_O, nullptr},
+                         ENTRY(tree_attention, 10), ENTRY(kv_commit, 6), ENTRY(norm_rope, 8), ENTRY(norm_kv_write, 12),
+                         ENTRY(prompt_plan, 10), ENTRY(prompt_attention, 10), ENTRY(token_logprobs, 9),
+                         {"error_class", error_class, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "specverify_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

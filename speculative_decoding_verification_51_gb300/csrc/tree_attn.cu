@@ -1,7 +1,6 @@
 // tree_attn.cu -- spec_tree_attention: argument checks, tensor maps and the
 // choice of the kernel.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <mutex>
@@ -10,31 +9,32 @@
 
 using namespace sv;
 
-namespace {
-
-std::mutex g_mu;
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
-bool encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_encode) {
+namespace sv {
+bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!encode) {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
                                              &q) != cudaSuccess ||
             q != cudaDriverEntryPointSuccess || !fn)
             return false;
-        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    *out = g_encode;
+    *out = encode;
     return true;
 }
+}  // namespace sv
+
+namespace {
 
 // One side of a cache as (channel, token of the page, head, page), in boxes
 // of 128 bytes of a row (channels past head_dim read as zeros) x `tokens` rows.
 spec_status cache_map(CUtensorMap* map, const spec_kv_cache& c, void* base, int tokens) {
     PFN_cuTensorMapEncodeTiled_v12000 enc;
-    if (!encoder(&enc)) return SPEC_ERR_CUDA;
+    if (!tensor_map_encoder(&enc)) return SPEC_ERR_CUDA;
     const cuuint64_t es = cuuint64_t(dtype_bytes(c.dtype));
     const cuuint64_t dims[4] = {cuuint64_t(c.head_dim), cuuint64_t(c.page_size),
                                 cuuint64_t(c.heads), cuuint64_t(c.num_pages)};

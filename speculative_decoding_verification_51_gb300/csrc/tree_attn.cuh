@@ -14,6 +14,7 @@
 #include <cuda.h>
 
 #include "cache.cuh"
+#include "tensor.cuh"
 
 namespace sv {
 
@@ -215,23 +216,6 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& A, const Lists& L,
 }
 
 // ---------------------------------------------------------------- small pieces
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            int w, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-    uint32_t r;
-    if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // A value of the cache that is not finite: element (token t of request b, key
 // head h, channel d), or 0 where it is finite.
