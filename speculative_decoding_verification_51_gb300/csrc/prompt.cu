@@ -289,9 +289,9 @@ spec_status spec_prompt_attention(const void* q, int64_t q_token_stride, int64_t
     if (r == SPEC_OK && M) r = heads_map(&L.mv, v, f16, D, 1, kv_heads, M, v_head_stride, v_token_stride, 1, PROMPT_KEYS);
     if (r != SPEC_OK) return r;
     if (!M) L.mk = L.mv = L.mq;
-    const long long ctas = prompt_max_items(B, T, G) * kv_heads * (D > 128 ? 2 : 1);
-    if (ctas > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
-    L.ctas = unsigned(ctas);
+    L.items = prompt_max_items(B, T, G) * kv_heads;
+    L.sms = sm_count();
+    if (L.sms <= 0) return SPEC_ERR_CUDA;
     L.st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = f16 ? launch_prompt_f16(L) : launch_prompt_bf16(L);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

@@ -54,7 +54,8 @@ struct PromptArgs {
 struct PromptLaunch {
     CUtensorMap mq, mk, mv;
     PromptArgs A;
-    unsigned ctas;
+    long long items;  // of all heads, at most
+    int sms;
     cudaStream_t st;
 };
 cudaError_t launch_prompt_bf16(const PromptLaunch& L);

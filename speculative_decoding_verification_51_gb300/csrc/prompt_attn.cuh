@@ -19,6 +19,8 @@
 // that O is seldom rescaled; weights are rounded to the queries' type, relative.
 #pragma once
 
+#include <algorithm>
+
 #include "prompt.cuh"
 
 namespace sv {
@@ -38,67 +40,124 @@ struct PromptShape {
     static constexpr int HIDDEN = 8;  // tiles of keys not seen whole, at most: two at either end of a row tile's
 };
 
+// Descriptors by their low words: the high one is a constant of the 128-byte swizzle (8 rows
+// 1024 bytes apart), and what follows within an operand adds to the address alone.  The thread that
+// issues the products has some 2000 cycles a step for all of its instructions.
+constexpr uint32_t DESC_HIGH = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t a) { return (a >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t a) { return (a >> 4) | uint32_t(16384 >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HIGH)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HIGH)
+        : "memory");
+}
+
+// A place in the ring.
+template <int ST>
+struct RingAt {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == ST) {
+            st = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// A CTA's items: the list's places c, 2 n - 1 - c, 2 n + c, ... of n CTAs.  The list has the
+// longest first, so that every CTA's share comes out alike.
+__device__ __forceinline__ long long place_of(int round) {
+    return (long long)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// One item as the roles see it: tile t's rows are tokens [t * tokens, ...), and its rows see the
+// tiles of keys [lo[t], hi[t]); [j0, j1) are those of all.
+template <int DP>
+struct PromptWork {
+    static constexpr int MT = PromptShape<DP>::MT;
+    int q0, n, k0, last, m, h;
+    int lo[MT], hi[MT], j0, j1;
+    int up[MT], down[MT];  // tile t's rows see tiles j of keys with down[t] <= j < up[t] whole
+    int all_up, all_down;  // and both of them these
+
+    __device__ __forceinline__ PromptWork() {}
+    __device__ __forceinline__ PromptWork(const PromptArgs& A, long long place) {
+        int sub = 0;
+        uint32_t at = uint32_t(place);
+        if (MT == 1) {  // a wide head: which of the item's row tiles
+            sub = int(place & 1);
+            at = uint32_t(place >> 1);
+        }
+        const uint32_t rank = at / uint32_t(A.Hkv);
+        h = int(at - rank * uint32_t(A.Hkv));
+        const int4* p = reinterpret_cast<const int4*>(A.plan + 4) + 2ll * rank;
+        const int4 x = __ldg(p);
+        m = __ldg(&p[1].x);
+        q0 = x.x + sub * A.tokens;
+        n = x.y - sub * A.tokens;
+        k0 = x.z;
+        last = x.w + sub * A.tokens;
+        j0 = all_up = 0x7fffffff;
+        j1 = all_down = 0;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const int tn = max(0, min(A.tokens, n - t * A.tokens)), first = last + t * A.tokens;
+            lo[t] = A.window ? max(0, first - A.window + 1) / PROMPT_KEYS : 0;
+            hi[t] = tn && first + tn > 0 ? (first + tn + PROMPT_KEYS - 1) / PROMPT_KEYS : 0;
+            up[t] = max(0, first + 1) / PROMPT_KEYS;
+            down[t] = A.window ? (max(0, first + tn - A.window) + PROMPT_KEYS - 1) / PROMPT_KEYS : 0;
+            if (hi[t] > lo[t]) {
+                j0 = min(j0, lo[t]);
+                j1 = max(j1, hi[t]);
+                all_up = min(all_up, up[t]);
+                all_down = max(all_down, down[t]);
+            } else {
+                lo[t] = hi[t] = 0;
+            }
+        }
+        if (j1 == 0) j0 = 0;
+    }
+    __device__ __forceinline__ bool in(int t, int j) const { return j >= lo[t] && j < hi[t]; }
+    __device__ __forceinline__ bool any_hidden(int j) const { return j >= all_up || j < all_down; }
+};
+
 template <bool F16, int DP>
 __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
              const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptArgs A) {
     using S = PromptShape<DP>;
-    constexpr int MT = S::MT, ST = S::STAGES, CHUNKS = S::CHUNKS;
+    using Work = PromptWork<DP>;
+    constexpr int MT = S::MT, ST = S::STAGES, C = S::CHUNKS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sm_q = smem;
     uint8_t* ring = smem + MT * S::Q_TILE;
-    __shared__ __align__(8) uint64_t full[ST], empty[ST];
-    __shared__ __align__(8) uint64_t qf[MT], sf[2], pf[2], pv, of[MT], near[S::HIDDEN], clean[S::HIDDEN], fin;
+    __shared__ __align__(8) uint64_t full[ST], empty[ST];  // of the ring
+    __shared__ __align__(8) uint64_t qf[MT], qe[MT];       // a tile's queries there, used
+    __shared__ __align__(8) uint64_t sf[2], pf[2];         // a buffer's scores there, its weights there
+    __shared__ __align__(8) uint64_t of[MT], oe[MT];       // a tile's sums there, read
+    __shared__ __align__(8) uint64_t pv, near, clean, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    __shared__ uint32_t bad[S::HIDDEN][4];  // tokens with values that are not finite
-    __shared__ int bad_at[S::HIDDEN];       // in which tile of keys
-    __shared__ int bad_any, bad_tiles;
+    // values that are not finite, by the parity of the CTA's item: in which tiles of keys, which tokens
+    __shared__ uint32_t bad[2][S::HIDDEN][4];
+    __shared__ int bad_at[2][S::HIDDEN], bad_tiles[2], bad_any[2];
 
     begin_after_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned unit = blockIdx.x;
-    const int sub = MT == 1 ? int(unit & 1u) : 0;  // a wide head: which of the item's row tiles
-    if (MT == 1) unit >>= 1;
-    const int rank = int(unit / unsigned(A.Hkv)), h = int(unit - unsigned(rank) * unsigned(A.Hkv));
     // a plan that was made for other sizes leads nowhere
-    if (rank >= A.plan->items || A.plan->T != A.T || A.plan->M != A.M || A.plan->tokens != A.tokens) return;
-    PromptItem item = reinterpret_cast<const PromptItem*>(A.plan + 4)[rank];
-    if (MT == 1 && sub) {
-        item.q0 += A.tokens;
-        item.n -= A.tokens;
-        item.last += A.tokens;
-        if (item.n <= 0) return;
-    }
-    // Tile t's tokens and the tiles of keys [lo, hi) that its rows see.
-    auto tokens_of = [&](int t) { return max(0, min(A.tokens, item.n - t * A.tokens)); };
-    int lo[MT], hi[MT];
-    int j0 = 0x7fffffff, j1 = 0;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int n = tokens_of(t), first = item.last + t * A.tokens;
-        lo[t] = A.window ? max(0, first - A.window + 1) / PROMPT_KEYS : 0;
-        hi[t] = n ? (first + n + PROMPT_KEYS - 1) / PROMPT_KEYS : 0;
-        if (first + n <= 0) hi[t] = 0;
-        if (hi[t] > lo[t]) {
-            j0 = min(j0, lo[t]);
-            j1 = max(j1, hi[t]);
-        } else {
-            lo[t] = hi[t] = 0;
-        }
-    }
-    if (j1 == 0) j0 = 0;
-    auto in = [&](int t, int j) { return j >= lo[t] && j < hi[t]; };
-    // whether some row of tile t does not see all of tile j of its keys
-    auto hidden = [&](int t, int j) {
-        const int first = item.last + t * A.tokens;
-        return j * PROMPT_KEYS + PROMPT_KEYS - 1 > first ||
-               (A.window && j * PROMPT_KEYS < first + tokens_of(t) - A.window);
-    };
-    auto any_hidden = [&](int j) {
-        return (in(0, j) && hidden(0, j)) || (MT == 2 && in(MT - 1, j) && hidden(MT - 1, j));
-    };
+    const bool fits = A.plan->T == A.T && A.plan->M == A.M && A.plan->tokens == A.tokens;
+    const long long total = fits ? (long long)A.plan->items * A.Hkv * (MT == 1 ? 2 : 1) : 0;
+    if (place_of(0) >= total) return;  // (the first round: no later one has an item either)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -108,19 +167,19 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sf[i], 1);
             mbar_init(&pf[i], 4);
+            bad_any[i] = bad_tiles[i] = 0;
         }
         for (int i = 0; i < MT; ++i) {
             mbar_init(&qf[i], 1);
+            mbar_init(&qe[i], 1);
             mbar_init(&of[i], 1);
+            mbar_init(&oe[i], 4);
         }
         mbar_init(&pv, 1);
-        for (int i = 0; i < S::HIDDEN; ++i) {
-            mbar_init(&near[i], 1);
-            mbar_init(&clean[i], 2);
-        }
+        mbar_init(&near, 1);
+        mbar_init(&clean, 2);
         mbar_init(&fin, 1);
         abort_flag = 0;
-        bad_any = 0;
         fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -140,295 +199,410 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         if (!at_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
     };
 
+    if (warp < 4) {
+    // (the launch's 384 x 168 registers: 128 x 88 and 256 x 208)
+    if constexpr (MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
         // ---- copies
         if (lane == 0) {
-            uint32_t i = 0;  // stages so far
-            auto query = [&](int t) {
-                if (hi[t] <= lo[t]) return;
-                mbar_arrive_expect_tx(&qf[t], uint32_t(DP / 64 * 128 * A.tokens * A.G));
-                for (int c = 0; c < DP / 64; ++c)
-                    tma_load_4d(sm_q + t * S::Q_TILE + c * 16384, &mq, c * 64, 0, h, item.q0 + t * A.tokens, &qf[t]);
-            };
-            auto keys = [&](const CUtensorMap* map, int j) {
-                for (int c = 0; c < CHUNKS; ++c, ++i) {
-                    const uint32_t st = i % ST;
-                    wait(&empty[st], (i / ST) ^ 1u);
+            uint32_t i = 0, uses[MT] = {};  // stages, and queries of a tile, so far
+            for (int round = 0; place_of(round) < total && !*gone; ++round) {
+                const Work w(A, place_of(round));
+                auto query = [&](int t) {
+                    if (w.hi[t] <= w.lo[t]) return;
+                    wait(&qe[t], uses[t] ^ 1u);
                     if (*gone) return;
-                    mbar_arrive_expect_tx(&full[st], uint32_t(S::STAGE));
-                    for (int x = 0; x < S::CH / 64; ++x)
-                        tma_load_4d(ring + st * S::STAGE + x * 16384, map, c * S::CH + x * 64, 0, h,
-                                    item.k0 + j * PROMPT_KEYS, &full[st]);
+                    mbar_arrive_expect_tx(&qf[t], uint32_t(DP / 64 * 128 * A.tokens * A.G));
+                    for (int c = 0; c < DP / 64; ++c)
+                        tma_load_4d(sm_q + t * S::Q_TILE + c * 16384, &mq, c * 64, 0, w.h, w.q0 + t * A.tokens, &qf[t]);
+                    ++uses[t];
+                };
+                auto keys = [&](const CUtensorMap* map, int j) {
+                    for (int c = 0; c < C; ++c) {
+                        const uint32_t st = i % ST;
+                        wait(&empty[st], (i / ST) ^ 1u);
+                        if (*gone) return;
+                        mbar_arrive_expect_tx(&full[st], uint32_t(S::STAGE));
+                        for (int x = 0; x < S::CH / 64; ++x)
+                            tma_load_4d(ring + st * S::STAGE + x * 16384, map, c * S::CH + x * 64, 0, w.h,
+                                        w.k0 + j * PROMPT_KEYS, &full[st]);
+                        ++i;
+                    }
+                };
+                query(0);
+                for (int j = w.j0; j < w.j1 && !*gone; ++j) {
+                    keys(&mk, j);
+                    if (MT == 2 && j == w.j0) query(MT - 1);
+                    keys(&mv, j);
                 }
-            };
-            query(0);
-            for (int j = j0; j < j1 && !*gone; ++j) {
-                keys(&mk, j);
-                if (MT == 2 && j == j0) query(MT - 1);
-                keys(&mv, j);
             }
             // every copy has landed before the CTA leaves (they have, unless a wait ran out)
             if (*gone) {
                 for (int t = 0; t < MT; ++t)
-                    if (hi[t] > lo[t]) at_wait_bounded(&qf[t], 0, AT_WAIT_NS / 8);
+                    if (uses[t]) at_wait_bounded(&qf[t], (uses[t] - 1) & 1u, AT_WAIT_NS / 8);
                 for (uint32_t x = i > ST ? i - ST : 0; x < i; ++x)
                     at_wait_bounded(&full[x % ST], (x / ST) & 1u, AT_WAIT_NS / 8);
             }
         }
     } else if (warp == 1) {
-        // ---- products
+        // ---- products.  A step is a tile of keys of an item; the scores of the next one, which may
+        // be the next item's, are issued between the sums of this one's two row tiles (or ahead
+        // of the one's).
         if (lane == 0) {
             constexpr uint32_t id_s = at_idesc<F16>(128, false), id_o = at_idesc<F16>(S::CH, true);
-            const uint32_t qa = smem_u32(sm_q), ra = smem_u32(ring);
-            auto k_stage = [&](int j) { return uint32_t(j - j0) * 2 * CHUNKS; };
-            auto v_stage = [&](int j) { return uint32_t(j - j0) * 2 * CHUNKS + CHUNKS; };
-            auto scores = [&](int t, int j) {  // (one tile: each chunk of K is released behind its products)
-                if (j == lo[t]) {
-                    wait(&qf[t], 0);
-                }
-                const uint32_t d = tbase + (MT == 2 ? t : (j - j0) & 1) * 128;
-                for (int c = 0; c < CHUNKS; ++c) {
-                    const uint32_t i = k_stage(j) + c, st = i % ST;
-                    wait(&full[st], i / ST);
+            const uint32_t qd = desc_k(smem_u32(sm_q)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
+            RingAt<ST> ks, vs;                              // the next scores' keys, the next sums' values
+            uint32_t queries[MT] = {}, outs[MT] = {};       // uses of a tile's queries and sums so far
+            uint32_t weights[MT] = {};                      // and its tiles of weights
+            uint32_t buf = 0;                               // one tile: the next scores' buffer
+            bool unread[MT] = {};                           // sums that softmax may not have read yet
+            uint32_t cleaned = 0;
+            auto scores = [&](const Work& w, int t, int j) {
+                if (j == w.lo[t]) wait(&qf[t], queries[t]++);
+                const uint32_t b = MT == 2 ? t : buf, d = tbase + b * 128;
+                RingAt<ST> at = ks;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    wait(&full[at.st], at.phase);
                     at_after();
-                    const uint32_t ka = ra + st * S::STAGE, q = qa + t * S::Q_TILE + c * S::STAGE;
+                    const uint32_t k0 = kd + at.st * (S::STAGE >> 4), q = qd + (t * S::Q_TILE + c * S::STAGE >> 4);
 #pragma unroll
                     for (int k = 0; k < S::CH / 16; ++k)
-                        at_mma_ss(d, at_desc_k(q + (k >> 2) * 16384 + (k & 3) * 32),
-                                  at_desc_k(ka + (k >> 2) * 16384 + (k & 3) * 32), id_s, c > 0 || k > 0);
-                    if (MT == 1) at_commit(&empty[st]);
+                        mma_ss(d, q + (k >> 2) * 1024 + (k & 3) * 2, k0 + (k >> 2) * 1024 + (k & 3) * 2, id_s, c > 0 || k > 0);
+                    if (MT == 1) at_commit(&empty[at.st]);
+                    at.next();
                 }
-                at_commit(&sf[MT == 2 ? t : (j - j0) & 1]);
+                at_commit(&sf[b]);
+                if (j + 1 == w.hi[t]) at_commit(&qe[t]);
+                if (MT == 1) buf ^= 1u;
             };
-            // The cleaners are told that a tile of keys comes up (they follow no ring of their own)
-            // while its softmax is under way, and waited for before its values are used.
-            int cleaned = 0;
-            auto tell = [&](int j) {
-                const bool unclean = any_hidden(j);
-                if (unclean) at_arrive(&near[cleaned]);
-                return unclean;
+            // past a step's keys, which both tiles have used, and its values
+            auto next_keys = [&]() {
+                if (MT == 2) at_commit(&empty[ks.st]);
+#pragma unroll
+                for (int c = 0; c < 2 * C; ++c) ks.next();
             };
-            auto sums = [&](int t, int j, bool wait_clean) {
-                const uint32_t n = uint32_t(j - lo[t]);
-                if (wait_clean) wait(&clean[cleaned++], 0);
-                wait(&pf[MT == 2 ? t : n & 1], MT == 2 ? n : n >> 1);
-                const uint32_t p = tbase + (MT == 2 ? t : (j - j0) & 1) * 128;
-                for (int c = 0; c < CHUNKS; ++c) {
-                    const uint32_t i = v_stage(j) + c, st = i % ST;
-                    wait(&full[st], i / ST);
+            auto next_values = [&]() {
+                if (MT == 2) at_commit(&empty[vs.st]);
+#pragma unroll
+                for (int c = 0; c < 2 * C; ++c) vs.next();
+            };
+#pragma unroll
+            for (int c = 0; c < C; ++c) vs.next();
+            auto sums = [&](const Work& w, int t, int j, bool unclean) {
+                if (unclean) wait(&clean, cleaned++);
+                if (j == w.lo[t] && unread[t]) {  // what the last item left has been read
+                    wait(&oe[t], outs[t] - 1);
+                    unread[t] = false;
+                }
+                const uint32_t b = MT == 2 ? t : weights[t] & 1u;
+                RingAt<ST> at = vs;
+                wait(&pf[b], MT == 2 ? weights[t] : weights[t] >> 1);
+                ++weights[t];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    wait(&full[at.st], at.phase);
                     at_after();
-                    const uint32_t va = ra + st * S::STAGE;
+                    const uint32_t v0 = vd + at.st * (S::STAGE >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        at_mma_ts(tbase + T_O + t * DP + c * S::CH, p + k * 8, at_desc_mn(va + k * 2048), id_o,
-                                  j > lo[t] || k > 0);
-                    if (MT == 1) at_commit(&empty[st]);
+                        mma_ts(tbase + T_O + t * DP + c * S::CH, tbase + b * 128 + k * 8, v0 + k * 128, id_o,
+                               j > w.lo[t] || k > 0);
+                    if (MT == 1) at_commit(&empty[at.st]);
+                    at.next();
                 }
                 if (MT == 1) at_commit(&pv);
-                if (j + 1 == hi[t]) at_commit(&of[t]);
+                if (j + 1 == w.hi[t]) {
+                    at_commit(&of[t]);
+                    ++outs[t];
+                    unread[t] = true;
+                }
             };
-            auto release = [&](uint32_t i) {
-                for (int c = 0; c < CHUNKS; ++c) at_commit(&empty[(i + c) % ST]);
+            // The cleaners are told that a tile of keys comes up while its softmax is under way.
+            auto tell = [&](const Work& w, int j) {
+                const bool unclean = w.any_hidden(j);
+                if (unclean) at_arrive(&near);
+                return unclean;
             };
-            if (j1 > j0) {
-                if constexpr (MT == 2) {
-                    for (int t = 0; t < MT; ++t)
-                        if (in(t, j0)) scores(t, j0);
-                    release(k_stage(j0));
-                    for (int j = j0; j < j1; ++j) {
-                        bool unclean = tell(j);
+            int round = 0;
+            // the next item with a step, from `round` on
+            auto next_of = [&](Work& w) {
+                for (; place_of(round) < total;) {
+                    w = Work(A, place_of(round++));
+                    if (w.j1 > w.j0) return true;
+                }
+                return false;
+            };
+            Work w, after;
+            bool more = next_of(w);
+            if (more) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    if (w.in(t, w.j0)) scores(w, t, w.j0);
+                next_keys();
+            }
+            while (more) {
+                const bool next = next_of(after);
+                // a step, and the scores of (x, jx) behind it
+                auto step = [&](int j, const Work& x, int jx, bool go) {
+                    if constexpr (MT == 2) {
+                        bool unclean = tell(w, j);
 #pragma unroll
                         for (int t = 0; t < MT; ++t) {
-                            if (in(t, j)) {
-                                sums(t, j, unclean);
+                            if (w.in(t, j)) {
+                                sums(w, t, j, unclean);
                                 unclean = false;
                             }
-                            if (in(t, j + 1)) scores(t, j + 1);
+                            if (go && x.in(t, jx)) scores(x, t, jx);
                         }
-                        release(v_stage(j));
-                        if (j + 1 < j1) release(k_stage(j + 1));
+                        next_values();
+                        if (go) next_keys();
+                    } else {
+                        if (go) {
+                            scores(x, 0, jx);
+                            next_keys();
+                        }
+                        sums(w, 0, j, tell(w, j));
+                        next_values();
                     }
-                } else {
-                    scores(0, j0);
-                    for (int j = j0; j < j1; ++j) {
-                        if (j + 1 < j1) scores(0, j + 1);
-                        sums(0, j, tell(j));
+                };
+                int j = w.j0;
+                for (; j + 1 < w.j1; ++j) step(j, w, j + 1, true);
+                step(j, after, after.j0, next);
+                // (the marks of an item are kept for one more: so whoever reads the last but one's is done)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    if (unread[t] && !w.hi[t]) {
+                        wait(&oe[t], outs[t] - 1);
+                        unread[t] = false;
                     }
-                }
+                w = after;
+                more = next;
             }
             at_commit(&fin);  // every product is done before TMEM is freed
             at_wait_bounded(&fin, 0, AT_WAIT_NS);
         }
-    } else if (warp < 4) {
+    } else {
         // ---- values that must not meet a weight of zero
         const int tid = threadIdx.x - 64;
-        int slot = 0;
-        for (int j = j0; j < j1; ++j) {
-            if (!any_hidden(j)) continue;
-            wait(&near[slot], 0);
-            if (tid < 4) bad[slot][tid] = 0;
-            if (tid == 0) bad_at[slot] = j;
-            asm volatile("bar.sync 2, 64;" ::: "memory");
-            for (int c = 0; c < CHUNKS; ++c) {
-                const uint32_t i = uint32_t(j - j0) * 2 * CHUNKS + CHUNKS + c, st = i % ST;
-                wait(&full[st], i / ST);
-                constexpr uint32_t EX = F16 ? 0x7c007c00u : 0x7f807f80u;
+        uint32_t step = 0, told = 0;
+        int gen = 0;
+        for (int round = 0; place_of(round) < total; ++round) {
+            const Work w(A, place_of(round));
+            int slot = 0;
+            if (w.j1 <= w.j0) continue;
+            for (int j = w.j0; j < w.j1; ++j, ++step) {
+                if (!w.any_hidden(j)) continue;
+                wait(&near, told++);
+                if (slot == 0 && tid == 0) bad_any[gen] = bad_tiles[gen] = 0;
+                if (tid < 4) bad[gen][slot][tid] = 0;
+                asm volatile("bar.sync 2, 64;" ::: "memory");
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t i = step * 2 * C + C + c, st = i % ST;
+                    wait(&full[st], i / ST);
+                    constexpr uint32_t EX = F16 ? 0x7c00u : 0x7f80u;
+                    const int rows = w.m - j * PROMPT_KEYS;  // of the prompt
 #pragma unroll 4
-                for (int x = tid; x < S::STAGE / 16; x += 64) {
-                    const int row = (x >> 3) & 127;
-                    uint4* p = reinterpret_cast<uint4*>(ring + st * S::STAGE) + x;
-                    if (j * PROMPT_KEYS + row >= item.m) {
-                        *p = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    const uint4 v = *p;
-                    uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                    bool hit = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) hit |= (u[e] & EX & 0xffffu) == (EX & 0xffffu) || (u[e] & EX) >> 16 == EX >> 16;
-                    if (__builtin_expect(hit, 0)) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((u[e] & EX & 0xffffu) == (EX & 0xffffu)) u[e] &= 0xffff0000u;
-                            if ((u[e] & EX) >> 16 == EX >> 16) u[e] &= 0xffffu;
+                    for (int x = tid; x < S::STAGE / 16; x += 64) {
+                        const int row = (x >> 3) & 127;
+                        uint4* p = reinterpret_cast<uint4*>(ring + st * S::STAGE) + x;
+                        if (row >= rows) {
+                            *p = make_uint4(0, 0, 0, 0);
+                            continue;
                         }
-                        *p = make_uint4(u[0], u[1], u[2], u[3]);
-                        atomicOr(&bad[slot][row >> 5], 1u << (row & 31));
-                        bad_any = 1;
+                        const uint4 v = *p;
+                        uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        bool hit = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) hit |= (u[e] & EX) == EX || (u[e] >> 16 & EX) == EX;
+                        if (__builtin_expect(hit, 0)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if ((u[e] & EX) == EX) u[e] &= 0xffff0000u;
+                                if ((u[e] >> 16 & EX) == EX) u[e] &= 0xffffu;
+                            }
+                            *p = make_uint4(u[0], u[1], u[2], u[3]);
+                            atomicOr(&bad[gen][slot][row >> 5], 1u << (row & 31));
+                            bad_any[gen] = 1;
+                        }
                     }
                 }
+                if (tid == 0) {
+                    bad_at[gen][slot] = j;
+                    bad_tiles[gen] = slot + 1;
+                }
+                ++slot;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) at_arrive(&clean);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) at_arrive(&clean[slot]);
-            ++slot;
+            gen ^= 1;
         }
-        if (tid == 0) bad_tiles = slot;
-        asm volatile("bar.arrive 1, %0;" ::"r"(64 + MT * 128) : "memory");
+    }
     } else {
         // ---- softmax: row = this thread's TMEM lane
+        if constexpr (MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = MT == 2 ? (warp - 4) >> 2 : 0, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const int tok = r / A.G, g = r - tok * A.G, token = t * A.tokens + tok;
-        const bool mine = tok < A.tokens && token < item.n;
-        const int end = item.last + token, begin = A.window ? end - A.window + 1 : 0;  // keys it sees: [begin, end]
         const uint32_t o = tbase + lanes + T_O + t * DP;
         const float c = A.c;
-        const int ja = t ? lo[MT - 1] : lo[0], jb = t ? hi[MT - 1] : hi[0];
-        float ref = -INFINITY, tot = 0.f;
-        for (int j = ja; j < jb; ++j) {
-            const uint32_t n = uint32_t(j - ja), buf = MT == 2 ? t : n & 1;
-            const uint32_t sa = tbase + lanes + buf * 128;
-            wait(&sf[buf], MT == 2 ? n : n >> 1);
-            at_after();
-            uint32_t x[4][32];
+        const uint64_t c2 = f2_pack(c, c);
+        uint32_t tiles = 0, outs = 0;  // tiles of weights, and finished rows, so far
+        int gen = 1;
+        for (int round = 0; place_of(round) < total; ++round) {
+            const Work w(A, place_of(round));
+            if (w.j1 > w.j0) gen ^= 1;
+            const bool mine = tok < A.tokens && token < w.n;
+            const int end = w.last + token, begin = A.window ? end - A.window + 1 : 0;  // keys it sees: [begin, end]
+            const int ja = t ? w.lo[MT - 1] : w.lo[0], jb = t ? w.hi[MT - 1] : w.hi[0];
+            const int up = t ? w.up[MT - 1] : w.up[0], down = t ? w.down[MT - 1] : w.down[0];
+            float ref = -INFINITY, tot = 0.f;
+            for (int j = ja; j < jb; ++j, ++tiles) {
+                const uint32_t buf = MT == 2 ? t : tiles & 1u;
+                const uint32_t sa = tbase + lanes + buf * 128;
+                wait(&sf[buf], MT == 2 ? tiles : tiles >> 1);
+                at_after();
+                uint32_t x[4][32];
+                float m0 = -INFINITY, m1 = -INFINITY, s0, s1;
+                auto largest = [&](int y) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) at_ld32(sa + y * 32, x[y]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) at_ld_wait(x[y]);
-            if (__builtin_expect(hidden(t, j), 0)) {
-                const int above = end - j * PROMPT_KEYS, below = begin - j * PROMPT_KEYS;
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int at = y * 32 + e;
-                        if (at > above || at < below) x[y][e] = 0xff800000u;
+                    for (int e = 0; e < 32; e += 4) {
+                        m0 = fmaxf(fmaxf(__uint_as_float(x[y][e]), __uint_as_float(x[y][e + 1])), m0);
+                        m1 = fmaxf(fmaxf(__uint_as_float(x[y][e + 2]), __uint_as_float(x[y][e + 3])), m1);
                     }
-            }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                };
+                auto hide = [&](int y) {
+                    const int above = end - j * PROMPT_KEYS - y * 32, below = begin - j * PROMPT_KEYS - y * 32;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+                    for (int e = 0; e < 32; ++e)
+                        if (e > above || e < below) x[y][e] = 0xff800000u;
+                };
+                uint64_t sum0, sum1, at2;
+                auto weigh = [&](int y) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    m4[y] = fmaxf(fmaxf(__uint_as_float(x[y][e]), __uint_as_float(x[y][e + 1])), m4[y]);
-            const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-            const bool raise = top > ref + TilesRange<F16>::SLACK;
-            if (__any_sync(0xffffffffu, raise)) {
-                const float to = raise ? top - TilesRange<F16>::TOP : ref;
-                const float f = ref == to ? 1.f : ex2_approx(ref - to);
-                ref = to;
-                tot *= f;
-                if (n > 0) {  // O holds sums by the old reference
-                    if (MT == 1) wait(&pv, n - 1);
-                    scale_rows<DP>(o, f);
+                    for (int e = 0; e < 16; ++e) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[y][2 * e]), __uint_as_float(x[y][2 * e + 1])), c2, at2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        if (e & 1) sum1 = f2_add(sum1, f2_pack(a, b));
+                        else sum0 = f2_add(sum0, f2_pack(a, b));
+                        p[e] = pack16<F16>(a, b);
+                    }
+                    at_st16(sa + y * 16, p);
+                };
+                auto begin_sums = [&]() {
+                    const float at = ref == -INFINITY ? 0.f : -ref;
+                    at2 = f2_pack(at, at);
+                    sum0 = sum1 = f2_pack(0.f, 0.f);
+                };
+                const bool masked = j >= up || j < down;
+                // Weights by the reference as it is, piece by piece as the scores come; where some
+                // row's largest passes it by too much (seldom, but for an item's first tile) the
+                // reference is raised and the weights are made again, from the scores in registers.
+                // (A piece's weights lie where scores were that have been read.)
+                bool again = masked || j == ja;
+                at_ld32(sa, x[0]);
+                if (!again) {
+                    begin_sums();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        at_ld_wait(x[y]);
+                        if (y < 3) at_ld32(sa + (y + 1) * 32, x[y + 1]);
+                        largest(y);
+                        weigh(y);
+                    }
+                    again = __any_sync(0xffffffffu, fmaxf(m0, m1) * c > ref + TilesRange<F16>::SLACK);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        at_ld_wait(x[y]);
+                        if (y < 3) at_ld32(sa + (y + 1) * 32, x[y + 1]);
+                        if (masked) hide(y);
+                        largest(y);
+                    }
                 }
-            }
-            const float at = ref == -INFINITY ? 0.f : -ref;
-            const uint64_t c2 = f2_pack(c, c), at2 = f2_pack(at, at);
-            uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
+                if (__builtin_expect(again, 0)) {
+                    const float top = fmaxf(m0, m1) * c;
+                    const bool raise = top > ref + TilesRange<F16>::SLACK;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float to = raise ? top - TilesRange<F16>::TOP : ref;
+                        const float f = ref == to ? 1.f : ex2_approx(ref - to);
+                        ref = to;
+                        tot *= f;
+                        if (j > ja) {  // O holds sums by the old reference
+                            if (MT == 1) wait(&pv, tiles - 1);
+                            scale_rows<DP>(o, f);
+                        }
+                    }
+                    begin_sums();
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float a, b;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[y][2 * e]), __uint_as_float(x[y][2 * e + 1])), c2, at2), a, b);
-                    a = ex2_approx(a);
-                    b = ex2_approx(b);
-                    if (e & 1) s1 = f2_add(s1, f2_pack(a, b));
-                    else s0 = f2_add(s0, f2_pack(a, b));
-                    p[e] = pack16<F16>(a, b);
+                    for (int y = 0; y < 4; ++y) weigh(y);
                 }
-                at_st16(sa + y * 16, p);
+                at_st_wait();
+                at_before();
+                __syncwarp();
+                if (lane == 0) at_arrive(&pf[buf]);
+                f2_unpack(f2_add(sum0, sum1), s0, s1);
+                tot += s0 + s1;
             }
-            at_st_wait();
-            at_before();
-            __syncwarp();
-            if (lane == 0) at_arrive(&pf[buf]);
-            float a, b;
-            f2_unpack(f2_add(s0, s1), a, b);
-            tot += a + b;
-        }
-        asm volatile("bar.sync 1, %0;" ::"r"(64 + MT * 128) : "memory");  // the cleaners' marks are there
-        if (jb > ja) wait(&of[t], 0);
-        at_after();
-        const bool none = tot == 0.f || jb <= ja;
-        const float inv = none ? 0.f : 1.f / tot;
-        uint16_t* out = static_cast<uint16_t*>(A.out) + ((long long)(item.q0 + token) * A.Hq + h * A.G + g) * A.D;
+            const bool none = tot == 0.f || jb <= ja;
+            const float inv = none ? 0.f : 1.f / tot;
+            if (jb > ja) wait(&of[t], outs++);
+            at_after();
+            uint16_t* out = static_cast<uint16_t*>(A.out) + ((long long)(w.q0 + token) * A.Hq + w.h * A.G + g) * A.D;
+            const bool odd = jb > ja && *static_cast<volatile int*>(&bad_any[gen]);
 #pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
-            uint32_t u[32];
-            at_ld32(o + d, u);
-            at_ld_wait(u);
-            float f[32];
+            for (int d = 0; d < DP; d += 32) {
+                uint32_t u[32];
+                at_ld32(o + d, u);
+                at_ld_wait(u);
+                float f[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(u[e]);
-            if (__builtin_expect(bad_any, 0) && mine) {
-                // what it sees of values that are not finite
-                for (int s = 0; s < bad_tiles; ++s) {
-                    if (bad_at[s] < ja || bad_at[s] >= jb) continue;
-                    for (int w = 0; w < 4; ++w)
-                        for (uint32_t b = bad[s][w]; b; b &= b - 1) {
-                            const int key = bad_at[s] * PROMPT_KEYS + w * 32 + __ffs(b) - 1;
-                            if (key > end || key < begin) continue;
-                            const uint16_t* v = static_cast<const uint16_t*>(A.v) + (item.k0 + key) * A.v_token + h * A.v_head;
+                for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(u[e]);
+                if (__builtin_expect(odd, 0) && mine) {
+                    // what it sees of values that are not finite
+                    for (int s = 0; s < bad_tiles[gen]; ++s) {
+                        const int at = bad_at[gen][s];
+                        if (at < ja || at >= jb) continue;
+                        for (int y = 0; y < 4; ++y)
+                            for (uint32_t b = bad[gen][s][y]; b; b &= b - 1) {
+                                const int key = at * PROMPT_KEYS + y * 32 + __ffs(b) - 1;
+                                if (key > end || key < begin) continue;
+                                const uint16_t* v = static_cast<const uint16_t*>(A.v) + (w.k0 + key) * A.v_token + w.h * A.v_head;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (d + e < A.D) {
-                                    const float z = F16 ? __half2float(reinterpret_cast<const __half*>(v)[d + e])
-                                                        : __uint_as_float(uint32_t(v[d + e]) << 16);
-                                    if (!(fabsf(z) < INFINITY)) f[e] += z;
-                                }
+                                for (int e = 0; e < 32; ++e)
+                                    if (d + e < A.D) {
+                                        const float z = F16 ? __half2float(reinterpret_cast<const __half*>(v)[d + e])
+                                                            : __uint_as_float(uint32_t(v[d + e]) << 16);
+                                        if (!(fabsf(z) < INFINITY)) f[e] += z;
+                                    }
+                            }
+                    }
+                }
+                if (mine) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (d + e < A.D) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) v[y] = none ? 0u : pack16<F16>(f[e + 2 * y] * inv, f[e + 2 * y + 1] * inv);
+                            *reinterpret_cast<uint4*>(out + d + e) = make_uint4(v[0], v[1], v[2], v[3]);
                         }
                 }
+                __syncwarp();
             }
-            if (mine) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    if (d + e < A.D) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) w[y] = pack16<F16>(f[e + 2 * y] * inv, f[e + 2 * y + 1] * inv);
-                        if (none) w[0] = w[1] = w[2] = w[3] = 0;
-                        *reinterpret_cast<uint4*>(out + d + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+            if (jb > ja) {
+                at_before();
+                __syncwarp();
+                if (lane == 0) at_arrive(&oe[t]);
             }
-            __syncwarp();
+            if (mine && A.lse)
+                A.lse[(long long)(w.q0 + token) * A.Hq + w.h * A.G + g] =
+                    none ? -INFINITY : (ref + log2f(tot)) * 0.6931471805599453f;
         }
-        if (mine && A.lse)
-            A.lse[(long long)(item.q0 + token) * A.Hq + h * A.G + g] =
-                none ? -INFINITY : (ref + log2f(tot)) * 0.6931471805599453f;
     }
 
     at_before();
@@ -452,7 +626,7 @@ cudaError_t launch_prompt_of(const PromptLaunch& L) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    return launch_behind(k_prompt<F16, DP>, dim3(L.ctas), S::THREADS, S::SMEM, L.st, L.mq, L.mk, L.mv, L.A);
+    return launch_behind(k_prompt<F16, DP>, dim3(unsigned(std::min<long long>(L.items * (S::MT == 1 ? 2 : 1), L.sms))), S::THREADS, S::SMEM, L.st, L.mq, L.mk, L.mv, L.A);
 }
 
 template <bool F16>
