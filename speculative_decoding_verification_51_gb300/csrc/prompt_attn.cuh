@@ -8,9 +8,9 @@
 // A CTA takes one item: two tiles of 128 rows (one of a wide head), whose softmax and
 // products take turns: while the weights of one are made, the tensor cores work for the other.
 //   warp 0        TMA: the rows of Q, then K and V of 128 keys by turns through one ring
-//   warp 1        one thread issues the products: S = Q K^T into TMEM, O += P V with
+//   warps 1, 2    one thread of a warp a row tile issues the products: S = Q K^T into TMEM, O += P V with
 //                 P in TMEM, over the columns that S had
-//   warps 2, 3    in tiles of keys that some row does not see whole: V's rows past the prompt, and
+//   warp 3        in tiles of keys that some row does not see whole: V's rows past the prompt, and
 //                 values that are not finite, become zero (a weight of zero would not hide them)
 //   warps 4..     softmax, one row a thread: the scores in registers, the weights back to
 //                 TMEM as 16 bits, the row's reference and total in registers; then the row of O
@@ -59,6 +59,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HIGH)
         : "memory");
+}
+
+// A value that is the same in all lanes, so that the compiler knows it: what the products are
+// given then stays in uniform registers (moved there for each product, an issue took 60 cycles).
+template <class T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
 }
 
 // A place in the ring.
@@ -137,6 +147,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     using S = PromptShape<DP>;
     using Work = PromptWork<DP>;
     constexpr int MT = S::MT, ST = S::STAGES, C = S::CHUNKS;
+    constexpr int CLEANERS = 3 - MT;  // warps
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sm_q = smem;
@@ -148,6 +159,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     __shared__ __align__(8) uint64_t pv, near, clean, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
+    __shared__ int busy[4];  // a warp of either row tile's softmax that works, by the quarter of the SM they share
     // values that are not finite, by the parity of the CTA's item: in which tiles of keys, which tokens
     __shared__ uint32_t bad[2][S::HIDDEN][4];
     __shared__ int bad_at[2][S::HIDDEN], bad_tiles[2], bad_any[2];
@@ -162,7 +174,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], MT);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sf[i], 1);
@@ -176,10 +188,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
             mbar_init(&oe[i], 4);
         }
         mbar_init(&pv, 1);
-        mbar_init(&near, 1);
-        mbar_init(&clean, 2);
-        mbar_init(&fin, 1);
+        mbar_init(&near, MT);
+        mbar_init(&clean, CLEANERS);
+        mbar_init(&fin, MT);
         abort_flag = 0;
+        busy[0] = busy[1] = busy[2] = busy[3] = 0;
         fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -244,186 +257,184 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     at_wait_bounded(&full[x % ST], (x / ST) & 1u, AT_WAIT_NS / 8);
             }
         }
-    } else if (warp == 1) {
-        // ---- products.  A step is a tile of keys of an item; the scores of the next one, which may
-        // be the next item's, are issued between the sums of this one's two row tiles (or ahead
-        // of the one's).
-        if (lane == 0) {
-            constexpr uint32_t id_s = at_idesc<F16>(128, false), id_o = at_idesc<F16>(S::CH, true);
-            const uint32_t qd = desc_k(smem_u32(sm_q)), kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
-            RingAt<ST> ks, vs;                              // the next scores' keys, the next sums' values
-            uint32_t queries[MT] = {}, outs[MT] = {};       // uses of a tile's queries and sums so far
-            uint32_t weights[MT] = {};                      // and its tiles of weights
-            uint32_t buf = 0;                               // one tile: the next scores' buffer
-            bool unread[MT] = {};                           // sums that softmax may not have read yet
-            uint32_t cleaned = 0;
-            auto scores = [&](const Work& w, int t, int j) {
-                if (j == w.lo[t]) wait(&qf[t], queries[t]++);
-                const uint32_t b = MT == 2 ? t : buf, d = tbase + b * 128;
-                RingAt<ST> at = ks;
+    } else if (warp <= MT) {
+        // ---- products, a warp a row tile: what one waits for and sends out of turn (some 600 cycles
+        // a step) is hidden behind the other's.  A step is a tile of keys of an item; the scores of the next
+        // one, which may be the next item's, are issued behind the sums of this one (ahead of
+        // them where there is one row tile, which has two buffers).
+        constexpr uint32_t id_s = at_idesc<F16>(128, false), id_o = at_idesc<F16>(S::CH, true);
+        const int t = MT == 2 ? uniform(warp) - 1 : 0;
+        const uint32_t qd = desc_k(smem_u32(sm_q)) + uint32_t(t * S::Q_TILE >> 4);
+        const uint32_t kd = desc_k(smem_u32(ring)), vd = desc_mn(smem_u32(ring));
+        const uint32_t t_s = uniform(tbase) + t * 128, t_o = t_s + T_O + t * (DP - 128);
+        const bool leader = elect_one();
+        RingAt<ST> ks, vs;                    // the next scores' keys, the next sums' values
+        uint32_t queries = 0, outs = 0;       // uses of the tile's queries and sums so far
+        uint32_t weights = 0;                 // and its tiles of weights
+        uint32_t buf = 0;                     // one tile: the next scores' buffer
+        bool unread = false;                  // sums that softmax may not have read yet
+        uint32_t cleaned = 0;
+        // (Both warps wait for every stage, used or not: a phase that is waited for is never two behind.)
+        auto scores = [&](bool in, bool first, bool last) {
+            if (in && first) wait(&qf[t], queries++);
+            const uint32_t d = t_s + buf * 128;
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    wait(&full[at.st], at.phase);
+            for (int c = 0; c < C; ++c) {
+                wait(&full[ks.st], ks.phase);
+                if (in && leader) {
                     at_after();
-                    const uint32_t k0 = kd + at.st * (S::STAGE >> 4), q = qd + (t * S::Q_TILE + c * S::STAGE >> 4);
+                    const uint32_t k0 = kd + ks.st * (S::STAGE >> 4), q = qd + (c * S::STAGE >> 4);
 #pragma unroll
                     for (int k = 0; k < S::CH / 16; ++k)
                         mma_ss(d, q + (k >> 2) * 1024 + (k & 3) * 2, k0 + (k >> 2) * 1024 + (k & 3) * 2, id_s, c > 0 || k > 0);
-                    if (MT == 1) at_commit(&empty[at.st]);
-                    at.next();
+                    if (c == C - 1) at_commit(&sf[MT == 2 ? t : buf]);
+                    at_commit(&empty[ks.st]);
+                } else if (leader) {
+                    at_arrive(&empty[ks.st]);
                 }
-                at_commit(&sf[b]);
-                if (j + 1 == w.hi[t]) at_commit(&qe[t]);
-                if (MT == 1) buf ^= 1u;
-            };
-            // past a step's keys, which both tiles have used, and its values
-            auto next_keys = [&]() {
-                if (MT == 2) at_commit(&empty[ks.st]);
+                ks.next();
+            }
 #pragma unroll
-                for (int c = 0; c < 2 * C; ++c) ks.next();
-            };
-            auto next_values = [&]() {
-                if (MT == 2) at_commit(&empty[vs.st]);
+            for (int c = 0; c < C; ++c) ks.next();
+            if (in && last && leader) at_commit(&qe[t]);
+            if (MT == 1) buf ^= 1u;
+        };
 #pragma unroll
-                for (int c = 0; c < 2 * C; ++c) vs.next();
-            };
+        for (int c = 0; c < C; ++c) vs.next();
+        // `unclean`: the cleaners, who were told when the weights were under way, have to be done
+        auto sums = [&](bool in, bool first, bool last, bool unclean) {
+            if (unclean && leader) at_arrive(&near);
+            const uint32_t p = t_s + (MT == 2 ? 0u : (weights & 1u) * 128);
+            if (in) {
+                if (first && unread) wait(&oe[t], outs - 1);  // what the last item left has been read
+                wait(&pf[MT == 2 ? t : weights & 1u], MT == 2 ? weights : weights >> 1);
+                ++weights;
+            }
+            if (unclean) wait(&clean, cleaned++);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                wait(&full[vs.st], vs.phase);
+                if (in && leader) {
+                    at_after();
+                    const uint32_t v0 = vd + vs.st * (S::STAGE >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mma_ts(t_o + c * S::CH, p + k * 8, v0 + k * 128, id_o, !first || k > 0);
+                    if (c == C - 1 && last) at_commit(&of[t]);
+                    at_commit(&empty[vs.st]);
+                } else if (leader) {
+                    at_arrive(&empty[vs.st]);
+                }
+                vs.next();
+            }
 #pragma unroll
             for (int c = 0; c < C; ++c) vs.next();
-            auto sums = [&](const Work& w, int t, int j, bool unclean) {
-                if (unclean) wait(&clean, cleaned++);
-                if (j == w.lo[t] && unread[t]) {  // what the last item left has been read
-                    wait(&oe[t], outs[t] - 1);
-                    unread[t] = false;
-                }
-                const uint32_t b = MT == 2 ? t : weights[t] & 1u;
-                RingAt<ST> at = vs;
-                wait(&pf[b], MT == 2 ? weights[t] : weights[t] >> 1);
-                ++weights[t];
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    wait(&full[at.st], at.phase);
-                    at_after();
-                    const uint32_t v0 = vd + at.st * (S::STAGE >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(tbase + T_O + t * DP + c * S::CH, tbase + b * 128 + k * 8, v0 + k * 128, id_o,
-                               j > w.lo[t] || k > 0);
-                    if (MT == 1) at_commit(&empty[at.st]);
-                    at.next();
-                }
-                if (MT == 1) at_commit(&pv);
-                if (j + 1 == w.hi[t]) {
-                    at_commit(&of[t]);
-                    ++outs[t];
-                    unread[t] = true;
-                }
-            };
-            // The cleaners are told that a tile of keys comes up while its softmax is under way.
-            auto tell = [&](const Work& w, int j) {
-                const bool unclean = w.any_hidden(j);
-                if (unclean) at_arrive(&near);
-                return unclean;
-            };
-            int round = 0;
-            // the next item with a step, from `round` on
-            auto next_of = [&](Work& w) {
-                for (; place_of(round) < total;) {
-                    w = Work(A, place_of(round++));
-                    if (w.j1 > w.j0) return true;
-                }
-                return false;
-            };
-            Work w, after;
-            bool more = next_of(w);
-            if (more) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    if (w.in(t, w.j0)) scores(w, t, w.j0);
-                next_keys();
+            if (MT == 1 && leader) at_commit(&pv);
+            if (in && last) {
+                ++outs;
+                unread = true;
             }
-            while (more) {
-                const bool next = next_of(after);
-                // a step, and the scores of (x, jx) behind it
-                auto step = [&](int j, const Work& x, int jx, bool go) {
-                    if constexpr (MT == 2) {
-                        bool unclean = tell(w, j);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            if (w.in(t, j)) {
-                                sums(w, t, j, unclean);
-                                unclean = false;
-                            }
-                            if (go && x.in(t, jx)) scores(x, t, jx);
-                        }
-                        next_values();
-                        if (go) next_keys();
-                    } else {
-                        if (go) {
-                            scores(x, 0, jx);
-                            next_keys();
-                        }
-                        sums(w, 0, j, tell(w, j));
-                        next_values();
-                    }
-                };
-                int j = w.j0;
-                for (; j + 1 < w.j1; ++j) step(j, w, j + 1, true);
-                step(j, after, after.j0, next);
-                // (the marks of an item are kept for one more: so whoever reads the last but one's is done)
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    if (unread[t] && !w.hi[t]) {
-                        wait(&oe[t], outs[t] - 1);
-                        unread[t] = false;
-                    }
-                w = after;
-                more = next;
+        };
+        int round = 0;
+        // the next item with a step, from `round` on: its steps, the tile's, and which are not seen whole
+        struct Steps {
+            int j0, j1, lo, hi, up, down;
+        };
+        auto next_of = [&](Steps& x) {
+            while (place_of(round) < total) {
+                const Work w(A, place_of(round++));
+                x = {uniform(w.j0), uniform(w.j1), uniform(t ? w.lo[MT - 1] : w.lo[0]), uniform(t ? w.hi[MT - 1] : w.hi[0]),
+                     uniform(w.all_up), uniform(w.all_down)};
+                if (x.j1 > x.j0) return true;
             }
-            at_commit(&fin);  // every product is done before TMEM is freed
-            at_wait_bounded(&fin, 0, AT_WAIT_NS);
+            return false;
+        };
+        auto scores_of = [&](const Steps& x, int j) { scores(j >= x.lo && j < x.hi, j == x.lo, j + 1 == x.hi); };
+        auto sums_of = [&](const Steps& x, int j) {
+            sums(j >= x.lo && j < x.hi, j == x.lo, j + 1 == x.hi, j >= x.up || j < x.down);
+        };
+        Steps w, after;
+        bool more = next_of(w);
+        if (more) scores_of(w, w.j0);
+        while (more) {
+            const bool next = next_of(after);
+            int j = w.j0;
+            for (; j + 1 < w.j1; ++j) {
+                if (MT == 1) scores_of(w, j + 1);
+                sums_of(w, j);
+                if (MT == 2) scores_of(w, j + 1);
+            }
+            if (MT == 1 && next) scores_of(after, after.j0);
+            sums_of(w, j);
+            if (MT == 2 && next) scores_of(after, after.j0);
+            // (the marks of an item are kept for one more: so whoever reads the last but one's is done)
+            if (unread && !w.hi) {
+                wait(&oe[t], outs - 1);
+                unread = false;
+            }
+            w = after;
+            more = next;
         }
+        if (leader) at_commit(&fin);  // every product is done before TMEM is freed
+        at_wait_bounded(&fin, 0, AT_WAIT_NS);
     } else {
         // ---- values that must not meet a weight of zero
-        const int tid = threadIdx.x - 64;
-        uint32_t step = 0, told = 0;
+        constexpr int N = CLEANERS * 32;
+        const int tid = int(threadIdx.x) - (128 - N);
+        uint32_t told = 0;
+        RingAt<ST> vs;
+#pragma unroll
+        for (int c = 0; c < C; ++c) vs.next();
         int gen = 0;
         for (int round = 0; place_of(round) < total; ++round) {
             const Work w(A, place_of(round));
             int slot = 0;
             if (w.j1 <= w.j0) continue;
-            for (int j = w.j0; j < w.j1; ++j, ++step) {
+            for (int j = w.j0; j < w.j1; ++j) {
+                const RingAt<ST> first = vs;
+#pragma unroll
+                for (int c = 0; c < 2 * C; ++c) vs.next();
                 if (!w.any_hidden(j)) continue;
                 wait(&near, told++);
                 if (slot == 0 && tid == 0) bad_any[gen] = bad_tiles[gen] = 0;
                 if (tid < 4) bad[gen][slot][tid] = 0;
-                asm volatile("bar.sync 2, 64;" ::: "memory");
-                for (int c = 0; c < C; ++c) {
-                    const uint32_t i = step * 2 * C + C + c, st = i % ST;
-                    wait(&full[st], i / ST);
-                    constexpr uint32_t EX = F16 ? 0x7c00u : 0x7f80u;
-                    const int rows = w.m - j * PROMPT_KEYS;  // of the prompt
-#pragma unroll 4
-                    for (int x = tid; x < S::STAGE / 16; x += 64) {
-                        const int row = (x >> 3) & 127;
-                        uint4* p = reinterpret_cast<uint4*>(ring + st * S::STAGE) + x;
-                        if (row >= rows) {
-                            *p = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        const uint4 v = *p;
-                        uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                        bool hit = false;
+                asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
+                RingAt<ST> at = first;
+                const int rows = w.m - j * PROMPT_KEYS;  // of the prompt
+                for (int c = 0; c < C; ++c, at.next()) {
+                    wait(&full[at.st], at.phase);
+                    uint4* stage = reinterpret_cast<uint4*>(ring + at.st * S::STAGE);
+                    if (rows < PROMPT_KEYS)
+                        for (int x = tid; x < S::STAGE / 16; x += N)
+                            if (((x >> 3) & 127) >= rows) stage[x] = make_uint4(0, 0, 0, 0);
+                    // an exponent of all ones carries into the bit above it
+                    constexpr uint32_t EX = F16 ? 0x7c007c00u : 0x7f807f80u, ONE = F16 ? 0x04000400u : 0x00800080u;
+#pragma unroll 1
+                    for (int x0 = tid; x0 < S::STAGE / 16; x0 += 8 * N) {
+                        uint32_t hit = 0;
+                        uint4 v[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) hit |= (u[e] & EX) == EX || (u[e] >> 16 & EX) == EX;
-                        if (__builtin_expect(hit, 0)) {
+                        for (int y = 0; y < 8; ++y) v[y] = stage[x0 + y * N];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((u[e] & EX) == EX) u[e] &= 0xffff0000u;
-                                if ((u[e] >> 16 & EX) == EX) u[e] &= 0xffffu;
+                        for (int y = 0; y < 8; ++y)
+                            hit |= ((v[y].x & EX) + ONE) | ((v[y].y & EX) + ONE) | ((v[y].z & EX) + ONE) | ((v[y].w & EX) + ONE);
+                        if (__builtin_expect(hit & 0x80008000u, 0)) {
+#pragma unroll 1
+                            for (int x = x0; x < x0 + 8 * N; x += N) {
+                                uint32_t u[4] = {stage[x].x, stage[x].y, stage[x].z, stage[x].w};
+                                uint32_t some = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t h = ((u[e] & EX) + ONE) & 0x80008000u;
+                                    some |= h;
+                                    u[e] &= ~((h >> 15) * 0xffffu);
+                                }
+                                if (some) {
+                                    stage[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                                    const int row = (x >> 3) & 127;
+                                    atomicOr(&bad[gen][slot][row >> 5], 1u << (row & 31));
+                                    bad_any[gen] = 1;
+                                }
                             }
-                            *p = make_uint4(u[0], u[1], u[2], u[3]);
-                            atomicOr(&bad[gen][slot][row >> 5], 1u << (row & 31));
-                            bad_any[gen] = 1;
                         }
                     }
                 }
@@ -448,6 +459,19 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         const uint32_t o = tbase + lanes + T_O + t * DP;
         const float c = A.c;
         const uint64_t c2 = f2_pack(c, c);
+        // The two warps that share a quarter of the SM make their weights one after the other, so that
+        // the products of one row tile go on under the softmax of the other: at the same time both
+        // would take as long, and both tiles' products wait for the end.  It orders nothing but time: a
+        // warp that has tried long goes on.
+        auto enter = [&]() {
+            if (MT == 1) return;
+            if (lane == 0)
+                for (int i = 0; i < 200 && atomicExch(&busy[warp & 3], 1); ++i) {}
+            __syncwarp();
+        };
+        auto leave = [&]() {
+            if (MT == 2 && lane == 0) *static_cast<volatile int*>(&busy[warp & 3]) = 0;
+        };
         uint32_t tiles = 0, outs = 0;  // tiles of weights, and finished rows, so far
         int gen = 1;
         for (int round = 0; place_of(round) < total; ++round) {
@@ -463,6 +487,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 const uint32_t sa = tbase + lanes + buf * 128;
                 wait(&sf[buf], MT == 2 ? tiles : tiles >> 1);
                 at_after();
+                enter();
                 uint32_t x[4][32];
                 float m0 = -INFINITY, m1 = -INFINITY, s0, s1;
                 auto largest = [&](int y) {
@@ -541,6 +566,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) weigh(y);
                 }
+                leave();
                 at_st_wait();
                 at_before();
                 __syncwarp();
