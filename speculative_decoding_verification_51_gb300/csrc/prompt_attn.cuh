@@ -26,6 +26,9 @@
 namespace sv {
 namespace {
 
+#ifndef NO_LOCK
+#define NO_LOCK 0
+#endif
 template <int DP>
 struct PromptShape {
     static constexpr int MT = DP <= 128 ? 2 : 1;          // row tiles
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     uint8_t* ring = smem + MT * S::Q_TILE;
     __shared__ __align__(8) uint64_t full[ST], empty[ST];  // of the ring
     __shared__ __align__(8) uint64_t qf[MT], qe[MT];       // a tile's queries there, used
-    __shared__ __align__(8) uint64_t sf[2], pf[2];         // a buffer's scores there, its weights there
+    __shared__ __align__(8) uint64_t sf[2], pf[2][2];      // a buffer's scores there, its weights of either half of the keys
     __shared__ __align__(8) uint64_t of[MT], oe[MT];       // a tile's sums there, read
     __shared__ __align__(8) uint64_t pv, near, clean, fin;
     __shared__ uint32_t tmem_base;
@@ -178,7 +181,8 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sf[i], 1);
-            mbar_init(&pf[i], 4);
+            mbar_init(&pf[i][0], 4);
+            mbar_init(&pf[i][1], 4);
             bad_any[i] = bad_tiles[i] = 0;
         }
         for (int i = 0; i < MT; ++i) {
@@ -307,18 +311,24 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
             const uint32_t p = t_s + (MT == 2 ? 0u : (weights & 1u) * 128);
             if (in) {
                 if (first && unread) wait(&oe[t], outs - 1);  // what the last item left has been read
-                wait(&pf[MT == 2 ? t : weights & 1u], MT == 2 ? weights : weights >> 1);
-                ++weights;
             }
             if (unclean) wait(&clean, cleaned++);
+            auto weighed = [&](int half) { wait(&pf[MT == 2 ? t : weights & 1u][half], MT == 2 ? weights : weights >> 1); };
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 wait(&full[vs.st], vs.phase);
-                if (in && leader) {
-                    at_after();
-                    const uint32_t v0 = vd + vs.st * (S::STAGE >> 4);
+                const uint32_t v0 = vd + vs.st * (S::STAGE >> 4);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) mma_ts(t_o + c * S::CH, p + k * 8, v0 + k * 128, id_o, !first || k > 0);
+                for (int half = 0; half < 2; ++half) {
+                    if (in && c == 0) weighed(half);
+                    if (in && leader) {
+                        at_after();
+#pragma unroll
+                        for (int k = 4 * half; k < 4 * half + 4; ++k)
+                            mma_ts(t_o + c * S::CH, p + k * 8, v0 + k * 128, id_o, !first || k > 0);
+                    }
+                }
+                if (in && leader) {
                     if (c == C - 1 && last) at_commit(&of[t]);
                     at_commit(&empty[vs.st]);
                 } else if (leader) {
@@ -329,6 +339,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < C; ++c) vs.next();
             if (MT == 1 && leader) at_commit(&pv);
+            if (in) ++weights;
             if (in && last) {
                 ++outs;
                 unread = true;
@@ -464,13 +475,13 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         // would take as long, and both tiles' products wait for the end.  It orders nothing but time: a
         // warp that has tried long goes on.
         auto enter = [&]() {
-            if (MT == 1) return;
+            if (MT == 1 || NO_LOCK) return;
             if (lane == 0)
                 for (int i = 0; i < 200 && atomicExch(&busy[warp & 3], 1); ++i) {}
             __syncwarp();
         };
         auto leave = [&]() {
-            if (MT == 2 && lane == 0) *static_cast<volatile int*>(&busy[warp & 3]) = 0;
+            if (MT == 2 && !NO_LOCK && lane == 0) *static_cast<volatile int*>(&busy[warp & 3]) = 0;
         };
         uint32_t tiles = 0, outs = 0;  // tiles of weights, and finished rows, so far
         int gen = 1;
@@ -524,53 +535,51 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     sum0 = sum1 = f2_pack(0.f, 0.f);
                 };
                 const bool masked = j >= up || j < down;
-                // Weights by the reference as it is, piece by piece as the scores come; where some
-                // row's largest passes it by too much (seldom, but for an item's first tile) the
-                // reference is raised and the weights are made again, from the scores in registers.
-                // (A piece's weights lie where scores were that have been read.)
-                bool again = masked || j == ja;
+                // (the pieces' largest while the next are on their way)
                 at_ld32(sa, x[0]);
-                if (!again) {
-                    begin_sums();
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        at_ld_wait(x[y]);
-                        if (y < 3) at_ld32(sa + (y + 1) * 32, x[y + 1]);
-                        largest(y);
-                        weigh(y);
-                    }
-                    again = __any_sync(0xffffffffu, fmaxf(m0, m1) * c > ref + TilesRange<F16>::SLACK);
-                } else {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        at_ld_wait(x[y]);
-                        if (y < 3) at_ld32(sa + (y + 1) * 32, x[y + 1]);
-                        if (masked) hide(y);
-                        largest(y);
+                at_ld32(sa + 32, x[1]);
+                at_ld_wait(x[0]);
+                at_ld_wait(x[1]);
+                at_ld32(sa + 64, x[2]);
+                at_ld32(sa + 96, x[3]);
+                if (__builtin_expect(masked, 0)) {
+                    hide(0);
+                    hide(1);
+                }
+                largest(0);
+                largest(1);
+                at_ld_wait(x[2]);
+                at_ld_wait(x[3]);
+                if (__builtin_expect(masked, 0)) {
+                    hide(2);
+                    hide(3);
+                }
+                largest(2);
+                largest(3);
+                const float top = fmaxf(m0, m1) * c;
+                const bool raise = top > ref + TilesRange<F16>::SLACK;
+                if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
+                    const float to = raise ? top - TilesRange<F16>::TOP : ref;
+                    const float f = ref == to ? 1.f : ex2_approx(ref - to);
+                    ref = to;
+                    tot *= f;
+                    if (j > ja) {  // O holds sums by the old reference
+                        if (MT == 1) wait(&pv, tiles - 1);
+                        scale_rows<DP>(o, f);
                     }
                 }
-                if (__builtin_expect(again, 0)) {
-                    const float top = fmaxf(m0, m1) * c;
-                    const bool raise = top > ref + TilesRange<F16>::SLACK;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float to = raise ? top - TilesRange<F16>::TOP : ref;
-                        const float f = ref == to ? 1.f : ex2_approx(ref - to);
-                        ref = to;
-                        tot *= f;
-                        if (j > ja) {  // O holds sums by the old reference
-                            if (MT == 1) wait(&pv, tiles - 1);
-                            scale_rows<DP>(o, f);
-                        }
-                    }
-                    begin_sums();
+                begin_sums();
+                // the products with the first half of the keys begin while the second is weighed
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) weigh(y);
+                for (int half = 0; half < 2; ++half) {
+                    weigh(2 * half);
+                    weigh(2 * half + 1);
+                    at_st_wait();
+                    at_before();
+                    __syncwarp();
+                    if (lane == 0) at_arrive(&pf[buf][half]);
                 }
                 leave();
-                at_st_wait();
-                at_before();
-                __syncwarp();
-                if (lane == 0) at_arrive(&pf[buf]);
                 f2_unpack(f2_add(sum0, sum1), s0, s1);
                 tot += s0 + s1;
             }
