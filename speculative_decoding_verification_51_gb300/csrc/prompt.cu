@@ -285,6 +285,7 @@ spec_status spec_prompt_attention(const void* q, int64_t q_token_stride, int64_t
     A.status = dev_status;
     // (without keys nothing is copied: any map will do)
     spec_status r = heads_map(&L.mq, q, f16, D, G, kv_heads, T, q_head_stride, q_token_stride, G, tokens);
+    if (r == SPEC_OK) r = heads_map(&L.mo, out, f16, D, G, kv_heads, T, D, (long long)q_heads * D, G, tokens);
     if (r == SPEC_OK && M) r = heads_map(&L.mk, k, f16, D, 1, kv_heads, M, k_head_stride, k_token_stride, 1, PROMPT_KEYS);
     if (r == SPEC_OK && M) r = heads_map(&L.mv, v, f16, D, 1, kv_heads, M, v_head_stride, v_token_stride, 1, PROMPT_KEYS);
     if (r != SPEC_OK) return r;

@@ -52,7 +52,7 @@ struct PromptArgs {
 };
 
 struct PromptLaunch {
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     PromptArgs A;
     long long items;  // of all heads, at most
     int sms;

@@ -26,9 +26,6 @@
 namespace sv {
 namespace {
 
-#ifndef NO_LOCK
-#define NO_LOCK 0
-#endif
 template <int DP>
 struct PromptShape {
     static constexpr int MT = DP <= 128 ? 2 : 1;          // row tiles
@@ -83,6 +80,11 @@ struct RingAt {
             st = 0;
             phase ^= 1u;
         }
+    }
+    __device__ __forceinline__ void skip(uint32_t n) {
+        const uint32_t x = st + n, q = x / ST;
+        st = x - q * ST;
+        phase ^= q & 1u;
     }
 };
 
@@ -141,12 +143,21 @@ struct PromptWork {
     }
     __device__ __forceinline__ bool in(int t, int j) const { return j >= lo[t] && j < hi[t]; }
     __device__ __forceinline__ bool any_hidden(int j) const { return j >= all_up || j < all_down; }
+    // stages of the ring, behind the item's values, for its rows of O on their way out: of row tiles
+    // that see something (the others' zeros go out directly)
+    __device__ __forceinline__ uint32_t out_stages() const {
+        uint32_t n = 0;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) n += hi[t] > lo[t] ? PromptShape<DP>::CHUNKS : 0;
+        return n;
+    }
 };
 
 template <bool F16, int DP>
 __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-             const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptArgs A) {
+             const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+             const __grid_constant__ PromptArgs A) {
     using S = PromptShape<DP>;
     using Work = PromptWork<DP>;
     constexpr int MT = S::MT, ST = S::STAGES, C = S::CHUNKS;
@@ -162,10 +173,10 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     __shared__ __align__(8) uint64_t pv, near, clean, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    __shared__ int busy[4];  // a warp of either row tile's softmax that works, by the quarter of the SM they share
+    __shared__ int busy[2][4];  // a row tile's softmax at work, by the quarter of the SM that it shares with the other's
     // values that are not finite, by the parity of the CTA's item: in which tiles of keys, which tokens
     __shared__ uint32_t bad[2][S::HIDDEN][4];
-    __shared__ int bad_at[2][S::HIDDEN], bad_tiles[2], bad_any[2];
+    __shared__ int bad_at[2][S::HIDDEN], bad_tiles[2], bad_item[2];  // (bad_item: whose they are)
 
     begin_after_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -183,7 +194,8 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
             mbar_init(&sf[i], 1);
             mbar_init(&pf[i][0], 4);
             mbar_init(&pf[i][1], 4);
-            bad_any[i] = bad_tiles[i] = 0;
+            bad_tiles[i] = 0;
+            bad_item[i] = -1;
         }
         for (int i = 0; i < MT; ++i) {
             mbar_init(&qf[i], 1);
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         mbar_init(&clean, CLEANERS);
         mbar_init(&fin, MT);
         abort_flag = 0;
-        busy[0] = busy[1] = busy[2] = busy[3] = 0;
+        for (int i = 0; i < 8; ++i) busy[i >> 2][i & 3] = 0;
         fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -251,6 +263,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     keys(&mk, j);
                     if (MT == 2 && j == w.j0) query(MT - 1);
                     keys(&mv, j);
+                }
+                for (uint32_t n = w.out_stages(); n && !*gone; --n, ++i) {
+                    const uint32_t st = i % ST;
+                    wait(&empty[st], (i / ST) ^ 1u);
+                    at_arrive(&full[st]);
                 }
             }
             // every copy has landed before the CTA leaves (they have, unless a wait ran out)
@@ -349,12 +366,13 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         // the next item with a step, from `round` on: its steps, the tile's, and which are not seen whole
         struct Steps {
             int j0, j1, lo, hi, up, down;
+            uint32_t outs;
         };
         auto next_of = [&](Steps& x) {
             while (place_of(round) < total) {
                 const Work w(A, place_of(round++));
                 x = {uniform(w.j0), uniform(w.j1), uniform(t ? w.lo[MT - 1] : w.lo[0]), uniform(t ? w.hi[MT - 1] : w.hi[0]),
-                     uniform(w.all_up), uniform(w.all_down)};
+                     uniform(w.all_up), uniform(w.all_down), uniform(w.out_stages())};
                 if (x.j1 > x.j0) return true;
             }
             return false;
@@ -374,9 +392,12 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 sums_of(w, j);
                 if (MT == 2) scores_of(w, j + 1);
             }
-            if (MT == 1 && next) scores_of(after, after.j0);
+            // (an item's end is alike for one row tile: its values, rows of O and the next keys, all at
+            // once, are more than the ring holds)
             sums_of(w, j);
-            if (MT == 2 && next) scores_of(after, after.j0);
+            ks.skip(w.outs);
+            vs.skip(w.outs);
+            if (next) scores_of(after, after.j0);
             // (the marks of an item are kept for one more: so whoever reads the last but one's is done)
             if (unread && !w.hi) {
                 wait(&oe[t], outs - 1);
@@ -406,7 +427,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 for (int c = 0; c < 2 * C; ++c) vs.next();
                 if (!w.any_hidden(j)) continue;
                 wait(&near, told++);
-                if (slot == 0 && tid == 0) bad_any[gen] = bad_tiles[gen] = 0;
+                if (slot == 0 && tid == 0) bad_tiles[gen] = 0;
                 if (tid < 4) bad[gen][slot][tid] = 0;
                 asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
                 RingAt<ST> at = first;
@@ -443,7 +464,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                                     stage[x] = make_uint4(u[0], u[1], u[2], u[3]);
                                     const int row = (x >> 3) & 127;
                                     atomicOr(&bad[gen][slot][row >> 5], 1u << (row & 31));
-                                    bad_any[gen] = 1;
+                                    bad_item[gen] = round;
                                 }
                             }
                         }
@@ -458,6 +479,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) at_arrive(&clean);
             }
+            vs.skip(w.out_stages());
             gen ^= 1;
         }
     }
@@ -472,17 +494,20 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         const uint64_t c2 = f2_pack(c, c);
         // The two warps that share a quarter of the SM make their weights one after the other, so that
         // the products of one row tile go on under the softmax of the other: at the same time both
-        // would take as long, and both tiles' products wait for the end.  It orders nothing but time: a
-        // warp that has tried long goes on.
+        // would take as long, and both tiles' products wait for the end (1368 us against 1706).  It orders
+        // nothing but time: both may begin at once, and who has waited long goes on.
+        volatile int* mine_busy = &busy[t][warp & 3];
+        volatile int* other_busy = &busy[MT - 1 - t][warp & 3];
         auto enter = [&]() {
-            if (MT == 1 || NO_LOCK) return;
-            if (lane == 0)
-                for (int i = 0; i < 200 && atomicExch(&busy[warp & 3], 1); ++i) {}
-            __syncwarp();
+            if constexpr (MT == 2) {
+                for (int i = 0; i < 100 && *other_busy; ++i) {}
+                *mine_busy = 1;
+            }
         };
         auto leave = [&]() {
-            if (MT == 2 && !NO_LOCK && lane == 0) *static_cast<volatile int*>(&busy[warp & 3]) = 0;
+            if (MT == 2) *mine_busy = 0;
         };
+        RingAt<ST> os;  // the item's first stage
         uint32_t tiles = 0, outs = 0;  // tiles of weights, and finished rows, so far
         int gen = 1;
         for (int round = 0; place_of(round) < total; ++round) {
@@ -514,6 +539,10 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     for (int e = 0; e < 32; ++e)
                         if (e > above || e < below) x[y][e] = 0xff800000u;
                 };
+                // (a warp's few tokens see most pieces whole)
+                auto partly = [&](int y) {
+                    return !__all_sync(0xffffffffu, end - j * PROMPT_KEYS - y * 32 >= 31 && begin - j * PROMPT_KEYS - y * 32 <= 0);
+                };
                 uint64_t sum0, sum1, at2;
                 auto weigh = [&](int y) {
                     uint32_t p[16];
@@ -543,16 +572,16 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 at_ld32(sa + 64, x[2]);
                 at_ld32(sa + 96, x[3]);
                 if (__builtin_expect(masked, 0)) {
-                    hide(0);
-                    hide(1);
+                    if (partly(0)) hide(0);
+                    if (partly(1)) hide(1);
                 }
                 largest(0);
                 largest(1);
                 at_ld_wait(x[2]);
                 at_ld_wait(x[3]);
                 if (__builtin_expect(masked, 0)) {
-                    hide(2);
-                    hide(3);
+                    if (partly(2)) hide(2);
+                    if (partly(3)) hide(3);
                 }
                 largest(2);
                 largest(3);
@@ -583,61 +612,103 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 f2_unpack(f2_add(sum0, sum1), s0, s1);
                 tot += s0 + s1;
             }
-            const bool none = tot == 0.f || jb <= ja;
+            const bool none = tot == 0.f;
             const float inv = none ? 0.f : 1.f / tot;
-            if (jb > ja) wait(&of[t], outs++);
-            at_after();
-            uint16_t* out = static_cast<uint16_t*>(A.out) + ((long long)(w.q0 + token) * A.Hq + w.h * A.G + g) * A.D;
-            const bool odd = jb > ja && *static_cast<volatile int*>(&bad_any[gen]);
+            uint16_t* out = static_cast<uint16_t*>(A.out) + ((long long)(w.q0 + t * A.tokens) * A.Hq + w.h * A.G) * A.D;
+            // (its stages: behind the first row tile's, if that has some)
+            const RingAt<ST> start = os;
+            os.skip(2 * C * uint32_t(w.j1 - w.j0));
+            if (t && w.hi[0] > w.lo[0]) os.skip(C);
+            if (jb > ja) {
+                // the row, 16 bits, to this row tile's stage, laid out as a copy by tensor map wants it
+                const RingAt<ST> o0 = os;
+                wait(&of[t], outs++);
+                at_after();
+                const bool odd = *static_cast<volatile int*>(&bad_item[gen]) == round;
+                for (int x = 0; x < C; ++x, os.next()) wait(&full[os.st], os.phase);
 #pragma unroll 1
-            for (int d = 0; d < DP; d += 32) {
-                uint32_t u[32];
-                at_ld32(o + d, u);
-                at_ld_wait(u);
-                float f[32];
+                for (int d = 0; d < DP; d += 32) {
+                    uint32_t u[32];
+                    at_ld32(o + d, u);
+                    at_ld_wait(u);
+                    float f[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(u[e]);
-                if (__builtin_expect(odd, 0) && mine) {
-                    // what it sees of values that are not finite
-                    for (int s = 0; s < bad_tiles[gen]; ++s) {
-                        const int at = bad_at[gen][s];
-                        if (at < ja || at >= jb) continue;
-                        for (int y = 0; y < 4; ++y)
-                            for (uint32_t b = bad[gen][s][y]; b; b &= b - 1) {
-                                const int key = at * PROMPT_KEYS + y * 32 + __ffs(b) - 1;
-                                if (key > end || key < begin) continue;
-                                const uint16_t* v = static_cast<const uint16_t*>(A.v) + (w.k0 + key) * A.v_token + w.h * A.v_head;
+                    for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(u[e]);
+                    if (__builtin_expect(odd, 0) && mine) {
+                        // what it sees of values that are not finite
+                        for (int s = 0; s < bad_tiles[gen]; ++s) {
+                            const int at = bad_at[gen][s];
+                            if (at < ja || at >= jb) continue;
+                            for (int y = 0; y < 4; ++y)
+                                for (uint32_t b = bad[gen][s][y]; b; b &= b - 1) {
+                                    const int key = at * PROMPT_KEYS + y * 32 + __ffs(b) - 1;
+                                    if (key > end || key < begin) continue;
+                                    const uint16_t* v = static_cast<const uint16_t*>(A.v) + (w.k0 + key) * A.v_token + w.h * A.v_head;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (d + e < A.D) {
-                                        const float z = F16 ? __half2float(reinterpret_cast<const __half*>(v)[d + e])
-                                                            : __uint_as_float(uint32_t(v[d + e]) << 16);
-                                        if (!(fabsf(z) < INFINITY)) f[e] += z;
-                                    }
-                            }
+                                    for (int e = 0; e < 32; ++e)
+                                        if (d + e < A.D) {
+                                            const float z = F16 ? __half2float(reinterpret_cast<const __half*>(v)[d + e])
+                                                                : __uint_as_float(uint32_t(v[d + e]) << 16);
+                                            if (!(fabsf(z) < INFINITY)) f[e] += z;
+                                        }
+                                }
+                        }
+                    }
+                    uint8_t* row = ring + (C > 1 && d >= S::CH ? (o0.st + 1) % ST : o0.st) * S::STAGE + (d % S::CH) / 64 * 16384 + r * 128;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = none ? 0u : pack16<F16>(f[8 * y + 2 * e] * inv, f[8 * y + 2 * e + 1] * inv);
+                        *reinterpret_cast<uint4*>(row + (((d % 64 / 8 + y) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
-                if (mine) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        if (d + e < A.D) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) v[y] = none ? 0u : pack16<F16>(f[e + 2 * y] * inv, f[e + 2 * y + 1] * inv);
-                            *reinterpret_cast<uint4*>(out + d + e) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                }
-                __syncwarp();
-            }
-            if (jb > ja) {
                 at_before();
                 __syncwarp();
                 if (lane == 0) at_arrive(&oe[t]);
+                // a whole tile by one copy, part of one row by row
+                const int rows = max(0, min(A.tokens, w.n - t * A.tokens)) * A.G;
+                const bool whole = rows == A.tokens * A.G;
+                if (whole) fence_proxy_async_smem();
+                auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(4 + t) : "memory"); };
+                sync();
+                if (!whole) {
+                    const uint32_t each = uint32_t(A.D) / 8;
+                    for (uint32_t x = threadIdx.x & 127; x < uint32_t(rows) * each; x += 128) {
+                        const uint32_t rr = x / each, d = (x - rr * each) * 8, tk = rr / uint32_t(A.G);
+                        const uint8_t* row = ring + (C > 1 && d >= S::CH ? (o0.st + 1) % ST : o0.st) * S::STAGE + (d % S::CH) / 64 * 16384 + rr * 128;
+                        *reinterpret_cast<uint4*>(out + ((long long)tk * A.Hq + (rr - tk * A.G)) * A.D + d) =
+                            *reinterpret_cast<const uint4*>(row + (((d % 64 / 8) ^ (rr & 7)) << 4));
+                    }
+                    // (what is copied in here next comes by another path)
+                    fence_proxy_async_smem();
+                    sync();
+                }
+                if ((threadIdx.x & 127) == 0) {
+                    if (whole) {
+                        for (int x = 0; x < DP / 64; ++x) {
+                            const uint32_t st = C > 1 && x >= 2 ? (o0.st + 1) % ST : o0.st;
+                            tma_store_4d(&mo, ring + st * S::STAGE + (x * 64 % S::CH) / 64 * 16384, x * 64, 0, w.h, w.q0 + t * A.tokens);
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
+                    RingAt<ST> at = o0;
+                    for (int x = 0; x < C; ++x, at.next())
+                        asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&empty[at.st])), "n"(MT) : "memory");
+                }
+            } else if (mine) {  // rows that see nothing
+                for (int d = 0; d < A.D; d += 8)
+                    *reinterpret_cast<uint4*>(out + ((long long)tok * A.Hq + g) * A.D + d) = make_uint4(0, 0, 0, 0);
             }
+            os = start;
+            os.skip(2 * C * uint32_t(w.j1 - w.j0) + w.out_stages());
             if (mine && A.lse)
                 A.lse[(long long)(w.q0 + token) * A.Hq + w.h * A.G + g] =
                     none ? -INFINITY : (ref + log2f(tot)) * 0.6931471805599453f;
         }
+        if ((threadIdx.x & 127) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     at_before();
@@ -661,7 +732,7 @@ cudaError_t launch_prompt_of(const PromptLaunch& L) {
         if (e != cudaSuccess) return e;
         ready[dev] = true;
     }
-    return launch_behind(k_prompt<F16, DP>, dim3(unsigned(std::min<long long>(L.items * (S::MT == 1 ? 2 : 1), L.sms))), S::THREADS, S::SMEM, L.st, L.mq, L.mk, L.mv, L.A);
+    return launch_behind(k_prompt<F16, DP>, dim3(unsigned(std::min<long long>(L.items * (S::MT == 1 ? 2 : 1), L.sms))), S::THREADS, S::SMEM, L.st, L.mq, L.mk, L.mv, L.mo, L.A);
 }
 
 template <bool F16>
