@@ -104,23 +104,34 @@ struct PromptWork {
     int up[MT], down[MT];  // tile t's rows see tiles j of keys with down[t] <= j < up[t] whole
     int all_up, all_down;  // and both of them these
 
-    __device__ __forceinline__ PromptWork() {}
-    __device__ __forceinline__ PromptWork(const PromptArgs& A, long long place) {
-        int sub = 0;
-        uint32_t at = uint32_t(place);
+    // The item's words as they lie in the plan (any place's: of one past the end, the last one's)
+    struct Words {
+        int4 x;
+        int m, h, sub;
+    };
+    __device__ __forceinline__ static Words words(const PromptArgs& A, long long place, long long total) {
+        Words r;
+        uint32_t at = uint32_t(min(place, total - 1));
+        r.sub = 0;
         if (MT == 1) {  // a wide head: which of the item's row tiles
-            sub = int(place & 1);
-            at = uint32_t(place >> 1);
+            r.sub = int(at & 1);
+            at >>= 1;
         }
         const uint32_t rank = at / uint32_t(A.Hkv);
-        h = int(at - rank * uint32_t(A.Hkv));
+        r.h = int(at - rank * uint32_t(A.Hkv));
         const int4* p = reinterpret_cast<const int4*>(A.plan + 4) + 2ll * rank;
-        const int4 x = __ldg(p);
-        m = __ldg(&p[1].x);
-        q0 = x.x + sub * A.tokens;
-        n = x.y - sub * A.tokens;
-        k0 = x.z;
-        last = x.w + sub * A.tokens;
+        r.x = __ldg(p);
+        r.m = __ldg(&p[1].x);
+        return r;
+    }
+    __device__ __forceinline__ PromptWork() {}
+    __device__ __forceinline__ PromptWork(const PromptArgs& A, const Words& r) {
+        h = r.h;
+        m = r.m;
+        q0 = r.x.x + r.sub * A.tokens;
+        n = r.x.y - r.sub * A.tokens;
+        k0 = r.x.z;
+        last = r.x.w + r.sub * A.tokens;
         j0 = all_up = 0x7fffffff;
         j1 = all_down = 0;
 #pragma unroll
@@ -235,8 +246,10 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         // ---- copies
         if (lane == 0) {
             uint32_t i = 0, uses[MT] = {};  // stages, and queries of a tile, so far
+            auto ahead = Work::words(A, place_of(0), total);
             for (int round = 0; place_of(round) < total && !*gone; ++round) {
-                const Work w(A, place_of(round));
+                const Work w(A, ahead);
+                ahead = Work::words(A, place_of(round + 1), total);
                 auto query = [&](int t) {
                     if (w.hi[t] <= w.lo[t]) return;
                     wait(&qe[t], uses[t] ^ 1u);
@@ -370,7 +383,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         };
         auto next_of = [&](Steps& x) {
             while (place_of(round) < total) {
-                const Work w(A, place_of(round++));
+                const Work w(A, Work::words(A, place_of(round++), total));
                 x = {uniform(w.j0), uniform(w.j1), uniform(t ? w.lo[MT - 1] : w.lo[0]), uniform(t ? w.hi[MT - 1] : w.hi[0]),
                      uniform(w.all_up), uniform(w.all_down), uniform(w.out_stages())};
                 if (x.j1 > x.j0) return true;
@@ -417,8 +430,10 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < C; ++c) vs.next();
         int gen = 0;
+        auto ahead = Work::words(A, place_of(0), total);
         for (int round = 0; place_of(round) < total; ++round) {
-            const Work w(A, place_of(round));
+            const Work w(A, ahead);
+            ahead = Work::words(A, place_of(round + 1), total);
             int slot = 0;
             if (w.j1 <= w.j0) continue;
             for (int j = w.j0; j < w.j1; ++j) {
@@ -507,17 +522,32 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         auto leave = [&]() {
             if (MT == 2) *mine_busy = 0;
         };
+        // The stage that the last rows of O were copied out of goes back to the ring behind the next
+        // item's first weights, when the copy has long read it.
+        RingAt<ST> lent;
+        bool owed = false;
+        auto release = [&]() {
+            if (!owed) return;  // (one thread of the row tile's owes)
+            owed = false;
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            RingAt<ST> at = lent;
+            for (int x = 0; x < C; ++x, at.next())
+                asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&empty[at.st])), "n"(MT) : "memory");
+        };
         RingAt<ST> os;  // the item's first stage
         uint32_t tiles = 0, outs = 0;  // tiles of weights, and finished rows, so far
         int gen = 1;
+        auto ahead = Work::words(A, place_of(0), total);
         for (int round = 0; place_of(round) < total; ++round) {
-            const Work w(A, place_of(round));
+            const Work w(A, ahead);
+            ahead = Work::words(A, place_of(round + 1), total);
             if (w.j1 > w.j0) gen ^= 1;
             const bool mine = tok < A.tokens && token < w.n;
             const int end = w.last + token, begin = A.window ? end - A.window + 1 : 0;  // keys it sees: [begin, end]
             const int ja = t ? w.lo[MT - 1] : w.lo[0], jb = t ? w.hi[MT - 1] : w.hi[0];
             const int up = t ? w.up[MT - 1] : w.up[0], down = t ? w.down[MT - 1] : w.down[0];
             float ref = -INFINITY, tot = 0.f;
+            if (jb <= ja) release();
             for (int j = ja; j < jb; ++j, ++tiles) {
                 const uint32_t buf = MT == 2 ? t : tiles & 1u;
                 const uint32_t sa = tbase + lanes + buf * 128;
@@ -564,50 +594,72 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     sum0 = sum1 = f2_pack(0.f, 0.f);
                 };
                 const bool masked = j >= up || j < down;
-                // (the pieces' largest while the next are on their way)
                 at_ld32(sa, x[0]);
                 at_ld32(sa + 32, x[1]);
                 at_ld_wait(x[0]);
                 at_ld_wait(x[1]);
                 at_ld32(sa + 64, x[2]);
                 at_ld32(sa + 96, x[3]);
-                if (__builtin_expect(masked, 0)) {
-                    if (partly(0)) hide(0);
-                    if (partly(1)) hide(1);
-                }
-                largest(0);
-                largest(1);
-                at_ld_wait(x[2]);
-                at_ld_wait(x[3]);
-                if (__builtin_expect(masked, 0)) {
-                    if (partly(2)) hide(2);
-                    if (partly(3)) hide(3);
-                }
-                largest(2);
-                largest(3);
-                const float top = fmaxf(m0, m1) * c;
-                const bool raise = top > ref + TilesRange<F16>::SLACK;
-                if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-                    const float to = raise ? top - TilesRange<F16>::TOP : ref;
-                    const float f = ref == to ? 1.f : ex2_approx(ref - to);
-                    ref = to;
-                    tot *= f;
-                    if (j > ja) {  // O holds sums by the old reference
-                        if (MT == 1) wait(&pv, tiles - 1);
-                        scale_rows<DP>(o, f);
+                // The first half's weights by the reference as it is, while the largest are sought; where
+                // some row's passes it by too much (seldom, but for an item's first tile) it is
+                // raised, and they are made again, from the scores in registers.
+                bool again = masked || j == ja;
+                if (!again) {
+                    begin_sums();
+                    weigh(0);
+                    largest(0);
+                    weigh(1);
+                    largest(1);
+                    at_ld_wait(x[2]);
+                    at_ld_wait(x[3]);
+                    largest(2);
+                    largest(3);
+                    again = __any_sync(0xffffffffu, fmaxf(m0, m1) * c > ref + TilesRange<F16>::SLACK);
+                } else {
+                    if (masked) {
+                        if (partly(0)) hide(0);
+                        if (partly(1)) hide(1);
                     }
+                    largest(0);
+                    largest(1);
+                    at_ld_wait(x[2]);
+                    at_ld_wait(x[3]);
+                    if (masked) {
+                        if (partly(2)) hide(2);
+                        if (partly(3)) hide(3);
+                    }
+                    largest(2);
+                    largest(3);
                 }
-                begin_sums();
+                if (__builtin_expect(again, 0)) {
+                    const float top = fmaxf(m0, m1) * c;
+                    const bool raise = top > ref + TilesRange<F16>::SLACK;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float to = raise ? top - TilesRange<F16>::TOP : ref;
+                        const float f = ref == to ? 1.f : ex2_approx(ref - to);
+                        ref = to;
+                        tot *= f;
+                        if (j > ja) {  // O holds sums by the old reference
+                            if (MT == 1) wait(&pv, tiles - 1);
+                            scale_rows<DP>(o, f);
+                        }
+                    }
+                    begin_sums();
+                    weigh(0);
+                    weigh(1);
+                }
                 // the products with the first half of the keys begin while the second is weighed
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    weigh(2 * half);
-                    weigh(2 * half + 1);
+                auto give = [&](int half) {
                     at_st_wait();
                     at_before();
                     __syncwarp();
                     if (lane == 0) at_arrive(&pf[buf][half]);
-                }
+                };
+                give(0);
+                weigh(2);
+                weigh(3);
+                give(1);
+                release();
                 leave();
                 f2_unpack(f2_add(sum0, sum1), s0, s1);
                 tot += s0 + s1;
@@ -625,12 +677,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 wait(&of[t], outs++);
                 at_after();
                 const bool odd = *static_cast<volatile int*>(&bad_item[gen]) == round;
-                for (int x = 0; x < C; ++x, os.next()) wait(&full[os.st], os.phase);
-#pragma unroll 1
-                for (int d = 0; d < DP; d += 32) {
-                    uint32_t u[32];
-                    at_ld32(o + d, u);
-                    at_ld_wait(u);
+                auto put = [&](const uint32_t (&u)[32], int d) {
                     float f[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(u[e]);
@@ -663,6 +710,18 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                             v[e] = none ? 0u : pack16<F16>(f[8 * y + 2 * e] * inv, f[8 * y + 2 * e + 1] * inv);
                         *reinterpret_cast<uint4*>(row + (((d % 64 / 8 + y) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
+                };
+                uint32_t u0[32], u1[32];
+                at_ld32(o, u0);
+                for (int x = 0; x < C; ++x, os.next()) wait(&full[os.st], os.phase);
+#pragma unroll 1
+                for (int d = 0; d < DP; d += 64) {
+                    at_ld_wait(u0);
+                    at_ld32(o + d + 32, u1);
+                    put(u0, d);
+                    at_ld_wait(u1);
+                    if (d + 64 < DP) at_ld32(o + d + 64, u0);
+                    put(u1, d + 32);
                 }
                 at_before();
                 __syncwarp();
@@ -692,11 +751,10 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                             tma_store_4d(&mo, ring + st * S::STAGE + (x * 64 % S::CH) / 64 * 16384, x * 64, 0, w.h, w.q0 + t * A.tokens);
                         }
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
-                    RingAt<ST> at = o0;
-                    for (int x = 0; x < C; ++x, at.next())
-                        asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&empty[at.st])), "n"(MT) : "memory");
+                    lent = o0;
+                    owed = true;
+                    if (!whole) release();
                 }
             } else if (mine) {  // rows that see nothing
                 for (int d = 0; d < A.D; d += 8)
@@ -708,6 +766,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 A.lse[(long long)(w.q0 + token) * A.Hq + w.h * A.G + g] =
                     none ? -INFINITY : (ref + log2f(tot)) * 0.6931471805599453f;
         }
+        release();
         if ((threadIdx.x & 127) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 

@@ -118,6 +118,25 @@ def test_windows(window, Hq, D):
     check(*case([50, 300], Hq, 1, D, HF, window % 89, ahead=[900, 77]), window=window)
 
 
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("D,Hq,Hkv,window", [(64, 4, 2, 0), (128, 4, 2, 0), (128, 3, 3, 100), (256, 2, 1, 0), (128, 128, 1, 0)])
+def test_many_items_a_cta(D, Hq, Hkv, window, dt):
+    """Items of one step to many behind one another, row tiles without tokens or keys among them."""
+    rng = np.random.default_rng(D + Hq)
+    lens = rng.choice([0, 1, 2, 30, 64, 65, 127, 128, 129, 200, 300, 513], 300 if Hq < 100 else 24).tolist()
+    ahead = rng.choice([0, 0, 0, 5, 128, -1, -64, -130, 400], len(lens)).tolist()
+    check(*case(lens, Hq, Hkv, D, dt, 21, ahead=ahead), window=window)
+
+
+def test_marks_belong_to_their_item():
+    """Values that are not finite in some items of a CTA's and not in others."""
+    lens = [200] * 250
+    q, k, v, off, koff = case(lens, 4, 2, 64, BF, 13)
+    for b in range(0, 250, 7):
+        v[off[b] + 30 * (b % 6), b % 2, b % 64] = (math.nan, math.inf, -math.inf)[b % 3]
+    check(q, k, v, off, koff)
+
+
 def test_front_rows_and_rows_behind():
     check(*case([100, 50], 4, 2, 64, BF, 1, front=13, pad=29))
 
