@@ -7,15 +7,18 @@
 // (Z, A) into f Z, f (A + d Z), f = 2^d, d the difference, and so do the joins of lanes,
 // warps and CTAs.
 //
-// Alternatives.  A row is cut into groups of 512 neighbours (256 of f32; of long rows several of
-// those), and the pass leaves each group's largest logit behind.  The k best tokens lie
-// in the k groups whose largest are best (by value, then by place: each of those k is itself a
-// token, and no other group's is as good), so that the k groups alone are read a second
-// time, out of L2, for tokens as good as the k-th group's largest.
+// Alternatives.  A row is cut into groups of 512 neighbours (256 of f32), and the pass
+// leaves each group's largest logit behind.  The k best tokens lie in the k groups whose largest are
+// best (by value, then by place: each of those k is itself a token, and no other group's is
+// as good), so that the k groups alone are read a second time for tokens as good as the k-th
+// group's largest.
 //
-// k_logprob takes a row with one CTA where there are two rows an SM and more, else
-// several share a row, and k_logprob_join, launched behind it, joins their sums.
-// Bound by HBM for many rows; by latency for few.
+// k_logprob streams tiles of 4 KB: all tiles of all rows that are read, in order, are cut into as
+// many equal shares as there are warps, so that a single row goes to many SMs and ragged ones
+// load every SM alike.  A warp has two tiles on their way into shared memory (192 KB an SM; with 32 KB
+// in registers, HBM ran at half its rate: 1024 rows of 151936 logits, 640 of them read, took 83 us).
+// It leaves a tile's (M, Z, A) and its four groups' largest in the workspace; k_logprob_join, behind
+// it, joins a row's and finds its best.  Bound by HBM for many rows; by latency for few.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -26,8 +29,12 @@
 namespace sv {
 namespace {
 
-constexpr int LP_THREADS = 512, LP_WARPS = LP_THREADS / 32;
-constexpr int LP_GROUPS = 1024;  // groups of a row between its ends, at most
+constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32;
+constexpr int LP_CTAS = 3;  // an SM
+constexpr int LP_JOIN = 128, LP_JOIN_WARPS = LP_JOIN / 32;  // threads that join a row (twelve such CTAs an SM: one round for most calls)
+constexpr int LP_VECS = 256, LP_STAGES = 2;  // of a tile; of a warp's ring
+constexpr int LP_BYTES = LP_VECS * 16;
+constexpr size_t LP_SMEM = size_t(LP_WARPS) * LP_STAGES * LP_BYTES;
 constexpr int LP_CANDIDATES = 1024;
 constexpr float LP_LOWEST = -3.4028234663852886e38f, LP_FAR = -200.f;  // 2^LP_FAR is 0 in float32
 
@@ -41,11 +48,12 @@ struct LogprobArgs {
     float* entropy;
     int32_t* ids;
     float* top_lp;
-    float4* part;  // [E][splits] {M, Z, A}
-    float* most;   // [E][groups + 2] largest logits, where several CTAs share a row
+    int32_t* list;  // entries whose rows are read, in order
+    float4* part;   // [E][tiles + 1] {M, Z, A} of the tiles and, last, of the row's ends
+    float4* most;   // [E][tiles + 1] largest logits of a tile's four groups; {head, tail} of the ends
     int32_t* status;
-    int V, top, splits, span;  // span: units of a group
-    int groups;                // of a row between its ends, at most
+    int V, top, tiles;  // tiles of a row, at most
+    long long E;
 };
 
 template <int DT>
@@ -101,14 +109,13 @@ template <int DT>
 struct Row {
     using T = typename Elem<DT>::T;
     const T* p;
-    int head, vecs, units, groups, tail;
+    int head, vecs, tiles, tail;
     __device__ __forceinline__ Row(const LogprobArgs& A, long long row) {
         p = static_cast<const T*>(A.logits) + row * A.stride;
         head = min(A.V, int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / Elem<DT>::SIZE);
         vecs = (A.V - head) / Elem<DT>::EPV;
         tail = A.V - head - vecs * Elem<DT>::EPV;
-        units = (vecs + 63) / 64;
-        groups = (units + A.span - 1) / A.span;
+        tiles = (vecs + LP_VECS - 1) / LP_VECS;
     }
     __device__ __forceinline__ uint4 vec(int i) const {
         return i < vecs ? __ldg(reinterpret_cast<const uint4*>(p + head) + i)
@@ -134,8 +141,8 @@ struct Sums {
 template <int DT, bool ENT>
 struct Lane {
     Sums s{LP_LOWEST, 0.f, 0.f};
-    __device__ __forceinline__ void take(const uint4& u, const uint4& v, float mx, float kappa) {
-        s.to(fmaxf(s.m, mx), kappa);
+    // two vectors, whose largest the reference is not below
+    __device__ __forceinline__ void take(const uint4& u, const uint4& v, float kappa) {
         float f[2 * Elem<DT>::EPV];
         unpack<DT>(u, f);
         unpack<DT>(v, f + Elem<DT>::EPV);
@@ -166,10 +173,11 @@ struct Lane {
 };
 
 // The sums of a warp's lanes, in every lane.
+template <bool ENT>
 __device__ __forceinline__ Sums warp_join(Sums s, float kappa) {
     s.to(redux_max_f32(s.m), kappa);
     s.z = warp_sum_f(s.z);
-    s.a = warp_sum_f(s.a);
+    if (ENT) s.a = warp_sum_f(s.a);
     return s;
 }
 
@@ -180,14 +188,15 @@ __device__ __forceinline__ float log_p(float l, const Sums& s, float log_z, floa
 }
 
 struct Best {  // what a CTA needs for the alternatives
-    float most[LP_GROUPS + 2];
     float value[LP_CANDIDATES];
     int id[LP_CANDIDATES];
     int group[SPEC_MAX_TOP];
     float at_least;
     int chosen, found;
-    float round_value[LP_WARPS];
-    int round_id[LP_WARPS];
+    int digits[256], digit, left;
+    bool exact;
+    float round_value[LP_JOIN_WARPS];
+    int round_id[LP_JOIN_WARPS];
 };
 
 // largest first, of equal ones the lowest index
@@ -197,95 +206,155 @@ __device__ __forceinline__ uint32_t ordered(float f) {  // (0 and -0 alike)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// f(value, index) for every element of a chosen group, by the warps of the CTA in turn
+// f(value, index) for the elements of chosen groups that are at least `least`, by the warps of the
+// CTA in turn.  Group 0 is the row's head, the last its tail.
 template <int DT, class F>
-__device__ __forceinline__ void of_groups(const LogprobArgs& A, const Row<DT>& row, const Best& B, F&& f) {
+__device__ __forceinline__ void of_groups(const LogprobArgs& A, const Row<DT>& row, const Best& B, float least, F&& f) {
     constexpr int EPV = Elem<DT>::EPV;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int c = warp; c < B.chosen; c += LP_WARPS) {
-        const int g = B.group[c] - 1;
-        if (g < 0 || g >= row.groups) {
-            const int e = row.end_of(lane);
-            if (e >= 0 && (lane < 16) == (g < 0)) f(to_f32(row.p[e]), e);
-            continue;
+    constexpr int U = 4;  // groups of a warp that are on their way at once
+    uint4 v[U][2];
+    for (int c0 = warp; c0 < B.chosen; c0 += U * LP_JOIN_WARPS) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * LP_JOIN_WARPS, g = c < B.chosen ? B.group[c] - 1 : -1;
+            const bool body = g >= 0 && g < row.tiles * 4;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) v[u][y] = row.vec(body ? g * 64 + y * 32 + lane : row.vecs);
         }
-        for (int u = g * A.span; u < min(row.units, (g + 1) * A.span); ++u)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * LP_JOIN_WARPS;
+            if (c >= B.chosen) break;
+            const int g = B.group[c] - 1;
+            if (g < 0 || g >= row.tiles * 4) {
+                const int e = row.end_of(lane);
+                if (e >= 0 && (lane < 16) == (g < 0) && to_f32(row.p[e]) >= least) f(to_f32(row.p[e]), e);
+                continue;
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const int i = u * 64 + y * 32 + lane;
+                const int i = g * 64 + y * 32 + lane;
+                if (i >= row.vecs || !(largest<DT>(v[u][y], v[u][y]) >= least)) continue;
                 float x[EPV];
-                unpack<DT>(row.vec(i), x);
-                if (i < row.vecs)
+                unpack<DT>(v[u][y], x);
 #pragma unroll
-                    for (int e = 0; e < EPV; ++e) f(x[e], row.head + i * EPV + e);
+                for (int e = 0; e < EPV; ++e)
+                    if (x[e] >= least) f(x[e], row.head + i * EPV + e);
             }
+        }
     }
 }
 
-// The alternatives of a row whose groups' largest logits lie in B.most (all of the CTA).
-template <int DT>
-__device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>& row, Best& B, const Sums& s, float T,
+// The alternatives of a row (all of the CTA); most(g): the largest logit of its group g.
+template <int DT, class F>
+__device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>& row, Best& B, F&& most, const Sums& s, float T,
                                             long long e) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = row.groups + 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = row.tiles * 4 + 2;
     const float log_z = log2f(s.z);
-    if (warp == 0) {
-        // the largest bound that `top` groups reach, bit by bit; those above it, and of
-        // those at it the first
-        auto reach = [&](uint32_t bound) {
-            int n = 0;
-            for (int i = lane; i < G; i += 32) n += ordered(B.most[i]) >= bound;
-            return int(__reduce_add_sync(0xffffffffu, unsigned(n)));
-        };
-        const uint32_t none = ordered(-INFINITY);
-        uint32_t bound = none + 1;
-        if (reach(bound) > A.top) {
-            uint32_t at = 0;
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t t = at | 1u << bit;
-                const int n = t > none ? reach(t) : A.top;
-                if (n >= A.top) at = t;
-                if (n == A.top && t > none) break;
+    // The largest bound that `top` groups reach, eight bits after eight, until as many as wanted
+    // reach it; those above it, and of those at it the first.
+    // (bf16 has no more bits than two digits hold, f16 as float no more than three)
+    constexpr int LAST = DT == SPEC_BF16 ? 16 : DT == SPEC_F16 ? 8 : 0;
+    const uint32_t none = ordered(-INFINITY) >> LAST << LAST;
+    uint32_t bound = 0;   // the digits so far
+    int want = A.top;     // groups to be taken with these digits
+    bool exact = false;   // as many have them
+    auto key = [&](int g) { return ordered(most(g)) >> LAST << LAST; };
+    for (int shift = 24; shift >= LAST && !exact; shift -= 8) {
+        for (int i = threadIdx.x; i < 256; i += LP_JOIN) B.digits[i] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < G; i += LP_JOIN) {
+            const uint32_t k = key(i);
+            if (k > none && (shift == 24 || (k ^ bound) >> (shift + 8) == 0)) atomicAdd(&B.digits[k >> shift & 255u], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {  // from the largest digit down, eight a lane
+            int n[8], all = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                n[i] = B.digits[255 - lane * 8 - i];
+                all += n[i];
             }
-            bound = max(at, none + 1);
+            int sum = all;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const unsigned reach = __ballot_sync(0xffffffffu, sum >= want);
+            if (reach == 0) {  // fewer than wanted: all of them
+                if (lane == 0) B.digit = -1;
+            } else if (lane == __ffs(reach) - 1) {
+                int before = sum - all, d = 255 - lane * 8, i = 0;
+                while (before + n[0] < want && i < 7) {
+                    before += n[0];
+#pragma unroll
+                    for (int x = 0; x < 7; ++x) n[x] = n[x + 1];
+                    --d;
+                    ++i;
+                }
+                B.digit = d;
+                B.left = want - before;
+                B.exact = before + n[0] == want;
+            }
         }
-        int chosen = 0, left = A.top - reach(bound + 1);
-        for (int i0 = 0; i0 < G; i0 += 32) {
-            const uint32_t k = i0 + lane < G ? ordered(B.most[i0 + lane]) : 0u;
-            const unsigned at = __ballot_sync(0xffffffffu, k == bound), below = (1u << lane) - 1u;
-            const bool take = k > bound || (k == bound && __popc(at & below) < left);
-            left -= min(left, __popc(at));
-            const unsigned all = __ballot_sync(0xffffffffu, take);
-            if (take) B.group[chosen + __popc(all & below)] = i0 + lane;
-            chosen += __popc(all);
+        __syncthreads();
+        if (B.digit < 0) {
+            bound = none + 1;
+            want = G;
+            break;
         }
-        if (lane == 0) {
-            B.chosen = chosen;
-            B.found = 0;
-            const uint32_t u = bound;
-            B.at_least = __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-        }
+        bound |= uint32_t(B.digit) << shift;
+        want = B.left;
+        exact = B.exact;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        B.chosen = B.found = 0;
+        const uint32_t u = max(bound, ordered(LP_LOWEST));
+        B.at_least = __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
     }
     __syncthreads();
-    const float bound = B.at_least;
-    of_groups<DT>(A, row, B, [&](float v, int i) {
-        if (v >= bound) {
-            const int n = atomicAdd(&B.found, 1);
-            if (n < LP_CANDIDATES) {
-                B.value[n] = v;
-                B.id[n] = i;
-            }
+    // (in any order: they are only looked through)
+    const bool all_at = exact || want == G;
+    for (int i = threadIdx.x; i < G; i += LP_JOIN) {
+        const uint32_t k = key(i);
+        if (k > none && (k > bound || (all_at && k == bound) || (exact && k >= bound))) B.group[atomicAdd(&B.chosen, 1)] = i;
+    }
+    __syncthreads();
+    if (!all_at && warp == 0) {  // equal ones: the first
+        int chosen = B.chosen, left = want;
+        for (int i0 = 0; i0 < G && left > 0; i0 += 32) {
+            const bool is = i0 + lane < G && key(i0 + lane) == bound;
+            const unsigned at = __ballot_sync(0xffffffffu, is), below = (1u << lane) - 1u;
+            const int r = __popc(at & below);
+            if (is && r < left) B.group[chosen + r] = i0 + lane;
+            const int n = min(left, __popc(at));
+            chosen += n;
+            left -= n;
+        }
+        if (lane == 0) B.chosen = chosen;
+    }
+    __syncthreads();
+    const float least = B.at_least;
+    of_groups<DT>(A, row, B, least, [&](float v, int i) {
+        const int n = atomicAdd(&B.found, 1);
+        if (n < LP_CANDIDATES) {
+            B.value[n] = v;
+            B.id[n] = i;
         }
     });
     __syncthreads();
     const int found = B.found;
     int32_t* ids = A.ids + e * A.top;
     float* lps = A.top_lp + e * A.top;
-    for (int i = min(found, A.top) + threadIdx.x; i < A.top; i += LP_THREADS) {
+    for (int i = min(found, A.top) + threadIdx.x; i < A.top; i += LP_JOIN) {
         ids[i] = -1;
         lps[i] = -INFINITY;
     }
     if (found <= LP_CANDIDATES) {
-        for (int i = threadIdx.x; i < found; i += LP_THREADS) {
+        for (int i = threadIdx.x; i < found; i += LP_JOIN) {
             const float v = B.value[i];
             const int id = B.id[i];
             int r = 0;
@@ -304,7 +373,7 @@ __device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>&
     for (int r = 0; r < A.top; ++r) {
         float v = -INFINITY;
         int id = 0x7fffffff;
-        of_groups<DT>(A, row, B, [&](float w, int j) {
+        of_groups<DT>(A, row, B, least, [&](float w, int j) {
             if (before(last_v, last_i, w, j) && before(w, j, v, id)) {
                 v = w;
                 id = j;
@@ -324,7 +393,7 @@ __device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>&
             B.round_id[warp] = id;
         }
         __syncthreads();
-        for (int w = 0; w < LP_WARPS; ++w)
+        for (int w = 0; w < LP_JOIN_WARPS; ++w)
             if (before(B.round_value[w], B.round_id[w], v, id)) {
                 v = B.round_value[w];
                 id = B.round_id[w];
@@ -367,115 +436,201 @@ __device__ __forceinline__ void left_out(const LogprobArgs& A, long long e, int 
         if (A.entropy) A.entropy[e] = 0.f;
         if (bits && A.status) atomicOr(A.status, bits);
     }
-    for (int i = threadIdx.x; i < A.top; i += LP_THREADS) {
+    for (int i = threadIdx.x; i < A.top; i += LP_JOIN) {
         A.ids[e * A.top + i] = -1;
         A.top_lp[e * A.top + i] = 0.f;
     }
 }
 // (one thread)
-template <int DT>
-__device__ __forceinline__ void put_entry(const LogprobArgs& A, const Row<DT>& row, const Entry& x, const Sums& s, long long e) {
+__device__ __forceinline__ void put_entry(const LogprobArgs& A, float given, const Entry& x, const Sums& s, long long e) {
     const float log_z = log2f(s.z);
     const bool empty = s.z == 0.f;
-    A.lp[e] = empty ? -INFINITY : log_p(to_f32(row.p[x.token]), s, log_z, x.T);
+    A.lp[e] = empty ? -INFINITY : log_p(given, s, log_z, x.T);
     if (A.entropy) A.entropy[e] = empty ? 0.f : 0.6931471805599453f * (log_z - s.a / s.z);
     if (empty && A.status) atomicOr(A.status, int(SPEC_BADBIT_EMPTY_ROW));
 }
 
 template <int DT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS, 2) k_logprob(const __grid_constant__ LogprobArgs A) {
-    begin_after_previous();
-    __shared__ Best B;
-    __shared__ float3 parts[LP_WARPS];
-    const long long e = blockIdx.x / unsigned(A.splits);
-    const int split = int(blockIdx.x - unsigned(e) * unsigned(A.splits));
-    const Entry x = entry_of(A, e);
-    const bool alone = A.splits == 1;
-    if (x.row < 0) {
-        if (alone) left_out(A, e, x.bits);
-        return;
-    }
-    const Row<DT> row(A, x.row);
+__global__ void __launch_bounds__(LP_THREADS, LP_CTAS) k_logprob(const __grid_constant__ LogprobArgs A) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[LP_WARPS][LP_STAGES];
+    __shared__ int counts[LP_WARPS];
+    __shared__ int32_t near_list[LP_THREADS];  // of few entries
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* most = alone ? B.most : A.most + e * (A.groups + 2);
-    const int g0 = int((long long)row.groups * split / A.splits), g1 = int((long long)row.groups * (split + 1) / A.splits);
-    Lane<DT, ENT> L;
-    // a group's units, the next one's loads under way while one is worked on
-    int g = g0 + warp, u = g * A.span;
-    uint4 a, b;
-    auto load = [&](int u) {
-        a = row.vec(u * 64 + lane);
-        b = row.vec(u * 64 + 32 + lane);
-    };
-    if (g < g1) load(u);
-    float in_group = -INFINITY;
-    while (g < g1) {
-        const uint4 va = a, vb = b;
-        const int of = g;
-        bool done = false;
-        if (++u == (g + 1) * A.span || u >= row.units) {
-            g += LP_WARPS;
-            u = g * A.span;
-            done = true;
-        }
-        if (g < g1) load(u);
-        const float mx = largest<DT>(va, vb);
-        in_group = fmaxf(in_group, mx);
-        L.take(va, vb, mx, x.kappa);
-        if (TOP && done) {
-            const float all = redux_max_f32(in_group);
-            if (lane == 0) most[of + 1] = all;
-            in_group = -INFINITY;
-        }
+    if (lane == 0) {
+        for (int i = 0; i < LP_STAGES; ++i) mbar_init(&bars[warp][i], 1);
+        fence_mbarrier_init();
     }
-    if (split == 0 && warp == LP_WARPS - 1) {  // the ends
-        const int end = row.end_of(lane);
-        const float l = end >= 0 ? to_f32(row.p[end]) : -INFINITY;
-        L.one(l, x.kappa);
+    begin_after_previous();
+
+    // The entries that are read: how many, and the list of this CTA's (which it writes for itself).
+    auto live = [&](long long e) { return e < A.E && entry_of(A, e).row >= 0; };
+    long long total = 0;
+    const bool first = live(threadIdx.x);
+    int32_t* list = A.E <= LP_THREADS ? near_list : A.list;
+    for (long long e0 = 0; e0 < A.E; e0 += LP_THREADS) total += __syncthreads_count(e0 ? live(e0 + threadIdx.x) : first);
+    const long long tiles = total * A.tiles, W = (long long)gridDim.x * LP_WARPS;
+    // shares of at least one tile: the first CTAs have the work where there is little, a warp each
+    const long long w = (long long)warp * gridDim.x + blockIdx.x;
+    const bool few = tiles <= W;
+    const long long mine = few ? w : (long long)blockIdx.x * LP_WARPS + warp;
+    const long long t0 = few ? min(w, tiles) : tiles * mine / W, t1 = few ? min(w + 1, tiles) : tiles * (mine + 1) / W;
+    const long long c0 = few ? 0 : tiles * (blockIdx.x * (long long)LP_WARPS) / W, c1 = few ? tiles : tiles * ((blockIdx.x + 1ll) * LP_WARPS) / W;
+    const long long a0 = c0 / A.tiles, a1 = (c1 + A.tiles - 1) / A.tiles;  // live entries of the CTA's
+    long long before = 0;
+    for (long long e0 = 0; e0 < A.E && before < a1; e0 += LP_THREADS) {
+        const bool on = e0 ? live(e0 + threadIdx.x) : first;
+        const unsigned b = __ballot_sync(0xffffffffu, on);
+        if (lane == 0) counts[warp] = __popc(b);
+        __syncthreads();
+        long long at = before + __popc(b & ((1u << lane) - 1u));
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i < LP_WARPS; ++i) {
+            if (i < warp) at += counts[i];
+            all += counts[i];
+        }
+        if (on && at >= a0 && at < a1) list[at] = int32_t(e0 + threadIdx.x);  // (the same by every CTA that writes it)
+        before += all;
+        __syncthreads();
+    }
+    if (t0 >= t1) return;
+
+    uint8_t* buf = smem + size_t(warp) * LP_STAGES * LP_BYTES;
+    uint64_t* bar = bars[warp];
+    // lane 0: the copies
+    long long pa = t0 / A.tiles;
+    int pc = int(t0 - pa * A.tiles);
+    auto bytes_of = [&](const Row<DT>& r, int c) { return uint32_t(max(0, min(LP_VECS, r.vecs - c * LP_VECS))) * 16u; };
+    Row<DT> prow(A, entry_of(A, list[pa]).row);
+    uint32_t begun = 0;
+    long long left = t1 - t0;
+    auto issue = [&]() {
+        if (left == 0) return;
+        const uint32_t st = begun % LP_STAGES, n = bytes_of(prow, pc);
+        mbar_arrive_expect_tx(&bar[st], n);
+        if (n) bulk_g2s(buf + st * LP_BYTES, reinterpret_cast<const char*>(prow.p + prow.head) + size_t(pc) * LP_BYTES, n, &bar[st]);
+        ++begun;
+        if (--left && ++pc == A.tiles) {
+            pc = 0;
+            prow = Row<DT>(A, entry_of(A, list[++pa]).row);
+        }
+    };
+    if (lane == 0)
+        for (int i = 0; i < LP_STAGES; ++i) issue();
+    long long a = t0 / A.tiles;
+    int c = int(t0 - a * A.tiles);
+    long long e = list[a];
+    Entry x = entry_of(A, e);
+    Row<DT> row(A, x.row);
+    uint32_t used = 0;
+    bool lost = false;
+    for (long long t = t0; t < t1; ++t, ++used) {
+        const uint32_t st = used % LP_STAGES;
+        lost = !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], (used / LP_STAGES) & 1u));
+        if (lost) break;
+        const int vecs = min(LP_VECS, row.vecs - c * LP_VECS);
+        const uint4* v = reinterpret_cast<const uint4*>(buf + st * LP_BYTES);
+        const uint4 none = make_uint4(Elem<DT>::NONE, Elem<DT>::NONE, Elem<DT>::NONE, Elem<DT>::NONE);
+        uint4 d[8];
+        if (vecs == LP_VECS) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = v[k * 32 + lane];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = k * 32 + lane < vecs ? v[k * 32 + lane] : none;
+        }
+        __syncwarp();  // every lane holds its share: the stage can be filled again
+        if (lane == 0) {
+            fence_proxy_async_smem();
+            issue();
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = largest<DT>(d[2 * k], d[2 * k + 1]);
+        Lane<DT, ENT> L;
+        L.s.m = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), LP_LOWEST);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) L.take(d[2 * k], d[2 * k + 1], x.kappa);
         if (TOP) {
-            const float h = redux_max_f32(lane < 16 ? l : -INFINITY), t = redux_max_f32(lane < 16 ? -INFINITY : l);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = redux_max_f32(mx[k]);
+        }
+        const Sums s = warp_join<ENT>(L.s, x.kappa);
+        if (lane == 0 && vecs > 0) {
+            A.part[e * (A.tiles + 1) + c] = make_float4(s.m, s.z, s.a, 0.f);
+            if (TOP) A.most[e * (A.tiles + 1) + c] = make_float4(mx[0], mx[1], mx[2], mx[3]);
+        }
+        if (c == 0) {  // the ends
+            const int end = row.end_of(lane);
+            const float l = end >= 0 ? to_f32(row.p[end]) : -INFINITY;
+            Lane<DT, ENT> K;
+            K.one(l, x.kappa);
+            const float h = redux_max_f32(lane < 16 ? l : -INFINITY), g = redux_max_f32(lane < 16 ? -INFINITY : l);
+            const Sums y = warp_join<ENT>(K.s, x.kappa);
             if (lane == 0) {
-                most[0] = h;
-                most[row.groups + 1] = t;
+                A.part[e * (A.tiles + 1) + A.tiles] = make_float4(y.m, y.z, y.a, 0.f);
+                if (TOP) A.most[e * (A.tiles + 1) + A.tiles] = make_float4(h, g, 0.f, 0.f);
             }
         }
+        if (++c == A.tiles && t + 1 < t1) {
+            c = 0;
+            e = list[++a];
+            x = entry_of(A, e);
+            row = Row<DT>(A, x.row);
+        }
     }
-    Sums s = warp_join(L.s, x.kappa);
-    if (lane == 0) parts[warp] = make_float3(s.m, s.z, s.a);
-    __syncthreads();
-    if (alone && TOP) {  // every warp needs the sums
-        const float3 p = lane < LP_WARPS ? parts[lane] : make_float3(LP_LOWEST, 0.f, 0.f);
-        s = warp_join(Sums{p.x, p.y, p.z}, x.kappa);
-        if (threadIdx.x == 0) put_entry<DT>(A, row, x, s, e);
-        best_tokens<DT>(A, row, B, s, x.T, e);
-    } else if (warp == 0) {
-        const float3 p = lane < LP_WARPS ? parts[lane] : make_float3(LP_LOWEST, 0.f, 0.f);
-        s = warp_join(Sums{p.x, p.y, p.z}, x.kappa);
+    if (lost) {
         if (lane == 0) {
-            if (alone) put_entry<DT>(A, row, x, s, e);
-            else A.part[e * A.splits + split] = make_float4(s.m, s.z, s.a, 0.f);
+            if (A.status) atomicOr(A.status, int(SPEC_BADBIT_TIMEOUT));
+            // copies in flight land before the shared memory is another's
+            for (uint32_t i = used; i != begun; ++i) mbar_wait_bounded(&bar[i % LP_STAGES], (i / LP_STAGES) & 1u, 100000000ull);
         }
     }
 }
 
-// One CTA an entry: the sums of its row's CTAs, and the alternatives.
+// One CTA an entry: the sums of its row's tiles, and the alternatives.
 template <int DT>
-__global__ void __launch_bounds__(LP_THREADS) k_logprob_join(const __grid_constant__ LogprobArgs A) {
+__global__ void __launch_bounds__(LP_JOIN) k_logprob_join(const __grid_constant__ LogprobArgs A) {
     begin_after_previous();
     __shared__ Best B;
+    constexpr int ROOM = 1280;  // (longer rows' groups are read where they lie)
+    __shared__ float kept[ROOM];
+    __shared__ float3 parts[LP_JOIN_WARPS];
     const long long e = blockIdx.x;
+    const float4* part = A.part + e * (A.tiles + 1);
+    const float4* most4 = A.most + e * (A.tiles + 1);
+    // (on their way before it is known whether they are used)
+    const int early = min(int(threadIdx.x), A.tiles);
+    const float4 part0 = __ldcg(part + early), most0 = A.top ? __ldcg(most4 + early) : part0;
+    const float4 part_end = __ldcg(part + A.tiles), most_end = A.top ? __ldcg(most4 + A.tiles) : part0;
     const Entry x = entry_of(A, e);
     if (x.row < 0) {
         left_out(A, e, x.bits);
         return;
     }
     const Row<DT> row(A, x.row);
-    const int lane = threadIdx.x & 31;
-    if (A.top)
-        for (int i = threadIdx.x; i < row.groups + 2; i += LP_THREADS) B.most[i] = __ldcg(A.most + e * (A.groups + 2) + i);
+    const float given = to_f32(row.p[x.token]);  // (on its way with the rest)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // groups in the order of their tokens: head, the tiles', tail
+    const int G = row.tiles * 4 + 2;
+    const bool fits = A.top && G <= ROOM;
     Sums s = {LP_LOWEST, 0.f, 0.f};
-    for (int i = lane; i < A.splits; i += 32) {
-        const float4 p = __ldcg(A.part + e * A.splits + i);
+    for (int i = threadIdx.x; i <= row.tiles; i += LP_JOIN) {
+        const bool end = i == row.tiles, mine = i == int(threadIdx.x);
+        const float4 p = end ? part_end : mine ? part0 : __ldcg(part + i);
+        if (fits) {
+            const float4 m = end ? most_end : mine ? most0 : __ldcg(most4 + i);
+            if (i < row.tiles) {
+                kept[1 + 4 * i] = m.x;
+                kept[2 + 4 * i] = m.y;
+                kept[3 + 4 * i] = m.z;
+                kept[4 + 4 * i] = m.w;
+            } else {
+                kept[0] = m.x;
+                kept[G - 1] = m.y;
+            }
+        }
         Sums y = {p.x, p.y, p.z};
         const float m = fmaxf(s.m, y.m);
         s.to(m, x.kappa);
@@ -483,41 +638,45 @@ __global__ void __launch_bounds__(LP_THREADS) k_logprob_join(const __grid_consta
         s.z += y.z;
         s.a += y.a;
     }
-    s = warp_join(s, x.kappa);
-    if (threadIdx.x == 0) put_entry<DT>(A, row, x, s, e);
-    if (!A.top) return;
+    s = warp_join<true>(s, x.kappa);
+    if (lane == 0) parts[warp] = make_float3(s.m, s.z, s.a);
     __syncthreads();
-    best_tokens<DT>(A, row, B, s, x.T, e);
+    const float3 p = lane < LP_JOIN_WARPS ? parts[lane] : make_float3(LP_LOWEST, 0.f, 0.f);
+    s = warp_join<true>(Sums{p.x, p.y, p.z}, x.kappa);
+    if (threadIdx.x == 0) put_entry(A, given, x, s, e);
+    if (!A.top) return;
+    auto most = [&](int g) {
+        if (fits) return kept[g];
+        const float* m = reinterpret_cast<const float*>(most4);
+        return __ldcg(g == 0 ? m + 4 * A.tiles : g == G - 1 ? m + 4 * A.tiles + 1 : m + g - 1);
+    };
+    best_tokens<DT>(A, row, B, most, s, x.T, e);
 }
 
 template <int DT>
-cudaError_t launch_logprob(const LogprobArgs& A, long long E, cudaStream_t st) {
+cudaError_t launch_logprob(const LogprobArgs& A, int sms, cudaStream_t st) {
     auto* kernel = A.entropy ? (A.top ? k_logprob<DT, true, true> : k_logprob<DT, true, false>)
                              : (A.top ? k_logprob<DT, false, true> : k_logprob<DT, false, false>);
-    const cudaError_t e = launch_behind(kernel, dim3(unsigned(E * A.splits)), LP_THREADS, 0, st, A);
-    if (e != cudaSuccess || A.splits == 1) return e;
-    return launch_behind(k_logprob_join<DT>, dim3(unsigned(E)), LP_THREADS, 0, st, A);
+    static bool ready[64][4] = {};  // per device; setting it twice does no harm
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    bool& set = ready[dev][(A.entropy ? 2 : 0) + (A.top ? 1 : 0)];
+    if (!set) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(LP_SMEM));
+        if (e != cudaSuccess) return e;
+        set = true;
+    }
+    e = launch_behind(kernel, dim3(unsigned(std::min<long long>((long long)LP_CTAS * sms, A.E * A.tiles))), LP_THREADS, LP_SMEM, st, A);
+    if (e != cudaSuccess) return e;
+    return launch_behind(k_logprob_join<DT>, dim3(unsigned(A.E)), LP_JOIN, 0, st, A);
 }
 
-// elements that a warp takes at once: two vectors a lane
-constexpr int unit_of(int bytes) { return 64 * 16 / bytes; }
-// How a call of E entries and V tokens is cut.
-// A row takes one CTA from two rows an SM on (an SM holds two CTAs), else as many as fill the
-// GPU twice, with a group a warp at least.
-struct Cut {
-    int span, groups, splits;
-};
-Cut cut_of(long long E, int V, int unit, int sms) {
-    Cut c;
-    const int units = (V + unit - 1) / unit;
-    c.span = (units + LP_GROUPS - 1) / LP_GROUPS;
-    c.groups = (units + c.span - 1) / c.span;
-    const long long want = (2ll * sms + E - 1) / E;
-    c.splits = int(std::max(1ll, std::min(want, (long long)(c.groups + LP_WARPS - 1) / LP_WARPS)));
-    return c;
-}
-size_t part_bytes(long long E, const Cut& c) { return align256(size_t(E) * c.splits * sizeof(float4)); }
-size_t most_bytes(long long E, const Cut& c) { return align256(size_t(E) * (c.groups + 2) * 4); }
+// tiles of a row, at most
+int tiles_of(int V, int bytes) { return std::max(1, (V / (16 / bytes) + LP_VECS - 1) / LP_VECS); }
+size_t list_bytes(long long E) { return align256(size_t(E) * 4); }
+size_t part_bytes(long long E, int tiles) { return align256(size_t(E) * (tiles + 1) * sizeof(float4)); }
 
 constexpr long long LP_MAX_ENTRIES = 1 << 24;
 
@@ -530,15 +689,8 @@ extern "C" {
 
 size_t spec_token_logprobs_workspace_size(int64_t E, int V) {
     if (E < 0 || E > LP_MAX_ENTRIES || V < 1 || V > (1 << 24)) return 0;
-    const int sms = sm_count();
-    if (sms <= 0) return 0;
-    if (E == 0) return 256;
-    size_t n = 256;  // (the element's size is not known here)
-    for (int bytes : {4, 2}) {
-        const Cut c = cut_of(E, V, unit_of(bytes), sms);
-        if (c.splits > 1) n = std::max(n, part_bytes(E, c) + most_bytes(E, c));
-    }
-    return n;
+    const int tiles = tiles_of(V, 4);  // (the element's size is not known here: the larger)
+    return list_bytes(E) + 2 * part_bytes(E, tiles) + 256;
 }
 
 spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int64_t R, int64_t row_stride, int V, const int32_t* rows,
@@ -558,7 +710,6 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int64_t R,
     const int sms = sm_count();
     if (sms <= 0) return SPEC_ERR_CUDA;
     if (!aligned(workspace, 256) || workspace_bytes < spec_token_logprobs_workspace_size(E, V)) return SPEC_ERR_WORKSPACE;
-    const Cut c = cut_of(E, V, unit_of(dtype_bytes(dtype)), sms);
     LogprobArgs A = {};
     A.logits = logits;
     A.R = R;
@@ -570,18 +721,19 @@ spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, int64_t R,
     A.entropy = entropy;
     A.ids = top_ids;
     A.top_lp = top_logprobs;
-    A.part = static_cast<float4*>(workspace);
-    A.most = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(E, c));
+    A.tiles = tiles_of(V, dtype_bytes(dtype));
+    char* room = static_cast<char*>(workspace);
+    A.list = reinterpret_cast<int32_t*>(room);
+    A.part = reinterpret_cast<float4*>(room += list_bytes(E));
+    A.most = reinterpret_cast<float4*>(room + part_bytes(E, A.tiles));
     A.status = dev_status;
     A.V = V;
     A.top = top;
-    A.splits = c.splits;
-    A.span = c.span;
-    A.groups = c.groups;
+    A.E = E;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == SPEC_F32    ? launch_logprob<SPEC_F32>(A, E, st)
-                          : dtype == SPEC_BF16 ? launch_logprob<SPEC_BF16>(A, E, st)
-                                               : launch_logprob<SPEC_F16>(A, E, st);
+    const cudaError_t e = dtype == SPEC_F32    ? launch_logprob<SPEC_F32>(A, sms, st)
+                          : dtype == SPEC_BF16 ? launch_logprob<SPEC_BF16>(A, sms, st)
+                                               : launch_logprob<SPEC_F16>(A, sms, st);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
