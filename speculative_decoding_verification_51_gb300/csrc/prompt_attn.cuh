@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
             }
             const bool none = tot == 0.f;
             const float inv = none ? 0.f : 1.f / tot;
+            const uint64_t inv2 = f2_pack(inv, inv);
             uint16_t* out = static_cast<uint16_t*>(A.out) + ((long long)(w.q0 + t * A.tokens) * A.Hq + w.h * A.G) * A.D;
             // (its stages: behind the first row tile's, if that has some)
             const RingAt<ST> start = os;
@@ -680,7 +681,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 auto put = [&](const uint32_t (&u)[32], int d) {
                     float f[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = none ? 0.f : __uint_as_float(u[e]);
+                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(u[e]);  // (0 of a row that sees nothing)
                     if (__builtin_expect(odd, 0) && mine) {
                         // what it sees of values that are not finite
                         for (int s = 0; s < bad_tiles[gen]; ++s) {
@@ -706,8 +707,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     for (int y = 0; y < 4; ++y) {
                         uint32_t v[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = none ? 0u : pack16<F16>(f[8 * y + 2 * e] * inv, f[8 * y + 2 * e + 1] * inv);
+                        for (int e = 0; e < 4; ++e) {
+                            float a, b;
+                            f2_unpack(f2_mul(f2_pack(f[8 * y + 2 * e], f[8 * y + 2 * e + 1]), inv2), a, b);
+                            v[e] = pack16<F16>(a, b);
+                        }
                         *reinterpret_cast<uint4*>(row + (((d % 64 / 8 + y) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 };
