@@ -280,7 +280,7 @@ spec_status spec_prompt_attention(const void* q, int64_t q_token_stride, int64_t
     A.G = G;
     A.D = D;
     A.tokens = tokens;
-    A.window = window;
+    A.window = window < M ? window : 0;  // (one that holds every key is none; sums with it stay in 32 bits)
     A.c = scale * 1.4426950408889634f;
     A.status = dev_status;
     // (without keys nothing is copied: any map will do)

@@ -447,39 +447,43 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
                 RingAt<ST> at = first;
                 const int rows = w.m - j * PROMPT_KEYS;  // of the prompt
+                // (keys that every row sees may hold anything: the first ones, but for a window's end)
+                const int from = j < w.all_down ? 0 : min(max(w.last + 1 - j * PROMPT_KEYS, 0), PROMPT_KEYS);
                 for (int c = 0; c < C; ++c, at.next()) {
                     wait(&full[at.st], at.phase);
-                    uint4* stage = reinterpret_cast<uint4*>(ring + at.st * S::STAGE);
-                    if (rows < PROMPT_KEYS)
-                        for (int x = tid; x < S::STAGE / 16; x += N)
-                            if (((x >> 3) & 127) >= rows) stage[x] = make_uint4(0, 0, 0, 0);
-                    // an exponent of all ones carries into the bit above it
-                    constexpr uint32_t EX = F16 ? 0x7c007c00u : 0x7f807f80u, ONE = F16 ? 0x04000400u : 0x00800080u;
 #pragma unroll 1
-                    for (int x0 = tid; x0 < S::STAGE / 16; x0 += 8 * N) {
-                        uint32_t hit = 0;
-                        uint4 v[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) v[y] = stage[x0 + y * N];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            hit |= ((v[y].x & EX) + ONE) | ((v[y].y & EX) + ONE) | ((v[y].z & EX) + ONE) | ((v[y].w & EX) + ONE);
-                        if (__builtin_expect(hit & 0x80008000u, 0)) {
+                    for (int half = 0; half < S::CH / 64; ++half) {
+                        uint4* part = reinterpret_cast<uint4*>(ring + at.st * S::STAGE + half * 16384);  // 8 of a row
+                        for (int x = max(rows, from) * 8 + tid; x < PROMPT_KEYS * 8; x += N) part[x] = make_uint4(0, 0, 0, 0);
+                        // an exponent of all ones carries into the bit above it
+                        constexpr uint32_t EX = F16 ? 0x7c007c00u : 0x7f807f80u, ONE = F16 ? 0x04000400u : 0x00800080u;
+                        const int end = min(rows, PROMPT_KEYS) * 8;
 #pragma unroll 1
-                            for (int x = x0; x < x0 + 8 * N; x += N) {
-                                uint32_t u[4] = {stage[x].x, stage[x].y, stage[x].z, stage[x].w};
-                                uint32_t some = 0;
+                        for (int x0 = from * 8 + tid; x0 < end; x0 += 8 * N) {
+                            uint32_t hit = 0;
+                            uint4 v[8];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t h = ((u[e] & EX) + ONE) & 0x80008000u;
-                                    some |= h;
-                                    u[e] &= ~((h >> 15) * 0xffffu);
-                                }
-                                if (some) {
-                                    stage[x] = make_uint4(u[0], u[1], u[2], u[3]);
-                                    const int row = (x >> 3) & 127;
-                                    atomicOr(&bad[gen][slot][row >> 5], 1u << (row & 31));
-                                    bad_item[gen] = round;
+                            for (int y = 0; y < 8; ++y) v[y] = part[min(x0 + y * N, end - 1)];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                hit |= ((v[y].x & EX) + ONE) | ((v[y].y & EX) + ONE) | ((v[y].z & EX) + ONE) | ((v[y].w & EX) + ONE);
+                            if (__builtin_expect(hit & 0x80008000u, 0)) {
+#pragma unroll 1
+                                for (int x = x0; x < min(end, x0 + 8 * N); x += N) {
+                                    uint32_t u[4] = {part[x].x, part[x].y, part[x].z, part[x].w};
+                                    uint32_t some = 0;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const uint32_t h = ((u[e] & EX) + ONE) & 0x80008000u;
+                                        some |= h;
+                                        u[e] &= ~((h >> 15) * 0xffffu);
+                                    }
+                                    if (some) {
+                                        part[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                                        const int row = x >> 3;
+                                        atomicOr(&bad[gen][slot][row >> 5], 1u << (row & 31));
+                                        bad_item[gen] = round;
+                                    }
                                 }
                             }
                         }
