@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["plan.cu", "row_stats.cu", "sample.cu", "verify.cu", "tree.cu", "lmhead.cu", "host_io.cu",
            "rope.cu", "nodes.cu", "tree_attn.cu", "tree_attn_bf16.cu", "tree_attn_f16.cu",
-           "tree_attn_e4m3.cu", "norm.cu", "prompt.cu", "prompt_attn_bf16.cu", "prompt_attn_f16.cu", "logprob.cu",
+           "tree_attn_e4m3.cu", "norm.cu", "norm_e4m3.cu", "prompt.cu", "prompt_attn_bf16.cu", "prompt_attn_f16.cu", "logprob.cu",
            "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"]

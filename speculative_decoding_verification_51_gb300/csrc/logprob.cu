@@ -35,7 +35,7 @@ constexpr int LP_JOIN = 128, LP_JOIN_WARPS = LP_JOIN / 32;  // threads that join
 constexpr int LP_VECS = 256, LP_STAGES = 2;  // of a tile; of a warp's ring
 constexpr int LP_BYTES = LP_VECS * 16;
 constexpr size_t LP_SMEM = size_t(LP_WARPS) * LP_STAGES * LP_BYTES;
-constexpr int LP_CANDIDATES = 1024;
+constexpr int LP_CANDIDATES = 1024, LP_SOME = 128;  // tokens that there is room for, and that are compared with one another
 constexpr float LP_LOWEST = -3.4028234663852886e38f, LP_FAR = -200.f;  // 2^LP_FAR is 0 in float32
 
 struct LogprobArgs {
@@ -191,7 +191,6 @@ struct Best {  // what a CTA needs for the alternatives
     float value[LP_CANDIDATES];
     int id[LP_CANDIDATES];
     int group[SPEC_MAX_TOP];
-    float at_least;
     int chosen, found;
     int digits[256], digit, left;
     bool exact;
@@ -246,28 +245,21 @@ __device__ __forceinline__ void of_groups(const LogprobArgs& A, const Row<DT>& r
     }
 }
 
-// The alternatives of a row (all of the CTA); most(g): the largest logit of its group g.
-template <int DT, class F>
-__device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>& row, Best& B, F&& most, const Sums& s, float T,
-                                            long long e) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = row.tiles * 4 + 2;
-    const float log_z = log2f(s.z);
-    // The largest bound that `top` groups reach, eight bits after eight, until as many as wanted
-    // reach it; those above it, and of those at it the first.
-    // (bf16 has no more bits than two digits hold, f16 as float no more than three)
-    constexpr int LAST = DT == SPEC_BF16 ? 16 : DT == SPEC_F16 ? 8 : 0;
-    const uint32_t none = ordered(-INFINITY) >> LAST << LAST;
-    uint32_t bound = 0;   // the digits so far
-    int want = A.top;     // groups to be taken with these digits
-    bool exact = false;   // as many have them
-    auto key = [&](int g) { return ordered(most(g)) >> LAST << LAST; };
+// The largest bound that `top` of the keys reach which each(f) gives f, eight bits after eight, until as
+// many as wanted reach it (then `exact`: those at or above it; else those above it and `want` of those at
+// it).  False where there are fewer: then all of them.  (All of the CTA.)
+template <int LAST, class F>
+__device__ __forceinline__ bool reach(Best& B, int top, F&& each, uint32_t& bound, int& want, bool& exact) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bound = 0;  // the digits so far
+    want = top;
+    exact = false;
     for (int shift = 24; shift >= LAST && !exact; shift -= 8) {
         for (int i = threadIdx.x; i < 256; i += LP_JOIN) B.digits[i] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < G; i += LP_JOIN) {
-            const uint32_t k = key(i);
-            if (k > none && (shift == 24 || (k ^ bound) >> (shift + 8) == 0)) atomicAdd(&B.digits[k >> shift & 255u], 1);
-        }
+        each([&](uint32_t k) {
+            if (shift == 24 || (k ^ bound) >> (shift + 8) == 0) atomicAdd(&B.digits[k >> shift & 255u], 1);
+        });
         __syncthreads();
         if (warp == 0) {  // from the largest digit down, eight a lane
             int n[8], all = 0;
@@ -282,10 +274,10 @@ __device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>&
                 const int y = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += y;
             }
-            const unsigned reach = __ballot_sync(0xffffffffu, sum >= want);
-            if (reach == 0) {  // fewer than wanted: all of them
+            const unsigned there = __ballot_sync(0xffffffffu, sum >= want);
+            if (there == 0) {
                 if (lane == 0) B.digit = -1;
-            } else if (lane == __ffs(reach) - 1) {
+            } else if (lane == __ffs(there) - 1) {
                 int before = sum - all, d = 255 - lane * 8, i = 0;
                 while (before + n[0] < want && i < 7) {
                     before += n[0];
@@ -300,30 +292,50 @@ __device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>&
             }
         }
         __syncthreads();
-        if (B.digit < 0) {
-            bound = none + 1;
-            want = G;
-            break;
-        }
+        if (B.digit < 0) return false;
         bound |= uint32_t(B.digit) << shift;
         want = B.left;
         exact = B.exact;
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        B.chosen = B.found = 0;
-        const uint32_t u = max(bound, ordered(LP_LOWEST));
-        B.at_least = __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-    }
+    return true;
+}
+
+// the least float whose key is `bound` or more (none of -inf)
+__device__ __forceinline__ float float_of(uint32_t bound) {
+    const uint32_t u = max(bound, ordered(LP_LOWEST));
+    return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+// The alternatives of a row (all of the CTA); most(g): the largest logit of its group g.
+template <int DT, class F>
+__device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>& row, Best& B, F&& most, const Sums& s, float T,
+                                            long long e) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = row.tiles * 4 + 2;
+    const float log_z = log2f(s.z);
+    // (bf16 has no more bits than two digits hold, f16 as float no more than three)
+    constexpr int LAST = DT == SPEC_BF16 ? 16 : DT == SPEC_F16 ? 8 : 0;
+    const uint32_t none = ordered(-INFINITY) >> LAST << LAST;
+    auto key = [&](int g) { return ordered(most(g)) >> LAST << LAST; };
+    uint32_t bound;
+    int want;
+    bool exact;
+    const bool enough = reach<LAST>(B, A.top, [&](auto&& f) {
+        for (int i = threadIdx.x; i < G; i += LP_JOIN) {
+            const uint32_t k = key(i);
+            if (k > none) f(k);
+        }
+    }, bound, want, exact);
+    if (!enough) bound = none + 1;
+    if (threadIdx.x == 0) B.chosen = B.found = 0;
     __syncthreads();
     // (in any order: they are only looked through)
-    const bool all_at = exact || want == G;
     for (int i = threadIdx.x; i < G; i += LP_JOIN) {
         const uint32_t k = key(i);
-        if (k > none && (k > bound || (all_at && k == bound) || (exact && k >= bound))) B.group[atomicAdd(&B.chosen, 1)] = i;
+        if (k > none && (k > bound || (k == bound && (exact || !enough)))) B.group[atomicAdd(&B.chosen, 1)] = i;
     }
     __syncthreads();
-    if (!all_at && warp == 0) {  // equal ones: the first
+    if (!exact && enough && warp == 0) {  // equal ones: the first
         int chosen = B.chosen, left = want;
         for (int i0 = 0; i0 < G && left > 0; i0 += 32) {
             const bool is = i0 + lane < G && key(i0 + lane) == bound;
@@ -337,16 +349,33 @@ __device__ __forceinline__ void best_tokens(const LogprobArgs& A, const Row<DT>&
         if (lane == 0) B.chosen = chosen;
     }
     __syncthreads();
-    const float least = B.at_least;
-    of_groups<DT>(A, row, B, least, [&](float v, int i) {
-        const int n = atomicAdd(&B.found, 1);
-        if (n < LP_CANDIDATES) {
-            B.value[n] = v;
-            B.id[n] = i;
+    float least = float_of(bound);
+    auto look = [&]() {
+        of_groups<DT>(A, row, B, least, [&](float v, int i) {
+            const int n = atomicAdd(&B.found, 1);
+            if (n < LP_CANDIDATES) {
+                B.value[n] = v;
+                B.id[n] = i;
+            }
+        });
+        __syncthreads();
+        return B.found;
+    };
+    int found = look();
+    if (found > LP_SOME) {
+        // few groups, or many as good as the worst group's largest (a small vocabulary): the bound that `top`
+        // of the tokens themselves reach
+        __syncthreads();
+        const float at = least;
+        if (reach<LAST>(B, A.top, [&](auto&& f) {
+                of_groups<DT>(A, row, B, at, [&](float v, int) { f(ordered(v) >> LAST << LAST); });
+            }, bound, want, exact)) {
+            least = float_of(bound);
+            if (threadIdx.x == 0) B.found = 0;
+            __syncthreads();
+            found = look();
         }
-    });
-    __syncthreads();
-    const int found = B.found;
+    }
     int32_t* ids = A.ids + e * A.top;
     float* lps = A.top_lp + e * A.top;
     for (int i = min(found, A.top) + threadIdx.x; i < A.top; i += LP_JOIN) {

@@ -122,14 +122,9 @@ spec_status spec_norm_kv_write(const spec_kv_cache* cache, const spec_head_norm*
     A.slots = reinterpret_cast<const long long*>(slots);
     A.status = dev_status;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (e4)
-        e = dtype == SPEC_F32    ? launch_rotate_vec<float, true, NORM>(A, st)
-            : dtype == SPEC_BF16 ? launch_rotate_vec<__nv_bfloat16, true, NORM>(A, st)
-                                 : launch_rotate_vec<__half, true, NORM>(A, st);
-    else
-        e = dtype == SPEC_BF16 ? launch_rotate_vec<__nv_bfloat16, false, NORM>(A, st)
-                               : launch_rotate_vec<__half, false, NORM>(A, st);
+    const cudaError_t e = e4                   ? launch_norm_e4m3(A, dtype, st)
+                          : dtype == SPEC_BF16 ? launch_rotate_vec<__nv_bfloat16, false, NORM>(A, st)
+                                               : launch_rotate_vec<__half, false, NORM>(A, st);
     return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -291,6 +291,7 @@ spec_status spec_prompt_attention(const void* q, int64_t q_token_stride, int64_t
     if (r != SPEC_OK) return r;
     if (!M) L.mk = L.mv = L.mq;
     L.items = prompt_max_items(B, T, G) * kv_heads;
+    if (L.items > (1ll << 30)) return SPEC_ERR_UNSUPPORTED;  // (places are 32 bits in the kernel)
     L.sms = sm_count();
     if (L.sms <= 0) return SPEC_ERR_CUDA;
     L.st = reinterpret_cast<cudaStream_t>(stream);

@@ -34,7 +34,6 @@
 #include "cache.cuh"
 
 namespace sv {
-namespace {
 
 constexpr int ROT_THREADS = 256;
 struct Heads {  // one side of a rotated tensor
@@ -63,6 +62,12 @@ struct RotArgs {
     int w_dtype;
     float eps;
 };
+
+// norm_e4m3.cu: norms on the way into an 8-bit cache (translation units of their own, to be compiled
+// side by side)
+cudaError_t launch_norm_e4m3(const RotArgs& A, int dtype, cudaStream_t st);
+
+namespace {
 
 // Whether a call has more than the rotation (spec_norm_rope, spec_norm_kv_write): each
 // head of q and k is divided by the root of its mean square and multiplied by the

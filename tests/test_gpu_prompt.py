@@ -103,6 +103,15 @@ def test_no_tokens():
     assert bool((out == 3).all())
 
 
+@pytest.mark.parametrize("D", [64, 256])
+def test_no_keys(D):
+    """Queries without any key: zeros, and no key tensor is touched."""
+    q = randn((40, 4, D), BF, gen(1))
+    k = torch.empty((0, 2, D), dtype=BF, device="cuda")
+    out = check(q, k, k, [0, 33, 40], [0, 0, 0])
+    assert bool((out == 0).all())
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_keys_ahead_and_queries_that_see_nothing(D):
     """With fewer keys than queries the first queries see nothing: zeros."""
