@@ -557,7 +557,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 const uint32_t sa = tbase + lanes + buf * 128;
                 wait(&sf[buf], MT == 2 ? tiles : tiles >> 1);
                 at_after();
-                enter();
+                // (in an item of few tiles of keys the first ones and those not seen whole are not ordered: products
+                // are not what they wait for.  64 prompts of 300 tokens 150 -> 126 us; in longer ones it pays
+                // there too, 16001 tokens 1286 -> 1263)
+                const bool masked = j >= up || j < down;
+                if (jb - ja >= 8 || !(masked || j == ja)) enter();
                 uint32_t x[4][32];
                 float m0 = -INFINITY, m1 = -INFINITY, s0, s1;
                 auto largest = [&](int y) {
@@ -567,11 +571,13 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                         m1 = fmaxf(fmaxf(__uint_as_float(x[y][e + 2]), __uint_as_float(x[y][e + 3])), m1);
                     }
                 };
-                auto hide = [&](int y) {
+                auto hide = [&](int y) {  // a bit for each key that the row sees
                     const int above = end - j * PROMPT_KEYS - y * 32, below = begin - j * PROMPT_KEYS - y * 32;
+                    const uint32_t seen = (above >= 31 ? ~0u : above < 0 ? 0u : (2u << above) - 1u) &
+                                          (below <= 0 ? ~0u : below > 31 ? 0u : ~0u << below);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (e > above || e < below) x[y][e] = 0xff800000u;
+                        if (!(seen & 1u << e)) x[y][e] = 0xff800000u;
                 };
                 // (a warp's few tokens see most pieces whole)
                 auto partly = [&](int y) {
@@ -597,7 +603,6 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     at2 = f2_pack(at, at);
                     sum0 = sum1 = f2_pack(0.f, 0.f);
                 };
-                const bool masked = j >= up || j < down;
                 at_ld32(sa, x[0]);
                 at_ld32(sa + 32, x[1]);
                 at_ld_wait(x[0]);
