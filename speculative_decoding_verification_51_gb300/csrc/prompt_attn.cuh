@@ -5,18 +5,28 @@
 // window, j > i + m - n - window): o = sum_j 2^(c s_j - r) v_j / sum_j 2^(c s_j - r), s = q k,
 // in one pass over the keys with a running reference r.
 //
-// A CTA takes one item: two tiles of 128 rows (one of a wide head), whose softmax and
-// products take turns: while the weights of one are made, the tensor cores work for the other.
-//   warp 0        TMA: the rows of Q, then K and V of 128 keys by turns through one ring
+// One CTA an SM, items one after another without a break between them.  An item is two tiles of 128
+// rows (one of a wide head), whose softmax and products take turns: while the weights of one are
+// made, the tensor cores work for the other.
+//   warp 0        TMA: the rows of Q, then K and V of 128 keys by turns through one ring, and behind an
+//                 item's last V a stage a row tile for its rows of O
 //   warps 1, 2    one thread of a warp a row tile issues the products: S = Q K^T into TMEM, O += P V with
-//                 P in TMEM, over the columns that S had
+//                 P in TMEM, over the columns that S had.  (A wide head has warp 1 alone.)
 //   warp 3        in tiles of keys that some row does not see whole: V's rows past the prompt, and
-//                 values that are not finite, become zero (a weight of zero would not hide them)
+//                 values that are not finite, become zero (a weight of zero would not hide them); what a row
+//                 sees of such values is added to its sums at the end
 //   warps 4..     softmax, one row a thread: the scores in registers, the weights back to
 //                 TMEM as 16 bits, the row's reference and total in registers; then the row of O
 //
 // As in k_attn_tiles the reference is raised only when a score passes it by some octaves, so
 // that O is seldom rescaled; weights are rounded to the queries' type, relative.
+//
+// 16001 tokens of 32 query heads over 8 of 128 channels take 1250 us out of L2 (1680 TFLOP/s, 0.86 of the
+// measured burst rate, 0.98 of the sustained one), 1360 out of HBM; 8192 of 32 over 32 heads 373.  What bounds it: of 2400 cycles
+// a step (a tile of keys for both row tiles) the tensor cores need 2048, and the scores' products, both
+// operands in shared memory, want all of its 128 bytes a cycle.  Heads of 256 channels run at
+// 1170 TFLOP/s (one row tile: its softmax and products wait for one another), of 64 at 830 (the softmax of a
+// tile takes as long, its products half).
 #pragma once
 
 #include <algorithm>
