@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "prompt.cuh"
+#include "ring.cuh"
 
 namespace sv {
 namespace {
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     __shared__ __align__(8) uint64_t pv, near, clean, fin;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
+    __shared__ uint32_t copied;  // stages that warp 0 has begun to fill
     __shared__ int busy[2][4];  // a row tile's softmax at work, by the quarter of the SM that it shares with the other's
     // values that are not finite, by the parity of the CTA's item: in which tiles of keys, which tokens
     __shared__ uint32_t bad[2][S::HIDDEN][4];
@@ -229,6 +231,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         mbar_init(&clean, CLEANERS);
         mbar_init(&fin, MT);
         abort_flag = 0;
+        copied = 0;
         for (int i = 0; i < 8; ++i) busy[i >> 2][i & 3] = 0;
         fence_mbarrier_init();
     }
@@ -243,10 +246,14 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     const uint32_t tbase = tmem_base;
     constexpr uint32_t T_O = 256;  // S buffers at 0 and 128 (and P over them), then O
     volatile int* gone = &abort_flag;
-    // a bounded wait; once one has run out nobody waits any more
+    // A bounded wait; once one has run out nobody waits any more.  Some last for many steps (until an item's
+    // first tile that is not seen whole; of a row tile that has nothing to do for an item), as many as
+    // there are keys: so what is bounded is the time in which no stage is copied, of which a step has several.
+    volatile uint32_t* moved = &copied;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity & 1u) || *gone) return;
-        if (!at_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) *gone = 1;
+        if (!wait_while_moving([&]() { return at_wait_bounded(bar, parity & 1u, AT_WAIT_NS) || *gone; }, [&]() { return *moved; }))
+            *gone = 1;
     };
 
     if (warp < 4) {
@@ -287,10 +294,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     if (MT == 2 && j == w.j0) query(MT - 1);
                     keys(&mv, j);
                 }
-                for (uint32_t n = w.out_stages(); n && !*gone; --n, ++i) {
+                for (uint32_t n = w.out_stages(); n && !*gone; --n) {
                     const uint32_t st = i % ST;
                     wait(&empty[st], (i / ST) ^ 1u);
                     at_arrive(&full[st]);
+                    *moved = ++i;
                 }
             }
             // every copy has landed before the CTA leaves (they have, unless a wait ran out)

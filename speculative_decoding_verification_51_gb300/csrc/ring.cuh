@@ -2,7 +2,8 @@
 // begins and waits for in order: which stage and phase comes next, and what is still to
 // be done once a wait has run out.  No copy is begun then (its stage's barrier may be
 // armed already, and the copy before it may still write there), and none is left in
-// flight when the kernel ends (its shared memory may be another CTA's by then).
+// flight when the kernel ends (its shared memory may be another CTA's by then).  And
+// waits that last as long as the work that others do meanwhile.
 // Plain C++: the host tests run it against copies that are late.
 #pragma once
 
@@ -36,5 +37,17 @@ struct CopyRing {
         for (uint32_t i = first_lost; i != begun; ++i) wait(i % STAGES, (i / STAGES) & 1u);
     }
 };
+
+// A wait for what may lie any number of steps ahead: `attempt` waits for a bounded time and
+// says whether it came; as long as `moved` (a count of the kernel's steps) changes during
+// an attempt in vain there is another.  False: nothing has moved for a whole attempt.
+template <class Try, class Count>
+SV_RING bool wait_while_moving(Try&& attempt, Count&& moved) {
+    for (;;) {
+        const uint32_t seen = moved();
+        if (attempt()) return true;
+        if (moved() == seen) return false;
+    }
+}
 
 }  // namespace sv
