@@ -589,7 +589,7 @@ class _CTable(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
-class _CNorm(ctypes.Structure):
+class _CNorm(ctypes.Structure):  # (for callers of the C entries)
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("dtype", ctypes.c_int),
                 ("eps", ctypes.c_float)]
 
@@ -656,25 +656,22 @@ def rope_table(rot: int, *, base: float = 10000.0, layout: str = "half", scaling
 class HeadNorm:
     """The norm of each head of queries and keys ahead of the rotation (spec_head_norm):
     x / sqrt(mean(x^2) + eps) * weight.  Weights [head_dim], float32, bfloat16 or
-    float16, the same type for both; None: ones.  The tensors stay the caller's."""
+    float16, the same type for both; None: ones.  The tensors stay the caller's, and every call
+    takes them as they are then: memory and type may be others than at first."""
 
     def __init__(self, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, *,
                  eps: float = 1e-6):
-        dtype = torch.float32
         for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if t is None:
                 continue
             if t.dtype not in _DTYPES:
                 raise ValueError(f"{n} must be float32, bfloat16 or float16, got {t.dtype}")
             _check(t, n, t.dtype)
-            dtype = t.dtype
         if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
             raise ValueError("q_weight and k_weight must have one type")
         if not 0 <= eps < 3.4e38:
             raise ValueError("eps must be finite and at least 0")
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
-        self._c = _CNorm(_ptr(q_weight), _ptr(k_weight), _DTYPES[dtype], eps)
-        self._ref = ctypes.addressof(self._c)
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, table: RopeTable | None, *,

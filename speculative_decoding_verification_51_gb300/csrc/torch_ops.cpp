@@ -53,7 +53,7 @@ struct Ref {  // an owned reference
 
 // Attribute names, made once.
 #define NAMES(X) X(_ref) X(k) X(v) X(k_scale) X(v_scale) X(turns) X(positions) X(slots) X(masks) X(context_len) X(page_table) X(page_size) \
-    X(num_pages) X(buffer) X(workspace) X(q_weight) X(k_weight) X(num_tokens) X(num_keys) X(q_heads) X(kv_heads) X(prompts) X(stream_id) X(device_index) X(device_type)
+    X(num_pages) X(buffer) X(workspace) X(q_weight) X(k_weight) X(eps) X(num_tokens) X(num_keys) X(q_heads) X(kv_heads) X(prompts) X(stream_id) X(device_index) X(device_type)
 struct Names {
 #define X(n) PyObject* n = nullptr;
     NAMES(X)
@@ -235,21 +235,32 @@ struct Cache {
     c10::Device device() const { return k.device(); }
 };
 
+// A norm as it is at this call: what is checked here is what the kernel reads (a module can give
+// its weights other memory, or another type, after the norm was made of them).
 struct Norm {
-    const spec_head_norm* n;
     Tensor q, k;  // weights, where there are some
-    explicit Norm(PyObject* o) : n(reinterpret_cast<const spec_head_norm*>(int_attr(o, N._ref))) {
-        Ref x(attr(o, N.q_weight)), y(attr(o, N.k_weight));
+    spec_head_norm n = {};
+    explicit Norm(PyObject* o) {
+        Ref x(attr(o, N.q_weight)), y(attr(o, N.k_weight)), e(attr(o, N.eps));
         if (const Tensor* t = maybe(x.p, "q_weight")) q = *t;
         if (const Tensor* t = maybe(y.p, "k_weight")) k = *t;
+        const double eps = PyFloat_AsDouble(e.p);
+        if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+        n.eps = float(eps);
+        n.dtype = SPEC_F32;
     }
-    void fits(int64_t D, c10::Device dev) const {
-        if (q.defined()) flat_of(q, "q_weight", D, dev);
-        if (k.defined()) flat_of(k, "k_weight", D, dev);
+    void fits(int64_t D, c10::Device dev) {
+        n.q_weight = weight(q, "q_weight", D, dev);
+        n.k_weight = weight(k, "k_weight", D, dev);
+        if (q.defined() && k.defined() && q.scalar_type() != k.scalar_type()) bad("q_weight and k_weight must have one type");
     }
-    static void flat_of(const Tensor& t, const char* name, int64_t D, c10::Device dev) {
+    const void* weight(const Tensor& t, const char* name, int64_t D, c10::Device dev) {
+        if (!t.defined()) return nullptr;
         on_device(t, name, dev);
+        n.dtype = dtype_of(t, name);
         if (t.numel() != D) bad(std::string(name) + " has " + std::to_string(t.numel()) + " entries for heads of " + std::to_string(D));
+        if (!t.is_contiguous()) bad(std::string(name) + " must be contiguous");
+        return t.data_ptr();
     }
 };
 
@@ -556,7 +567,7 @@ PyObject* norm_rope(PyObject* const* a) {
     OnStream on(a[7]);
     const Tensor& q = tensor(a[0], "q");
     const Tensor *k = maybe(a[1], "k"), *pos = maybe(a[2], "positions");
-    const Norm norm(a[4]);
+    Norm norm(a[4]);
     if (!pos != (a[3] == Py_None)) bad("a rotation needs positions and a table");
     const spec_rope_table* table = nullptr;
     if (pos) table = reinterpret_cast<const spec_rope_table*>(int_attr(a[3], N._ref));
@@ -583,7 +594,7 @@ PyObject* norm_rope(PyObject* const* a) {
     on.uses({&q, k, pos, &oq, &ok, &norm.q, &norm.k});
     if (pos) on.uses_attrs(a[3], {N.turns});
     run("spec_norm_rope", dev, [&](spec_stream_t st) {
-        return spec_norm_rope(norm.n, rq.p, rq.heads, rq.step, rq.head, ro.p, ro.step, ro.head, rk.p, rk.heads, rk.step,
+        return spec_norm_rope(&norm.n, rq.p, rq.heads, rq.step, rq.head, ro.p, ro.step, ro.head, rk.p, rk.heads, rk.step,
                               rk.head, rp.p, rp.step, rp.head, dt, int(D), rq.n, pp, table, st);
     });
     if (!k) return same(a[5], oq);
@@ -630,7 +641,7 @@ PyObject* norm_kv_write(PyObject* const* a) {
     on.uses_cache(a[0]);
     if (table) on.uses_attrs(a[5], {N.turns});
     run("spec_norm_kv_write", dev, [&](spec_stream_t st) {
-        return spec_norm_kv_write(c.c, norm ? norm->n : nullptr, rk.p, rk.step, rk.head, rp.p, rp.step, rp.head, rv.p, rv.step,
+        return spec_norm_kv_write(c.c, norm ? &norm->n : nullptr, rk.p, rk.step, rk.head, rp.p, rp.step, rp.head, rv.p, rv.step,
                                   rv.head, dt, rk.n, sp, pp, table, rq.p, rq.heads, rq.step, rq.head, ro.p, ro.step,
                                   ro.head, st_word, st);
     });
