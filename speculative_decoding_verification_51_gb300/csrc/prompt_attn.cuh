@@ -246,14 +246,40 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
     const uint32_t tbase = tmem_base;
     constexpr uint32_t T_O = 256;  // S buffers at 0 and 128 (and P over them), then O
     volatile int* gone = &abort_flag;
-    // A bounded wait; once one has run out nobody waits any more.  Some last for many steps (until an item's
-    // first tile that is not seen whole; of a row tile that has nothing to do for an item), as many as
-    // there are keys: so what is bounded is the time in which no stage is copied, of which a step has several.
-    volatile uint32_t* moved = &copied;
+    // A bounded wait; once one has run out nobody waits any more.  Whoever was not waited for to the
+    // end (`lost`) leaves its loop, warps that meet at a barrier together.  Until then a warp may
+    // arrive at barriers that it had to wait for first, so arrivals are single ones (of several at once
+    // some could be more than are pending, which is undefined), and at `full` and `qf`, which count
+    // bytes too, warp 0 alone arrives, behind a wait that was not cut short.
+    bool lost = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity & 1u) || *gone) return;
-        if (!wait_while_moving([&]() { return at_wait_bounded(bar, parity & 1u, AT_WAIT_NS) || *gone; }, [&]() { return *moved; }))
+        if (mbar_try_wait(bar, parity & 1u)) return;
+        if (*gone || !at_wait_bounded(bar, parity & 1u, AT_WAIT_NS)) {
             *gone = 1;
+            lost = true;
+        }
+    };
+    // For what may be many steps ahead, as many as there are keys (an item's first tile that is not seen whole; the
+    // next item's scores for a row tile that has nothing to do for this one): what is bounded is the time in
+    // which no stage is copied, of which a step has several.  (All waits in this form, whose code is longer:
+    // 32 prompts of 20 to 2000 tokens 402 us, 8192 tokens of 256 channels 505; in this way 385 and 467.)
+    volatile uint32_t* moved = &copied;
+    auto wait_long = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity & 1u)) return;
+        if (!wait_while_moving([&]() { return at_try_wait(bar, parity & 1u); }, [&]() { return *gone != 0; }, [&]() { return *moved; },
+                               []() { return globaltimer_ns(); }, AT_WAIT_NS)) {
+            *gone = 1;
+            lost = true;
+        }
+    };
+    // a barrier of `n` threads: whether it is lost to any of them
+    auto any_lost = [&](int id, int n) {
+        uint32_t any;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(any)
+                     : "r"(uint32_t(lost)), "r"(id), "r"(n)
+                     : "memory");
+        return any != 0;
     };
 
     if (warp < 4) {
@@ -297,17 +323,16 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 for (uint32_t n = w.out_stages(); n && !*gone; --n) {
                     const uint32_t st = i % ST;
                     wait(&empty[st], (i / ST) ^ 1u);
+                    if (*gone) break;
                     at_arrive(&full[st]);
                     *moved = ++i;
                 }
             }
-            // every copy has landed before the CTA leaves (they have, unless a wait ran out)
-            if (*gone) {
-                for (int t = 0; t < MT; ++t)
-                    if (uses[t]) at_wait_bounded(&qf[t], (uses[t] - 1) & 1u, AT_WAIT_NS / 8);
-                for (uint32_t x = i > ST ? i - ST : 0; x < i; ++x)
-                    at_wait_bounded(&full[x % ST], (x / ST) & 1u, AT_WAIT_NS / 8);
-            }
+            // every copy has landed before the CTA leaves, whoever used it
+            for (int t = 0; t < MT; ++t)
+                if (uses[t]) at_wait_bounded(&qf[t], (uses[t] - 1) & 1u, AT_WAIT_NS / 8);
+            for (uint32_t x = i > ST ? i - ST : 0; x < i; ++x)
+                at_wait_bounded(&full[x % ST], (x / ST) & 1u, AT_WAIT_NS / 8);
         }
     } else if (warp <= MT) {
         // ---- products, a warp a row tile: what one waits for and sends out of turn (some 600 cycles
@@ -415,10 +440,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
         Steps w, after;
         bool more = next_of(w);
         if (more) scores_of(w, w.j0);
-        while (more) {
+        while (more && !__any_sync(0xffffffffu, lost)) {
             const bool next = next_of(after);
             int j = w.j0;
             for (; j + 1 < w.j1; ++j) {
+                if (__any_sync(0xffffffffu, lost)) break;
                 if (MT == 1) scores_of(w, j + 1);
                 sums_of(w, j);
                 if (MT == 2) scores_of(w, j + 1);
@@ -448,8 +474,9 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < C; ++c) vs.next();
         int gen = 0;
+        bool left = false;
         auto ahead = Work::words(A, place_of(0), total);
-        for (int round = 0; place_of(round) < total; ++round) {
+        for (int round = 0; place_of(round) < total && !left; ++round) {
             const Work w(A, ahead);
             ahead = Work::words(A, place_of(round + 1), total);
             int slot = 0;
@@ -459,10 +486,11 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 2 * C; ++c) vs.next();
                 if (!w.any_hidden(j)) continue;
-                wait(&near, told++);
+                wait_long(&near, told++);
                 if (slot == 0 && tid == 0) bad_tiles[gen] = 0;
                 if (tid < 4) bad[gen][slot][tid] = 0;
-                asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
+                left = any_lost(2, N);
+                if (left) break;
                 RingAt<ST> at = first;
                 const int rows = w.m - j * PROMPT_KEYS;  // of the prompt
                 // (keys that every row sees may hold anything: the first ones, but for a window's end)
@@ -554,7 +582,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             RingAt<ST> at = lent;
             for (int x = 0; x < C; ++x, at.next())
-                asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&empty[at.st])), "n"(MT) : "memory");
+                for (int y = 0; y < MT; ++y) at_arrive(&empty[at.st]);
         };
         RingAt<ST> os;  // the item's first stage
         uint32_t tiles = 0, outs = 0;  // tiles of weights, and finished rows, so far
@@ -570,6 +598,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
             const int up = t ? w.up[MT - 1] : w.up[0], down = t ? w.down[MT - 1] : w.down[0];
             float ref = -INFINITY, tot = 0.f;
             if (jb <= ja) release();
+            else wait_long(&sf[MT == 2 ? t : tiles & 1u], MT == 2 ? tiles : tiles >> 1);
             for (int j = ja; j < jb; ++j, ++tiles) {
                 const uint32_t buf = MT == 2 ? t : tiles & 1u;
                 const uint32_t sa = tbase + lanes + buf * 128;
@@ -641,7 +670,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     at_ld_wait(x[3]);
                     largest(2);
                     largest(3);
-                    again = __any_sync(0xffffffffu, fmaxf(m0, m1) * c > ref + TilesRange<F16>::SLACK);
+                    again = __any_sync(0xffffffffu, lost || fmaxf(m0, m1) * c > ref + TilesRange<F16>::SLACK);
                 } else {
                     if (masked) {
                         if (partly(0)) hide(0);
@@ -659,6 +688,10 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     largest(3);
                 }
                 if (__builtin_expect(again, 0)) {
+                    if (__any_sync(0xffffffffu, lost)) {
+                        at_st_wait();
+                        break;
+                    }
                     const float top = fmaxf(m0, m1) * c;
                     const bool raise = top > ref + TilesRange<F16>::SLACK;
                     if (__any_sync(0xffffffffu, raise)) {
@@ -761,8 +794,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 const int rows = max(0, min(A.tokens, w.n - t * A.tokens)) * A.G;
                 const bool whole = rows == A.tokens * A.G;
                 if (whole) fence_proxy_async_smem();
-                auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(4 + t) : "memory"); };
-                sync();
+                if (any_lost(4 + t, 128)) break;
                 if (!whole) {
                     const uint32_t each = uint32_t(A.D) / 8;
                     for (uint32_t x = threadIdx.x & 127; x < uint32_t(rows) * each; x += 128) {
@@ -773,7 +805,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                     }
                     // (what is copied in here next comes by another path)
                     fence_proxy_async_smem();
-                    sync();
+                    asm volatile("bar.sync %0, 128;" ::"r"(4 + t) : "memory");
                 }
                 if ((threadIdx.x & 127) == 0) {
                     if (whole) {

@@ -38,15 +38,24 @@ struct CopyRing {
     }
 };
 
-// A wait for what may lie any number of steps ahead: `attempt` waits for a bounded time and
-// says whether it came; as long as `moved` (a count of the kernel's steps) changes during
-// an attempt in vain there is another.  False: nothing has moved for a whole attempt.
-template <class Try, class Count>
-SV_RING bool wait_while_moving(Try&& attempt, Count&& moved) {
-    for (;;) {
-        const uint32_t seen = moved();
+// A wait for what may lie any number of steps ahead: `attempt` waits for a short time and says
+// whether it came.  False: others have given up, or `moved` (a count of the kernel's steps) has
+// not changed for `limit` by the clock.  (Nothing is looked at ahead of the first attempt, which
+// is the last one of nearly every wait.)
+template <class Try, class Gone, class Count, class Clock>
+SV_RING bool wait_while_moving(Try&& attempt, Gone&& gone, Count&& moved, Clock&& clock, uint64_t limit) {
+    uint64_t since = 0;
+    for (uint32_t seen = 0;;) {
         if (attempt()) return true;
-        if (moved() == seen) return false;
+        if (gone()) return false;
+        const uint64_t now = clock();
+        const uint32_t count = moved();
+        if (!since || count != seen) {
+            since = now;
+            seen = count;
+        } else if (now - since > limit) {
+            return false;
+        }
     }
 }
 

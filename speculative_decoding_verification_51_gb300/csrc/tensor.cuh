@@ -19,21 +19,24 @@ struct TilesRange {
 };
 constexpr uint64_t AT_WAIT_NS = 200000000ull;
 
-// As mbar_wait_bounded, for warps that wait long: the hint lets the hardware suspend
-// the thread for up to 20 us a try, where bare tries take issue slots from
-// the SM's other warps.
+// As mbar_try_wait and mbar_wait_bounded, for warps that wait long: the hint lets the
+// hardware suspend the thread for up to 20 us a try, where bare tries take issue slots
+// from the SM's other warps.
+__device__ __forceinline__ bool at_try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool at_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-            : "memory");
-        if (ok) return true;
+        if (at_try_wait(bar, parity)) return true;
         const uint64_t t = globaltimer_ns();
         if (!t0) t0 = t;
         else if (t - t0 > limit_ns) return false;
