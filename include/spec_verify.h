@@ -746,8 +746,12 @@ spec_status spec_kv_commit(const spec_kv_cache* caches, int num_caches, const ui
  * The norm of each head: y = x / sqrt(mean(x^2) + eps) * weight over the head's
  * channels, ahead of the rotation.  Squares, sums and products are float32 (so that
  * |x| has to stay below 2^63 or so), the result of norm and rotation is rounded once.
- *   q_weight, k_weight  [head_dim] of `dtype` (f32, bf16 or f16), device; NULL: ones.
- *   eps                 finite and at least 0.  With 0 a head of zeros gives NaN.
+ * A head with an infinity gives NaN there (and in the channel that it turns with) and
+ * zeros elsewhere; one with a NaN gives NaN.
+ *   q_weight, k_weight  [head_dim] of `dtype` (f32, bf16 or f16), device, finite; NULL:
+ *                       ones.
+ *   eps                 finite and at least 0.  With 0 a head of zeros gives NaN (and
+ *                       squares must not vanish: of |x| below 2^-75 they do).
  */
 typedef struct {
     const void* q_weight;

@@ -229,6 +229,10 @@ __global__ void __launch_bounds__(ROT_THREADS, N ? 2 : 3) k_rotate(const __grid_
     // With a norm: weights and angles of this lane's item in one factor each, two side by side (what a head costs
     // in instructions bounds the kernel: with the weights read for each head, 32771 tokens took 129 us).
     // Half layout: y_a = fac0 a + fac1 b, y_b = fac2 a + fac3 b; else y = fac0 x + fac1 (x, the pair's exchanged).
+    // Where nothing turns fac1 is 0, and the pair's other channel, which may be infinite, is masked to 0 (2% of
+    // the time of pairs side by side; a choice made for each head or by a branch for infinite ones took 4 to 6).
+    const uint32_t other_bits = pt.turns ? ~0u : 0u;
+    auto masked = [&](float f) { return __uint_as_float(__float_as_uint(f) & other_bits); };
     uint64_t fac[N ? (PAIR ? 2 * VEC : VEC) : 1];
     auto factors = [&](int kind) {
         if constexpr (N) {
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(ROT_THREADS, N ? 2 : 3) k_rotate(const __grid_
                         f2_unpack(f2_mul(ff, f2_fma(fac[e], a2[e], f2_mul(fac[VEC / 2 + e], b2[e]))), va[2 * e], va[2 * e + 1]);
                         f2_unpack(f2_mul(ff, f2_fma(fac[VEC + e], a2[e], f2_mul(fac[VEC * 3 / 2 + e], b2[e]))), vb[2 * e], vb[2 * e + 1]);
                     } else {
-                        const uint64_t other = f2_pack(va[2 * e + 1], va[2 * e]);
+                        const uint64_t other = f2_pack(masked(va[2 * e + 1]), masked(va[2 * e]));
                         f2_unpack(f2_mul(ff, f2_fma(fac[e], a2[e], f2_mul(fac[VEC / 2 + e], other))), va[2 * e], va[2 * e + 1]);
                     }
                 }
