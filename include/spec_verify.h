@@ -840,7 +840,8 @@ spec_status spec_prompt_plan(const int32_t* offsets, const int32_t* k_offsets, i
  * Scores and sums are float32; weights are rounded to q's type before they meet v, and of
  * f16 weights those below 2^-33 of the row's largest may add nothing, though the total
  * has them.  What a query does not see has no effect on it, whatever it holds (infinities and
- * NaN too).
+ * NaN too).  A value that it sees and that is not finite makes its channel infinite or NaN (NaN where
+ * the weight is too small for q's type).  Behind SPEC_BADBIT_TIMEOUT out and lse hold nothing of use.
  */
 spec_status spec_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                   const void* k, int64_t k_token_stride, int64_t k_head_stride,

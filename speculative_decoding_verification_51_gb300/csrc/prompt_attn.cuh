@@ -163,7 +163,6 @@ struct PromptWork {
         }
         if (j1 == 0) j0 = 0;
     }
-    __device__ __forceinline__ bool in(int t, int j) const { return j >= lo[t] && j < hi[t]; }
     __device__ __forceinline__ bool any_hidden(int j) const { return j >= all_up || j < all_down; }
     // stages of the ring, behind the item's values, for its rows of O on their way out: of row tiles
     // that see something (the others' zeros go out directly)
