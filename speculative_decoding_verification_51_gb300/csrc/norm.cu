@@ -8,7 +8,7 @@
 // up their squares and join the sums by shuffles; weights and angles are one factor each,
 // made when a lane turns to another tensor.  Bound by instructions and HBM: 32771 tokens of 40
 // heads of 128 channels take 114 us (0.87 of the measured copy rate) at two CTAs an SM; 4608
-// tokens into an 8-bit cache and back 35.
+// tokens into an 8-bit cache and back 36.
 #include "rotate.cuh"
 
 using namespace sv;

@@ -21,12 +21,13 @@
 // As in k_attn_tiles the reference is raised only when a score passes it by some octaves, so
 // that O is seldom rescaled; weights are rounded to the queries' type, relative.
 //
-// 16001 tokens of 32 query heads over 8 of 128 channels take 1250 us out of L2 (1680 TFLOP/s, 0.86 of the
-// measured burst rate, 0.98 of the sustained one), 1360 out of HBM; 8192 of 32 over 32 heads 373.  What bounds it: of 2400 cycles
-// a step (a tile of keys for both row tiles) the tensor cores need 2048, and the scores' products, both
-// operands in shared memory, want all of its 128 bytes a cycle.  Heads of 256 channels run at
-// 1170 TFLOP/s (one row tile: its softmax and products wait for one another), of 64 at 830 (the softmax of a
-// tile takes as long, its products half).
+// 16001 tokens of 32 query heads over 8 of 128 channels take 1380 us (1520 TFLOP/s, 0.78 of the measured burst rate,
+// 0.88 of the sustained one), and 1270 in ten passes over the same inputs, which end before the power limit lowers the clock
+// (1.99 GHz, then 1.82 to 1.85); 8192 of 32 over 32 heads 374.  What bounds it: of some 3020 cycles a step (a tile of
+// keys for both row tiles) the tensor cores need 2048, and the scores' products, both operands in shared memory, want
+// all of its 128 bytes a cycle; the rest is what the two tiles' softmax and products wait for one another.
+// Heads of 256 channels run at 1180 TFLOP/s (one row tile: its softmax and products wait for one another), of 64 at
+// 820 (the softmax of a tile takes as long, its products half).  At 168 registers a thread some 50 bytes spill.
 #pragma once
 
 #include <algorithm>
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(PromptShape<DP>::THREADS, 1)
                 wait(&sf[buf], MT == 2 ? tiles : tiles >> 1);
                 at_after();
                 // (in an item of few tiles of keys the first ones and those not seen whole are not ordered: products
-                // are not what they wait for.  64 prompts of 300 tokens 150 -> 126 us; in longer ones it pays
+                // are not what they wait for.  64 prompts of 300 tokens 150 -> 125 us; in longer ones it pays
                 // there too, 16001 tokens 1286 -> 1263)
                 const bool masked = j >= up || j < down;
                 if (jb - ja >= 8 || !(masked || j == ja)) enter();
